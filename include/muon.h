@@ -445,6 +445,147 @@ MUON_API int muon_newton_schulz_noalloc(const void* X, void* Y, int rows, int co
                                         int io_dtype, int ns_method, int ns_steps,
                                         int operand_mode, void* stream);
 
+/* ---------------------------------------------------------------------
+ * The two ends of a language model.
+ *
+ * A Muon run keeps the embedding and the output head in its auxiliary
+ * groups.  These calls compute what feeds them: the embedding lookup and its
+ * gradient (summed in FP32 straight into the flat accumulation buffer, as
+ * muon_accumulate adds a dense gradient), and the losses of a post-training
+ * run with the gradient of the logits.
+ *
+ * Conventions, beside those above:
+ *   - Element types are muon_dtype_t; token indexes are muon_index_t (int32
+ *     or int64, device memory).  A NEGATIVE index means "no token here"
+ *     (padding, prompt): the row takes no part, whatever it holds.  An index
+ *     past the table or the vocabulary is treated the same and recorded:
+ *     muon_device_error then returns 17.
+ *   - Strides are in elements between the starts of rows; the elements of a
+ *     row are contiguous.  Any stride >= the row's length and any base
+ *     aligned to its type is taken; rows whose starts are 16-byte aligned run
+ *     fastest.
+ *   - Sums, maxima and statistics are FP32 or wider; results are rounded
+ *     once, when they are written.  Every sum has a fixed order: the same
+ *     inputs give the same bits.
+ *   - No call allocates, synchronises or keeps state: scratch, where a call
+ *     needs any, is the caller's `workspace` (16-byte aligned device memory
+ *     of at least the bytes its *_workspace function returns, which the call
+ *     may write until its work on `stream` is done).  All may be captured
+ *     into CUDA graphs once each has run on the device.
+ *   - n_tokens = 0 is valid (losses then write zero statistics).
+ * ------------------------------------------------------------------- */
+typedef enum { MUON_INDEX_INT32 = 0, MUON_INDEX_INT64 = 1 } muon_index_t;
+
+/* out[t][c] = scale * table[ids[t]][c], rounded once to out_dtype; zeros for
+ * a negative id.
+ *   table : device, rows x cols of table_dtype, table_stride >= cols
+ *   out   : device, n_tokens x cols of out_dtype, out_stride >= cols; may
+ *           not overlap the table
+ * Errors: MUON_ERR_INVALID for NULL or misaligned pointers, unknown types,
+ * rows or cols < 1, n_tokens < 0 or > 2^30, strides < cols, a non-finite
+ * scale. */
+MUON_API int muon_embedding(const void* table, int table_dtype, int64_t table_stride, int rows,
+                            int cols, const void* ids, int ids_type, int64_t n_tokens,
+                            float scale, void* out, int out_dtype, int64_t out_stride,
+                            void* stream);
+
+/* The lookup's gradient, for the parameter `param` (rows x cols at flat
+ * index offset; num_heads and use_muon are not looked at):
+ *     accum[row v] = (overwrite ? 0 : accum[row v])
+ *                    + scale * sum over t with ids[t] = v of dout[t]
+ * The sum runs in FP32 over the tokens in order of their position, in blocks
+ * of a fixed length, and is scaled once.  Without overwrite only rows of
+ * tokens that occur are read and written; with overwrite every row is written
+ * (zeros where no token occurs).  Nothing outside the parameter is touched.
+ *   accum : device float storage buffer, 16-byte aligned
+ *   dout  : device, n_tokens x cols of dout_dtype, dout_stride >= cols
+ *   param : host
+ *   parts, nparts : host table of the buffer's partitions; nparts = 0: the
+ *           storage index is the flat index
+ *   workspace : muon_embedding_grad_workspace(n_tokens, cols) bytes
+ * Errors: MUON_ERR_INVALID as muon_embedding, for a bad table (as muon_step),
+ * a short or misaligned workspace; MUON_ERR_UNSUPPORTED if the parameter lies
+ * in more than MUON_EMBEDDING_MAX_SEGMENTS partitions. */
+#define MUON_EMBEDDING_MAX_SEGMENTS 128
+MUON_API int muon_embedding_grad_workspace(int64_t n_tokens, int cols, size_t* bytes);
+MUON_API int muon_embedding_grad(float* accum, const void* dout, int dout_dtype,
+                                 int64_t dout_stride, const void* ids, int ids_type,
+                                 int64_t n_tokens, float scale, int overwrite,
+                                 const muon_param_t* param, const muon_partition_t* parts,
+                                 int nparts, void* workspace, size_t workspace_bytes,
+                                 void* stream);
+
+/* logp[t] = log softmax(logit_scale * logits[t])[targets[t]], 0 where the
+ * target is negative (that row is not read).  What a reference or sampling
+ * policy's scores are made with, and the forward half of the two losses.
+ * Logits of minus infinity have probability 0; a row with a NaN, a plus
+ * infinity or nothing but minus infinities has logp NaN.
+ *   logits : device, n_tokens x vocab of dtype, stride >= vocab
+ *   logp   : device float[n_tokens]
+ *   logit_scale : > 0 and finite (1 / temperature)
+ * Errors: MUON_ERR_INVALID. */
+MUON_API int muon_token_logprobs(const void* logits, int dtype, int64_t stride, int64_t n_tokens,
+                                 int vocab, const void* targets, int targets_type,
+                                 float logit_scale, float* logp, void* stream);
+
+/* The clipped policy loss with a KL term, and its gradient.  For each token t
+ * with a target >= 0 and weights[t] != 0 (the others take no part: their
+ * logits and inputs are not read, their logp is 0 and their gradient row 0):
+ *     r  = exp(logp - old_logp[t])           (1 if old_logp is NULL)
+ *     p  = -min(r A, clamp(r, 1 - clip_low, 1 + clip_high) A),  A = advantages[t]
+ *     k  = exp(ref_logp[t] - logp) - (ref_logp[t] - logp) - 1   (0 if NULL)
+ *     loss = sum_t weights[t] (p + kl_coef k)
+ * The gradient takes p as -r A where r A <= clamp(r) A, else as constant
+ * (old_logp, NULL or not, is a constant).  weights carry the mask and the
+ * normalisation (1 / active tokens, 1 / (sequences * length), over the whole
+ * step when micro-batches are accumulated).
+ *   stats   : device float[4]: loss, sum w p, sum w k, sum of the weights of
+ *             tokens whose ratio is clipped
+ *   logp    : device float[n_tokens]
+ *   dlogits : device, n_tokens x vocab of dtype, dlogits_stride >= vocab:
+ *             the gradient of the loss, every element written; or NULL (loss
+ *             only).  It may be the logits themselves (same address and
+ *             stride): they are then replaced.  Any other overlap is an error.
+ * Errors: MUON_ERR_INVALID, also for negative or non-finite clip_low,
+ * clip_high or kl_coef, and kl_coef > 0 without ref_logp. */
+MUON_API int muon_policy_loss(const void* logits, int dtype, int64_t stride, int64_t n_tokens,
+                              int vocab, const void* targets, int targets_type,
+                              const float* advantages, const float* weights,
+                              const float* old_logp, const float* ref_logp, float clip_low,
+                              float clip_high, float kl_coef, float logit_scale, float* stats,
+                              float* logp, void* dlogits, int64_t dlogits_stride, void* stream);
+
+/* The preference loss of paired log ratios, and its gradient.  Sequence i
+ * holds the tokens [offsets[i], offsets[i + 1]); sequence i < n_pairs is the
+ * preferred answer of pair i and sequence n_pairs + i the other one.
+ *     s_i = sum over the sequence's tokens with a target >= 0 of
+ *           logp[t] - ref_logp[t]            (ref_logp NULL: logp[t])
+ *     h_i = beta (s_i - s_{n_pairs + i})
+ *     loss = sum_i w_i (-(1 - label_smoothing) log sigmoid(h_i)
+ *                       - label_smoothing log sigmoid(-h_i))
+ *   offsets : device, 2 * n_pairs + 1 of offsets_type (muon_index_t), not
+ *             decreasing, within [0, n_tokens] (else they are clamped and
+ *             muon_device_error returns 18); tokens outside every sequence
+ *             get logp and a zero gradient
+ *   pair_weights : device float[n_pairs], or NULL: 1 / n_pairs.  A pair of
+ *             weight 0 adds nothing, and its gradient rows are 0
+ *   stats   : device float[4]: loss, sum w h, sum of w over pairs with h > 0,
+ *             sum w
+ *   margins : device float[n_pairs], h
+ *   logp, dlogits : as muon_policy_loss (logp 0 where the target is negative)
+ *   workspace : muon_preference_loss_workspace(n_tokens) bytes
+ * Errors: MUON_ERR_INVALID, also for a non-finite beta, label_smoothing
+ * outside [0, 1], a short or misaligned workspace. */
+MUON_API int muon_preference_loss_workspace(int64_t n_tokens, size_t* bytes);
+MUON_API int muon_preference_loss(const void* logits, int dtype, int64_t stride, int64_t n_tokens,
+                                  int vocab, const void* targets, int targets_type,
+                                  const void* offsets, int offsets_type, int n_pairs,
+                                  const float* ref_logp, const float* pair_weights, float beta,
+                                  float label_smoothing, float logit_scale, float* stats,
+                                  float* margins, float* logp, void* dlogits,
+                                  int64_t dlogits_stride, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
 /* Host-side counters (no GPU work).  Returns MUON_OK. */
 MUON_API int muon_get_stats(muon_stats_t* out);
 
@@ -512,6 +653,8 @@ MUON_API void muon_release_workspace(void);
  * 4 = a dependency of the SM-pair kernel).  A library built with MUON_DEBUG
  * also checks every streaming-kernel tile against the extents its tables
  * describe and records 16 for a tile that would leave them (and skips it).
+ * 17 and 18 are bad token indexes and sequence offsets (see "The two ends of a
+ * language model").
  * A step whose products hit such an error also reports applied = -1. */
 MUON_API int muon_device_error(void);
 

@@ -39,7 +39,9 @@ EXPORTED = ["muon_accumulate", "muon_accumulate_n", "muon_step", "muon_newton_sc
             "muon_step_ex", "muon_profile_enable_phases", "muon_describe_tables",
             "muon_testing_set", "muon_dp_plan_create", "muon_dp_plan_destroy",
             "muon_dp_plan_sizes", "muon_dp_plan_tables", "muon_dp_pack", "muon_dp_unpack",
-            "muon_dp_finish"]
+            "muon_dp_finish", "muon_embedding", "muon_embedding_grad",
+            "muon_embedding_grad_workspace", "muon_token_logprobs", "muon_policy_loss",
+            "muon_preference_loss", "muon_preference_loss_workspace"]
 CLIP_MODES = {"update": 0, "grad": 1}
 
 
@@ -128,11 +130,25 @@ def lib():
         L.muon_describe_tables.argtypes = [P, I, P, I, I, I, ctypes.POINTER(TableInfo)]
         L.muon_profile_read.argtypes = [ctypes.POINTER(PhaseTime), I, I]
         L.muon_testing_set.argtypes = [I, I]
+        S = ctypes.POINTER(ctypes.c_size_t)
+        L.muon_embedding.argtypes = [P, I, I64, I, I, P, I, I64, F, P, I, I64, P]
+        L.muon_embedding_grad_workspace.argtypes = [I64, I, S]
+        L.muon_embedding_grad.argtypes = [P, P, I, I64, P, I, I64, F, I, P, P, I, P,
+                                          ctypes.c_size_t, P]
+        L.muon_token_logprobs.argtypes = [P, I, I64, I64, I, P, I, F, P, P]
+        L.muon_policy_loss.argtypes = [P, I, I64, I64, I, P, I, P, P, P, P, F, F, F, F, P, P, P,
+                                       I64, P]
+        L.muon_preference_loss_workspace.argtypes = [I64, S]
+        L.muon_preference_loss.argtypes = [P, I, I64, I64, I, P, I, P, I, I, P, P, F, F, F, P, P,
+                                           P, P, I64, P, ctypes.c_size_t, P]
         for name in ("muon_accumulate", "muon_accumulate_n", "muon_step", "muon_step_ex",
                      "muon_newton_schulz", "muon_newton_schulz_noalloc", "muon_get_stats",
                      "muon_device_error", "muon_profile_enable", "muon_profile_read",
                      "muon_profile_enable_phases", "muon_describe_tables",
-                     "muon_testing_set"):
+                     "muon_testing_set", "muon_embedding", "muon_embedding_grad",
+                     "muon_embedding_grad_workspace", "muon_token_logprobs",
+                     "muon_policy_loss", "muon_preference_loss",
+                     "muon_preference_loss_workspace"):
             getattr(L, name).restype = I
         _lib = L
     return _lib
@@ -320,6 +336,256 @@ def newton_schulz(X, Y=None, ns_method="gram", ns_steps: int = 5, operand_mode="
     _check(lib().muon_newton_schulz(_ptr(X), _ptr(Y), X.shape[0], X.shape[1], io, method,
                                     ns_steps, mode, _stream(stream)))
     return Y
+
+
+# ------------------------------------------------------------------ the two ends of a model
+
+def _dtype(x, name):
+    import torch
+    if x.dtype == torch.bfloat16:
+        return DTYPES["bf16"]
+    if x.dtype == torch.float32:
+        return DTYPES["fp32"]
+    raise ValueError(f"{name} must be bfloat16 or float32, not {x.dtype}")
+
+
+def _index(x, name):
+    import torch
+    if not x.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if x.dtype == torch.int64:
+        return 1
+    if x.dtype == torch.int32:
+        return 0
+    raise ValueError(f"{name} must be int32 or int64, not {x.dtype}")
+
+
+def _rows(x, name):
+    """The stride between the rows of a 2-D tensor whose rows are contiguous."""
+    if x.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    if x.shape[1] > 1 and x.stride(1) != 1:
+        raise ValueError(f"{name}'s rows must be contiguous")
+    return x.stride(0) if x.shape[0] > 1 else max(x.stride(0), x.shape[1])
+
+
+def _per_token(x, n, name):
+    """A contiguous float32 tensor of n elements (or None)."""
+    import torch
+    if x is None:
+        return None
+    if x.dtype != torch.float32 or x.numel() != n or not x.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 tensor of {n} elements")
+    return x.data_ptr()
+
+
+def _same_device(x, *others):
+    for o in others:
+        if o is not None and o.device != x.device:
+            raise ValueError("every tensor must be on one device")
+
+
+class _On:
+    """The device of `x` made current, and torch's current stream set to
+    `stream` (a torch stream, a cudaStream_t or None), so that tensors made
+    inside belong to the stream the kernels run on."""
+
+    def __init__(self, x, stream):
+        import torch
+        self.ctx = []
+        if x.device.type != "cuda":
+            raise ValueError("tensors must be on a CUDA device")
+        if x.device.index != torch.cuda.current_device():
+            self.ctx.append(torch.cuda.device(x.device))
+        if stream is not None:
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream, device=x.device)
+            self.ctx.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for c in self.ctx:
+            c.__enter__()
+        return _stream(None)
+
+    def __exit__(self, *exc):
+        for c in reversed(self.ctx):
+            c.__exit__(*exc)
+        return False
+
+
+def embedding(table, ids, scale: float = 1.0, out=None, out_dtype=None, stream=None):
+    """scale * table[ids] (muon_embedding): table rows x cols, bf16 or fp32;
+    ids int32 or int64 of any shape, a negative id giving zeros.  Returns a
+    tensor of ids' shape plus cols, of out_dtype (default: the table's), or
+    fills `out` (2-D with any row stride, or contiguous)."""
+    import torch
+    stride, it = _rows(table, "table"), _index(ids, "ids")
+    cols, n = table.shape[1], ids.numel()
+    _same_device(table, ids, out)
+    with _On(table, stream) as s:
+        if out is None:
+            out = torch.empty((*ids.shape, cols), dtype=out_dtype or table.dtype, device=table.device)
+        elif out.shape[-1] != cols or out.numel() != n * cols or (out_dtype not in (None, out.dtype)):
+            raise ValueError("out must hold ids' shape plus the table's columns")
+        ostride = _rows(out, "out") if out.dim() == 2 else cols
+        if out.dim() != 2 and not out.is_contiguous():
+            raise ValueError("out must be contiguous or 2-D")
+        _check(lib().muon_embedding(table.data_ptr(), _dtype(table, "table"), stride, table.shape[0],
+                                    cols, ids.data_ptr(), it, n, scale, out.data_ptr(),
+                                    _dtype(out, "out"), ostride, s))
+    return out
+
+
+def embedding_grad(accum, dout, ids, param, parts=None, scale: float = 1.0,
+                   overwrite: bool = False, workspace=None, stream=None):
+    """The lookup's gradient added to (or, with overwrite, put in place of)
+    the parameter's elements of the flat FP32 buffer `accum`
+    (muon_embedding_grad).  dout: tokens x cols, bf16 or fp32; ids as given to
+    embedding(); param: (offset, rows, cols) or a row of a PARAM_DTYPE table;
+    parts: the buffer's partition table, None where the storage index is the
+    flat index; workspace: a CUDA tensor of at least
+    embedding_grad_workspace(tokens, cols) bytes (default: a new one)."""
+    import torch
+    if hasattr(param, "dtype"):
+        param = (param["offset"], param["rows"], param["cols"])
+    offset, rows, cols = (int(v) for v in param)
+    if accum.dtype != torch.float32 or not accum.is_contiguous():
+        raise ValueError("accum must be a contiguous float32 tensor")
+    if dout.dim() != 2:
+        dout = dout.reshape(-1, cols)
+    n, it = ids.numel(), _index(ids, "ids")
+    if dout.shape[0] != n or dout.shape[1] != cols:
+        raise ValueError("dout must be tokens x cols")
+    stride = _rows(dout, "dout")
+    _same_device(accum, dout, ids, workspace)
+    q, nq = _table(parts, PART_DTYPE)
+    need = offset + rows * cols if nq == 0 else int((q["storage_offset"] + q["flat_end"] - q["flat_begin"]).max())
+    if accum.numel() < need:
+        raise ValueError(f"accum holds {accum.numel()} elements, the tables describe {need}")
+    p = np.array([(offset, rows, cols, 0, 0)], dtype=PARAM_DTYPE)
+    with _On(accum, stream) as s:
+        if workspace is None:
+            workspace = torch.empty(embedding_grad_workspace(n, cols), dtype=torch.uint8,
+                                    device=accum.device)
+        _check(lib().muon_embedding_grad(accum.data_ptr(), dout.data_ptr(), _dtype(dout, "dout"), stride,
+                                         ids.data_ptr(), it, n, scale, int(overwrite), p.ctypes.data,
+                                         q.ctypes.data if nq else None, nq, workspace.data_ptr(),
+                                         workspace.numel() * workspace.element_size(), s))
+    return accum
+
+
+def embedding_grad_workspace(n_tokens: int, cols: int) -> int:
+    """Bytes of scratch embedding_grad needs."""
+    b = ctypes.c_size_t()
+    _check(lib().muon_embedding_grad_workspace(n_tokens, cols, ctypes.byref(b)))
+    return b.value
+
+
+def _logits(logits, targets):
+    """(2-D logits, stride, tokens, vocab, type of the targets)."""
+    if logits.dim() != 2:
+        logits = logits.view(-1, logits.shape[-1])
+    stride, n = _rows(logits, "logits"), targets.numel()
+    if logits.shape[0] != n:
+        raise ValueError("one target per row of logits")
+    return logits, stride, n, logits.shape[1], _index(targets, "targets")
+
+
+def token_logprobs(logits, targets, logit_scale: float = 1.0, out=None, stream=None):
+    """log softmax(logit_scale * logits) at the targets (muon_token_logprobs):
+    logits tokens x vocab, bf16 or fp32 (leading dimensions are joined);
+    targets int32 or int64, a negative one giving 0.  Returns float32 of
+    targets' shape."""
+    import torch
+    logits, stride, n, vocab, tt = _logits(logits, targets)
+    _same_device(logits, targets, out)
+    with _On(logits, stream) as s:
+        if out is None:
+            out = torch.empty(targets.shape, dtype=torch.float32, device=logits.device)
+        _check(lib().muon_token_logprobs(logits.data_ptr(), _dtype(logits, "logits"), stride, n, vocab,
+                                         targets.data_ptr(), tt, logit_scale, _per_token(out, n, "out"), s))
+    return out
+
+
+def _dlogits(logits, stride, dlogits):
+    """The gradient's buffer: as given, a new one (True; with the logits' row
+    stride, so that its rows are aligned as theirs), or None (False)."""
+    import torch
+    if dlogits is True:
+        n, vocab = logits.shape
+        d = torch.empty((n, stride), dtype=logits.dtype, device=logits.device)
+        return d if stride == vocab else d[:, :vocab], stride
+    if dlogits is False or dlogits is None:
+        return None, 0
+    if dlogits.dim() != 2:
+        dlogits = dlogits.view(-1, dlogits.shape[-1])
+    if dlogits.dtype != logits.dtype or dlogits.shape != logits.shape:
+        raise ValueError("dlogits must match the logits' shape and type")
+    return dlogits, _rows(dlogits, "dlogits")
+
+
+def policy_loss(logits, targets, advantages, weights, old_logp=None, ref_logp=None,
+                clip_low: float = 0.2, clip_high: float = 0.2, kl_coef: float = 0.0,
+                logit_scale: float = 1.0, dlogits=True, stream=None) -> dict:
+    """The clipped policy loss with a KL term and the gradient of its logits
+    (muon_policy_loss).  advantages, weights, old_logp, ref_logp: float32, one
+    per token; weights hold mask and normalisation.  dlogits: True (a new
+    buffer), False (loss only), or a tensor to fill -- the logits themselves
+    to replace them.  Returns {"stats": float32[4] (loss, policy term, KL,
+    clipped weight), "logp": per token, "dlogits"}, all on the device."""
+    import torch
+    logits, stride, n, vocab, tt = _logits(logits, targets)
+    _same_device(logits, targets, advantages, weights, old_logp, ref_logp)
+    with _On(logits, stream) as s:
+        d, dstride = _dlogits(logits, stride, dlogits)
+        _same_device(logits, d)
+        logp = torch.empty(targets.shape, dtype=torch.float32, device=logits.device)
+        stats = torch.empty(4, dtype=torch.float32, device=logits.device)
+        _check(lib().muon_policy_loss(
+            logits.data_ptr(), _dtype(logits, "logits"), stride, n, vocab, targets.data_ptr(), tt,
+            _per_token(advantages, n, "advantages"), _per_token(weights, n, "weights"),
+            _per_token(old_logp, n, "old_logp"), _per_token(ref_logp, n, "ref_logp"), clip_low,
+            clip_high, kl_coef, logit_scale, stats.data_ptr(), logp.data_ptr(), _ptr(d), dstride, s))
+    return {"stats": stats, "logp": logp, "dlogits": d}
+
+
+def preference_loss(logits, targets, offsets, ref_logp=None, beta: float = 0.1,
+                    label_smoothing: float = 0.0, pair_weights=None, logit_scale: float = 1.0,
+                    dlogits=True, workspace=None, stream=None) -> dict:
+    """The preference loss of paired log ratios and the gradient of its logits
+    (muon_preference_loss).  offsets: 2 * pairs + 1 positions (int32 or int64,
+    on the device); sequence i < pairs is pair i's preferred answer, sequence
+    pairs + i the other; tokens with a negative target (prompts) are left out.
+    Returns {"stats": float32[4] (loss, mean margin, share of positive
+    margins, weight), "margins": float32[pairs], "logp", "dlogits"}."""
+    import torch
+    logits, stride, n, vocab, tt = _logits(logits, targets)
+    if offsets.numel() % 2 != 1:
+        raise ValueError("offsets must hold 2 * pairs + 1 positions")
+    pairs, ot = offsets.numel() // 2, _index(offsets, "offsets")
+    _same_device(logits, targets, offsets, ref_logp, pair_weights, workspace)
+    with _On(logits, stream) as s:
+        d, dstride = _dlogits(logits, stride, dlogits)
+        _same_device(logits, d)
+        logp = torch.empty(targets.shape, dtype=torch.float32, device=logits.device)
+        out = torch.empty(4 + pairs, dtype=torch.float32, device=logits.device)
+        stats, margins = out[:4], out[4:]
+        if workspace is None:
+            workspace = torch.empty(preference_loss_workspace(n), dtype=torch.uint8, device=logits.device)
+        _check(lib().muon_preference_loss(
+            logits.data_ptr(), _dtype(logits, "logits"), stride, n, vocab, targets.data_ptr(), tt,
+            offsets.data_ptr(), ot, pairs, _per_token(ref_logp, n, "ref_logp"),
+            _per_token(pair_weights, pairs, "pair_weights"), beta, label_smoothing, logit_scale,
+            stats.data_ptr(), margins.data_ptr(), logp.data_ptr(), _ptr(d), dstride,
+            workspace.data_ptr(), workspace.numel() * workspace.element_size(), s))
+    return {"stats": stats, "margins": margins, "logp": logp, "dlogits": d}
+
+
+def preference_loss_workspace(n_tokens: int) -> int:
+    """Bytes of scratch preference_loss needs."""
+    b = ctypes.c_size_t()
+    _check(lib().muon_preference_loss_workspace(n_tokens, ctypes.byref(b)))
+    return b.value
 
 
 def get_stats() -> dict:

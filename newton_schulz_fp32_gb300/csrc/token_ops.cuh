@@ -1,0 +1,107 @@
+// Shared by the operators at the two ends of a language model (embedding.cu,
+// losses.cu): element types, token indexes, the device error flag.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "muon_internal.h"
+
+namespace muon {
+
+// Codes these operators record for muon_device_error.
+constexpr int kErrIndex = 17;     // a token id or target >= the table's rows / the vocabulary
+constexpr int kErrOffsets = 18;   // sequence offsets that decrease or leave [0, tokens]
+
+namespace tok {
+
+// 16 bytes of T as floats and back.
+template <typename T> struct Vec;
+
+template <> struct Vec<float> {
+  static constexpr int N = 4;
+  static __device__ __forceinline__ void unpack(const uint4& v, float* f) {
+    f[0] = __uint_as_float(v.x); f[1] = __uint_as_float(v.y);
+    f[2] = __uint_as_float(v.z); f[3] = __uint_as_float(v.w);
+  }
+  static __device__ __forceinline__ uint4 pack(const float* f) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                      __float_as_uint(f[3]));
+  }
+};
+
+template <> struct Vec<__nv_bfloat16> {
+  static constexpr int N = 8;
+  static __device__ __forceinline__ void unpack2(uint32_t u, float* f) {
+    f[0] = __uint_as_float(u << 16);
+    f[1] = __uint_as_float(u & 0xffff0000u);
+  }
+  static __device__ __forceinline__ void unpack(const uint4& v, float* f) {
+    unpack2(v.x, f); unpack2(v.y, f + 2); unpack2(v.z, f + 4); unpack2(v.w, f + 6);
+  }
+  static __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<uint32_t*>(&b);
+  }
+  static __device__ __forceinline__ uint4 pack(const float* f) {
+    return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+  }
+};
+
+__device__ __forceinline__ float to_float(float x) { return x; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <typename T> __device__ __forceinline__ T from_float(float x);
+template <> __device__ __forceinline__ float from_float<float>(float x) { return x; }
+template <> __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float x) {
+  return __float2bfloat16_rn(x);
+}
+
+// Token indexes: int32 or int64.  Values above INT32_MAX are kept apart from
+// the valid ones by saturating, those below 0 all mean "no token".
+__device__ __forceinline__ int load_index(const void* p, int is64, int64_t i) {
+  if (!is64) return reinterpret_cast<const int32_t*>(p)[i];
+  const int64_t v = reinterpret_cast<const int64_t*>(p)[i];
+  return v < 0 ? -1 : v > 0x7fffffff ? 0x7fffffff : static_cast<int>(v);
+}
+
+}  // namespace tok
+
+// Runs the body of a C entry point: no C++ exception leaves it (the only ones
+// that can arise are failed host allocations).
+template <typename F>
+int entry(F&& body) {
+  try {
+    return body();
+  } catch (...) {
+    return MUON_ERR_OOM;
+  }
+}
+
+// Host side.  Which devices have run these operators (bit per device; the
+// caller holds the library lock), so that muon_device_error reads their flags.
+void note_token_device(int dev);
+// The flags' first nonzero code on every device noted, cleared once read.
+int embedding_take_device_error();
+int losses_take_device_error();
+uint64_t token_devices();
+
+// Reads and clears a TU's flag on every noted device.  `symbol` is the TU's
+// own __device__ int.
+template <typename S>
+int take_flag(S& symbol) {
+  int worst = 0, now = 0;
+  if (!token_devices() || cudaGetDevice(&now) != cudaSuccess) return 0;
+  for (int d = 0; d < 64; ++d) {
+    if (!(token_devices() >> d & 1)) continue;
+    int v = 0;
+    const int zero = 0;
+    if (cudaSetDevice(d) == cudaSuccess &&
+        cudaMemcpyFromSymbol(&v, symbol, sizeof(int)) == cudaSuccess && v) {
+      if (!worst) worst = v;
+      cudaMemcpyToSymbol(symbol, &zero, sizeof(int));
+    }
+  }
+  cudaSetDevice(now);
+  return worst;
+}
+
+}  // namespace muon
