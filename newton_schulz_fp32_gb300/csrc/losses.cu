@@ -14,22 +14,31 @@
 //
 // Maxima, sums and e are FP32 whatever the logits' type; sums over tokens are
 // FP64 (a few thousand terms, off the hot path) in a fixed order.
+#include <algorithm>
 #include <cfloat>
 #include <cmath>
 #include <string>
+
+#include <cooperative_groups.h>
 
 #include "token_ops.cuh"
 
 namespace muon {
 namespace {
 
+namespace cg = cooperative_groups;
 using tok::Vec;
 
 __device__ int g_losses_err;
 
 constexpr int kRowThreads = 512;     // k_rows: threads of a row
 constexpr int kSumThreads = 1024;
+constexpr int kHeldThreads = 256;    // k_held: threads of a block
+constexpr int kHeldVecs = 8;         // and the vectors a thread holds before a row takes more blocks
+constexpr int kSms = 152;
 constexpr int kPairThreads = 256;
+constexpr int kGivenThreads = 256;
+constexpr int kGivenVecs = 8 * kGivenThreads;   // 16-byte vectors of a row per block of k_given
 
 int lfail(int code, const std::string& msg) {
   set_last_error(msg.c_str());
@@ -66,24 +75,32 @@ struct Policy {
   float clip_low, clip_high, kl_coef;
 };
 
+struct Token {
+  float a, w, old, ref;
+};
+
 struct PolicyTerms {
   float term, kl;
   float coef;   // d (term + kl_coef kl) / d logp
   bool cut;
 };
 
-__device__ __forceinline__ PolicyTerms policy_terms(const Policy& p, int64_t t, float logp) {
+__device__ __forceinline__ Token load_token(const Policy& p, int64_t t) {
+  return {p.advantages[t], p.weights[t], p.old_logp ? p.old_logp[t] : 0.f,
+          p.ref_logp ? p.ref_logp[t] : 0.f};
+}
+
+__device__ __forceinline__ PolicyTerms policy_terms(const Token& k, const Policy& p, float logp) {
   PolicyTerms o;
-  const float a = p.advantages[t];
-  const float r = p.old_logp ? expf(logp - p.old_logp[t]) : (logp == logp ? 1.f : logp);
-  const float free = r * a;
-  const float held = fminf(fmaxf(r, 1.f - p.clip_low), 1.f + p.clip_high) * a;
+  const float r = p.old_logp ? expf(logp - k.old) : (logp == logp ? 1.f : logp);
+  const float free = r * k.a;
+  const float held = fminf(fmaxf(r, 1.f - p.clip_low), 1.f + p.clip_high) * k.a;
   o.cut = free > held;
   o.term = o.cut ? -held : -free;
   o.coef = o.cut ? 0.f : -free;
   o.kl = 0.f;
   if (p.ref_logp) {
-    const float q = p.ref_logp[t] - logp;
+    const float q = k.ref - logp;
     const float g = expm1f(q);
     o.kl = g - q;
     if (p.kl_coef != 0.f) o.coef -= p.kl_coef * g;   // 0 times infinity would spoil the gradient
@@ -132,16 +149,24 @@ struct RowShape {
 
 enum RowMode {
   kLogp = 0,     // logp
-  kStats = 1,    // logp and (m, 1/S) for a later gradient pass
-  kPolicy = 2,   // logp and the policy loss's gradient
-  kGiven = 3     // the gradient alone, from (m, 1/S) and c
+  kStats = 1,    // logp and (m, 1/S) for k_given
+  kPolicy = 2    // logp and the policy loss's gradient
 };
 
 struct Extra {
   Policy policy;
-  float2* stats;      // kStats, kGiven: (m, 1/S) per row
-  float* coef;        // kGiven: c per row; kStats zeroes it
+  float2* stats;      // kStats: (m, 1/S) per row
+  float* coef;        // kStats: c per row, zero here (k_pairs writes it)
+  float* logp_lo;     // kStats: log-probability - logp
 };
+
+// What a row's log-probability loses when it is rounded to FP32.  Margins are
+// differences of sums of hundreds of them, so the preference loss adds it
+// back: one FP64 logarithm per row, by one thread.
+__device__ __noinline__ float logp_rest(float scale, float zy, float m, float s, float logp) {
+  const double v = double(scale) * (double(zy) - double(m)) - log(double(s)) - double(logp);
+  return fabs(v) <= 1.0 ? static_cast<float>(v) : 0.f;   // 0 beside infinities and NaN
+}
 
 // Writes one row's gradient: g = s c, e scaled by -g / S, plus g at y.
 template <typename T>
@@ -191,20 +216,18 @@ template <typename T, int MODE>
 __global__ void __launch_bounds__(kRowThreads) k_rows(const Rows a, const Extra x) {
   constexpr int N = Vec<T>::N;
   __shared__ float sm[kRowThreads / 32], ss[kRowThreads / 32];
+  tok::allow_next();
   const int64_t t = blockIdx.x;
   const T* row = static_cast<const T*>(a.logits) + t * a.stride;
   T* drow = a.dlogits ? static_cast<T*>(a.dlogits) + t * a.dstride : nullptr;
   const int y = row_target(a, t);
-  if (MODE == kGiven) {
-    const float c = x.coef[t];
-    if (y < 0 || c == 0.f) return write_zeros<T>(a, drow);
-    const float2 st = x.stats[t];
-    return write_grad<T>(a, row, drow, y, st.x, st.y, a.scale * c);
-  }
   if (y < 0 || (MODE == kPolicy && x.policy.weights[t] == 0.f)) {
     if (threadIdx.x == 0) {
       a.logp[t] = 0.f;
-      if (MODE == kStats) x.coef[t] = 0.f;
+      if (MODE == kStats) {
+        x.coef[t] = 0.f;
+        x.logp_lo[t] = 0.f;
+      }
     }
     if (MODE == kPolicy && drow) write_zeros<T>(a, drow);
     return;
@@ -242,49 +265,74 @@ __global__ void __launch_bounds__(kRowThreads) k_rows(const Rows a, const Extra 
     if (MODE == kStats) {
       x.stats[t] = make_float2(m, 1.f / s);
       x.coef[t] = 0.f;
+      x.logp_lo[t] = logp_rest(a.scale, zy, m, s, logp);
     }
   }
   if (MODE == kPolicy && drow) {
-    const float c = x.policy.weights[t] * policy_terms(x.policy, t, logp).coef;
+    const float c = x.policy.weights[t] * policy_terms(load_token(x.policy, t), x.policy, logp).coef;
     if (c == 0.f) return write_zeros<T>(a, drow);
     write_grad<T>(a, row, drow, y, m, 1.f / s, a.scale * c);
   }
 }
 
-template <int NT>
-__device__ __forceinline__ double block_sum(double v, double* sh) {
+// The sum over the cluster's threads, valid in thread 0 of its first block.
+// sh: one entry per warp and quantity; every block of the cluster calls it.
+template <int NT, int Q>
+__device__ __forceinline__ void cluster_sum(tok::Two (&v)[Q], tok::Two (*sh)[NT / 32]) {
+  cg::cluster_group cl = cg::this_cluster();
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  for (int q = 0; q < Q; ++q) {
+    v[q].warp_sum();
+    if (lane == 0) sh[q][warp] = v[q];
+  }
   __syncthreads();
-  if (threadIdx.x % 32 == 0) sh[threadIdx.x / 32] = v;
-  __syncthreads();
-  v = 0.0;
-  for (int w = 0; w < NT / 32; ++w) v += sh[w];
-  return v;
+  if (warp == 0) {
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      v[q] = lane < NT / 32 ? sh[q][lane] : tok::Two();
+      v[q].warp_sum();
+    }
+    __syncwarp();
+    if (lane == 0)
+#pragma unroll
+      for (int q = 0; q < Q; ++q) sh[q][0] = v[q];
+  }
+  cl.sync();
+  if (cl.block_rank() == 0 && threadIdx.x == 0)
+    for (int b = 1; b < int(cl.num_blocks()); ++b)
+#pragma unroll
+      for (int q = 0; q < Q; ++q) v[q].add(*cl.map_shared_rank(&sh[q][0], b));
+  cl.sync();   // no block leaves while its sums are read
 }
 
-// The policy loss's statistics from the tokens' logp.
+// The policy loss's statistics from the tokens' logp.  One cluster: up to
+// 8 x 1024 tokens at once.
 __global__ void __launch_bounds__(kSumThreads) k_policy_sum(const Rows a, const Policy p,
                                                             float* stats) {
-  __shared__ double sh[kSumThreads / 32];
-  double term = 0.0, kl = 0.0, cut = 0.0;
-  for (int64_t t = threadIdx.x; t < a.n; t += kSumThreads) {
+  __shared__ tok::Two sh[3][kSumThreads / 32];
+  tok::Two v[3];   // term, kl, cut
+  tok::wait_before();
+  for (int64_t t = blockIdx.x * kSumThreads + threadIdx.x; t < a.n; t += int64_t(gridDim.x) * kSumThreads) {
     const int y = tok::load_index(a.targets, a.targets64, t);
     const float w = p.weights[t];
     if (y < 0 || y >= a.vocab || w == 0.f) continue;
-    const PolicyTerms o = policy_terms(p, t, a.logp[t]);
-    term += double(w) * o.term;
-    kl += double(w) * o.kl;
-    if (o.cut) cut += w;
+    const PolicyTerms o = policy_terms(load_token(p, t), p, a.logp[t]);
+    v[0].add(w * o.term);
+    v[1].add(w * o.kl);
+    if (o.cut) v[2].add(w);
   }
-  term = block_sum<kSumThreads>(term, sh);
-  kl = block_sum<kSumThreads>(kl, sh);
-  cut = block_sum<kSumThreads>(cut, sh);
-  if (threadIdx.x == 0) {
-    stats[0] = static_cast<float>(p.kl_coef != 0.f ? term + double(p.kl_coef) * kl : term);
-    stats[1] = static_cast<float>(term);
-    stats[2] = static_cast<float>(kl);
-    stats[3] = static_cast<float>(cut);
+  cluster_sum<kSumThreads, 3>(v, sh);
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    const float term = v[0].value(), kl = v[1].value();
+    if (p.kl_coef != 0.f) {
+      v[0].add(p.kl_coef * v[1].hi);
+      v[0].lo += p.kl_coef * v[1].lo;
+    }
+    stats[0] = v[0].value();
+    stats[1] = term;
+    stats[2] = kl;
+    stats[3] = v[2].value();
   }
 }
 
@@ -295,8 +343,9 @@ struct Pairs {
   const float* ref_logp;
   const float* weights;
   float beta, smoothing;
+  const float* logp_lo;   // what the tokens' logp lost when it was rounded
   float* margins;
-  float* coef;
+  float* coef;            // c per token; NULL: no gradient
 };
 
 // log(1 + exp(x)) and 1 / (1 + exp(-x)) without overflow.
@@ -323,64 +372,386 @@ __device__ __forceinline__ void sequence(const Rows& a, const Pairs& q, int i, i
 // One block per pair: the two sequences' sums, the margin, and c of every
 // token of the pair.
 __global__ void __launch_bounds__(kPairThreads) k_pairs(const Rows a, const Pairs q) {
-  __shared__ double sh[kPairThreads / 32];
-  double sum[2];
+  __shared__ tok::Two sh[2][kPairThreads / 32];
+  __shared__ float grad;
+  tok::wait_before();
+  tok::allow_next();
+  tok::Two sum[2];
   int64_t b[2], e[2];
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     sequence(a, q, blockIdx.x + j * q.n, b[j], e[j]);
-    double v = 0.0;
-    for (int64_t t = b[j] + threadIdx.x; t < e[j]; t += kPairThreads)
-      if (row_target(a, t) >= 0) v += double(a.logp[t]) - (q.ref_logp ? double(q.ref_logp[t]) : 0.0);
-    sum[j] = block_sum<kPairThreads>(v, sh);
+    for (int64_t t = b[j] + threadIdx.x; t < e[j]; t += kPairThreads) {
+      if (row_target(a, t) < 0) continue;
+      sum[j].add(a.logp[t]);
+      sum[j].lo += q.logp_lo[t];
+      if (q.ref_logp) sum[j].add(-q.ref_logp[t]);
+    }
+    sum[j].warp_sum();
+    if (threadIdx.x % 32 == 0) sh[j][threadIdx.x / 32] = sum[j];
   }
-  const float h = static_cast<float>(double(q.beta) * (sum[0] - sum[1]));
-  if (threadIdx.x == 0) q.margins[blockIdx.x] = h;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      sum[j] = sh[j][0];
+      for (int w = 1; w < kPairThreads / 32; ++w) sum[j].add(sh[j][w]);
+    }
+    float h;
+    if (fabsf(sum[0].hi) <= FLT_MAX && fabsf(sum[1].hi) <= FLT_MAX) {
+      sum[0].add(-sum[1].hi);
+      sum[0].lo -= sum[1].lo;
+      h = q.beta * sum[0].value();
+    } else {
+      h = q.beta * (sum[0].hi - sum[1].hi);
+    }
+    q.margins[blockIdx.x] = h;
+    const float w = q.weights ? q.weights[blockIdx.x] : 1.f / q.n;
+    // d loss / d h = sigmoid(h) - (1 - smoothing), written so that neither term cancels
+    const float dh = q.smoothing * sigmoid(h) - (1.f - q.smoothing) * sigmoid(-h);
+    grad = w == 0.f ? 0.f : w * q.beta * dh;
+  }
   if (!q.coef) return;
-  const float w = q.weights ? q.weights[blockIdx.x] : 1.f / q.n;
-  // d loss / d h = sigmoid(h) - (1 - smoothing), written so that neither term cancels
-  const float dh = q.smoothing * sigmoid(h) - (1.f - q.smoothing) * sigmoid(-h);
-  const float g = w == 0.f ? 0.f : w * q.beta * dh;
+  __syncthreads();
+  const float g = grad;
 #pragma unroll
   for (int j = 0; j < 2; ++j)
     for (int64_t t = b[j] + threadIdx.x; t < e[j]; t += kPairThreads) q.coef[t] = j ? -g : g;
 }
 
-__global__ void __launch_bounds__(kSumThreads) k_pair_sum(const Pairs q, float* stats) {
-  __shared__ double sh[kSumThreads / 32];
-  double loss = 0.0, mean = 0.0, won = 0.0, weight = 0.0;
-  for (int i = threadIdx.x; i < q.n; i += kSumThreads) {
-    const double w = q.weights ? double(q.weights[i]) : 1.0 / q.n;
-    if (w == 0.0) continue;
+// The preference loss's statistics from the margins, by one cluster of
+// `blocks` blocks of NT threads, `block` this one.
+template <int NT>
+__device__ __forceinline__ void pair_sum(const Pairs& q, float* stats, int block, int blocks) {
+  __shared__ tok::Two sh[4][NT / 32];
+  tok::Two v[4];   // loss, margin, won, weight
+  for (int i = block * NT + threadIdx.x; i < q.n; i += blocks * NT) {
+    const float w = q.weights ? q.weights[i] : 1.f;
+    if (w == 0.f) continue;
     const float h = q.margins[i];
     float l = 0.f;
     if (q.smoothing < 1.f) l += (1.f - q.smoothing) * softplus(-h);
     if (q.smoothing > 0.f) l += q.smoothing * softplus(h);
-    loss += w * l;
-    mean += w * h;
-    won += h > 0.f ? w : 0.0;
-    weight += w;
+    v[0].add(w * l);
+    v[1].add(w * h);
+    if (h > 0.f) v[2].add(w);
+    v[3].add(w);
   }
-  loss = block_sum<kSumThreads>(loss, sh);
-  mean = block_sum<kSumThreads>(mean, sh);
-  won = block_sum<kSumThreads>(won, sh);
-  weight = block_sum<kSumThreads>(weight, sh);
-  if (threadIdx.x == 0) {
-    stats[0] = static_cast<float>(loss);
-    stats[1] = static_cast<float>(mean);
-    stats[2] = static_cast<float>(won);
-    stats[3] = static_cast<float>(weight);
+  cluster_sum<NT, 4>(v, sh);
+  if (block == 0 && threadIdx.x == 0)
+    for (int k = 0; k < 4; ++k) stats[k] = v[k].value() / (q.weights || q.n == 0 ? 1.f : float(q.n));
+}
+
+__global__ void __launch_bounds__(kSumThreads) k_pair_sum(const Pairs q, float* stats) {
+  tok::wait_before();
+  pair_sum<kSumThreads>(q, stats, blockIdx.x, gridDim.x);
+}
+
+// The gradient from (m, 1/S) and c of every row.  Block 0 sums the
+// statistics; the others take kGivenVecs vectors of a row each, the last rows
+// first: the statistics pass read those last, so some are still in L2.
+template <typename T>
+__global__ void __launch_bounds__(kGivenThreads) k_given(const Rows a, const Extra x, const Pairs q,
+                                                         float* stats, int slices) {
+  constexpr int N = Vec<T>::N;
+  constexpr int NV = kGivenVecs / kGivenThreads;
+  tok::wait_before();
+  if (blockIdx.x == 0) return pair_sum<kGivenThreads>(q, stats, 0, 1);
+  const unsigned task = gridDim.x - 1 - blockIdx.x;
+  const int64_t t = task / slices;
+  const int slice = task % slices;
+  const T* row = static_cast<const T*>(a.logits) + t * a.stride;
+  T* drow = static_cast<T*>(a.dlogits) + t * a.dstride;
+  const int y = row_target(a, t);
+  const float c = x.coef[t];
+  const bool on = y >= 0 && c != 0.f;   // else zeros, and the row is not read
+  const float2 st = x.stats[t];
+  const float g = a.scale * c, ga = -g * st.y, m = st.x;
+  const bool aligned =
+      ((reinterpret_cast<uintptr_t>(drow) ^ reinterpret_cast<uintptr_t>(row)) & 15) == 0;
+  const RowShape<T> sh(on || aligned ? row : drow, a.vocab);
+  const int i0 = slice * kGivenVecs + threadIdx.x;
+  uint4 v[NV];
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    v[k] = make_uint4(0, 0, 0, 0);
+    const int i = i0 + k * kGivenThreads;
+    if (on && i < sh.nvec) v[k] = __ldcs(reinterpret_cast<const uint4*>(row + sh.head + i * N));
+  }
+  auto one = [&](int u, float z) {
+    const float d = ga * ex2((z - m) * a.scale2);
+    return !on ? 0.f : u == y ? d + g : d;
+  };
+  if (slice == 0) {   // the elements before and after the vectors
+    const int u = threadIdx.x < sh.head ? threadIdx.x : sh.tail0 + threadIdx.x - 32;
+    if (threadIdx.x < sh.head || (threadIdx.x >= 32 && u < a.vocab))
+      drow[u] = tok::from_float<T>(one(u, on ? tok::to_float(row[u]) : 0.f));
+  }
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int i = i0 + k * kGivenThreads;
+    if (i >= sh.nvec) break;
+    const int v0 = sh.head + i * N;
+    float f[N];
+    Vec<T>::unpack(v[k], f);
+#pragma unroll
+    for (int j = 0; j < N; ++j) f[j] = one(v0 + j, f[j]);
+    if (aligned || !on) {
+      __stcs(reinterpret_cast<uint4*>(drow + v0), Vec<T>::pack(f));
+    } else {
+#pragma unroll
+      for (int j = 0; j < N; ++j) drow[v0 + j] = tok::from_float<T>(f[j]);
+    }
   }
 }
 
+int sum_blocks(int64_t n) {
+  int blocks = 1;
+  while (blocks < 8 && n > blocks * int64_t(kSumThreads)) blocks *= 2;
+  return blocks;
+}
+
+// ---- a row held in registers
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// 16 bytes of minus infinities.
+template <typename T> __device__ __forceinline__ uint4 lowest();
+template <> __device__ __forceinline__ uint4 lowest<float>() {
+  return make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u);
+}
+template <> __device__ __forceinline__ uint4 lowest<__nv_bfloat16>() {
+  return make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
+}
+
+// Keeps the row in its packed form: without it the compiler carries the
+// unpacked values from one pass over the registers to the next (116 registers
+// instead of 64 for 8 vectors of bf16, half the blocks per SM).
+template <int NV>
+__device__ __forceinline__ void keep_packed(uint4 (&v)[NV]) {
+#pragma unroll
+  for (int k = 0; k < NV; ++k) asm volatile("" : "+r"(v[k].x), "+r"(v[k].y), "+r"(v[k].z), "+r"(v[k].w));
+}
+
+template <typename T, int NV>
+__device__ __forceinline__ float vec_max(const uint4 (&v)[NV]) {
+  if constexpr (sizeof(T) == 2) {
+    auto two = [](uint32_t u) { return *reinterpret_cast<__nv_bfloat162*>(&u); };
+    __nv_bfloat162 m = two(lowest<T>().x);
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+      m = __hmax2(m, __hmax2(__hmax2(two(v[k].x), two(v[k].y)), __hmax2(two(v[k].z), two(v[k].w))));
+    return fmaxf(__low2float(m), __high2float(m));
+  } else {
+    float f[4], m = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      Vec<T>::unpack(v[k], f);
+      m = fmaxf(m, fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3])));
+    }
+    return m;
+  }
+}
+
+template <typename T, int NV>
+__device__ __forceinline__ float vec_sum(const uint4 (&v)[NV], float m, float scale2) {
+  float f[Vec<T>::N], s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    Vec<T>::unpack(v[k], f);
+#pragma unroll
+    for (int j = 0; j < Vec<T>::N; ++j) s[j & 3] += ex2((f[j] - m) * scale2);
+  }
+  return (s[0] + s[1]) + (s[2] + s[3]);
+}
+
+// Zeros in block `rank`'s share of a row.
+template <typename T, int NT, int NV>
+__device__ __forceinline__ void zero_slice(const Rows& a, T* drow, int rank) {
+  const RowShape<T> sh(drow, a.vocab);
+  const T zero = tok::from_float<T>(0.f);
+  if (rank == 0) {
+    if (threadIdx.x < sh.head) drow[threadIdx.x] = zero;
+    else if (threadIdx.x >= 32 && sh.tail0 + int(threadIdx.x) - 32 < a.vocab) drow[sh.tail0 + threadIdx.x - 32] = zero;
+  }
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int i = rank * NT * NV + k * NT + threadIdx.x;
+    if (i < sh.nvec) __stcs(reinterpret_cast<uint4*>(drow + sh.head + i * Vec<T>::N), make_uint4(0, 0, 0, 0));
+  }
+}
+
+// A row held in registers: one cluster of blocks per row, NV 16-byte vectors
+// per thread, loaded at once.  The row is read from memory exactly once, also
+// where its gradient is written, and a row is spread over up to eight SMs, so
+// a call with few rows is short.  Several blocks per SM, of different rows,
+// overlap one row's loads with another's arithmetic and writes.
+template <typename T, int NT, int NV, int MODE>
+__global__ void __launch_bounds__(NT) k_held(const Rows a, const Extra x) {
+  constexpr int N = Vec<T>::N;
+  constexpr int W = NT / 32;
+  __shared__ float2 warp_part[W];
+  __shared__ float2 part[8];     // (m, s) of every block of the cluster
+  __shared__ float2 out;         // (-g / S, g)
+  __shared__ float out_m;
+  tok::allow_next();
+  cg::cluster_group cl = cg::this_cluster();
+  const int c = cl.num_blocks(), rank = cl.block_rank();
+  const int64_t t = blockIdx.x / unsigned(c);
+  const T* row = static_cast<const T*>(a.logits) + t * a.stride;
+  T* drow = a.dlogits ? static_cast<T*>(a.dlogits) + t * a.dstride : nullptr;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int y = row_target(a, t);
+  Token tk{};
+  if (MODE == kPolicy) tk = load_token(x.policy, t);
+  if (y < 0 || (MODE == kPolicy && tk.w == 0.f)) {   // the same for the whole cluster
+    if (rank == 0 && threadIdx.x == 0) {
+      a.logp[t] = 0.f;
+      if (MODE == kStats) {
+        x.coef[t] = 0.f;
+        x.logp_lo[t] = 0.f;
+      }
+    }
+    if (MODE == kPolicy && drow) zero_slice<T, NT, NV>(a, drow, rank);
+    return;
+  }
+  if (c > 1) cluster_arrive();   // waited for before the first write to another block
+  const RowShape<T> sh(row, a.vocab);
+  const int i0 = rank * NT * NV + threadIdx.x;
+  uint4 v[NV];
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int i = i0 + k * NT;
+    v[k] = i < sh.nvec ? __ldcs(reinterpret_cast<const uint4*>(row + sh.head + i * N)) : lowest<T>();
+  }
+  // elements before and after the vectors: one per thread of the first block
+  int single = -1;
+  if (rank == 0) {
+    if (threadIdx.x < sh.head) single = threadIdx.x;
+    else if (threadIdx.x >= 32 && sh.tail0 + int(threadIdx.x) - 32 < a.vocab) single = sh.tail0 + threadIdx.x - 32;
+  }
+  const float zs = single >= 0 ? tok::to_float(row[single]) : -INFINITY;
+  const float zy = threadIdx.x < 32 ? tok::to_float(row[y]) : 0.f;
+  float m = fmaxf(fmaxf(-FLT_MAX, zs), vec_max<T, NV>(v));
+  keep_packed(v);
+  float s = ex2((zs - m) * a.scale2) + vec_sum<T, NV>(v, m, a.scale2);
+  keep_packed(v);
+  warp_join(m, s, a.scale2);
+  if (lane == 0) warp_part[warp] = make_float2(m, s);
+  __syncthreads();
+  if (warp == 0) {
+    m = lane < W ? warp_part[lane].x : -FLT_MAX;
+    s = lane < W ? warp_part[lane].y : 0.f;
+    warp_join(m, s, a.scale2);
+  }
+  if (c > 1) {
+    cluster_wait();
+    if (warp == 0 && lane < c) *cl.map_shared_rank(&part[rank], lane) = make_float2(m, s);
+    cluster_arrive();
+    cluster_wait();
+    if (warp == 0) {
+      const float2 p = lane < c ? part[lane] : make_float2(-FLT_MAX, 0.f);
+      m = p.x;
+      s = p.y;
+      warp_join(m, s, a.scale2);
+    }
+  }
+  if (warp == 0) {
+    const float logp = a.scale * (zy - m) - logf(s);
+    if (rank == 0 && lane == 0) {
+      a.logp[t] = logp;
+      if (MODE == kStats) {
+        x.stats[t] = make_float2(m, 1.f / s);
+        x.coef[t] = 0.f;
+        x.logp_lo[t] = logp_rest(a.scale, zy, m, s, logp);
+      }
+    }
+    if (MODE == kPolicy && lane == 0) {
+      const float g = a.scale * (tk.w * policy_terms(tk, x.policy, logp).coef);
+      out = make_float2(-g / s, g);
+      out_m = m;
+    }
+  }
+  if (MODE != kPolicy || !drow) return;
+  __syncthreads();
+  const float ga = out.x, g = out.y;
+  m = out_m;
+  if (g == 0.f) return zero_slice<T, NT, NV>(a, drow, rank);
+  if (single >= 0) {
+    const float d = ga * ex2((zs - m) * a.scale2);
+    drow[single] = tok::from_float<T>(single == y ? d + g : d);
+  }
+  const bool aligned =
+      ((reinterpret_cast<uintptr_t>(drow) ^ reinterpret_cast<uintptr_t>(row)) & 15) == 0;
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int i = i0 + k * NT;
+    if (i >= sh.nvec) break;
+    const int v0 = sh.head + i * N;
+    float f[N];
+    Vec<T>::unpack(v[k], f);
+#pragma unroll
+    for (int j = 0; j < N; ++j) f[j] = ga * ex2((f[j] - m) * a.scale2);
+    if (unsigned(y - v0) < unsigned(N)) {
+#pragma unroll
+      for (int j = 0; j < N; ++j) f[j] += y - v0 == j ? g : 0.f;
+    }
+    if (aligned) {
+      __stcs(reinterpret_cast<uint4*>(drow + v0), Vec<T>::pack(f));
+    } else {
+#pragma unroll
+      for (int j = 0; j < N; ++j) drow[v0 + j] = tok::from_float<T>(f[j]);
+    }
+  }
+}
+
+// The smallest hold of a row: NV vectors per thread in c blocks.  Many rows
+// take the fewest blocks per row; few rows (under one block per SM) up to
+// eight, to use the SMs that there are.
+struct Hold {
+  int nv, c;   // nv = 0: the row does not fit
+};
+
+Hold hold_of(int64_t n, int vocab, int per_vec) {
+  const int nvec = vocab / per_vec;
+  int c = 1, nv = 1;
+  while (nv < kHeldVecs && nv * c * kHeldThreads < nvec) nv *= 2;
+  while (c < 8 && nv * c * kHeldThreads < nvec) c *= 2;
+  while (nv < 2 * kHeldVecs && nv * c * kHeldThreads < nvec) nv *= 2;
+  if (nv * c * kHeldThreads < nvec) return {0, 0};
+  while (c < 8 && nv > 1 && n * c * 2 <= kSms) {
+    c *= 2;
+    nv /= 2;
+  }
+  return {nv, c};
+}
+
+template <typename T, int MODE>
+cudaError_t launch_held(const Rows& a, const Extra& x, Hold h, cudaStream_t s) {
+  const unsigned grid = static_cast<unsigned>(a.n * h.c);
+  switch (h.nv) {
+    case 1: return launch(k_held<T, kHeldThreads, 1, MODE>, grid, kHeldThreads, h.c, false, s, a, x);
+    case 2: return launch(k_held<T, kHeldThreads, 2, MODE>, grid, kHeldThreads, h.c, false, s, a, x);
+    case 4: return launch(k_held<T, kHeldThreads, 4, MODE>, grid, kHeldThreads, h.c, false, s, a, x);
+    case 8: return launch(k_held<T, kHeldThreads, 8, MODE>, grid, kHeldThreads, h.c, false, s, a, x);
+    default: return launch(k_held<T, kHeldThreads, 16, MODE>, grid, kHeldThreads, h.c, false, s, a, x);
+  }
+}
+
+template <typename T, int MODE>
+cudaError_t launch_rows_of(const Rows& a, const Extra& x, cudaStream_t s) {
+  const Hold h = hold_of(a.n, a.vocab, Vec<T>::N);
+  const bool grad = MODE == kPolicy && a.dlogits;
+  if (h.nv && (grad || a.n < 2 * kSms) && a.n * h.c <= 0x7fffffff) return launch_held<T, MODE>(a, x, h, s);
+  return launch(k_rows<T, MODE>, static_cast<unsigned>(a.n), kRowThreads, 1, false, s, a, x);
+}
+
 template <int MODE>
-int launch_rows(const Rows& a, const Extra& x, int dtype, cudaStream_t s) {
-  if (a.n == 0) return 0;
-  if (dtype == MUON_DTYPE_BF16)
-    k_rows<__nv_bfloat16, MODE><<<static_cast<unsigned>(a.n), kRowThreads, 0, s>>>(a, x);
-  else
-    k_rows<float, MODE><<<static_cast<unsigned>(a.n), kRowThreads, 0, s>>>(a, x);
-  return 1;
+cudaError_t launch_rows(const Rows& a, const Extra& x, int dtype, cudaStream_t s) {
+  if (a.n == 0) return cudaSuccess;
+  return dtype == MUON_DTYPE_BF16 ? launch_rows_of<__nv_bfloat16, MODE>(a, x, s)
+                                  : launch_rows_of<float, MODE>(a, x, s);
 }
 
 // ------------------------------------------------------------------ arguments
@@ -446,15 +817,16 @@ int begin_call() {
   return MUON_OK;
 }
 
-int end_call(int launches) {
+int end_call(int launches, cudaError_t e) {
   count_launches(launches);
-  const cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) e = cudaGetLastError();
+  else cudaGetLastError();
   if (e != cudaSuccess)
     return lfail(MUON_ERR_CUDA, std::string("kernel launch: ") + cudaGetErrorString(e));
   return MUON_OK;
 }
 
-size_t preference_bytes(int64_t n) { return (size_t(n) * (sizeof(float2) + sizeof(float)) + 15) & ~size_t(15); }
+size_t preference_bytes(int64_t n) { return (size_t(n) * (sizeof(float2) + 2 * sizeof(float)) + 15) & ~size_t(15); }
 
 }  // namespace
 
@@ -477,7 +849,7 @@ extern "C" int muon_token_logprobs(const void* logits, int dtype, int64_t stride
     if ((rc = begin_call()) != MUON_OK) return rc;
     const Rows a = make_rows(logits, stride, n_tokens, vocab, targets, targets_type, logit_scale, logp,
                              nullptr, 0);
-    return end_call(launch_rows<kLogp>(a, Extra{}, dtype, static_cast<cudaStream_t>(stream)));
+    return end_call(1, launch_rows<kLogp>(a, Extra{}, dtype, static_cast<cudaStream_t>(stream)));
   });
 }
 
@@ -510,9 +882,11 @@ extern "C" int muon_policy_loss(const void* logits, int dtype, int64_t stride, i
                              dlogits, dlogits_stride);
     Extra x{};
     x.policy = {advantages, weights, old_logp, ref_logp, clip_low, clip_high, kl_coef};
-    const int k = launch_rows<kPolicy>(a, x, dtype, s);
-    k_policy_sum<<<1, kSumThreads, 0, s>>>(a, x.policy, stats);
-    return end_call(k + 1);
+    cudaError_t e = launch_rows<kPolicy>(a, x, dtype, s);
+    const int blocks = sum_blocks(n_tokens);
+    if (e == cudaSuccess)
+      e = launch(k_policy_sum, blocks, kSumThreads, blocks, n_tokens > 0, s, a, x.policy, stats);
+    return end_call((n_tokens > 0) + 1, e);
   });
 }
 
@@ -554,6 +928,8 @@ extern "C" int muon_preference_loss(const void* logits, int dtype, int64_t strid
     if (!std::isfinite(beta)) return lfail(MUON_ERR_INVALID, "beta must be finite");
     if (!(label_smoothing >= 0.f && label_smoothing <= 1.f))
       return lfail(MUON_ERR_INVALID, "label_smoothing must be in [0, 1]");
+    if (n_tokens * ((int64_t(vocab) + 16383) / 16384 + 1) >= 0x7fffffff)
+      return lfail(MUON_ERR_UNSUPPORTED, "too many tokens of a vocabulary this large for one call");
     if (n_tokens > 0 && (!workspace || misaligned(workspace, 16) || workspace_bytes < preference_bytes(n_tokens)))
       return lfail(MUON_ERR_INVALID, "workspace is NULL, misaligned or too small");
     if ((rc = begin_call()) != MUON_OK) return rc;
@@ -563,15 +939,23 @@ extern "C" int muon_preference_loss(const void* logits, int dtype, int64_t strid
     Extra x{};
     x.stats = static_cast<float2*>(workspace);
     x.coef = reinterpret_cast<float*>(x.stats + n_tokens);
-    Pairs q{offsets, offsets_type == MUON_INDEX_INT64, n_pairs, ref_logp, pair_weights, beta,
-            label_smoothing, margins, dlogits ? x.coef : nullptr};
-    int k = dlogits ? launch_rows<kStats>(a, x, dtype, s) : launch_rows<kLogp>(a, x, dtype, s);
-    if (n_pairs > 0) {
-      k_pairs<<<n_pairs, kPairThreads, 0, s>>>(a, q);
-      ++k;
+    x.logp_lo = x.coef + n_tokens;
+    const Pairs q{offsets, offsets_type == MUON_INDEX_INT64, n_pairs, ref_logp, pair_weights, beta,
+                  label_smoothing, x.logp_lo, margins, dlogits ? x.coef : nullptr};
+    cudaError_t e = launch_rows<kStats>(a, x, dtype, s);
+    if (e == cudaSuccess && n_pairs > 0)
+      e = launch(k_pairs, n_pairs, kPairThreads, 1, n_tokens > 0, s, a, q);
+    const int vec = dtype == MUON_DTYPE_BF16 ? Vec<__nv_bfloat16>::N : Vec<float>::N;
+    const int slices = std::max(1, (vocab / vec + kGivenVecs - 1) / kGivenVecs);
+    if (e == cudaSuccess && dlogits && n_tokens > 0) {
+      const unsigned grid = static_cast<unsigned>(n_tokens * slices + 1);
+      e = dtype == MUON_DTYPE_BF16
+              ? launch(k_given<__nv_bfloat16>, grid, kGivenThreads, 1, true, s, a, x, q, stats, slices)
+              : launch(k_given<float>, grid, kGivenThreads, 1, true, s, a, x, q, stats, slices);
+    } else if (e == cudaSuccess) {
+      const int blocks = sum_blocks(n_pairs);
+      e = launch(k_pair_sum, blocks, kSumThreads, blocks, n_tokens > 0 || n_pairs > 0, s, q, stats);
     }
-    k_pair_sum<<<1, kSumThreads, 0, s>>>(q, stats);
-    if (dlogits) k += launch_rows<kGiven>(a, x, dtype, s);
-    return end_call(k + 1);
+    return end_call((n_tokens > 0) + (n_pairs > 0) + 1, e);
   });
 }

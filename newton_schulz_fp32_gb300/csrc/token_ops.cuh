@@ -63,7 +63,69 @@ __device__ __forceinline__ int load_index(const void* p, int is64, int64_t i) {
   return v < 0 ? -1 : v > 0x7fffffff ? 0x7fffffff : static_cast<int>(v);
 }
 
+// Sums of FP32 values kept as hi + lo (Knuth's two-sum), about 48 bits: FP64
+// adds run at 1/64 of the FP32 rate here (a block's sum of 1024 doubles took
+// 10 us).  An infinite or NaN hi is the sum.
+struct Two {
+  float hi = 0.f, lo = 0.f;
+  __device__ __forceinline__ void add(float x) {
+    const float s = hi + x, b = s - hi;
+    lo += (hi - (s - b)) + (x - b);
+    hi = s;
+  }
+  __device__ __forceinline__ void add(const Two& o) {
+    add(o.hi);
+    lo += o.lo;
+  }
+  __device__ __forceinline__ float value() const { return fabsf(hi) <= 3.402823466e38f ? hi + lo : hi; }
+  __device__ __forceinline__ void warp_sum() {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      Two b;
+      b.hi = __shfl_xor_sync(0xffffffffu, hi, o);
+      b.lo = __shfl_xor_sync(0xffffffffu, lo, o);
+      // the lanes of a pair add the same two values in the same order
+      const bool up = (threadIdx.x & o) != 0;
+      Two x = up ? b : *this;
+      x.add(up ? *this : b);
+      *this = x;
+    }
+  }
+};
+
+// Programmatic dependent launch: wait until the kernels before this one in
+// the stream have written what they write; let the next one be scheduled.
+__device__ __forceinline__ void wait_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void allow_next() { asm volatile("griddepcontrol.launch_dependents;"); }
+
 }  // namespace tok
+
+// Launches `kernel` in clusters of `cluster` blocks; early: it may be
+// scheduled while the kernel before it drains (it then calls wait_before).
+template <typename... A, typename... B>
+cudaError_t launch(void (*kernel)(A...), unsigned grid, unsigned block, int cluster, bool early,
+                   cudaStream_t s, B... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  unsigned n = 0;
+  if (cluster > 1) {
+    at[n].id = cudaLaunchAttributeClusterDimension;
+    at[n].val.clusterDim.x = cluster;
+    at[n].val.clusterDim.y = at[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  if (early) {
+    at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[n].val.programmaticStreamSerializationAllowed = 1;
+    ++n;
+  }
+  cfg.attrs = at;
+  cfg.numAttrs = n;
+  return cudaLaunchKernelEx(&cfg, kernel, A(args)...);
+}
 
 // Runs the body of a C entry point: no C++ exception leaves it (the only ones
 // that can arise are failed host allocations).
