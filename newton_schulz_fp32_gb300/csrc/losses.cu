@@ -21,6 +21,7 @@
 
 #include <cooperative_groups.h>
 
+#include "tc_common.cuh"
 #include "token_ops.cuh"
 
 namespace muon {
@@ -33,8 +34,10 @@ __device__ int g_losses_err;
 
 constexpr int kRowThreads = 512;     // k_rows: threads of a row
 constexpr int kSumThreads = 1024;
-constexpr int kHeldThreads = 256;    // k_held: threads of a block
-constexpr int kHeldVecs = 8;         // and the vectors a thread holds before a row takes more blocks
+constexpr int kHeldThreads = 256;    // k_held: most threads of a block,
+constexpr int kHeldBlocks = 6;       // blocks per SM,
+constexpr int kHeldVecs = 2048;      // 16-byte vectors of a block before a row takes more blocks,
+constexpr int kHeldMost = 13824;     // and at most (216 KB)
 constexpr int kSms = 152;
 constexpr int kPairThreads = 256;
 constexpr int kGivenThreads = 256;
@@ -126,12 +129,13 @@ __device__ __forceinline__ void join(float& m, float& s, float m2, float s2, flo
 }
 
 __device__ __forceinline__ void warp_join(float& m, float& s, float scale2) {
+  float top = m;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const float m2 = __shfl_xor_sync(0xffffffffu, m, o);
-    const float s2 = __shfl_xor_sync(0xffffffffu, s, o);
-    join(m, s, m2, s2, scale2);
-  }
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  s *= ex2((m - top) * scale2);
+  m = top;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
 }
 
 // A row's elements as `head` single ones up to a 16-byte boundary, `nvec`
@@ -513,88 +517,100 @@ int sum_blocks(int64_t n) {
 
 // ---- a row held in registers
 
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// The blocks of a cluster have started (arrive, then wait before the first
+// write to another's shared memory).  Relaxed: it orders no data.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
 
-// 16 bytes of minus infinities.
-template <typename T> __device__ __forceinline__ uint4 lowest();
-template <> __device__ __forceinline__ uint4 lowest<float>() {
-  return make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u);
-}
-template <> __device__ __forceinline__ uint4 lowest<__nv_bfloat16>() {
-  return make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
-}
-
-// Keeps the row in its packed form: without it the compiler carries the
-// unpacked values from one pass over the registers to the next (116 registers
-// instead of 64 for 8 vectors of bf16, half the blocks per SM).
-template <int NV>
-__device__ __forceinline__ void keep_packed(uint4 (&v)[NV]) {
-#pragma unroll
-  for (int k = 0; k < NV; ++k) asm volatile("" : "+r"(v[k].x), "+r"(v[k].y), "+r"(v[k].z), "+r"(v[k].w));
+// Sends (m, s) to `slot` in block `rank`, counted in bytes on its barrier
+// there.  A release barrier of the whole cluster instead makes every warp wait
+// for its own earlier loads and stores (the largest stall it measured).
+__device__ __forceinline__ void send(uint32_t slot, uint32_t bar, int rank, float m, float s) {
+  asm volatile(
+      "st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];" ::"r"(
+          tc::mapa_shared(slot, rank)),
+      "r"(__float_as_uint(m)), "r"(__float_as_uint(s)), "r"(tc::mapa_shared(bar, rank))
+      : "memory");
 }
 
-template <typename T, int NV>
-__device__ __forceinline__ float vec_max(const uint4 (&v)[NV]) {
+template <typename T>
+__device__ __forceinline__ float vec_max(const uint4& v) {
   if constexpr (sizeof(T) == 2) {
-    auto two = [](uint32_t u) { return *reinterpret_cast<__nv_bfloat162*>(&u); };
-    __nv_bfloat162 m = two(lowest<T>().x);
-#pragma unroll
-    for (int k = 0; k < NV; ++k)
-      m = __hmax2(m, __hmax2(__hmax2(two(v[k].x), two(v[k].y)), __hmax2(two(v[k].z), two(v[k].w))));
+    auto pair = [](uint32_t u) { return *reinterpret_cast<__nv_bfloat162*>(&u); };
+    const __nv_bfloat162 m = __hmax2(__hmax2(pair(v.x), pair(v.y)), __hmax2(pair(v.z), pair(v.w)));
     return fmaxf(__low2float(m), __high2float(m));
   } else {
-    float f[4], m = -INFINITY;
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      Vec<T>::unpack(v[k], f);
-      m = fmaxf(m, fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3])));
-    }
-    return m;
+    return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)),
+                 fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
   }
 }
 
-template <typename T, int NV>
-__device__ __forceinline__ float vec_sum(const uint4 (&v)[NV], float m, float scale2) {
-  float f[Vec<T>::N], s[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    Vec<T>::unpack(v[k], f);
-#pragma unroll
-    for (int j = 0; j < Vec<T>::N; ++j) s[j & 3] += ex2((f[j] - m) * scale2);
-  }
-  return (s[0] + s[1]) + (s[2] + s[3]);
+// Two FP32 lanes per instruction.
+__device__ __forceinline__ uint64_t two(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void split(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
-// Zeros in block `rank`'s share of a row.
-template <typename T, int NT, int NV>
-__device__ __forceinline__ void zero_slice(const Rows& a, T* drow, int rank) {
+// e of 16 bytes of logits, in pairs: 2^((z - m) scale2).
+template <typename T>
+__device__ __forceinline__ void vec_exp(const uint4& v, uint64_t minus_m, uint64_t scale2,
+                                        uint64_t (&e)[Vec<T>::N / 2]) {
+  float f[Vec<T>::N];
+  Vec<T>::unpack(v, f);
+#pragma unroll
+  for (int j = 0; j < Vec<T>::N / 2; ++j) {
+    float lo, hi;
+    split(mul2(add2(two(f[2 * j], f[2 * j + 1]), minus_m), scale2), lo, hi);
+    e[j] = two(ex2(lo), ex2(hi));
+  }
+}
+
+// Zeros in vectors [v0, v1) of a row, and around them in block 0.
+template <typename T>
+__device__ __forceinline__ void zero_share(const Rows& a, T* drow, int v0, int per_block, int rank) {
   const RowShape<T> sh(drow, a.vocab);
   const T zero = tok::from_float<T>(0.f);
   if (rank == 0) {
     if (threadIdx.x < sh.head) drow[threadIdx.x] = zero;
     else if (threadIdx.x >= 32 && sh.tail0 + int(threadIdx.x) - 32 < a.vocab) drow[sh.tail0 + threadIdx.x - 32] = zero;
   }
-#pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    const int i = rank * NT * NV + k * NT + threadIdx.x;
-    if (i < sh.nvec) __stcs(reinterpret_cast<uint4*>(drow + sh.head + i * Vec<T>::N), make_uint4(0, 0, 0, 0));
-  }
+  const int v1 = min(sh.nvec, v0 + per_block);
+  for (int i = v0 + threadIdx.x; i < v1; i += blockDim.x)
+    __stcs(reinterpret_cast<uint4*>(drow + sh.head + i * Vec<T>::N), make_uint4(0, 0, 0, 0));
 }
 
-// A row held in registers: one cluster of blocks per row, NV 16-byte vectors
-// per thread, loaded at once.  The row is read from memory exactly once, also
-// where its gradient is written, and a row is spread over up to eight SMs, so
-// a call with few rows is short.  Several blocks per SM, of different rows,
-// overlap one row's loads with another's arithmetic and writes.
-template <typename T, int NT, int NV, int MODE>
-__global__ void __launch_bounds__(NT) k_held(const Rows a, const Extra x) {
+// A row held on chip: one cluster of blocks per row, each with `per_block` of
+// the row's 16-byte vectors in shared memory, brought there by a bulk copy.
+// The row is read from memory exactly
+// once, also where its gradient is written (reading it again from L2 costs as
+// much as from memory: the SMs' traffic with L2 is the bound then), and a row
+// is spread over up to eight SMs, so a call with few rows is short.  Blocks of
+// different rows on one SM overlap one row's loads with another's arithmetic
+// and writes; holding rows in shared memory leaves registers for six of them.
+template <typename T, int MODE>
+__global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) k_held(const Rows a, const Extra x, int per_block) {
   constexpr int N = Vec<T>::N;
-  constexpr int W = NT / 32;
-  __shared__ float2 warp_part[W];
-  __shared__ float2 part[8];     // (m, s) of every block of the cluster
+  extern __shared__ __align__(128) uint4 held[];
+  __shared__ __align__(8) uint64_t full, joined;
+  __shared__ float2 warp_part[kHeldThreads / 32];
+  __shared__ __align__(8) float2 part[8];   // (m, s) of every block of the cluster
   __shared__ float2 out;         // (-g / S, g)
   __shared__ float out_m;
+  __shared__ int stopped;
   tok::allow_next();
   cg::cluster_group cl = cg::this_cluster();
   const int c = cl.num_blocks(), rank = cl.block_rank();
@@ -602,6 +618,7 @@ __global__ void __launch_bounds__(NT) k_held(const Rows a, const Extra x) {
   const T* row = static_cast<const T*>(a.logits) + t * a.stride;
   T* drow = a.dlogits ? static_cast<T*>(a.dlogits) + t * a.dstride : nullptr;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int base = rank * per_block;
   const int y = row_target(a, t);
   Token tk{};
   if (MODE == kPolicy) tk = load_token(x.policy, t);
@@ -613,18 +630,27 @@ __global__ void __launch_bounds__(NT) k_held(const Rows a, const Extra x) {
         x.logp_lo[t] = 0.f;
       }
     }
-    if (MODE == kPolicy && drow) zero_slice<T, NT, NV>(a, drow, rank);
+    if (MODE == kPolicy && drow) zero_share<T>(a, drow, base, per_block, rank);
     return;
   }
-  if (c > 1) cluster_arrive();   // waited for before the first write to another block
   const RowShape<T> sh(row, a.vocab);
-  const int i0 = rank * NT * NV + threadIdx.x;
-  uint4 v[NV];
-#pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    const int i = i0 + k * NT;
-    v[k] = i < sh.nvec ? __ldcs(reinterpret_cast<const uint4*>(row + sh.head + i * N)) : lowest<T>();
+  const int mine = max(0, min(per_block, sh.nvec - base));   // this block's vectors
+  if (threadIdx.x == 0) {
+    stopped = 0;
+    tc::mbar_init(tc::smem_u32(&full), 1);
+    tc::mbar_init(tc::smem_u32(&joined), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    if (c > 1) tc::mbar_expect_tx(tc::smem_u32(&joined), c * 8);
+    tc::mbar_expect_tx(tc::smem_u32(&full), mine * 16);
+    if (mine > 0)
+      asm volatile(
+          "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+              tc::smem_u32(held)),
+          "l"(row + sh.head + int64_t(base) * N), "r"(mine * 16), "r"(tc::smem_u32(&full))
+          : "memory");
   }
+  __syncthreads();
+  if (c > 1) cluster_arrive();   // waited for before the first write to another block
   // elements before and after the vectors: one per thread of the first block
   int single = -1;
   if (rank == 0) {
@@ -632,34 +658,55 @@ __global__ void __launch_bounds__(NT) k_held(const Rows a, const Extra x) {
     else if (threadIdx.x >= 32 && sh.tail0 + int(threadIdx.x) - 32 < a.vocab) single = sh.tail0 + threadIdx.x - 32;
   }
   const float zs = single >= 0 ? tok::to_float(row[single]) : -INFINITY;
-  const float zy = threadIdx.x < 32 ? tok::to_float(row[y]) : 0.f;
-  float m = fmaxf(fmaxf(-FLT_MAX, zs), vec_max<T, NV>(v));
-  keep_packed(v);
-  float s = ex2((zs - m) * a.scale2) + vec_sum<T, NV>(v, m, a.scale2);
-  keep_packed(v);
+  const float zy = warp == 0 ? tok::to_float(row[y]) : 0.f;
+  const uint64_t ss = two(a.scale2, a.scale2);
+  float m = -FLT_MAX, s;
+  {
+    uint64_t acc[2] = {0, 0};
+    tc::mbar_wait(tc::smem_u32(&full), 0, &stopped, &g_losses_err, 1);
+#pragma unroll 2
+    for (int i = threadIdx.x; i < mine; i += blockDim.x) {
+      const uint4 v = held[i];
+      const float top = vec_max<T>(v);
+      if (top > m) {
+        const float k = ex2((m - top) * a.scale2);
+        acc[0] = mul2(acc[0], two(k, k));
+        acc[1] = mul2(acc[1], two(k, k));
+        m = top;
+      }
+      uint64_t e[N / 2];
+      vec_exp<T>(v, two(-m, -m), ss, e);
+#pragma unroll
+      for (int j = 0; j < N / 2; ++j) acc[j & 1] = add2(acc[j & 1], e[j]);
+    }
+    float lo, hi;
+    split(add2(acc[0], acc[1]), lo, hi);
+    s = lo + hi;
+  }
+  if (single >= 0) join(m, s, zs, 1.f, a.scale2);
   warp_join(m, s, a.scale2);
   if (lane == 0) warp_part[warp] = make_float2(m, s);
   __syncthreads();
   if (warp == 0) {
-    m = lane < W ? warp_part[lane].x : -FLT_MAX;
-    s = lane < W ? warp_part[lane].y : 0.f;
+    const bool on = lane < int(blockDim.x) / 32;
+    m = on ? warp_part[lane].x : -FLT_MAX;
+    s = on ? warp_part[lane].y : 0.f;
     warp_join(m, s, a.scale2);
   }
   if (c > 1) {
     cluster_wait();
-    if (warp == 0 && lane < c) *cl.map_shared_rank(&part[rank], lane) = make_float2(m, s);
-    cluster_arrive();
-    cluster_wait();
     if (warp == 0) {
+      if (lane < c) send(tc::smem_u32(&part[rank]), tc::smem_u32(&joined), lane, m, s);
+      tc::mbar_wait_cluster(tc::smem_u32(&joined), 0, &stopped, &g_losses_err, 4);
       const float2 p = lane < c ? part[lane] : make_float2(-FLT_MAX, 0.f);
       m = p.x;
       s = p.y;
       warp_join(m, s, a.scale2);
     }
   }
-  if (warp == 0) {
+  if (warp == 0 && lane == 0) {
     const float logp = a.scale * (zy - m) - logf(s);
-    if (rank == 0 && lane == 0) {
+    if (rank == 0) {
       a.logp[t] = logp;
       if (MODE == kStats) {
         x.stats[t] = make_float2(m, 1.f / s);
@@ -667,32 +714,35 @@ __global__ void __launch_bounds__(NT) k_held(const Rows a, const Extra x) {
         x.logp_lo[t] = logp_rest(a.scale, zy, m, s, logp);
       }
     }
-    if (MODE == kPolicy && lane == 0) {
+    if (MODE == kPolicy) {
       const float g = a.scale * (tk.w * policy_terms(tk, x.policy, logp).coef);
       out = make_float2(-g / s, g);
       out_m = m;
     }
   }
-  if (MODE != kPolicy || !drow) return;
+  if (MODE != kPolicy || !drow) {
+    __syncthreads();   // no thread leaves while the others' values are still on their way here
+    return;
+  }
   __syncthreads();
   const float ga = out.x, g = out.y;
   m = out_m;
-  if (g == 0.f) return zero_slice<T, NT, NV>(a, drow, rank);
+  if (g == 0.f) return zero_share<T>(a, drow, base, per_block, rank);
   if (single >= 0) {
     const float d = ga * ex2((zs - m) * a.scale2);
     drow[single] = tok::from_float<T>(single == y ? d + g : d);
   }
   const bool aligned =
       ((reinterpret_cast<uintptr_t>(drow) ^ reinterpret_cast<uintptr_t>(row)) & 15) == 0;
-#pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    const int i = i0 + k * NT;
-    if (i >= sh.nvec) break;
-    const int v0 = sh.head + i * N;
+  const uint64_t mm = two(-m, -m), gg = two(ga, ga);
+#pragma unroll 2
+  for (int i = threadIdx.x; i < mine; i += blockDim.x) {
+    const int v0 = sh.head + (base + i) * N;
     float f[N];
-    Vec<T>::unpack(v[k], f);
+    uint64_t e[N / 2];
+    vec_exp<T>(held[i], mm, ss, e);
 #pragma unroll
-    for (int j = 0; j < N; ++j) f[j] = ga * ex2((f[j] - m) * a.scale2);
+    for (int j = 0; j < N / 2; ++j) split(mul2(e[j], gg), f[2 * j], f[2 * j + 1]);
     if (unsigned(y - v0) < unsigned(N)) {
 #pragma unroll
       for (int j = 0; j < N; ++j) f[j] += y - v0 == j ? g : 0.f;
@@ -706,45 +756,41 @@ __global__ void __launch_bounds__(NT) k_held(const Rows a, const Extra x) {
   }
 }
 
-// The smallest hold of a row: NV vectors per thread in c blocks.  Many rows
-// take the fewest blocks per row; few rows (under one block per SM) up to
-// eight, to use the SMs that there are.
+// How a row is held: c blocks of `threads` with `vecs` vectors each; c = 0:
+// it does not fit.
 struct Hold {
-  int nv, c;   // nv = 0: the row does not fit
+  int c, vecs, threads;
 };
 
 Hold hold_of(int64_t n, int vocab, int per_vec) {
-  const int nvec = vocab / per_vec;
-  int c = 1, nv = 1;
-  while (nv < kHeldVecs && nv * c * kHeldThreads < nvec) nv *= 2;
-  while (c < 8 && nv * c * kHeldThreads < nvec) c *= 2;
-  while (nv < 2 * kHeldVecs && nv * c * kHeldThreads < nvec) nv *= 2;
-  if (nv * c * kHeldThreads < nvec) return {0, 0};
-  while (c < 8 && nv > 1 && n * c * 2 <= kSms) {
-    c *= 2;
-    nv /= 2;
-  }
-  return {nv, c};
+  const int nvec = std::max(1, vocab / per_vec);
+  int c = 1;
+  while (c < 8 && (nvec + c - 1) / c > kHeldVecs) c *= 2;
+  while (c < 8 && n * c * 2 <= kSms && nvec / c > 64) c *= 2;   // few rows: use the SMs that there are
+  const int vecs = (nvec + c - 1) / c;
+  if (vecs > kHeldMost) return {0, 0, 0};
+  int threads = 64;
+  while (threads < kHeldThreads && threads * 4 < vecs) threads *= 2;
+  return {c, vecs, threads};
 }
 
 template <typename T, int MODE>
 cudaError_t launch_held(const Rows& a, const Extra& x, Hold h, cudaStream_t s) {
-  const unsigned grid = static_cast<unsigned>(a.n * h.c);
-  switch (h.nv) {
-    case 1: return launch(k_held<T, kHeldThreads, 1, MODE>, grid, kHeldThreads, h.c, false, s, a, x);
-    case 2: return launch(k_held<T, kHeldThreads, 2, MODE>, grid, kHeldThreads, h.c, false, s, a, x);
-    case 4: return launch(k_held<T, kHeldThreads, 4, MODE>, grid, kHeldThreads, h.c, false, s, a, x);
-    case 8: return launch(k_held<T, kHeldThreads, 8, MODE>, grid, kHeldThreads, h.c, false, s, a, x);
-    default: return launch(k_held<T, kHeldThreads, 16, MODE>, grid, kHeldThreads, h.c, false, s, a, x);
+  const int bytes = h.vecs * 16;
+  if (bytes > 40 * 1024) {   // beyond what a launch may ask without it
+    const cudaError_t e = cudaFuncSetAttribute(k_held<T, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               kHeldMost * 16);
+    if (e != cudaSuccess) return e;
   }
+  return launch(k_held<T, MODE>, static_cast<unsigned>(a.n * h.c), h.threads, h.c, false, s, bytes, a, x, h.vecs);
 }
 
 template <typename T, int MODE>
 cudaError_t launch_rows_of(const Rows& a, const Extra& x, cudaStream_t s) {
   const Hold h = hold_of(a.n, a.vocab, Vec<T>::N);
   const bool grad = MODE == kPolicy && a.dlogits;
-  if (h.nv && (grad || a.n < 2 * kSms) && a.n * h.c <= 0x7fffffff) return launch_held<T, MODE>(a, x, h, s);
-  return launch(k_rows<T, MODE>, static_cast<unsigned>(a.n), kRowThreads, 1, false, s, a, x);
+  if (h.c && (grad || a.n < 2 * kSms) && a.n * h.c <= 0x7fffffff) return launch_held<T, MODE>(a, x, h, s);
+  return launch(k_rows<T, MODE>, static_cast<unsigned>(a.n), kRowThreads, 1, false, s, 0, a, x);
 }
 
 template <int MODE>
@@ -885,7 +931,7 @@ extern "C" int muon_policy_loss(const void* logits, int dtype, int64_t stride, i
     cudaError_t e = launch_rows<kPolicy>(a, x, dtype, s);
     const int blocks = sum_blocks(n_tokens);
     if (e == cudaSuccess)
-      e = launch(k_policy_sum, blocks, kSumThreads, blocks, n_tokens > 0, s, a, x.policy, stats);
+      e = launch(k_policy_sum, blocks, kSumThreads, blocks, n_tokens > 0, s, 0, a, x.policy, stats);
     return end_call((n_tokens > 0) + 1, e);
   });
 }
@@ -944,17 +990,17 @@ extern "C" int muon_preference_loss(const void* logits, int dtype, int64_t strid
                   label_smoothing, x.logp_lo, margins, dlogits ? x.coef : nullptr};
     cudaError_t e = launch_rows<kStats>(a, x, dtype, s);
     if (e == cudaSuccess && n_pairs > 0)
-      e = launch(k_pairs, n_pairs, kPairThreads, 1, n_tokens > 0, s, a, q);
+      e = launch(k_pairs, n_pairs, kPairThreads, 1, n_tokens > 0, s, 0, a, q);
     const int vec = dtype == MUON_DTYPE_BF16 ? Vec<__nv_bfloat16>::N : Vec<float>::N;
     const int slices = std::max(1, (vocab / vec + kGivenVecs - 1) / kGivenVecs);
     if (e == cudaSuccess && dlogits && n_tokens > 0) {
       const unsigned grid = static_cast<unsigned>(n_tokens * slices + 1);
       e = dtype == MUON_DTYPE_BF16
-              ? launch(k_given<__nv_bfloat16>, grid, kGivenThreads, 1, true, s, a, x, q, stats, slices)
-              : launch(k_given<float>, grid, kGivenThreads, 1, true, s, a, x, q, stats, slices);
+              ? launch(k_given<__nv_bfloat16>, grid, kGivenThreads, 1, true, s, 0, a, x, q, stats, slices)
+              : launch(k_given<float>, grid, kGivenThreads, 1, true, s, 0, a, x, q, stats, slices);
     } else if (e == cudaSuccess) {
       const int blocks = sum_blocks(n_pairs);
-      e = launch(k_pair_sum, blocks, kSumThreads, blocks, n_tokens > 0 || n_pairs > 0, s, q, stats);
+      e = launch(k_pair_sum, blocks, kSumThreads, blocks, n_tokens > 0 || n_pairs > 0, s, 0, q, stats);
     }
     return end_call((n_tokens > 0) + (n_pairs > 0) + 1, e);
   });

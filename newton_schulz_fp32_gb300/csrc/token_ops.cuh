@@ -104,11 +104,12 @@ __device__ __forceinline__ void allow_next() { asm volatile("griddepcontrol.laun
 // scheduled while the kernel before it drains (it then calls wait_before).
 template <typename... A, typename... B>
 cudaError_t launch(void (*kernel)(A...), unsigned grid, unsigned block, int cluster, bool early,
-                   cudaStream_t s, B... args) {
+                   cudaStream_t s, int shared_bytes, B... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(block);
   cfg.stream = s;
+  cfg.dynamicSmemBytes = shared_bytes;
   cudaLaunchAttribute at[2];
   unsigned n = 0;
   if (cluster > 1) {
