@@ -493,8 +493,9 @@ MUON_API int muon_embedding(const void* table, int table_dtype, int64_t table_st
  * index offset; num_heads and use_muon are not looked at):
  *     accum[row v] = (overwrite ? 0 : accum[row v])
  *                    + scale * sum over t with ids[t] = v of dout[t]
- * The sum runs in FP32 over the tokens in order of their position, in blocks
- * of a fixed length, and is scaled once.  Without overwrite only rows of
+ * The sum runs in FP32 in an order that depends on ids and n_tokens alone
+ * (tokens in order of position within blocks, then the blocks), and is scaled
+ * once.  Without overwrite only rows of
  * tokens that occur are read and written; with overwrite every row is written
  * (zeros where no token occurs).  Nothing outside the parameter is touched.
  *   accum : device float storage buffer, 16-byte aligned

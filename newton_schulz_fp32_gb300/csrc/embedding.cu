@@ -5,12 +5,13 @@
 // ids repeat with a long tail (a few rows get thousands of tokens, most get
 // none or one), so adding with atomics would serialise on the frequent rows
 // and make the sum's order, and its bits, depend on timing.  Instead:
-//   k_embed_sort   sorts (id, position) by id, stably (radix, 9 bits a pass,
-//                  one cluster of thread blocks);
-//   k_embed_sum    walks the sorted tokens in blocks of kRun: a run of equal
-//                  ids inside a block goes straight to its row of accum, a run
-//                  that crosses blocks leaves partial sums;
-//   k_embed_join   adds the partial sums of each crossing run in block order.
+//   k_embed_sort   sorts (id, position) by id, stably (radix, up to 9 bits a
+//                  pass, one cluster of thread blocks);
+//   k_embed_sum    walks the sorted tokens in blocks: a run of equal ids goes
+//                  straight to its row of accum, one that covers a block or
+//                  more leaves partial sums;
+//   k_embed_join   adds the partial sums of each such run in block order.
+// Up to 1024 tokens k_embed_few does all of it in one launch.
 // So every sum has one fixed order, and the work is balanced whatever the ids.
 #include <algorithm>
 #include <cmath>
@@ -114,80 +115,375 @@ void launch_lookup(const Lookup& a, cudaStream_t s) {
 // ------------------------------------------------------------------ gradient
 
 constexpr int kSortThreads = 512;
+constexpr int kSortBlocks = 16;      // most blocks of its cluster
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortBits = 9;
 constexpr int kSortBins = 1 << kSortBits;
-constexpr int kRun = 32;             // sorted tokens per block of k_embed_sum
-constexpr int kSumX = 128;           // threads of k_embed_sum and k_embed_join
+constexpr int kSortItems = 8;        // tokens a thread has in hand
+constexpr int kSortShared = kSortWarps * kSortBins * int(sizeof(int));
+constexpr int kRunMost = 32;         // sorted tokens per block of k_embed_sum, at most
+constexpr int kSumX = 128;           // its threads
+constexpr int kJoinGroups = 8;      // k_embed_join: warps of a block, each adding every 16th partial sum
+constexpr int kFew = 1024;           // tokens up to which k_embed_few is taken
+constexpr int kFewX = 256;
+constexpr int kFillRows = 256;       // rows of the table per filling block, at most
+
+// The parameter's runs in storage: elements [rel[i], rel[i + 1]) of the
+// parameter start at storage index at[i].
+struct Segments {
+  int n;
+  int64_t rel[MUON_EMBEDDING_MAX_SEGMENTS];
+  int64_t at[MUON_EMBEDDING_MAX_SEGMENTS];
+  int64_t numel;
+
+  // storage index of element i, and how many elements follow in one piece
+  __device__ __forceinline__ int64_t place(int64_t i, int64_t* room) const {
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (rel[mid] <= i) lo = mid; else hi = mid - 1;
+    }
+    *room = (lo + 1 < n ? rel[lo + 1] : numel) - i;
+    return at[lo] + (i - rel[lo]);
+  }
+};
+
+struct Grad {
+  float* accum;
+  const void* dout;
+  const void* ids;
+  int64_t dstride;
+  int ids64;
+  int n, rows, cols;
+  float scale;
+  int overwrite;
+  const int2* sorted;   // (id, position) of the tokens, by id
+  float* partial;   // two rows of `cols` per block of `run` tokens
+  int* crossing;    // [0]: how many runs have partial sums; then the blocks they start in
+  int run;          // tokens per block
+  int blocks;       // blocks of tokens
+  int slabs;        // blocks of columns
+  int fill_rows;    // rows of the table per filling block (overwrite)
+};
+
+__device__ __forceinline__ int grad_id(const Grad& g, int t) {
+  return lookup_id(g.ids, g.ids64, t, g.rows);
+}
+
+// Where row `row` of the parameter lies.  `whole`: in one piece.
+struct RowPlace {
+  float* p;
+  bool whole;
+  __device__ __forceinline__ RowPlace() : p(nullptr), whole(false) {}
+  __device__ __forceinline__ RowPlace(const Grad& g, const Segments& sg, int row) {
+    int64_t room;
+    p = g.accum + sg.place(int64_t(row) * g.cols, &room);
+    whole = room >= g.cols;
+  }
+};
+
+// A thread's columns within a block of `width` threads.  VEC: N consecutive
+// ones, moved as 16 bytes; else N columns `width` apart (each access of a warp
+// then covers consecutive ones).
+template <int N, bool VEC>
+__device__ __forceinline__ int column(int slab, int width, int x, int k) {
+  return VEC ? (slab * width + x) * N + k : slab * width * N + k * width + x;
+}
+
+// One token's columns of dout as they lie in memory.
+template <typename T, bool VEC>
+struct Piece {
+  static constexpr int N = Vec<T>::N;
+  uint4 v;                     // VEC
+  float f[VEC ? 1 : N];
+  __device__ __forceinline__ void load(const Grad& g, int64_t t, int slab, int width, int x, bool on) {
+    const T* row = static_cast<const T*>(g.dout) + t * g.dstride;
+    if constexpr (VEC) {
+      const int c = column<N, true>(slab, width, x, 0);
+      v = make_uint4(0, 0, 0, 0);
+      if (on && c < g.cols) v = *reinterpret_cast<const uint4*>(row + c);
+    } else {
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        const int c = column<N, false>(slab, width, x, k);
+        f[k] = on && c < g.cols ? tok::to_float(row[c]) : 0.f;
+      }
+    }
+  }
+  __device__ __forceinline__ void add_to(float* acc) const {
+    if constexpr (VEC) {
+      float u[N];
+      Vec<T>::unpack(v, u);
+#pragma unroll
+      for (int k = 0; k < N; ++k) acc[k] += u[k];
+    } else {
+#pragma unroll
+      for (int k = 0; k < N; ++k) acc[k] += f[k];
+    }
+  }
+};
+
+// The old value, or 0 where it is overwritten, plus scale * sum.
+template <int W>
+__device__ __forceinline__ void add_at(const Grad& g, float* p, const float* sum) {
+  if constexpr (W == 4) {
+    float4* q = reinterpret_cast<float4*>(p);
+    const float4 o = g.overwrite ? make_float4(0.f, 0.f, 0.f, 0.f) : *q;
+    *q = make_float4(o.x + g.scale * sum[0], o.y + g.scale * sum[1], o.z + g.scale * sum[2],
+                     o.w + g.scale * sum[3]);
+  } else {
+    *p = (g.overwrite ? 0.f : *p) + g.scale * sum[0];
+  }
+}
+
+// A thread's columns of a row that lies in one piece at p.  ADD: added to
+// accum; else a partial sum.
+template <int N, bool VEC, bool ADD>
+__device__ __forceinline__ void put(const Grad& g, float* p, int slab, int width, int x, const float* sum) {
+  if constexpr (VEC) {
+    const int c = column<N, VEC>(slab, width, x, 0);
+    if (c < g.cols)
+#pragma unroll
+      for (int k = 0; k < N; k += 4) {
+        if constexpr (ADD) add_at<4>(g, p + c + k, sum + k);
+        else *reinterpret_cast<float4*>(p + c + k) = make_float4(sum[k], sum[k + 1], sum[k + 2], sum[k + 3]);
+      }
+  } else {
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int c = column<N, VEC>(slab, width, x, k);
+      if (c >= g.cols) continue;
+      if constexpr (ADD) add_at<1>(g, p + c, sum + k);
+      else p[c] = sum[k];
+    }
+  }
+}
+
+// The same for a row cut by partitions, element by element.
+template <int N, bool VEC>
+__device__ __forceinline__ void scatter(const Grad& g, const Segments& sg, int id, int slab, int width, int x,
+                                        const float* sum) {
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const int c = column<N, VEC>(slab, width, x, k);
+    if (c >= g.cols) continue;
+    int64_t room;
+    add_at<1>(g, g.accum + sg.place(int64_t(id) * g.cols + c, &room), sum + k);
+  }
+}
+
+// accum[row] = old + scale * sum for a thread's columns.
+template <int N, bool VEC>
+__device__ __forceinline__ void commit(const Grad& g, const Segments& sg, int id, int slab, int width, int x,
+                                       const float* sum) {
+  const RowPlace row(g, sg, id);
+  if (row.whole) put<N, VEC, true>(g, row.p, slab, width, x, sum);
+  else scatter<N, VEC>(g, sg, id, slab, width, x, sum);
+}
+
+// What k_embed_sum does after a token.
+enum { kGoOn = 0, kCommit = 1, kPartial = 2, kScattered = 3 };
+struct __align__(16) Step {
+  float* p;
+  int act;
+};
+
+// Zeros in the rows of [r0, r1) that are not `named`, neighbours together.
+__device__ void fill_zeros(const Grad& g, const Segments& sg, int r0, int r1, const uint8_t* named) {
+  for (int r = r0; r < r1;) {
+    if (named[r - r0]) {
+      ++r;
+      continue;
+    }
+    int e = r + 1;
+    while (e < r1 && !named[e - r0]) ++e;
+    int64_t i = int64_t(r) * g.cols, left = int64_t(e - r) * g.cols;
+    while (left > 0) {
+      int64_t room;
+      float* p = g.accum + sg.place(i, &room);
+      const int n = static_cast<int>(room < left ? room : left);
+      int head = static_cast<int>((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / 4;
+      head = min(head, n);
+      if (int(threadIdx.x) < head) p[threadIdx.x] = 0.f;
+      const int quads = (n - head) / 4;
+      for (int q = threadIdx.x; q < quads; q += blockDim.x)
+        *reinterpret_cast<float4*>(p + head + 4 * q) = make_float4(0.f, 0.f, 0.f, 0.f);
+      const int tail = head + 4 * quads + threadIdx.x;
+      if (tail < n) p[tail] = 0.f;
+      i += n;
+      left -= n;
+    }
+    r = e;
+  }
+}
+
+// ---- few tokens: one launch, no sort
+
+// One block per token and block of columns.  The block of an id's first token
+// finds the others (every block reads all the ids: at most 8 KB, from L2),
+// adds them in order of position and writes the row; the others leave.
+// Further blocks zero the rows that no token names (overwrite).
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kFewX) k_embed_few(const Grad g, const __grid_constant__ Segments sg) {
+  constexpr int N = Vec<T>::N;
+  constexpr int U = 4;
+  __shared__ unsigned found[kFew / 32];
+  __shared__ int list[kFew];
+  __shared__ uint8_t named[kFillRows];
+  const int lane = threadIdx.x % 32;
+  if (blockIdx.x >= unsigned(g.n) * g.slabs) {
+    const int r0 = (blockIdx.x - g.n * g.slabs) * g.fill_rows, r1 = min(g.rows, r0 + g.fill_rows);
+    for (int r = threadIdx.x; r < r1 - r0; r += blockDim.x) named[r] = 0;
+    __syncthreads();
+    for (int t = threadIdx.x; t < g.n; t += blockDim.x) {
+      const int id = grad_id(g, t);
+      if (id >= r0 && id < r1) named[id - r0] = 1;
+    }
+    __syncthreads();
+    return fill_zeros(g, sg, r0, r1, named);
+  }
+  const int t = blockIdx.x / g.slabs, slab = blockIdx.x % g.slabs;
+  const int id = grad_id(g, t);
+  if (id < 0) return;
+  const int words = (g.n + 31) / 32;
+  for (int j0 = threadIdx.x - lane; j0 < words * 32; j0 += blockDim.x) {
+    const int j = j0 + lane;
+    const unsigned same = __ballot_sync(0xffffffffu, j < g.n && grad_id(g, j) == id);
+    if (lane == 0) found[j0 / 32] = same;
+  }
+  __syncthreads();
+  int count = 0;
+  for (int w = 0; w < words; ++w) {
+    const unsigned m = found[w];
+    if (w == t / 32 ? (m & ((1u << (t % 32)) - 1)) != 0 : w < t / 32 && m != 0) return;   // not the first
+    if (threadIdx.x < 32 && (m >> lane & 1)) list[count + __popc(m & ((1u << lane) - 1))] = w * 32 + lane;
+    count += __popc(m);
+  }
+  __syncthreads();
+  float acc[N];
+#pragma unroll
+  for (int k = 0; k < N; ++k) acc[k] = 0.f;
+  for (int j0 = 0; j0 < count; j0 += U) {
+    Piece<T, VEC> p[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      p[u].load(g, list[min(j0 + u, count - 1)], slab, blockDim.x, threadIdx.x, j0 + u < count);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (j0 + u < count) p[u].add_to(acc);
+  }
+  commit<N, VEC>(g, sg, id, slab, blockDim.x, threadIdx.x, acc);
+}
+
+// ---- more tokens: sort, sum runs, join the runs that cross blocks
 
 struct SortArgs {
   const void* ids;
   int ids64;
   int n, rows;
   int passes, bits;      // bits per pass
-  int *key0, *val0;      // the result
-  int *key1, *val1;
+  int2* sorted;          // (id, position): the result
+  int2* other;
+  int* crossing;
 };
 
 // Stable radix sort of (id, position) by id, tokens without a row last (key =
 // rows).  One cluster; block r takes the r-th contiguous share of the tokens
 // and each warp a contiguous share of that, so ranks in order of (bin, block,
 // warp, token) keep the sort stable.  Per pass: each warp counts its tokens'
-// bins (equal bins within a warp found by match_any, so no atomics), the
-// counts become offsets, and each warp places its tokens.
-__global__ void __launch_bounds__(kSortThreads) k_embed_sort(const SortArgs a) {
-  __shared__ int count[kSortWarps][kSortBins];   // 32 KB
-  __shared__ int total[kSortBins];               // this block's tokens per bin
-  __shared__ int scan[kSortWarps];
+// bins (equal bins within a warp found by one ballot per bit, so no atomics;
+// match_any took 3 times as long), the counts become offsets, and each warp
+// places its tokens.  A thread fetches kSortItems tokens at a time; up to
+// 65536 tokens they stay in registers, with their ranks, from the count to the
+// placing.
+__global__ void __launch_bounds__(kSortThreads, 1) k_embed_sort(const SortArgs a) {
+  extern __shared__ int count[];                  // kSortWarps x kSortBins
+  __shared__ int total[kSortBlocks][kSortBins];   // every block's tokens per bin
+  __shared__ int scan[kSortBins / 32];
   cg::cluster_group cl = cg::this_cluster();
   const int nb = cl.num_blocks(), rank = cl.block_rank();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  tok::allow_next();
+  if (rank == 0 && threadIdx.x == 0) a.crossing[0] = 0;
+  cl.sync();   // every block has started: total may be written from outside
   const int share = (a.n + nb * kSortWarps - 1) / (nb * kSortWarps);
   const int64_t from = int64_t(rank * kSortWarps + warp) * share;
   const int lo = static_cast<int>(from < a.n ? from : a.n);
   const int hi = static_cast<int>(from + share < a.n ? from + share : a.n);
+  const bool once = share <= 32 * kSortItems;
   const unsigned below = (1u << lane) - 1;
   const int mask = (1 << a.bits) - 1;
+  int* mine = count + warp * kSortBins;
+  int key[kSortItems], val[kSortItems], rank_in[kSortItems];
   for (int p = 0; p < a.passes; ++p) {
     const bool to0 = ((a.passes - 1 - p) & 1) == 0;
-    const int* ki = to0 ? a.key1 : a.key0;
-    const int* vi = to0 ? a.val1 : a.val0;
-    int* ko = to0 ? a.key0 : a.key1;
-    int* vo = to0 ? a.val0 : a.val1;
-    auto load = [&](int t) -> int {
-      if (p) return ki[t];
-      const int id = tok::load_index(a.ids, a.ids64, t);
-      if (id >= a.rows) atomicCAS(&g_embedding_err, 0, kErrIndex);
-      return id < 0 || id >= a.rows ? a.rows : id;
+    const int2* src = to0 ? a.other : a.sorted;
+    int2* dst = to0 ? a.sorted : a.other;
+    auto fetch = [&](int t0) {
+#pragma unroll
+      for (int i = 0; i < kSortItems; ++i) {
+        const int t = t0 + 32 * i + lane;
+        key[i] = val[i] = 0;
+        if (t < hi) {
+          if (p) {
+            const int2 q = src[t];
+            key[i] = q.x;
+            val[i] = q.y;
+          } else {
+            const int id = lookup_id(a.ids, a.ids64, t, a.rows);
+            key[i] = id < 0 ? a.rows : id;
+            val[i] = t;
+          }
+        }
+      }
     };
     const int shift = p * a.bits;
-    for (int i = threadIdx.x; i < kSortWarps * kSortBins; i += kSortThreads) (&count[0][0])[i] = 0;
-    __syncthreads();
-    for (int t0 = lo; t0 < hi; t0 += 32) {
-      const int t = t0 + lane;
-      const unsigned on = __ballot_sync(0xffffffffu, t < hi);
-      if (t < hi) {
-        const int bin = static_cast<int>(static_cast<unsigned>(load(t)) >> shift) & mask;
-        const unsigned same = __match_any_sync(on, bin);
-        if ((same & below) == 0) count[warp][bin] += __popc(same);
+    auto bin_of = [&](int i) { return static_cast<int>(static_cast<unsigned>(key[i]) >> shift) & mask; };
+    // each token's place among its bin's, counted on from mine[]
+    auto place = [&](int t0) {
+#pragma unroll
+      for (int i = 0; i < kSortItems; ++i) {
+        if (t0 + 32 * i >= hi) break;
+        const bool in = t0 + 32 * i + lane < hi;
+        const int b = bin_of(i);
+        unsigned same = __ballot_sync(0xffffffffu, in);
+#pragma unroll
+        for (int q = 0; q < kSortBits; ++q) {
+          const unsigned set = __ballot_sync(0xffffffffu, b >> q & 1);
+          same &= (b >> q & 1) ? set : ~set;
+        }
+        if (in) rank_in[i] = mine[b] + __popc(same & below);
+        __syncwarp();
+        if (in && (same & below) == 0) mine[b] += __popc(same);
+        __syncwarp();
       }
-      __syncwarp();
+    };
+    fetch(lo);
+    for (int i = threadIdx.x; i < kSortWarps * kSortBins; i += kSortThreads) count[i] = 0;
+    __syncthreads();
+    for (int t0 = lo; t0 < hi; t0 += 32 * kSortItems) {
+      if (t0 > lo) fetch(t0);
+      place(t0);
     }
     __syncthreads();
-    // per bin: offsets of the warps within the block, and the block's total
-    const int bin = threadIdx.x;   // kSortThreads == kSortBins
+    // per bin: the warps' offsets within the block, and the block's total
+    static_assert(kSortThreads == kSortBins, "one bin per thread");
+    const int bin = threadIdx.x;
     int run = 0;
 #pragma unroll
     for (int w = 0; w < kSortWarps; ++w) {
-      const int c = count[w][bin];
-      count[w][bin] = run;
+      const int c = count[w * kSortBins + bin];
+      count[w * kSortBins + bin] = run;
       run += c;
     }
-    total[bin] = run;
+#pragma unroll
+    for (int b = 0; b < kSortBlocks; ++b)
+      if (b < nb) *cl.map_shared_rank(&total[rank][bin], b) = run;
     cl.sync();
     int all = 0, before = 0;
-    for (int b = 0; b < nb; ++b) {
-      const int c = *cl.map_shared_rank(&total[bin], b);
+#pragma unroll
+    for (int b = 0; b < kSortBlocks; ++b) {
+      const int c = b < nb ? total[b][bin] : 0;
       if (b < rank) before += c;
       all += c;
     }
@@ -200,245 +496,196 @@ __global__ void __launch_bounds__(kSortThreads) k_embed_sort(const SortArgs a) {
     if (lane == 31) scan[warp] = incl;
     __syncthreads();
     int base = incl - all + before;
-    for (int w = 0; w < warp; ++w) base += scan[w];
 #pragma unroll
-    for (int w = 0; w < kSortWarps; ++w) count[w][bin] += base;
+    for (int w = 0; w < kSortWarps; ++w) base += w < warp ? scan[w] : 0;
+#pragma unroll
+    for (int w = 0; w < kSortWarps; ++w) count[w * kSortBins + bin] += base;
     __syncthreads();
-    for (int t0 = lo; t0 < hi; t0 += 32) {
-      const int t = t0 + lane;
-      const unsigned on = __ballot_sync(0xffffffffu, t < hi);
-      if (t < hi) {
-        const int key = load(t);
-        const int b = static_cast<int>(static_cast<unsigned>(key) >> shift) & mask;
-        const unsigned same = __match_any_sync(on, b);
-        const int at = count[warp][b] + __popc(same & below);
-        __syncwarp(on);
-        if ((same & below) == 0) count[warp][b] += __popc(same);
-        ko[at] = key;
-        vo[at] = p ? vi[t] : t;
+    for (int t0 = lo; t0 < hi; t0 += 32 * kSortItems) {
+      if (!once) {
+        fetch(t0);
+        place(t0);
       }
-      __syncwarp();
-    }
-    cl.sync();   // the other blocks read ko / vo, and total, in the next pass
-  }
-}
-
-// The parameter's runs in storage: elements [rel[i], rel[i + 1]) of the
-// parameter start at storage index at[i].
-struct Segments {
-  int n;
-  int64_t rel[MUON_EMBEDDING_MAX_SEGMENTS];
-  int64_t at[MUON_EMBEDDING_MAX_SEGMENTS];
-  int64_t numel;
-
-  __device__ __forceinline__ int find(int64_t i) const {
-    int lo = 0, hi = n - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) / 2;
-      if (rel[mid] <= i) lo = mid; else hi = mid - 1;
-    }
-    return lo;
-  }
-  // storage index of element i, and how many elements follow in one piece
-  __device__ __forceinline__ int64_t place(int64_t i, int64_t* room) const {
-    const int k = find(i);
-    *room = (k + 1 < n ? rel[k + 1] : numel) - i;
-    return at[k] + (i - rel[k]);
-  }
-};
-
-struct Grad {
-  float* accum;
-  const void* dout;
-  int64_t dstride;
-  int n, rows, cols;
-  float scale;
-  int overwrite;
-  const int* key;
-  const int* val;
-  float* partial;   // two rows of `cols` per block of kRun tokens
-  int blocks;       // blocks of kRun tokens
-  int slabs;        // blocks of columns
-  int fill_rows;    // rows of the table per filling block (overwrite)
-};
-
-// Thread columns.  VEC: N consecutive columns, moved as 16 bytes; else N
-// columns kSumX apart (each access of a warp then covers consecutive ones).
-template <int N, bool VEC>
-__device__ __forceinline__ int column(int slab, int k) {
-  return VEC ? (slab * kSumX + int(threadIdx.x)) * N + k
-             : slab * kSumX * N + k * kSumX + int(threadIdx.x);
-}
-
-// accum[row] = old + scale * f
-template <int N, bool VEC>
-__device__ __forceinline__ void add_row(const Grad& g, const Segments& sg, int row, int slab,
-                                        const float* f) {
-  if constexpr (VEC) {
-    const int c = column<N, VEC>(slab, 0);
-    if (c >= g.cols) return;
-    int64_t room;
-    float* d = g.accum + sg.place(int64_t(row) * g.cols + c, &room);
-    if (room >= N && (reinterpret_cast<uintptr_t>(d) & 15) == 0) {
 #pragma unroll
-      for (int k = 0; k < N; k += 4) {
-        float4* q = reinterpret_cast<float4*>(d + k);
-        float4 o = g.overwrite ? make_float4(0.f, 0.f, 0.f, 0.f) : *q;
-        o.x += g.scale * f[k]; o.y += g.scale * f[k + 1];
-        o.z += g.scale * f[k + 2]; o.w += g.scale * f[k + 3];
-        *q = o;
-      }
-      return;
+      for (int i = 0; i < kSortItems; ++i)
+        if (t0 + 32 * i + lane < hi)
+          dst[rank_in[i] + (once ? mine[bin_of(i)] : 0)] = make_int2(key[i], val[i]);
     }
-  }
-#pragma unroll
-  for (int k = 0; k < N; ++k) {
-    const int c = column<N, VEC>(slab, k);
-    if (c >= g.cols) continue;
-    int64_t room;
-    float* d = g.accum + sg.place(int64_t(row) * g.cols + c, &room);
-    *d = (g.overwrite ? 0.f : *d) + g.scale * f[k];
-  }
-}
-
-template <int N, bool VEC>
-__device__ __forceinline__ float* partial_at(const Grad& g, int block, int which, int slab, int k) {
-  return g.partial + (int64_t(block) * 2 + which) * g.cols + column<N, VEC>(slab, k);
-}
-
-// Rows that no token names, in [r0, r1): zeros.
-__device__ void fill_rows(const Grad& g, const Segments& sg, int r0, int r1) {
-  int lo = 0, hi = g.n;   // first sorted token with id >= r0
-  while (lo < hi) {
-    const int mid = lo + (hi - lo) / 2;
-    if (g.key[mid] < r0) lo = mid + 1; else hi = mid;
-  }
-  for (int r = r0; r < r1; ++r) {
-    bool named = false;
-    while (lo < g.n && g.key[lo] <= r) {
-      named = true;
-      // step over the run of r
-      int a = lo, b = g.n;
-      while (a < b) {
-        const int mid = a + (b - a) / 2;
-        if (g.key[mid] <= r) a = mid + 1; else b = mid;
-      }
-      lo = a;
-    }
-    if (named) continue;
-    int64_t room;
-    for (int c = threadIdx.x; c < g.cols; c += kSumX)
-      g.accum[sg.place(int64_t(r) * g.cols + c, &room)] = 0.f;
+    cl.sync();   // dst is complete, and total read everywhere
   }
 }
 
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kSumX) k_embed_sum(const Grad g, const __grid_constant__ Segments sg) {
   constexpr int N = Vec<T>::N;
-  constexpr int U = 4;    // rows in flight
+  constexpr int U = 4;    // tokens in flight
+  __shared__ int key[2 * kRunMost + 1], val[2 * kRunMost];   // this block's tokens and the next one's
+  __shared__ int edge[3];   // ids of the token before, the one before the block before, the one after the next
+  __shared__ Step step[2 * kRunMost];
+  __shared__ uint8_t named[kFillRows];
+  tok::wait_before();
+  tok::allow_next();
   if (blockIdx.x >= unsigned(g.blocks) * g.slabs) {
-    const int r0 = (blockIdx.x - g.blocks * g.slabs) * g.fill_rows;
-    return fill_rows(g, sg, r0, min(g.rows, r0 + g.fill_rows));
+    const int r0 = (blockIdx.x - g.blocks * g.slabs) * g.fill_rows, r1 = min(g.rows, r0 + g.fill_rows);
+    for (int r = threadIdx.x; r < r1 - r0; r += kSumX) named[r] = 0;
+    int lo = 0, hi = g.n;   // the first sorted token with id >= r0
+    while (lo < hi) {
+      const int mid = lo + (hi - lo) / 2;
+      if (g.sorted[mid].x < r0) lo = mid + 1; else hi = mid;
+    }
+    __syncthreads();
+    for (int t = lo + threadIdx.x; t < g.n; t += kSumX) {
+      const int id = g.sorted[t].x;
+      if (id >= r1) break;
+      named[id - r0] = 1;
+    }
+    __syncthreads();
+    return fill_zeros(g, sg, r0, r1, named);
   }
-  __shared__ int key[kRun + 2], val[kRun];   // key[0], key[n + 1]: the neighbours' ids
   const int block = blockIdx.x / g.slabs, slab = blockIdx.x % g.slabs;
-  const int t0 = block * kRun, n = min(kRun, g.n - t0);
-  for (int i = threadIdx.x; i < n + 2; i += kSumX) {
-    const int t = t0 + i - 1;
-    key[i] = t >= 0 && t < g.n ? g.key[t] : -1;
-    if (i >= 1 && i <= n) val[i - 1] = g.val[t];
+  const int x = threadIdx.x;
+  const int64_t t0 = int64_t(block) * g.run;
+  auto key_at = [&](int64_t t) { return t >= 0 && t < g.n ? g.sorted[t].x : -1; };
+  for (int i = x; i < 2 * g.run; i += kSumX) {
+    const int2 q = t0 + i < g.n ? g.sorted[t0 + i] : make_int2(-1, 0);
+    key[i] = q.x;
+    val[i] = q.y;
+  }
+  if (x >= kSumX - 3) {
+    const int e = x - (kSumX - 3);
+    edge[e] = key_at(e == 0 ? t0 - 1 : e == 1 ? t0 - g.run - 1 : t0 + 2 * g.run);
   }
   __syncthreads();
-  if (key[1] >= g.rows) return;   // only tokens without a row from here on
-  const T* dout = static_cast<const T*>(g.dout);
+  const int n = static_cast<int>(min(int64_t(g.run), g.n - t0));
+  const int id0 = key[0], id1 = key[n - 1];
+  if (id0 >= g.rows) return;   // only tokens without a row from here on
+  const int lane = x % 32;
+  auto count = [&](int from, int id) {   // tokens of `id` among the g.run from `from` on
+    return __popc(__ballot_sync(0xffffffffu, lane < g.run && key[from + min(lane, g.run - 1)] == id));
+  };
+  // The first run, where it comes from an earlier block: its tokens here.
+  const int begun = edge[0] == id0 ? count(0, id0) : 0;
+  // The last run, where it goes on into the next block: its tokens there.
+  const int beyond = n == g.run && id1 < g.rows && key[g.run] == id1 ? count(g.run, id1) : 0;
+  // A run over one border belongs to the block it starts in; a longer one
+  // leaves a partial sum in every block (slot 1 where it starts, else 0).
+  const bool begun_long = begun > 0 && (edge[1] == id0 || (begun == n && beyond > 0));
+  const bool last_starts = begun < n;
+  const bool last_long = beyond == g.run && edge[2] == id1;
+  const int from = begun > 0 && !begun_long ? begun : 0;
+  int end = last_starts && !last_long ? n + beyond : n;
+  if (slab == 0 && x == 0 && last_starts && last_long) g.crossing[1 + atomicAdd(g.crossing, 1)] = block;
+  while (end > from && key[end - 1] >= g.rows) --end;   // tokens without a row are the last
+  // What to do after each token, worked out once per block: finding a row
+  // among the partitions costs more than adding a token's columns.
+  for (int j = from + x; j < end; j += kSumX) {
+    Step st{nullptr, kGoOn};
+    if (j + 1 == end || key[j + 1] != key[j]) {
+      const bool first_part = j < begun, last_part = j + 1 == end && last_starts && last_long;
+      if (first_part || last_part) {
+        st = {g.partial + (int64_t(block) * 2 + (first_part ? 0 : 1)) * g.cols, kPartial};
+      } else {
+        const RowPlace row(g, sg, key[j]);
+        st = {row.p, row.whole ? kCommit : kScattered};
+      }
+    }
+    step[j] = st;
+  }
+  __syncthreads();
   float acc[N];
 #pragma unroll
   for (int k = 0; k < N; ++k) acc[k] = 0.f;
-  bool from_before = key[0] == key[1];
-  auto flush = [&](int id, bool goes_on) {
-    if (from_before || goes_on) {
+  for (int j0 = from; j0 < end; j0 += U) {
+    Piece<T, VEC> p[U];
 #pragma unroll
-      for (int k = 0; k < N; ++k)
-        if (column<N, VEC>(slab, k) < g.cols)
-          *partial_at<N, VEC>(g, block, from_before ? 0 : 1, slab, k) = acc[k];
-    } else {
-      add_row<N, VEC>(g, sg, id, slab, acc);
-    }
-    from_before = false;
-#pragma unroll
-    for (int k = 0; k < N; ++k) acc[k] = 0.f;
-  };
-  for (int j0 = 0; j0 < n; j0 += U) {
-    float f[U][N];
+    for (int u = 0; u < U; ++u) p[u].load(g, val[min(j0 + u, end - 1)], slab, kSumX, x, j0 + u < end);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int j = j0 + u;
-      const bool on = j < n && key[j + 1] < g.rows;
-      const T* row = dout + (on ? int64_t(val[j]) : 0) * g.dstride;
-      if constexpr (VEC) {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        const int c = column<N, VEC>(slab, 0);
-        if (on && c < g.cols) v = *reinterpret_cast<const uint4*>(row + c);
-        Vec<T>::unpack(v, f[u]);
-      } else {
+      if (j0 + u >= end) break;
+      p[u].add_to(acc);
+      const Step st = step[j0 + u];
+      if (st.act == kGoOn) continue;
+      if (st.act == kPartial) put<N, VEC, false>(g, st.p, slab, kSumX, x, acc);
+      else if (st.act == kCommit) put<N, VEC, true>(g, st.p, slab, kSumX, x, acc);
+      else scatter<N, VEC>(g, sg, key[j0 + u], slab, kSumX, x, acc);
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-          const int c = column<N, VEC>(slab, k);
-          f[u][k] = on && c < g.cols ? tok::to_float(row[c]) : 0.f;
-        }
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int j = j0 + u;
-      if (j >= n || key[j + 1] >= g.rows) break;
-#pragma unroll
-      for (int k = 0; k < N; ++k) acc[k] += f[u][k];
-      const int next = key[j + 2];
-      if (j + 1 == n || next != key[j + 1]) flush(key[j + 1], j + 1 == n && next == key[j + 1]);
+      for (int k = 0; k < N; ++k) acc[k] = 0.f;
     }
   }
 }
 
-// Block b joins the run that starts inside block b of tokens and goes on past
-// it (if there is one).
-template <int N, bool VEC>
-__global__ void __launch_bounds__(kSumX) k_embed_join(const Grad g, const __grid_constant__ Segments sg) {
-  const int block = blockIdx.x / g.slabs, slab = blockIdx.x % g.slabs;
-  const int t0 = block * kRun, last = t0 + kRun - 1;
-  if (last + 1 >= g.n) return;
-  const int id = g.key[last];
-  if (id >= g.rows || g.key[last + 1] != id) return;
-  if (t0 > 0 && g.key[t0] == id && g.key[t0 - 1] == id) return;   // started earlier
-  float acc[N];
+// Each run with partial sums: that of the block it starts in,
+// then those of the blocks it goes on through.  Warp w of kJoinGroups adds
+// every kJoinGroups-th of them, and the warps' sums are added in order.
+template <bool VEC>
+__global__ void __launch_bounds__(32 * kJoinGroups) k_embed_join(const Grad g, const __grid_constant__ Segments sg,
+                                                                 int slabs) {
+  constexpr int U = 4;
+  constexpr int N = 4;     // columns of a lane: partial sums are FP32 whatever dout is
+  __shared__ float sum[kJoinGroups][N][32];
+  tok::wait_before();
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int64_t tasks = int64_t(g.crossing[0]) * slabs;
+  for (int64_t task = blockIdx.x; task < tasks; task += gridDim.x) {
+    const int block = g.crossing[1 + task / slabs], slab = static_cast<int>(task % slabs);
+    const int id = g.sorted[block * g.run + g.run - 1].x;
+    float acc[N];
 #pragma unroll
-  for (int k = 0; k < N; ++k)
-    acc[k] = column<N, VEC>(slab, k) < g.cols ? *partial_at<N, VEC>(g, block, 1, slab, k) : 0.f;
-  for (int b = block + 1; b < g.blocks && g.key[b * kRun] == id; ++b)
+    for (int k = 0; k < N; ++k) acc[k] = 0.f;
+    bool more = true;
+    for (int64_t i0 = warp; more; i0 += kJoinGroups * U) {   // the run's i-th block
+      float f[U][N];
+      bool on[U];
 #pragma unroll
-    for (int k = 0; k < N; ++k)
-      if (column<N, VEC>(slab, k) < g.cols) acc[k] += *partial_at<N, VEC>(g, b, 0, slab, k);
-  add_row<N, VEC>(g, sg, id, slab, acc);
+      for (int u = 0; u < U; ++u) {
+        const int64_t b = block + i0 + u * kJoinGroups;
+        on[u] = b == block || (b < g.blocks && g.sorted[b * g.run].x == id);
+        const float* partial = g.partial + (b * 2 + (b == block)) * g.cols;
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+          f[u][k] = on[u] && column<N, VEC>(slab, 32, lane, k) < g.cols
+                        ? partial[column<N, VEC>(slab, 32, lane, k)] : 0.f;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int k = 0; k < N; ++k) acc[k] += f[u][k];
+      more = on[U - 1];
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k) sum[warp][k][lane] = acc[k];
+    __syncthreads();
+    if (warp == 0) {
+      for (int w = 1; w < kJoinGroups; ++w)
+#pragma unroll
+        for (int k = 0; k < N; ++k) acc[k] += sum[w][k][lane];
+      commit<N, VEC>(g, sg, id, slab, 32, lane, acc);
+    }
+    __syncthreads();
+  }
 }
 
 struct Workspace {
-  size_t key0, val0, key1, val1, partial, bytes;
+  size_t sorted, other, crossing, partial, bytes;
 };
 
-int64_t token_blocks(int64_t n) { return (n + kRun - 1) / kRun; }
+// Sorted tokens per block of k_embed_sum: long enough that few runs cross
+// blocks, short enough that a few thousand tokens still fill the SMs.
+int run_of(int64_t n) { return n >= 16384 ? 32 : n >= 8192 ? 16 : 8; }
+int64_t token_blocks(int64_t n) { return (n + run_of(n) - 1) / run_of(n); }
 
 Workspace workspace_of(int64_t n, int cols) {
   Workspace w{};
+  if (n <= kFew) return w;
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t p = at;
     at += (bytes + 255) & ~size_t(255);
     return p;
   };
-  w.key0 = take(n * sizeof(int));
-  w.val0 = take(n * sizeof(int));
-  w.key1 = take(n * sizeof(int));
-  w.val1 = take(n * sizeof(int));
+  w.sorted = take(n * sizeof(int2));
+  w.other = take(n * sizeof(int2));
+  w.crossing = take((token_blocks(n) + 1) * sizeof(int));
   w.partial = take(size_t(token_blocks(n)) * 2 * cols * sizeof(float));
   w.bytes = at;
   return w;
@@ -486,47 +733,46 @@ int segments_of(const muon_param_t& p, const muon_partition_t* parts, int nparts
   return MUON_OK;
 }
 
-int launch_sort(const SortArgs& a, cudaStream_t s) {
-  // one warp per 128 tokens, up to a cluster of eight blocks
+cudaError_t launch_sort(const SortArgs& a, cudaStream_t s) {
+  // 2048 tokens per block (4 per thread), up to a cluster of 16 blocks
   int blocks = 1;
-  while (blocks < 8 && a.n > blocks * 2048) blocks *= 2;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(blocks);
-  cfg.blockDim = dim3(kSortThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = blocks;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_embed_sort, a) == cudaSuccess;
+  while (blocks < kSortBlocks && a.n > blocks * 2048) blocks *= 2;
+  if (blocks > 8) {
+    const cudaError_t e = cudaFuncSetAttribute(k_embed_sort, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+  }
+  const cudaError_t e = cudaFuncSetAttribute(k_embed_sort, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortShared);
+  if (e != cudaSuccess) return e;
+  return launch(k_embed_sort, blocks, kSortThreads, blocks, false, s, kSortShared, a);
 }
 
+// The gradient's kernels after the sort, or the one for few tokens; *launches
+// counts them.
 template <typename T>
-int launch_grad(Grad g, const Segments& sg, cudaStream_t s) {
+cudaError_t launch_grad(Grad g, const Segments& sg, bool few, cudaStream_t s, int* launches) {
   constexpr int N = Vec<T>::N;
   bool vec = reinterpret_cast<uintptr_t>(g.dout) % 16 == 0 && g.dstride * sizeof(T) % 16 == 0 &&
              g.cols % N == 0;
   for (int i = 0; i < sg.n && vec; ++i) vec = (sg.at[i] - sg.rel[i]) % 4 == 0 && sg.rel[i] % 4 == 0;
-  g.slabs = (g.cols + kSumX * N - 1) / (kSumX * N);
-  g.fill_rows = std::max(1, 16384 / g.cols);
+  g.fill_rows = std::min(kFillRows, std::max(1, 16384 / g.cols));
   const int64_t fills = g.overwrite ? (g.rows + g.fill_rows - 1) / g.fill_rows : 0;
-  const int64_t grid = int64_t(g.blocks) * g.slabs + fills;
-  if (grid > 0x7fffffff) return -1;
-  int k = 0;
-  if (grid > 0) {
-    if (vec) k_embed_sum<T, true><<<static_cast<unsigned>(grid), kSumX, 0, s>>>(g, sg);
-    else k_embed_sum<T, false><<<static_cast<unsigned>(grid), kSumX, 0, s>>>(g, sg);
-    ++k;
+  int width = kSumX;
+  if (few) {
+    width = 64;
+    while (width < kFewX && width * N < g.cols) width *= 2;
   }
-  if (g.blocks > 1) {
-    const unsigned jg = static_cast<unsigned>(int64_t(g.blocks) * g.slabs);
-    if (vec) k_embed_join<N, true><<<jg, kSumX, 0, s>>>(g, sg);
-    else k_embed_join<N, false><<<jg, kSumX, 0, s>>>(g, sg);
-    ++k;
-  }
-  return k;
+  g.slabs = static_cast<int>((int64_t(g.cols) + width * N - 1) / (width * N));
+  const int64_t grid = int64_t(few ? g.n : g.blocks) * g.slabs + fills;
+  if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  const unsigned blocks = static_cast<unsigned>(grid);
+  ++*launches;
+  if (few) return launch(vec ? k_embed_few<T, true> : k_embed_few<T, false>, blocks, width, 1, false, s, 0, g, sg);
+  cudaError_t e = launch(vec ? k_embed_sum<T, true> : k_embed_sum<T, false>, blocks, kSumX, 1, true, s, 0, g, sg);
+  if (e != cudaSuccess) return e;
+  ++*launches;
+  const int slabs = static_cast<int>((int64_t(g.cols) + 127) / 128);
+  const unsigned join = static_cast<unsigned>(std::min<int64_t>(int64_t(g.blocks) * slabs, 8 * 152));
+  return launch(vec ? k_embed_join<true> : k_embed_join<false>, join, 32 * kJoinGroups, 1, true, s, 0, g, sg, slabs);
 }
 
 bool misaligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
@@ -560,9 +806,10 @@ int begin_call() {
   return MUON_OK;
 }
 
-int end_call(int launches) {
+int end_call(int launches, cudaError_t e) {
   count_launches(launches);
-  const cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) e = cudaGetLastError();
+  else cudaGetLastError();
   if (e != cudaSuccess)
     return efail(MUON_ERR_CUDA, std::string("kernel launch: ") + cudaGetErrorString(e));
   return MUON_OK;
@@ -603,7 +850,7 @@ extern "C" int muon_embedding(const void* table, int table_dtype, int64_t table_
     else if (te == 2) launch_lookup<__nv_bfloat16, float>(a, s);
     else if (oe == 2) launch_lookup<float, __nv_bfloat16>(a, s);
     else launch_lookup<float, float>(a, s);
-    return end_call(1);
+    return end_call(1, cudaSuccess);
   });
 }
 
@@ -645,7 +892,6 @@ extern "C" int muon_embedding_grad(float* accum, const void* dout, int dout_dtyp
     if ((rc = begin_call()) != MUON_OK) return rc;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     char* base = static_cast<char*>(workspace);
-    auto ints = [&](size_t at) { return reinterpret_cast<int*>(base + at); };
     SortArgs so{};
     so.ids = ids;
     so.ids64 = ids_type == MUON_INDEX_INT64;
@@ -655,31 +901,37 @@ extern "C" int muon_embedding_grad(float* accum, const void* dout, int dout_dtyp
     while (bits < 32 && (int64_t(1) << bits) <= param->rows) ++bits;   // keys 0 .. rows
     so.passes = (bits + kSortBits - 1) / kSortBits;
     so.bits = (bits + so.passes - 1) / so.passes;
-    so.key0 = ints(w.key0);
-    so.val0 = ints(w.val0);
-    so.key1 = ints(w.key1);
-    so.val1 = ints(w.val1);
+    so.sorted = reinterpret_cast<int2*>(base + w.sorted);
+    so.other = reinterpret_cast<int2*>(base + w.other);
+    so.crossing = reinterpret_cast<int*>(base + w.crossing);
+    const bool few = n_tokens <= kFew;
     int launches = 0;
-    if (n_tokens > 0) {
-      if (!launch_sort(so, s)) return end_call(0);
+    if (!few) {
+      const cudaError_t e = launch_sort(so, s);
+      if (e != cudaSuccess) return end_call(0, e);
       ++launches;
     }
     Grad g{};
     g.accum = accum;
     g.dout = dout;
+    g.ids = ids;
+    g.ids64 = so.ids64;
     g.dstride = dout_stride;
     g.n = so.n;
     g.rows = param->rows;
     g.cols = param->cols;
     g.scale = scale;
     g.overwrite = overwrite;
-    g.key = so.key0;
-    g.val = so.val0;
+    g.sorted = so.sorted;
     g.partial = reinterpret_cast<float*>(base + w.partial);
+    g.crossing = so.crossing;
+    g.run = run_of(n_tokens);
     g.blocks = static_cast<int>(token_blocks(n_tokens));
-    const int k = dout_dtype == MUON_DTYPE_BF16 ? launch_grad<__nv_bfloat16>(g, sg, s)
-                                                : launch_grad<float>(g, sg, s);
-    if (k < 0) return efail(MUON_ERR_UNSUPPORTED, "too many tokens and columns for one launch");
-    return end_call(launches + k);
+    const cudaError_t e = dout_dtype == MUON_DTYPE_BF16
+                              ? launch_grad<__nv_bfloat16>(g, sg, few, s, &launches)
+                              : launch_grad<float>(g, sg, few, s, &launches);
+    if (e == cudaErrorInvalidConfiguration)
+      return efail(MUON_ERR_UNSUPPORTED, "too many tokens, rows and columns for one launch");
+    return end_call(launches, e);
   });
 }

@@ -1,11 +1,23 @@
 """What the embedding and loss entry points refuse, on the host before any
-CUDA call, and their workspace sizes."""
+CUDA call, and their workspace sizes.  The addresses are made up, so these
+run only where no GPU could be handed them."""
 import ctypes
 
 import numpy as np
 import pytest
 
 import newton_schulz_fp32_gb300 as nsg
+
+
+def _gpu():
+    try:
+        import torch
+    except ImportError:
+        return False
+    return torch.cuda.is_available()
+
+
+pytestmark = pytest.mark.skipif(_gpu(), reason="made-up addresses stay away from a GPU")
 
 FAKE = 1 << 20   # a non-NULL, aligned address that is never dereferenced
 
@@ -40,9 +52,9 @@ def test_lookup_refuses(lib, change, word):
 def grad_args(param=(0, 10, 64, 0, 0), parts=None, **change):
     p = np.array([param], dtype=nsg.PARAM_DTYPE)
     q = np.array(parts or [], dtype=nsg.PART_DTYPE)
-    a = dict(accum=FAKE, dout=FAKE, dt=0, ds=64, ids=FAKE, it=1, n=4, scale=1.0, overwrite=0,
+    a = dict(accum=FAKE, dout=FAKE, dt=0, ds=64, ids=FAKE, it=1, n=4096, scale=1.0, overwrite=0,
              pp=p.ctypes.data, qq=q.ctypes.data if len(q) else None, nparts=len(q), ws=FAKE,
-             wb=1 << 20, stream=None)
+             wb=1 << 24, stream=None)
     a.update(change)
     return list(a.values()), (p, q)
 
@@ -115,7 +127,7 @@ def test_preference_loss_refuses(lib, change, word):
 
 def test_workspace_sizes(lib):
     assert nsg.embedding_grad_workspace(0, 8) == 0 and nsg.preference_loss_workspace(0) == 0
-    small, large = nsg.embedding_grad_workspace(100, 64), nsg.embedding_grad_workspace(1000, 64)
+    small, large = nsg.embedding_grad_workspace(2000, 64), nsg.embedding_grad_workspace(20000, 64)
     assert 0 < small < large
     assert nsg.preference_loss_workspace(1000) >= 1000 * 12
     for bad in ((-1, 8), (1 << 31, 8), (10, 0)):
