@@ -493,12 +493,13 @@ MUON_API int muon_embedding(const void* table, int table_dtype, int64_t table_st
  * index offset; num_heads and use_muon are not looked at):
  *     accum[row v] = (overwrite ? 0 : accum[row v])
  *                    + scale * sum over t with ids[t] = v of dout[t]
- * The sum runs in FP32 in an order that depends on ids and n_tokens alone
+ * The sum runs in FP32 in an order that depends on ids, n_tokens and cols alone
  * (tokens in order of position within blocks, then the blocks), and is scaled
  * once.  Without overwrite only rows of
  * tokens that occur are read and written; with overwrite every row is written
  * (zeros where no token occurs).  Nothing outside the parameter is touched.
  *   accum : device float storage buffer, 16-byte aligned
+ *   accum_elems : its elements; a table that leaves it is refused
  *   dout  : device, n_tokens x cols of dout_dtype, dout_stride >= cols
  *   param : host
  *   parts, nparts : host table of the buffer's partitions; nparts = 0: the
@@ -509,8 +510,8 @@ MUON_API int muon_embedding(const void* table, int table_dtype, int64_t table_st
  * in more than MUON_EMBEDDING_MAX_SEGMENTS partitions. */
 #define MUON_EMBEDDING_MAX_SEGMENTS 128
 MUON_API int muon_embedding_grad_workspace(int64_t n_tokens, int cols, size_t* bytes);
-MUON_API int muon_embedding_grad(float* accum, const void* dout, int dout_dtype,
-                                 int64_t dout_stride, const void* ids, int ids_type,
+MUON_API int muon_embedding_grad(float* accum, int64_t accum_elems, const void* dout,
+                                 int dout_dtype, int64_t dout_stride, const void* ids, int ids_type,
                                  int64_t n_tokens, float scale, int overwrite,
                                  const muon_param_t* param, const muon_partition_t* parts,
                                  int nparts, void* workspace, size_t workspace_bytes,

@@ -13,7 +13,9 @@ Table formats match the C structs of ``include/muon.h``:
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+import struct
 
 import numpy as np
 
@@ -133,7 +135,7 @@ def lib():
         S = ctypes.POINTER(ctypes.c_size_t)
         L.muon_embedding.argtypes = [P, I, I64, I, I, P, I, I64, F, P, I, I64, P]
         L.muon_embedding_grad_workspace.argtypes = [I64, I, S]
-        L.muon_embedding_grad.argtypes = [P, P, I, I64, P, I, I64, F, I, P, P, I, P,
+        L.muon_embedding_grad.argtypes = [P, I64, P, I, I64, P, I, I64, F, I, P, P, I, P,
                                           ctypes.c_size_t, P]
         L.muon_token_logprobs.argtypes = [P, I, I64, I64, I, P, I, F, P, P]
         L.muon_policy_loss.argtypes = [P, I, I64, I64, I, P, I, P, P, P, P, F, F, F, F, P, P, P,
@@ -341,36 +343,44 @@ def newton_schulz(X, Y=None, ns_method="gram", ns_steps: int = 5, operand_mode="
 # ------------------------------------------------------------------ the two ends of a model
 
 def _dtype(x, name):
+    """muon_dtype_t of a tensor."""
     import torch
-    if x.dtype == torch.bfloat16:
-        return DTYPES["bf16"]
-    if x.dtype == torch.float32:
-        return DTYPES["fp32"]
-    raise ValueError(f"{name} must be bfloat16 or float32, not {x.dtype}")
+    d = x.dtype
+    if d == torch.bfloat16:
+        return 0
+    if d == torch.float32:
+        return 1
+    raise ValueError(f"{name} must be bfloat16 or float32, not {d}")
 
 
 def _index(x, name):
+    """muon_index_t of a tensor of token indexes."""
     import torch
     if not x.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if x.dtype == torch.int64:
+    d = x.dtype
+    if d == torch.int64:
         return 1
-    if x.dtype == torch.int32:
+    if d == torch.int32:
         return 0
-    raise ValueError(f"{name} must be int32 or int64, not {x.dtype}")
+    raise ValueError(f"{name} must be int32 or int64, not {d}")
 
 
 def _rows(x, name):
-    """The stride between the rows of a 2-D tensor whose rows are contiguous."""
-    if x.dim() != 2:
+    """(rows, columns, elements between rows) of a 2-D tensor whose rows are
+    contiguous."""
+    shape = x.shape
+    if len(shape) != 2:
         raise ValueError(f"{name} must be 2-D")
-    if x.shape[1] > 1 and x.stride(1) != 1:
+    n, cols = shape
+    across, along = x.stride()
+    if along != 1 and cols > 1:
         raise ValueError(f"{name}'s rows must be contiguous")
-    return x.stride(0) if x.shape[0] > 1 else max(x.stride(0), x.shape[1])
+    return n, cols, across if n > 1 else max(across, cols)
 
 
 def _per_token(x, n, name):
-    """A contiguous float32 tensor of n elements (or None)."""
+    """The address of a contiguous float32 tensor of n elements (or None)."""
     import torch
     if x is None:
         return None
@@ -379,38 +389,41 @@ def _per_token(x, n, name):
     return x.data_ptr()
 
 
-def _same_device(x, *others):
+def _same_device(device, *others):
     for o in others:
-        if o is not None and o.device != x.device:
+        if o is not None and o.device != device:
             raise ValueError("every tensor must be on one device")
 
 
-class _On:
-    """The device of `x` made current, and torch's current stream set to
-    `stream` (a torch stream, a cudaStream_t or None), so that tensors made
-    inside belong to the stream the kernels run on."""
+def _elsewhere(device, stream):
+    """None where `device` is torch's current one and no stream is asked for;
+    else a context that makes them current, so that tensors made inside belong
+    to the stream the kernels run on.  Each call enters it and starts again."""
+    import contextlib
 
-    def __init__(self, x, stream):
-        import torch
-        self.ctx = []
-        if x.device.type != "cuda":
-            raise ValueError("tensors must be on a CUDA device")
-        if x.device.index != torch.cuda.current_device():
-            self.ctx.append(torch.cuda.device(x.device))
-        if stream is not None:
-            if isinstance(stream, int):
-                stream = torch.cuda.ExternalStream(stream, device=x.device)
-            self.ctx.append(torch.cuda.stream(stream))
+    import torch
+    if device.type != "cuda":
+        raise ValueError("tensors must be on a CUDA device")
+    here = torch.cuda.current_device() == device.index
+    if stream is None and here:
+        return None
+    ctx = contextlib.ExitStack()
+    if not here:
+        ctx.enter_context(torch.cuda.device(device))
+    if stream is not None:
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=device)
+        ctx.enter_context(torch.cuda.stream(stream))
+    return ctx
 
-    def __enter__(self):
-        for c in self.ctx:
-            c.__enter__()
-        return _stream(None)
 
-    def __exit__(self, *exc):
-        for c in reversed(self.ctx):
-            c.__exit__(*exc)
-        return False
+def _raw_stream(device):
+    """torch's current stream of the current device, as a cudaStream_t."""
+    import torch
+    try:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    except AttributeError:
+        return torch.cuda.current_stream(device).cuda_stream
 
 
 def embedding(table, ids, scale: float = 1.0, out=None, out_dtype=None, stream=None):
@@ -419,20 +432,29 @@ def embedding(table, ids, scale: float = 1.0, out=None, out_dtype=None, stream=N
     tensor of ids' shape plus cols, of out_dtype (default: the table's), or
     fills `out` (2-D with any row stride, or contiguous)."""
     import torch
-    stride, it = _rows(table, "table"), _index(ids, "ids")
-    cols, n = table.shape[1], ids.numel()
-    _same_device(table, ids, out)
-    with _On(table, stream) as s:
-        if out is None:
-            out = torch.empty((*ids.shape, cols), dtype=out_dtype or table.dtype, device=table.device)
-        elif out.shape[-1] != cols or out.numel() != n * cols or (out_dtype not in (None, out.dtype)):
+    rows, cols, stride = _rows(table, "table")
+    it, device = _index(ids, "ids"), table.device
+    _same_device(device, ids, out)
+    ctx = _elsewhere(device, stream)
+    if ctx is not None:
+        with ctx:
+            return embedding(table, ids, scale, out, out_dtype)
+    n = ids.numel()
+    if out is None:
+        out = torch.empty((*ids.shape, cols), dtype=out_dtype or table.dtype, device=device)
+        ostride = cols
+    else:
+        if out.shape[-1] != cols or out.numel() != n * cols or out_dtype not in (None, out.dtype):
             raise ValueError("out must hold ids' shape plus the table's columns")
-        ostride = _rows(out, "out") if out.dim() == 2 else cols
-        if out.dim() != 2 and not out.is_contiguous():
+        if out.dim() == 2:
+            ostride = _rows(out, "out")[2]
+        elif out.is_contiguous():
+            ostride = cols
+        else:
             raise ValueError("out must be contiguous or 2-D")
-        _check(lib().muon_embedding(table.data_ptr(), _dtype(table, "table"), stride, table.shape[0],
-                                    cols, ids.data_ptr(), it, n, scale, out.data_ptr(),
-                                    _dtype(out, "out"), ostride, s))
+    _check(lib().muon_embedding(table.data_ptr(), _dtype(table, "table"), stride, rows, cols,
+                                ids.data_ptr(), it, n, scale, out.data_ptr(), _dtype(out, "out"),
+                                ostride, _raw_stream(device)))
     return out
 
 
@@ -448,32 +470,42 @@ def embedding_grad(accum, dout, ids, param, parts=None, scale: float = 1.0,
     import torch
     if hasattr(param, "dtype"):
         param = (param["offset"], param["rows"], param["cols"])
-    offset, rows, cols = (int(v) for v in param)
+    offset, rows, cols = param
     if accum.dtype != torch.float32 or not accum.is_contiguous():
         raise ValueError("accum must be a contiguous float32 tensor")
     if dout.dim() != 2:
         dout = dout.reshape(-1, cols)
-    n, it = ids.numel(), _index(ids, "ids")
-    if dout.shape[0] != n or dout.shape[1] != cols:
+    n, it, device = ids.numel(), _index(ids, "ids"), accum.device
+    got, width, stride = _rows(dout, "dout")
+    if got != n or width != cols:
         raise ValueError("dout must be tokens x cols")
-    stride = _rows(dout, "dout")
-    _same_device(accum, dout, ids, workspace)
-    q, nq = _table(parts, PART_DTYPE)
-    need = offset + rows * cols if nq == 0 else int((q["storage_offset"] + q["flat_end"] - q["flat_begin"]).max())
-    if accum.numel() < need:
-        raise ValueError(f"accum holds {accum.numel()} elements, the tables describe {need}")
-    p = np.array([(offset, rows, cols, 0, 0)], dtype=PARAM_DTYPE)
-    with _On(accum, stream) as s:
-        if workspace is None:
-            workspace = torch.empty(embedding_grad_workspace(n, cols), dtype=torch.uint8,
-                                    device=accum.device)
-        _check(lib().muon_embedding_grad(accum.data_ptr(), dout.data_ptr(), _dtype(dout, "dout"), stride,
-                                         ids.data_ptr(), it, n, scale, int(overwrite), p.ctypes.data,
-                                         q.ctypes.data if nq else None, nq, workspace.data_ptr(),
-                                         workspace.numel() * workspace.element_size(), s))
+    if parts is None:
+        table, nparts = None, 0
+        if accum.numel() < offset + rows * cols:
+            raise ValueError(f"accum holds {accum.numel()} elements, the parameter ends at {offset + rows * cols}")
+    else:
+        parts, nparts = _table(parts, PART_DTYPE)
+        table = parts.tobytes()
+    _same_device(device, dout, ids, workspace)
+    ctx = _elsewhere(device, stream)
+    if ctx is not None:
+        with ctx:
+            return embedding_grad(accum, dout, ids, param, parts, scale, overwrite, workspace)
+    need = embedding_grad_workspace(n, cols)
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    have = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib().muon_embedding_grad(
+        accum.data_ptr(), accum.numel(), dout.data_ptr(), _dtype(dout, "dout"), stride, ids.data_ptr(), it,
+        n, scale, 1 if overwrite else 0, _PARAM.pack(offset, rows, cols, 0, 0), table, nparts,
+        workspace.data_ptr() if have else None, have, _raw_stream(device)))
     return accum
 
 
+_PARAM = struct.Struct("<qiiii")   # one row of a PARAM_DTYPE table
+
+
+@functools.lru_cache(maxsize=256)
 def embedding_grad_workspace(n_tokens: int, cols: int) -> int:
     """Bytes of scratch embedding_grad needs."""
     b = ctypes.c_size_t()
@@ -482,13 +514,13 @@ def embedding_grad_workspace(n_tokens: int, cols: int) -> int:
 
 
 def _logits(logits, targets):
-    """(2-D logits, stride, tokens, vocab, type of the targets)."""
+    """(2-D logits, tokens, vocabulary, row stride, type of the targets)."""
     if logits.dim() != 2:
         logits = logits.view(-1, logits.shape[-1])
-    stride, n = _rows(logits, "logits"), targets.numel()
-    if logits.shape[0] != n:
+    n, vocab, stride = _rows(logits, "logits")
+    if targets.numel() != n:
         raise ValueError("one target per row of logits")
-    return logits, stride, n, logits.shape[1], _index(targets, "targets")
+    return logits, n, vocab, stride, _index(targets, "targets")
 
 
 def token_logprobs(logits, targets, logit_scale: float = 1.0, out=None, stream=None):
@@ -497,22 +529,27 @@ def token_logprobs(logits, targets, logit_scale: float = 1.0, out=None, stream=N
     targets int32 or int64, a negative one giving 0.  Returns float32 of
     targets' shape."""
     import torch
-    logits, stride, n, vocab, tt = _logits(logits, targets)
-    _same_device(logits, targets, out)
-    with _On(logits, stream) as s:
-        if out is None:
-            out = torch.empty(targets.shape, dtype=torch.float32, device=logits.device)
-        _check(lib().muon_token_logprobs(logits.data_ptr(), _dtype(logits, "logits"), stride, n, vocab,
-                                         targets.data_ptr(), tt, logit_scale, _per_token(out, n, "out"), s))
+    logits, n, vocab, stride, tt = _logits(logits, targets)
+    device = logits.device
+    _same_device(device, targets, out)
+    ctx = _elsewhere(device, stream)
+    if ctx is not None:
+        with ctx:
+            return token_logprobs(logits, targets, logit_scale, out)
+    if out is None:
+        out = torch.empty(targets.shape, dtype=torch.float32, device=device)
+    _check(lib().muon_token_logprobs(logits.data_ptr(), _dtype(logits, "logits"), stride, n, vocab,
+                                     targets.data_ptr(), tt, logit_scale, _per_token(out, n, "out"),
+                                     _raw_stream(device)))
     return out
 
 
-def _dlogits(logits, stride, dlogits):
-    """The gradient's buffer: as given, a new one (True; with the logits' row
-    stride, so that its rows are aligned as theirs), or None (False)."""
+def _dlogits(logits, n, vocab, stride, dlogits):
+    """The gradient's buffer and its row stride: as given, a new one (True;
+    with the logits' row stride, so that its rows are aligned as theirs), or
+    none (False)."""
     import torch
     if dlogits is True:
-        n, vocab = logits.shape
         d = torch.empty((n, stride), dtype=logits.dtype, device=logits.device)
         return d if stride == vocab else d[:, :vocab], stride
     if dlogits is False or dlogits is None:
@@ -521,7 +558,8 @@ def _dlogits(logits, stride, dlogits):
         dlogits = dlogits.view(-1, dlogits.shape[-1])
     if dlogits.dtype != logits.dtype or dlogits.shape != logits.shape:
         raise ValueError("dlogits must match the logits' shape and type")
-    return dlogits, _rows(dlogits, "dlogits")
+    _same_device(logits.device, dlogits)
+    return dlogits, _rows(dlogits, "dlogits")[2]
 
 
 def policy_loss(logits, targets, advantages, weights, old_logp=None, ref_logp=None,
@@ -534,18 +572,23 @@ def policy_loss(logits, targets, advantages, weights, old_logp=None, ref_logp=No
     to replace them.  Returns {"stats": float32[4] (loss, policy term, KL,
     clipped weight), "logp": per token, "dlogits"}, all on the device."""
     import torch
-    logits, stride, n, vocab, tt = _logits(logits, targets)
-    _same_device(logits, targets, advantages, weights, old_logp, ref_logp)
-    with _On(logits, stream) as s:
-        d, dstride = _dlogits(logits, stride, dlogits)
-        _same_device(logits, d)
-        logp = torch.empty(targets.shape, dtype=torch.float32, device=logits.device)
-        stats = torch.empty(4, dtype=torch.float32, device=logits.device)
-        _check(lib().muon_policy_loss(
-            logits.data_ptr(), _dtype(logits, "logits"), stride, n, vocab, targets.data_ptr(), tt,
-            _per_token(advantages, n, "advantages"), _per_token(weights, n, "weights"),
-            _per_token(old_logp, n, "old_logp"), _per_token(ref_logp, n, "ref_logp"), clip_low,
-            clip_high, kl_coef, logit_scale, stats.data_ptr(), logp.data_ptr(), _ptr(d), dstride, s))
+    logits, n, vocab, stride, tt = _logits(logits, targets)
+    device = logits.device
+    _same_device(device, targets, advantages, weights, old_logp, ref_logp)
+    ctx = _elsewhere(device, stream)
+    if ctx is not None:
+        with ctx:
+            return policy_loss(logits, targets, advantages, weights, old_logp, ref_logp, clip_low,
+                               clip_high, kl_coef, logit_scale, dlogits)
+    d, dstride = _dlogits(logits, n, vocab, stride, dlogits)
+    logp = torch.empty(targets.shape, dtype=torch.float32, device=device)
+    stats = torch.empty(4, dtype=torch.float32, device=device)
+    _check(lib().muon_policy_loss(
+        logits.data_ptr(), _dtype(logits, "logits"), stride, n, vocab, targets.data_ptr(), tt,
+        _per_token(advantages, n, "advantages"), _per_token(weights, n, "weights"),
+        _per_token(old_logp, n, "old_logp"), _per_token(ref_logp, n, "ref_logp"), clip_low, clip_high,
+        kl_coef, logit_scale, stats.data_ptr(), logp.data_ptr(), None if d is None else d.data_ptr(),
+        dstride, _raw_stream(device)))
     return {"stats": stats, "logp": logp, "dlogits": d}
 
 
@@ -559,28 +602,33 @@ def preference_loss(logits, targets, offsets, ref_logp=None, beta: float = 0.1,
     Returns {"stats": float32[4] (loss, mean margin, share of positive
     margins, weight), "margins": float32[pairs], "logp", "dlogits"}."""
     import torch
-    logits, stride, n, vocab, tt = _logits(logits, targets)
-    if offsets.numel() % 2 != 1:
+    logits, n, vocab, stride, tt = _logits(logits, targets)
+    places = offsets.numel()
+    if places % 2 != 1:
         raise ValueError("offsets must hold 2 * pairs + 1 positions")
-    pairs, ot = offsets.numel() // 2, _index(offsets, "offsets")
-    _same_device(logits, targets, offsets, ref_logp, pair_weights, workspace)
-    with _On(logits, stream) as s:
-        d, dstride = _dlogits(logits, stride, dlogits)
-        _same_device(logits, d)
-        logp = torch.empty(targets.shape, dtype=torch.float32, device=logits.device)
-        out = torch.empty(4 + pairs, dtype=torch.float32, device=logits.device)
-        stats, margins = out[:4], out[4:]
-        if workspace is None:
-            workspace = torch.empty(preference_loss_workspace(n), dtype=torch.uint8, device=logits.device)
-        _check(lib().muon_preference_loss(
-            logits.data_ptr(), _dtype(logits, "logits"), stride, n, vocab, targets.data_ptr(), tt,
-            offsets.data_ptr(), ot, pairs, _per_token(ref_logp, n, "ref_logp"),
-            _per_token(pair_weights, pairs, "pair_weights"), beta, label_smoothing, logit_scale,
-            stats.data_ptr(), margins.data_ptr(), logp.data_ptr(), _ptr(d), dstride,
-            workspace.data_ptr(), workspace.numel() * workspace.element_size(), s))
+    pairs, ot, device = places // 2, _index(offsets, "offsets"), logits.device
+    _same_device(device, targets, offsets, ref_logp, pair_weights, workspace)
+    ctx = _elsewhere(device, stream)
+    if ctx is not None:
+        with ctx:
+            return preference_loss(logits, targets, offsets, ref_logp, beta, label_smoothing,
+                                   pair_weights, logit_scale, dlogits, workspace)
+    d, dstride = _dlogits(logits, n, vocab, stride, dlogits)
+    logp = torch.empty(targets.shape, dtype=torch.float32, device=device)
+    stats = torch.empty(4, dtype=torch.float32, device=device)
+    margins = torch.empty(pairs, dtype=torch.float32, device=device)
+    if workspace is None:
+        workspace = torch.empty(preference_loss_workspace(n), dtype=torch.uint8, device=device)
+    _check(lib().muon_preference_loss(
+        logits.data_ptr(), _dtype(logits, "logits"), stride, n, vocab, targets.data_ptr(), tt,
+        offsets.data_ptr(), ot, pairs, _per_token(ref_logp, n, "ref_logp"),
+        _per_token(pair_weights, pairs, "pair_weights"), beta, label_smoothing, logit_scale,
+        stats.data_ptr(), margins.data_ptr(), logp.data_ptr(), None if d is None else d.data_ptr(), dstride,
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _raw_stream(device)))
     return {"stats": stats, "margins": margins, "logp": logp, "dlogits": d}
 
 
+@functools.lru_cache(maxsize=256)
 def preference_loss_workspace(n_tokens: int) -> int:
     """Bytes of scratch preference_loss needs."""
     b = ctypes.c_size_t()

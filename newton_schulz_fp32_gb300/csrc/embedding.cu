@@ -37,6 +37,8 @@ int efail(int code, const std::string& msg) {
 
 // ------------------------------------------------------------------ lookup
 
+constexpr int kTokens = 2;   // k_lookup: rows a thread has under way
+
 struct Lookup {
   const void* table;
   const void* ids;
@@ -55,45 +57,74 @@ __device__ __forceinline__ int lookup_id(const void* ids, int ids64, int64_t t, 
   return id < 0 ? -1 : id;
 }
 
-// blockDim.y tokens per block, blockDim.x threads along a row.  VEC: 16 bytes
-// of the table per thread and step (rows of both arrays 16-byte aligned).
+// kTokens * blockDim.y tokens per block, blockDim.x threads along a row, each
+// with kTokens rows under way at once.  VEC: 16 bytes of the table per thread
+// and step (rows of both arrays 16-byte aligned); else eight elements,
+// blockDim.x apart, so that a warp's accesses lie together.
 template <typename TI, typename TO, bool VEC>
 __global__ void __launch_bounds__(256) k_lookup(const Lookup a) {
-  constexpr int N = VEC ? Vec<TI>::N : 1;
-  const int64_t t = int64_t(blockIdx.x) * blockDim.y + threadIdx.y;
-  if (t >= a.n) return;
-  const int id = lookup_id(a.ids, a.ids64, t, a.rows);
-  const TI* src = static_cast<const TI*>(a.table) + int64_t(id < 0 ? 0 : id) * a.stride;
-  TO* dst = static_cast<TO*>(a.out) + t * a.ostride;
-  const float scale = a.scale;
-  const int nvec = a.cols / N;
-#pragma unroll 4
-  for (int i = threadIdx.x; i < nvec; i += blockDim.x) {
-    float f[N];
-    if constexpr (VEC) {
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (id >= 0) v = *reinterpret_cast<const uint4*>(src + i * N);
-      Vec<TI>::unpack(v, f);
-    } else {
-      f[0] = id >= 0 ? tok::to_float(src[i]) : 0.f;
-    }
+  const TI* src[kTokens];
+  TO* dst[kTokens];
+  bool on[kTokens], in[kTokens];
 #pragma unroll
-    for (int k = 0; k < N; ++k) f[k] = id >= 0 ? f[k] * scale : 0.f;
-    if constexpr (VEC && sizeof(TI) == sizeof(TO)) {
-      *reinterpret_cast<uint4*>(dst + i * N) = Vec<TO>::pack(f);
-    } else if constexpr (VEC && sizeof(TO) == 4) {
-      float4* d = reinterpret_cast<float4*>(dst + i * N);
-      d[0] = make_float4(f[0], f[1], f[2], f[3]);
-      d[1] = make_float4(f[4], f[5], f[6], f[7]);
-    } else if constexpr (VEC) {
-      *reinterpret_cast<uint2*>(dst + i * N) =
-          make_uint2(Vec<TO>::pack2(f[0], f[1]), Vec<TO>::pack2(f[2], f[3]));
-    } else {
-      dst[i] = tok::from_float<TO>(f[0]);
-    }
+  for (int q = 0; q < kTokens; ++q) {
+    const int64_t t = (int64_t(blockIdx.x) * kTokens + q) * blockDim.y + threadIdx.y;
+    in[q] = t < a.n;
+    const int id = in[q] ? lookup_id(a.ids, a.ids64, t, a.rows) : -1;
+    on[q] = id >= 0;
+    src[q] = static_cast<const TI*>(a.table) + int64_t(on[q] ? id : 0) * a.stride;
+    dst[q] = static_cast<TO*>(a.out) + t * a.ostride;
   }
-  for (int c = nvec * N + threadIdx.x; c < a.cols; c += blockDim.x)
-    dst[c] = tok::from_float<TO>(id >= 0 ? tok::to_float(src[c]) * scale : 0.f);
+  const float scale = a.scale;
+  int done = 0;
+  if constexpr (VEC) {
+    constexpr int N = Vec<TI>::N;
+    const int nvec = a.cols / N;
+#pragma unroll 2
+    for (int i = threadIdx.x; i < nvec; i += blockDim.x) {
+      uint4 v[kTokens];
+#pragma unroll
+      for (int q = 0; q < kTokens; ++q)
+        v[q] = on[q] ? *reinterpret_cast<const uint4*>(src[q] + i * N) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int q = 0; q < kTokens; ++q) {
+        if (!in[q]) continue;
+        float f[N];
+        Vec<TI>::unpack(v[q], f);
+#pragma unroll
+        for (int k = 0; k < N; ++k) f[k] = on[q] ? f[k] * scale : 0.f;
+        if constexpr (sizeof(TI) == sizeof(TO)) {
+          __stcs(reinterpret_cast<uint4*>(dst[q] + i * N), Vec<TO>::pack(f));
+        } else if constexpr (sizeof(TO) == 4) {
+          float4* d = reinterpret_cast<float4*>(dst[q] + i * N);
+          __stcs(d, make_float4(f[0], f[1], f[2], f[3]));
+          __stcs(d + 1, make_float4(f[4], f[5], f[6], f[7]));
+        } else {
+          __stcs(reinterpret_cast<uint2*>(dst[q] + i * N),
+                 make_uint2(Vec<TO>::pack2(f[0], f[1]), Vec<TO>::pack2(f[2], f[3])));
+        }
+      }
+    }
+    done = nvec * N;
+  }
+  constexpr int U = VEC ? 1 : 8;
+  for (int c0 = done + threadIdx.x; c0 < a.cols; c0 += U * blockDim.x) {
+    float f[kTokens][U];
+#pragma unroll
+    for (int q = 0; q < kTokens; ++q)
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const int c = c0 + k * blockDim.x;
+        f[q][k] = on[q] && c < a.cols ? tok::to_float(src[q][c]) * scale : 0.f;
+      }
+#pragma unroll
+    for (int q = 0; q < kTokens; ++q)
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const int c = c0 + k * blockDim.x;
+        if (in[q] && c < a.cols) dst[q][c] = tok::from_float<TO>(f[q][k]);
+      }
+  }
 }
 
 template <typename TI, typename TO>
@@ -104,16 +135,18 @@ void launch_lookup(const Lookup& a, cudaStream_t s) {
   const bool vec = whole(a.table, a.stride, sizeof(TI)) && whole(a.out, a.ostride, sizeof(TO)) &&
                    a.cols >= Vec<TI>::N;
   const int steps = vec ? a.cols / Vec<TI>::N : a.cols;
-  int tx = 32;
-  while (tx < 256 && tx * 4 < steps) tx *= 2;   // up to four loads in flight per thread
-  const dim3 block(tx, 256 / tx);
-  const unsigned grid = static_cast<unsigned>((a.n + block.y - 1) / block.y);
+  const int per = vec ? 4 : 8;   // steps of a thread; a thread per step of a short row
+  int tx = 1;
+  while (tx < steps && (tx < 32 || (tx < 256 && tx * per < steps))) tx *= 2;
+  const dim3 block(tx, std::max(1, 128 / tx));
+  const unsigned grid = static_cast<unsigned>((a.n + block.y * kTokens - 1) / (block.y * kTokens));
   if (vec) k_lookup<TI, TO, true><<<grid, block, 0, s>>>(a);
   else k_lookup<TI, TO, false><<<grid, block, 0, s>>>(a);
 }
 
 // ------------------------------------------------------------------ gradient
 
+constexpr int kSms = 152;
 constexpr int kSortThreads = 512;
 constexpr int kSortBlocks = 16;      // most blocks of its cluster
 constexpr int kSortWarps = kSortThreads / 32;
@@ -122,7 +155,7 @@ constexpr int kSortBins = 1 << kSortBits;
 constexpr int kSortItems = 8;        // tokens a thread has in hand
 constexpr int kSortShared = kSortWarps * kSortBins * int(sizeof(int));
 constexpr int kRunMost = 32;         // sorted tokens per block of k_embed_sum, at most
-constexpr int kSumX = 128;           // its threads
+constexpr int kSumX = 128;           // its threads, at most
 constexpr int kJoinGroups = 8;      // k_embed_join: warps of a block, each adding every 16th partial sum
 constexpr int kFew = 1024;           // tokens up to which k_embed_few is taken
 constexpr int kFewX = 256;
@@ -170,17 +203,12 @@ __device__ __forceinline__ int grad_id(const Grad& g, int t) {
   return lookup_id(g.ids, g.ids64, t, g.rows);
 }
 
-// Where row `row` of the parameter lies.  `whole`: in one piece.
-struct RowPlace {
-  float* p;
-  bool whole;
-  __device__ __forceinline__ RowPlace() : p(nullptr), whole(false) {}
-  __device__ __forceinline__ RowPlace(const Grad& g, const Segments& sg, int row) {
-    int64_t room;
-    p = g.accum + sg.place(int64_t(row) * g.cols, &room);
-    whole = room >= g.cols;
-  }
-};
+// Where row `row` of the parameter lies; NULL if it is cut by partitions.
+__device__ __forceinline__ float* row_of(const Grad& g, const Segments& sg, int row) {
+  int64_t room;
+  float* p = g.accum + sg.place(int64_t(row) * g.cols, &room);
+  return room >= g.cols ? p : nullptr;
+}
 
 // A thread's columns within a block of `width` threads.  VEC: N consecutive
 // ones, moved as 16 bytes; else N columns `width` apart (each access of a warp
@@ -223,66 +251,74 @@ struct Piece {
   }
 };
 
-// The old value, or 0 where it is overwritten, plus scale * sum.
-template <int W>
-__device__ __forceinline__ void add_at(const Grad& g, float* p, const float* sum) {
-  if constexpr (W == 4) {
-    float4* q = reinterpret_cast<float4*>(p);
-    const float4 o = g.overwrite ? make_float4(0.f, 0.f, 0.f, 0.f) : *q;
-    *q = make_float4(o.x + g.scale * sum[0], o.y + g.scale * sum[1], o.z + g.scale * sum[2],
-                     o.w + g.scale * sum[3]);
-  } else {
-    *p = (g.overwrite ? 0.f : *p) + g.scale * sum[0];
-  }
-}
-
-// A thread's columns of a row that lies in one piece at p.  ADD: added to
-// accum; else a partial sum.
+// A thread's columns of a row that lies in one piece at p.  ADD: scale * sum
+// added to accum, or put in its place; else a partial sum.  All old values are
+// fetched before the first store: the compiler cannot move a load over a store
+// that may be to its address, and each would wait for the one before.
 template <int N, bool VEC, bool ADD>
 __device__ __forceinline__ void put(const Grad& g, float* p, int slab, int width, int x, const float* sum) {
+  float out[N];
+  const bool add = ADD && !g.overwrite;
+  const float scale = ADD ? g.scale : 1.f;
   if constexpr (VEC) {
     const int c = column<N, VEC>(slab, width, x, 0);
-    if (c < g.cols)
+    if (c >= g.cols) return;
 #pragma unroll
-      for (int k = 0; k < N; k += 4) {
-        if constexpr (ADD) add_at<4>(g, p + c + k, sum + k);
-        else *reinterpret_cast<float4*>(p + c + k) = make_float4(sum[k], sum[k + 1], sum[k + 2], sum[k + 3]);
-      }
+    for (int k = 0; k < N; k += 4) {
+      const float4 o = add ? *reinterpret_cast<const float4*>(p + c + k) : make_float4(0.f, 0.f, 0.f, 0.f);
+      out[k] = o.x; out[k + 1] = o.y; out[k + 2] = o.z; out[k + 3] = o.w;
+    }
+#pragma unroll
+    for (int k = 0; k < N; k += 4)
+      *reinterpret_cast<float4*>(p + c + k) =
+          make_float4(out[k] + scale * sum[k], out[k + 1] + scale * sum[k + 1], out[k + 2] + scale * sum[k + 2],
+                      out[k + 3] + scale * sum[k + 3]);
   } else {
 #pragma unroll
     for (int k = 0; k < N; ++k) {
       const int c = column<N, VEC>(slab, width, x, k);
-      if (c >= g.cols) continue;
-      if constexpr (ADD) add_at<1>(g, p + c, sum + k);
-      else p[c] = sum[k];
+      out[k] = add && c < g.cols ? p[c] : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int c = column<N, VEC>(slab, width, x, k);
+      if (c < g.cols) p[c] = out[k] + scale * sum[k];
     }
   }
 }
 
-// The same for a row cut by partitions, element by element.
-template <int N, bool VEC>
-__device__ __forceinline__ void scatter(const Grad& g, const Segments& sg, int id, int slab, int width, int x,
-                                        const float* sum) {
+// The same for any row of accum (p = NULL: cut by partitions, then element by
+// element).  Where rows do not all start on 16 bytes (ALIGNED false) the
+// columns of a VEC thread are exchanged through `stage` for ones that a warp
+// stores side by side.  `lanes` threads (a block or a warp) hold a row's
+// columns.
+template <int N, bool VEC, bool ALIGNED, typename Sync>
+__device__ __forceinline__ void put_any(const Grad& g, const Segments& sg, float* p, int id, int slab, int lanes,
+                                        int x, float* sum, float* stage, Sync sync) {
+  constexpr bool kDirect = !VEC || ALIGNED;
+  if (kDirect && p) return put<N, VEC, true>(g, p, slab, lanes, x, sum);
 #pragma unroll
-  for (int k = 0; k < N; ++k) {
-    const int c = column<N, VEC>(slab, width, x, k);
-    if (c >= g.cols) continue;
-    int64_t room;
-    add_at<1>(g, g.accum + sg.place(int64_t(id) * g.cols + c, &room), sum + k);
+  for (int k = 0; k < N; ++k) stage[column<N, VEC>(0, lanes, x, k)] = sum[k];
+  sync();
+  if (!kDirect && p) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) sum[k] = stage[column<N, false>(0, lanes, x, k)];
+    put<N, false, true>(g, p, slab, lanes, x, sum);
+  } else {
+#pragma unroll 1
+    for (int i = x; i < lanes * N; i += lanes) {
+      const int c = slab * lanes * N + i;
+      if (c >= g.cols) break;
+      int64_t room;
+      float* q = g.accum + sg.place(int64_t(id) * g.cols + c, &room);
+      *q = (g.overwrite ? 0.f : *q) + g.scale * stage[i];
+    }
   }
-}
-
-// accum[row] = old + scale * sum for a thread's columns.
-template <int N, bool VEC>
-__device__ __forceinline__ void commit(const Grad& g, const Segments& sg, int id, int slab, int width, int x,
-                                       const float* sum) {
-  const RowPlace row(g, sg, id);
-  if (row.whole) put<N, VEC, true>(g, row.p, slab, width, x, sum);
-  else scatter<N, VEC>(g, sg, id, slab, width, x, sum);
+  sync();
 }
 
 // What k_embed_sum does after a token.
-enum { kGoOn = 0, kCommit = 1, kPartial = 2, kScattered = 3 };
+enum { kGoOn = 0, kCommit = 1, kPartial = 2 };
 struct __align__(16) Step {
   float* p;
   int act;
@@ -323,40 +359,48 @@ __device__ void fill_zeros(const Grad& g, const Segments& sg, int r0, int r1, co
 // finds the others (every block reads all the ids: at most 8 KB, from L2),
 // adds them in order of position and writes the row; the others leave.
 // Further blocks zero the rows that no token names (overwrite).
-template <typename T, bool VEC>
+template <typename T, bool VEC, bool ALIGNED>
 __global__ void __launch_bounds__(kFewX) k_embed_few(const Grad g, const __grid_constant__ Segments sg) {
   constexpr int N = Vec<T>::N;
   constexpr int U = 4;
+  constexpr int F = 8;    // ids in flight
   __shared__ unsigned found[kFew / 32];
   __shared__ int list[kFew];
   __shared__ uint8_t named[kFillRows];
-  const int lane = threadIdx.x % 32;
+  __shared__ float stage[kFewX * N];
+  const int x = threadIdx.x, lane = x % 32, width = blockDim.x;
+  auto each_id = [&](auto use) {   // use(position, id) for all positions up to a multiple of 32
+    for (int j0 = x; j0 - lane < g.n; j0 += F * width) {
+      int id[F];
+#pragma unroll
+      for (int k = 0; k < F; ++k) id[k] = j0 + k * width < g.n ? tok::load_index(g.ids, g.ids64, j0 + k * width) : -1;
+#pragma unroll
+      for (int k = 0; k < F; ++k) use(j0 + k * width, id[k]);
+    }
+  };
   if (blockIdx.x >= unsigned(g.n) * g.slabs) {
     const int r0 = (blockIdx.x - g.n * g.slabs) * g.fill_rows, r1 = min(g.rows, r0 + g.fill_rows);
-    for (int r = threadIdx.x; r < r1 - r0; r += blockDim.x) named[r] = 0;
+    for (int r = x; r < r1 - r0; r += width) named[r] = 0;
     __syncthreads();
-    for (int t = threadIdx.x; t < g.n; t += blockDim.x) {
-      const int id = grad_id(g, t);
+    each_id([&](int, int id) {
       if (id >= r0 && id < r1) named[id - r0] = 1;
-    }
+    });
     __syncthreads();
     return fill_zeros(g, sg, r0, r1, named);
   }
   const int t = blockIdx.x / g.slabs, slab = blockIdx.x % g.slabs;
   const int id = grad_id(g, t);
   if (id < 0) return;
-  const int words = (g.n + 31) / 32;
-  for (int j0 = threadIdx.x - lane; j0 < words * 32; j0 += blockDim.x) {
-    const int j = j0 + lane;
-    const unsigned same = __ballot_sync(0xffffffffu, j < g.n && grad_id(g, j) == id);
-    if (lane == 0) found[j0 / 32] = same;
-  }
+  each_id([&](int j, int other) {
+    const unsigned same = __ballot_sync(0xffffffffu, other == id);
+    if (lane == 0 && j < g.n) found[j / 32] = same;
+  });
   __syncthreads();
   int count = 0;
-  for (int w = 0; w < words; ++w) {
+  for (int w = 0; w < (g.n + 31) / 32; ++w) {
     const unsigned m = found[w];
     if (w == t / 32 ? (m & ((1u << (t % 32)) - 1)) != 0 : w < t / 32 && m != 0) return;   // not the first
-    if (threadIdx.x < 32 && (m >> lane & 1)) list[count + __popc(m & ((1u << lane) - 1))] = w * 32 + lane;
+    if (x < 32 && (m >> lane & 1)) list[count + __popc(m & ((1u << lane) - 1))] = w * 32 + lane;
     count += __popc(m);
   }
   __syncthreads();
@@ -366,13 +410,12 @@ __global__ void __launch_bounds__(kFewX) k_embed_few(const Grad g, const __grid_
   for (int j0 = 0; j0 < count; j0 += U) {
     Piece<T, VEC> p[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      p[u].load(g, list[min(j0 + u, count - 1)], slab, blockDim.x, threadIdx.x, j0 + u < count);
+    for (int u = 0; u < U; ++u) p[u].load(g, list[min(j0 + u, count - 1)], slab, width, x, j0 + u < count);
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (j0 + u < count) p[u].add_to(acc);
   }
-  commit<N, VEC>(g, sg, id, slab, blockDim.x, threadIdx.x, acc);
+  put_any<N, VEC, ALIGNED>(g, sg, row_of(g, sg, id), id, slab, width, x, acc, stage, [] { __syncthreads(); });
 }
 
 // ---- more tokens: sort, sum runs, join the runs that cross blocks
@@ -515,26 +558,28 @@ __global__ void __launch_bounds__(kSortThreads, 1) k_embed_sort(const SortArgs a
   }
 }
 
-template <typename T, bool VEC>
+template <typename T, bool VEC, bool ALIGNED>
 __global__ void __launch_bounds__(kSumX) k_embed_sum(const Grad g, const __grid_constant__ Segments sg) {
   constexpr int N = Vec<T>::N;
   constexpr int U = 4;    // tokens in flight
   __shared__ int key[2 * kRunMost + 1], val[2 * kRunMost];   // this block's tokens and the next one's
   __shared__ int edge[3];   // ids of the token before, the one before the block before, the one after the next
   __shared__ Step step[2 * kRunMost];
+  __shared__ float stage[kSumX * N];
   __shared__ uint8_t named[kFillRows];
+  const int width = blockDim.x;
   tok::wait_before();
   tok::allow_next();
   if (blockIdx.x >= unsigned(g.blocks) * g.slabs) {
     const int r0 = (blockIdx.x - g.blocks * g.slabs) * g.fill_rows, r1 = min(g.rows, r0 + g.fill_rows);
-    for (int r = threadIdx.x; r < r1 - r0; r += kSumX) named[r] = 0;
+    for (int r = threadIdx.x; r < r1 - r0; r += width) named[r] = 0;
     int lo = 0, hi = g.n;   // the first sorted token with id >= r0
     while (lo < hi) {
       const int mid = lo + (hi - lo) / 2;
       if (g.sorted[mid].x < r0) lo = mid + 1; else hi = mid;
     }
     __syncthreads();
-    for (int t = lo + threadIdx.x; t < g.n; t += kSumX) {
+    for (int t = lo + threadIdx.x; t < g.n; t += width) {
       const int id = g.sorted[t].x;
       if (id >= r1) break;
       named[id - r0] = 1;
@@ -546,13 +591,13 @@ __global__ void __launch_bounds__(kSumX) k_embed_sum(const Grad g, const __grid_
   const int x = threadIdx.x;
   const int64_t t0 = int64_t(block) * g.run;
   auto key_at = [&](int64_t t) { return t >= 0 && t < g.n ? g.sorted[t].x : -1; };
-  for (int i = x; i < 2 * g.run; i += kSumX) {
+  for (int i = x; i < 2 * g.run; i += width) {
     const int2 q = t0 + i < g.n ? g.sorted[t0 + i] : make_int2(-1, 0);
     key[i] = q.x;
     val[i] = q.y;
   }
-  if (x >= kSumX - 3) {
-    const int e = x - (kSumX - 3);
+  if (x >= width - 3) {
+    const int e = x - (width - 3);
     edge[e] = key_at(e == 0 ? t0 - 1 : e == 1 ? t0 - g.run - 1 : t0 + 2 * g.run);
   }
   __syncthreads();
@@ -578,15 +623,14 @@ __global__ void __launch_bounds__(kSumX) k_embed_sum(const Grad g, const __grid_
   while (end > from && key[end - 1] >= g.rows) --end;   // tokens without a row are the last
   // What to do after each token, worked out once per block: finding a row
   // among the partitions costs more than adding a token's columns.
-  for (int j = from + x; j < end; j += kSumX) {
+  for (int j = from + x; j < end; j += width) {
     Step st{nullptr, kGoOn};
     if (j + 1 == end || key[j + 1] != key[j]) {
       const bool first_part = j < begun, last_part = j + 1 == end && last_starts && last_long;
       if (first_part || last_part) {
         st = {g.partial + (int64_t(block) * 2 + (first_part ? 0 : 1)) * g.cols, kPartial};
       } else {
-        const RowPlace row(g, sg, key[j]);
-        st = {row.p, row.whole ? kCommit : kScattered};
+        st = {row_of(g, sg, key[j]), kCommit};
       }
     }
     step[j] = st;
@@ -598,16 +642,15 @@ __global__ void __launch_bounds__(kSumX) k_embed_sum(const Grad g, const __grid_
   for (int j0 = from; j0 < end; j0 += U) {
     Piece<T, VEC> p[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) p[u].load(g, val[min(j0 + u, end - 1)], slab, kSumX, x, j0 + u < end);
+    for (int u = 0; u < U; ++u) p[u].load(g, val[min(j0 + u, end - 1)], slab, width, x, j0 + u < end);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (j0 + u >= end) break;
       p[u].add_to(acc);
       const Step st = step[j0 + u];
       if (st.act == kGoOn) continue;
-      if (st.act == kPartial) put<N, VEC, false>(g, st.p, slab, kSumX, x, acc);
-      else if (st.act == kCommit) put<N, VEC, true>(g, st.p, slab, kSumX, x, acc);
-      else scatter<N, VEC>(g, sg, key[j0 + u], slab, kSumX, x, acc);
+      if (st.act == kPartial) put<N, VEC, false>(g, st.p, slab, width, x, acc);
+      else put_any<N, VEC, ALIGNED>(g, sg, st.p, key[j0 + u], slab, width, x, acc, stage, [] { __syncthreads(); });
 #pragma unroll
       for (int k = 0; k < N; ++k) acc[k] = 0.f;
     }
@@ -659,7 +702,7 @@ __global__ void __launch_bounds__(32 * kJoinGroups) k_embed_join(const Grad g, c
       for (int w = 1; w < kJoinGroups; ++w)
 #pragma unroll
         for (int k = 0; k < N; ++k) acc[k] += sum[w][k][lane];
-      commit<N, VEC>(g, sg, id, slab, 32, lane, acc);
+      put_any<N, VEC, VEC>(g, sg, row_of(g, sg, id), id, slab, 32, lane, acc, &sum[0][0][0], [] { __syncwarp(); });
     }
     __syncthreads();
   }
@@ -669,10 +712,20 @@ struct Workspace {
   size_t sorted, other, crossing, partial, bytes;
 };
 
-// Sorted tokens per block of k_embed_sum: long enough that few runs cross
-// blocks, short enough that a few thousand tokens still fill the SMs.
-int run_of(int64_t n) { return n >= 16384 ? 32 : n >= 8192 ? 16 : 8; }
-int64_t token_blocks(int64_t n) { return (n + run_of(n) - 1) / run_of(n); }
+// Sorted tokens per block of k_embed_sum: 32, so that few runs leave partial
+// sums, or down to 8 where that would leave too few blocks to fill the SMs
+// (5003 tokens of 1001 columns: 36 us at 8, 107 at 32).
+int run_of(int64_t n, int cols) {
+  const int64_t slabs = (int64_t(cols) + 1023) / 1024;
+  int run = kRunMost;
+  while (run > 8 && (n + run - 1) / run * slabs < 12 * kSms) run /= 2;
+  return run;
+}
+
+int64_t token_blocks(int64_t n, int cols) {
+  const int run = run_of(n, cols);
+  return (n + run - 1) / run;
+}
 
 Workspace workspace_of(int64_t n, int cols) {
   Workspace w{};
@@ -685,8 +738,8 @@ Workspace workspace_of(int64_t n, int cols) {
   };
   w.sorted = take(n * sizeof(int2));
   w.other = take(n * sizeof(int2));
-  w.crossing = take((token_blocks(n) + 1) * sizeof(int));
-  w.partial = take(size_t(token_blocks(n)) * 2 * cols * sizeof(float));
+  w.crossing = take((token_blocks(n, cols) + 1) * sizeof(int));
+  w.partial = take(size_t(token_blocks(n, cols)) * 2 * cols * sizeof(float));
   w.bytes = at;
   return w;
 }
@@ -751,28 +804,30 @@ cudaError_t launch_sort(const SortArgs& a, cudaStream_t s) {
 template <typename T>
 cudaError_t launch_grad(Grad g, const Segments& sg, bool few, cudaStream_t s, int* launches) {
   constexpr int N = Vec<T>::N;
-  bool vec = reinterpret_cast<uintptr_t>(g.dout) % 16 == 0 && g.dstride * sizeof(T) % 16 == 0 &&
-             g.cols % N == 0;
-  for (int i = 0; i < sg.n && vec; ++i) vec = (sg.at[i] - sg.rel[i]) % 4 == 0 && sg.rel[i] % 4 == 0;
+  const bool vec = reinterpret_cast<uintptr_t>(g.dout) % 16 == 0 && g.dstride * sizeof(T) % 16 == 0 &&
+                   g.cols % N == 0;
+  bool aligned = g.cols % 4 == 0;   // every row of accum (and of partial sums) starts on 16 bytes
+  for (int i = 0; i < sg.n && aligned; ++i) aligned = (sg.at[i] - sg.rel[i]) % 4 == 0 && sg.rel[i] % 4 == 0;
   g.fill_rows = std::min(kFillRows, std::max(1, 16384 / g.cols));
   const int64_t fills = g.overwrite ? (g.rows + g.fill_rows - 1) / g.fill_rows : 0;
-  int width = kSumX;
-  if (few) {
-    width = 64;
-    while (width < kFewX && width * N < g.cols) width *= 2;
-  }
+  int width = few ? 64 : 32;   // as many threads as a row has columns for
+  while (width < (few ? kFewX : kSumX) && width * N < g.cols) width *= 2;
   g.slabs = static_cast<int>((int64_t(g.cols) + width * N - 1) / (width * N));
   const int64_t grid = int64_t(few ? g.n : g.blocks) * g.slabs + fills;
   if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
   const unsigned blocks = static_cast<unsigned>(grid);
   ++*launches;
-  if (few) return launch(vec ? k_embed_few<T, true> : k_embed_few<T, false>, blocks, width, 1, false, s, 0, g, sg);
-  cudaError_t e = launch(vec ? k_embed_sum<T, true> : k_embed_sum<T, false>, blocks, kSumX, 1, true, s, 0, g, sg);
+  if (few)
+    return launch(!vec ? k_embed_few<T, false, false> : aligned ? k_embed_few<T, true, true> : k_embed_few<T, true, false>,
+                  blocks, width, 1, false, s, 0, g, sg);
+  cudaError_t e =
+      launch(!vec ? k_embed_sum<T, false, false> : aligned ? k_embed_sum<T, true, true> : k_embed_sum<T, true, false>,
+             blocks, width, 1, true, s, 0, g, sg);
   if (e != cudaSuccess) return e;
   ++*launches;
   const int slabs = static_cast<int>((int64_t(g.cols) + 127) / 128);
-  const unsigned join = static_cast<unsigned>(std::min<int64_t>(int64_t(g.blocks) * slabs, 8 * 152));
-  return launch(vec ? k_embed_join<true> : k_embed_join<false>, join, 32 * kJoinGroups, 1, true, s, 0, g, sg, slabs);
+  const unsigned join = static_cast<unsigned>(std::min<int64_t>(int64_t(g.blocks) * slabs, 8 * kSms));
+  return launch(aligned ? k_embed_join<true> : k_embed_join<false>, join, 32 * kJoinGroups, 1, true, s, 0, g, sg, slabs);
 }
 
 bool misaligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
@@ -865,8 +920,8 @@ extern "C" int muon_embedding_grad_workspace(int64_t n_tokens, int cols, size_t*
   });
 }
 
-extern "C" int muon_embedding_grad(float* accum, const void* dout, int dout_dtype,
-                                   int64_t dout_stride, const void* ids, int ids_type,
+extern "C" int muon_embedding_grad(float* accum, int64_t accum_elems, const void* dout,
+                                   int dout_dtype, int64_t dout_stride, const void* ids, int ids_type,
                                    int64_t n_tokens, float scale, int overwrite,
                                    const muon_param_t* param, const muon_partition_t* parts,
                                    int nparts, void* workspace, size_t workspace_bytes,
@@ -885,6 +940,9 @@ extern "C" int muon_embedding_grad(float* accum, const void* dout, int dout_dtyp
     if (nparts < 0 || (nparts > 0 && !parts)) return efail(MUON_ERR_INVALID, "parts is NULL");
     Segments sg;
     if ((rc = segments_of(*param, parts, nparts, &sg)) != MUON_OK) return rc;
+    for (int i = 0; i < sg.n; ++i)
+      if (sg.at[i] + ((i + 1 < sg.n ? sg.rel[i + 1] : sg.numel) - sg.rel[i]) > accum_elems)
+        return efail(MUON_ERR_INVALID, "accum_elems is less than the tables describe");
     const Workspace w = workspace_of(n_tokens, param->cols);
     if (w.bytes > 0 && (!workspace || misaligned(workspace, 16) || workspace_bytes < w.bytes))
       return efail(MUON_ERR_INVALID, "workspace is NULL, misaligned or too small");
@@ -925,8 +983,8 @@ extern "C" int muon_embedding_grad(float* accum, const void* dout, int dout_dtyp
     g.sorted = so.sorted;
     g.partial = reinterpret_cast<float*>(base + w.partial);
     g.crossing = so.crossing;
-    g.run = run_of(n_tokens);
-    g.blocks = static_cast<int>(token_blocks(n_tokens));
+    g.run = run_of(n_tokens, param->cols);
+    g.blocks = static_cast<int>(token_blocks(n_tokens, param->cols));
     const cudaError_t e = dout_dtype == MUON_DTYPE_BF16
                               ? launch_grad<__nv_bfloat16>(g, sg, few, s, &launches)
                               : launch_grad<float>(g, sg, few, s, &launches);

@@ -38,6 +38,7 @@ constexpr int kHeldThreads = 256;    // k_held: most threads of a block,
 constexpr int kHeldBlocks = 6;       // blocks per SM,
 constexpr int kHeldVecs = 2048;      // 16-byte vectors of a block before a row takes more blocks,
 constexpr int kHeldMost = 13824;     // and at most (216 KB)
+constexpr int kHeldRow = 65536;      // bytes of a row up to which it is held without a gradient too
 constexpr int kSms = 152;
 constexpr int kPairThreads = 256;
 constexpr int kGivenThreads = 256;
@@ -423,13 +424,11 @@ __global__ void __launch_bounds__(kPairThreads) k_pairs(const Rows a, const Pair
     for (int64_t t = b[j] + threadIdx.x; t < e[j]; t += kPairThreads) q.coef[t] = j ? -g : g;
 }
 
-// The preference loss's statistics from the margins, by one cluster of
-// `blocks` blocks of NT threads, `block` this one.
-template <int NT>
-__device__ __forceinline__ void pair_sum(const Pairs& q, float* stats, int block, int blocks) {
-  __shared__ tok::Two sh[4][NT / 32];
+// The preference loss's statistics from the margins, by one block.
+__device__ __forceinline__ void pair_sum(const Pairs& q, float* stats) {
+  __shared__ tok::Two sh[4][kGivenThreads / 32];
   tok::Two v[4];   // loss, margin, won, weight
-  for (int i = block * NT + threadIdx.x; i < q.n; i += blocks * NT) {
+  for (int i = threadIdx.x; i < q.n; i += kGivenThreads) {
     const float w = q.weights ? q.weights[i] : 1.f;
     if (w == 0.f) continue;
     const float h = q.margins[i];
@@ -441,14 +440,14 @@ __device__ __forceinline__ void pair_sum(const Pairs& q, float* stats, int block
     if (h > 0.f) v[2].add(w);
     v[3].add(w);
   }
-  cluster_sum<NT, 4>(v, sh);
-  if (block == 0 && threadIdx.x == 0)
+  cluster_sum<kGivenThreads, 4>(v, sh);
+  if (threadIdx.x == 0)
     for (int k = 0; k < 4; ++k) stats[k] = v[k].value() / (q.weights || q.n == 0 ? 1.f : float(q.n));
 }
 
-__global__ void __launch_bounds__(kSumThreads) k_pair_sum(const Pairs q, float* stats) {
+__global__ void __launch_bounds__(kGivenThreads) k_pair_sum(const Pairs q, float* stats) {
   tok::wait_before();
-  pair_sum<kSumThreads>(q, stats, blockIdx.x, gridDim.x);
+  pair_sum(q, stats);
 }
 
 // The gradient from (m, 1/S) and c of every row.  Block 0 sums the
@@ -460,7 +459,7 @@ __global__ void __launch_bounds__(kGivenThreads) k_given(const Rows a, const Ext
   constexpr int N = Vec<T>::N;
   constexpr int NV = kGivenVecs / kGivenThreads;
   tok::wait_before();
-  if (blockIdx.x == 0) return pair_sum<kGivenThreads>(q, stats, 0, 1);
+  if (blockIdx.x == 0) return pair_sum(q, stats);
   const unsigned task = gridDim.x - 1 - blockIdx.x;
   const int64_t t = task / slices;
   const int slice = task % slices;
@@ -586,7 +585,7 @@ __device__ __forceinline__ void zero_share(const Rows& a, T* drow, int v0, int p
   const T zero = tok::from_float<T>(0.f);
   if (rank == 0) {
     if (threadIdx.x < sh.head) drow[threadIdx.x] = zero;
-    else if (threadIdx.x >= 32 && sh.tail0 + int(threadIdx.x) - 32 < a.vocab) drow[sh.tail0 + threadIdx.x - 32] = zero;
+    else if (threadIdx.x >= 8 && sh.tail0 + int(threadIdx.x) - 8 < a.vocab) drow[sh.tail0 + threadIdx.x - 8] = zero;
   }
   const int v1 = min(sh.nvec, v0 + per_block);
   for (int i = v0 + threadIdx.x; i < v1; i += blockDim.x)
@@ -655,7 +654,7 @@ __global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) k_held(const Rows a
   int single = -1;
   if (rank == 0) {
     if (threadIdx.x < sh.head) single = threadIdx.x;
-    else if (threadIdx.x >= 32 && sh.tail0 + int(threadIdx.x) - 32 < a.vocab) single = sh.tail0 + threadIdx.x - 32;
+    else if (threadIdx.x >= 8 && sh.tail0 + int(threadIdx.x) - 8 < a.vocab) single = sh.tail0 + threadIdx.x - 8;   // fewer than 8 of either
   }
   const float zs = single >= 0 ? tok::to_float(row[single]) : -INFINITY;
   const float zy = warp == 0 ? tok::to_float(row[y]) : 0.f;
@@ -769,8 +768,13 @@ Hold hold_of(int64_t n, int vocab, int per_vec) {
   while (c < 8 && n * c * 2 <= kSms && nvec / c > 64) c *= 2;   // few rows: use the SMs that there are
   const int vecs = (nvec + c - 1) / c;
   if (vecs > kHeldMost) return {0, 0, 0};
-  int threads = 64;
-  while (threads < kHeldThreads && threads * 4 < vecs) threads *= 2;
+  // Few rows: as many threads as help.  Many rows: 16 vectors per thread, so that
+  // an SM has blocks of more rows to turn to (16384 rows of 8192 bf16: 41 us, 57
+  // at 4 vectors); 8 where shared memory limits the blocks (8192 rows of
+  // 131072 bf16 with their gradient: 654 us, 693 at 16).
+  const int per_thread = n * c < 4 * kSms ? 2 : vecs * 7 > kHeldMost ? 8 : 16;
+  int threads = 32;
+  while (threads < kHeldThreads && threads * per_thread < vecs) threads *= 2;
   return {c, vecs, threads};
 }
 
@@ -789,7 +793,10 @@ template <typename T, int MODE>
 cudaError_t launch_rows_of(const Rows& a, const Extra& x, cudaStream_t s) {
   const Hold h = hold_of(a.n, a.vocab, Vec<T>::N);
   const bool grad = MODE == kPolicy && a.dlogits;
-  if (h.c && (grad || a.n < 2 * kSms) && a.n * h.c <= 0x7fffffff) return launch_held<T, MODE>(a, x, h, s);
+  // Without a gradient, many long rows are read faster by streams of loads
+  // (8192 rows of 131072 bf16: 279 us, 6.9 TB/s).
+  const bool stream = !grad && a.n >= 2 * kSms && int64_t(a.vocab) * int64_t(sizeof(T)) > kHeldRow;
+  if (h.c && !stream && a.n * h.c <= 0x7fffffff) return launch_held<T, MODE>(a, x, h, s);
   return launch(k_rows<T, MODE>, static_cast<unsigned>(a.n), kRowThreads, 1, false, s, 0, a, x);
 }
 
@@ -999,8 +1006,7 @@ extern "C" int muon_preference_loss(const void* logits, int dtype, int64_t strid
               ? launch(k_given<__nv_bfloat16>, grid, kGivenThreads, 1, true, s, 0, a, x, q, stats, slices)
               : launch(k_given<float>, grid, kGivenThreads, 1, true, s, 0, a, x, q, stats, slices);
     } else if (e == cudaSuccess) {
-      const int blocks = sum_blocks(n_pairs);
-      e = launch(k_pair_sum, blocks, kSumThreads, blocks, n_tokens > 0 || n_pairs > 0, s, 0, q, stats);
+      e = launch(k_pair_sum, 1, kGivenThreads, 1, n_tokens > 0 || n_pairs > 0, s, 0, q, stats);
     }
     return end_call((n_tokens > 0) + (n_pairs > 0) + 1, e);
   });

@@ -52,7 +52,7 @@ def test_lookup_refuses(lib, change, word):
 def grad_args(param=(0, 10, 64, 0, 0), parts=None, **change):
     p = np.array([param], dtype=nsg.PARAM_DTYPE)
     q = np.array(parts or [], dtype=nsg.PART_DTYPE)
-    a = dict(accum=FAKE, dout=FAKE, dt=0, ds=64, ids=FAKE, it=1, n=4096, scale=1.0, overwrite=0,
+    a = dict(accum=FAKE, ae=1 << 20, dout=FAKE, dt=0, ds=64, ids=FAKE, it=1, n=4096, scale=1.0, overwrite=0,
              pp=p.ctypes.data, qq=q.ctypes.data if len(q) else None, nparts=len(q), ws=FAKE,
              wb=1 << 24, stream=None)
     a.update(change)
@@ -64,7 +64,7 @@ def grad_args(param=(0, 10, 64, 0, 0), parts=None, **change):
     (dict(dt=5), "dout_dtype"), (dict(ds=63), "dout_stride"), (dict(it=-1), "ids_type"), (dict(n=-1), "n_tokens"),
     (dict(scale=float("nan")), "scale"), (dict(overwrite=2), "overwrite"), (dict(ws=None), "workspace"),
     (dict(ws=FAKE + 8), "workspace"), (dict(wb=100), "workspace"), (dict(pp=None), "param"),
-    (dict(nparts=1), "parts is NULL"), (dict(nparts=-1), "parts is NULL")])
+    (dict(ae=639), "accum_elems"), (dict(ae=-1), "accum_elems"), (dict(nparts=1), "parts is NULL"), (dict(nparts=-1), "parts is NULL")])
 def test_gradient_refuses(lib, change, word):
     args, _keep = grad_args(**change)
     refused(lib, lib.muon_embedding_grad(*args), word)
@@ -77,6 +77,7 @@ def test_gradient_refuses(lib, change, word):
     ((0, 10, 64, 0, 0), [(300, 700, 300), (0, 300, 0)], "sorted", -1),
     ((0, 10, 64, 0, 0), [(0, 300, 0), (300, 700, 200)], "storage", -1),
     ((0, 10, 64, 0, 0), [(0, 700, -4)], "bad range", -1),
+    ((0, 10, 64, 0, 0), [(0, 320, 0), (320, 700, (1 << 20) - 300)], "accum_elems", -1),
     ((0, 10, 64, 0, 0), [(4 * i, 4 * i + 4, 4 * i) for i in range(160)], "MAX_SEGMENTS", -2)])
 def test_gradient_refuses_tables(lib, param, parts, word, code):
     args, _keep = grad_args(param, parts)
