@@ -12,6 +12,7 @@ Table formats match the C structs of ``include/muon.h``:
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import os
@@ -389,41 +390,40 @@ def _per_token(x, n, name):
     return x.data_ptr()
 
 
-def _same_device(device, *others):
+def _same_device(index, *others):
     for o in others:
-        if o is not None and o.device != device:
+        if o is not None and o.get_device() != index:
             raise ValueError("every tensor must be on one device")
 
 
-def _elsewhere(device, stream):
-    """None where `device` is torch's current one and no stream is asked for;
-    else a context that makes them current, so that tensors made inside belong
-    to the stream the kernels run on.  Each call enters it and starts again."""
-    import contextlib
-
+def _elsewhere(index, stream):
+    """None where device `index` is torch's current one and no stream is asked
+    for; else a context that makes them current, so that tensors made inside
+    belong to the stream the kernels run on.  Each call enters it and starts
+    again."""
     import torch
-    if device.type != "cuda":
+    if index < 0:
         raise ValueError("tensors must be on a CUDA device")
-    here = torch.cuda.current_device() == device.index
+    here = torch.cuda.current_device() == index
     if stream is None and here:
         return None
     ctx = contextlib.ExitStack()
     if not here:
-        ctx.enter_context(torch.cuda.device(device))
+        ctx.enter_context(torch.cuda.device(index))
     if stream is not None:
         if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream, device=device)
+            stream = torch.cuda.ExternalStream(stream, device=index)
         ctx.enter_context(torch.cuda.stream(stream))
     return ctx
 
 
-def _raw_stream(device):
-    """torch's current stream of the current device, as a cudaStream_t."""
+def _raw_stream(index):
+    """torch's current stream of device `index`, as a cudaStream_t."""
     import torch
     try:
-        return torch._C._cuda_getCurrentRawStream(device.index)
+        return torch._C._cuda_getCurrentRawStream(index)
     except AttributeError:
-        return torch.cuda.current_stream(device).cuda_stream
+        return torch.cuda.current_stream(index).cuda_stream
 
 
 def embedding(table, ids, scale: float = 1.0, out=None, out_dtype=None, stream=None):
@@ -433,7 +433,7 @@ def embedding(table, ids, scale: float = 1.0, out=None, out_dtype=None, stream=N
     fills `out` (2-D with any row stride, or contiguous)."""
     import torch
     rows, cols, stride = _rows(table, "table")
-    it, device = _index(ids, "ids"), table.device
+    it, device = _index(ids, "ids"), table.get_device()
     _same_device(device, ids, out)
     ctx = _elsewhere(device, stream)
     if ctx is not None:
@@ -441,7 +441,7 @@ def embedding(table, ids, scale: float = 1.0, out=None, out_dtype=None, stream=N
             return embedding(table, ids, scale, out, out_dtype)
     n = ids.numel()
     if out is None:
-        out = torch.empty((*ids.shape, cols), dtype=out_dtype or table.dtype, device=device)
+        out = torch.empty((*ids.shape, cols), dtype=out_dtype or table.dtype, device=table.device)
         ostride = cols
     else:
         if out.shape[-1] != cols or out.numel() != n * cols or out_dtype not in (None, out.dtype):
@@ -475,7 +475,7 @@ def embedding_grad(accum, dout, ids, param, parts=None, scale: float = 1.0,
         raise ValueError("accum must be a contiguous float32 tensor")
     if dout.dim() != 2:
         dout = dout.reshape(-1, cols)
-    n, it, device = ids.numel(), _index(ids, "ids"), accum.device
+    n, it, device = ids.numel(), _index(ids, "ids"), accum.get_device()
     got, width, stride = _rows(dout, "dout")
     if got != n or width != cols:
         raise ValueError("dout must be tokens x cols")
@@ -484,8 +484,9 @@ def embedding_grad(accum, dout, ids, param, parts=None, scale: float = 1.0,
         if accum.numel() < offset + rows * cols:
             raise ValueError(f"accum holds {accum.numel()} elements, the parameter ends at {offset + rows * cols}")
     else:
-        parts, nparts = _table(parts, PART_DTYPE)
-        table = parts.tobytes()
+        if getattr(parts, "dtype", None) is not PART_DTYPE:
+            parts = _table(parts, PART_DTYPE)[0]
+        table, nparts = parts.tobytes(), len(parts)
     _same_device(device, dout, ids, workspace)
     ctx = _elsewhere(device, stream)
     if ctx is not None:
@@ -493,7 +494,7 @@ def embedding_grad(accum, dout, ids, param, parts=None, scale: float = 1.0,
             return embedding_grad(accum, dout, ids, param, parts, scale, overwrite, workspace)
     need = embedding_grad_workspace(n, cols)
     if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        workspace = torch.empty(need, dtype=torch.uint8, device=accum.device)
     have = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib().muon_embedding_grad(
         accum.data_ptr(), accum.numel(), dout.data_ptr(), _dtype(dout, "dout"), stride, ids.data_ptr(), it,
@@ -530,14 +531,14 @@ def token_logprobs(logits, targets, logit_scale: float = 1.0, out=None, stream=N
     targets' shape."""
     import torch
     logits, n, vocab, stride, tt = _logits(logits, targets)
-    device = logits.device
+    device = logits.get_device()
     _same_device(device, targets, out)
     ctx = _elsewhere(device, stream)
     if ctx is not None:
         with ctx:
             return token_logprobs(logits, targets, logit_scale, out)
     if out is None:
-        out = torch.empty(targets.shape, dtype=torch.float32, device=device)
+        out = torch.empty(targets.shape, dtype=torch.float32, device=logits.device)
     _check(lib().muon_token_logprobs(logits.data_ptr(), _dtype(logits, "logits"), stride, n, vocab,
                                      targets.data_ptr(), tt, logit_scale, _per_token(out, n, "out"),
                                      _raw_stream(device)))
@@ -558,7 +559,7 @@ def _dlogits(logits, n, vocab, stride, dlogits):
         dlogits = dlogits.view(-1, dlogits.shape[-1])
     if dlogits.dtype != logits.dtype or dlogits.shape != logits.shape:
         raise ValueError("dlogits must match the logits' shape and type")
-    _same_device(logits.device, dlogits)
+    _same_device(logits.get_device(), dlogits)
     return dlogits, _rows(dlogits, "dlogits")[2]
 
 
@@ -573,7 +574,7 @@ def policy_loss(logits, targets, advantages, weights, old_logp=None, ref_logp=No
     clipped weight), "logp": per token, "dlogits"}, all on the device."""
     import torch
     logits, n, vocab, stride, tt = _logits(logits, targets)
-    device = logits.device
+    device = logits.get_device()
     _same_device(device, targets, advantages, weights, old_logp, ref_logp)
     ctx = _elsewhere(device, stream)
     if ctx is not None:
@@ -581,8 +582,8 @@ def policy_loss(logits, targets, advantages, weights, old_logp=None, ref_logp=No
             return policy_loss(logits, targets, advantages, weights, old_logp, ref_logp, clip_low,
                                clip_high, kl_coef, logit_scale, dlogits)
     d, dstride = _dlogits(logits, n, vocab, stride, dlogits)
-    logp = torch.empty(targets.shape, dtype=torch.float32, device=device)
-    stats = torch.empty(4, dtype=torch.float32, device=device)
+    logp = torch.empty(targets.shape, dtype=torch.float32, device=logits.device)
+    stats = torch.empty(4, dtype=torch.float32, device=logits.device)
     _check(lib().muon_policy_loss(
         logits.data_ptr(), _dtype(logits, "logits"), stride, n, vocab, targets.data_ptr(), tt,
         _per_token(advantages, n, "advantages"), _per_token(weights, n, "weights"),
@@ -606,7 +607,7 @@ def preference_loss(logits, targets, offsets, ref_logp=None, beta: float = 0.1,
     places = offsets.numel()
     if places % 2 != 1:
         raise ValueError("offsets must hold 2 * pairs + 1 positions")
-    pairs, ot, device = places // 2, _index(offsets, "offsets"), logits.device
+    pairs, ot, device = places // 2, _index(offsets, "offsets"), logits.get_device()
     _same_device(device, targets, offsets, ref_logp, pair_weights, workspace)
     ctx = _elsewhere(device, stream)
     if ctx is not None:
@@ -614,11 +615,11 @@ def preference_loss(logits, targets, offsets, ref_logp=None, beta: float = 0.1,
             return preference_loss(logits, targets, offsets, ref_logp, beta, label_smoothing,
                                    pair_weights, logit_scale, dlogits, workspace)
     d, dstride = _dlogits(logits, n, vocab, stride, dlogits)
-    logp = torch.empty(targets.shape, dtype=torch.float32, device=device)
-    stats = torch.empty(4, dtype=torch.float32, device=device)
-    margins = torch.empty(pairs, dtype=torch.float32, device=device)
+    logp = torch.empty(targets.shape, dtype=torch.float32, device=logits.device)
+    stats = torch.empty(4, dtype=torch.float32, device=logits.device)
+    margins = torch.empty(pairs, dtype=torch.float32, device=logits.device)
     if workspace is None:
-        workspace = torch.empty(preference_loss_workspace(n), dtype=torch.uint8, device=device)
+        workspace = torch.empty(preference_loss_workspace(n), dtype=torch.uint8, device=logits.device)
     _check(lib().muon_preference_loss(
         logits.data_ptr(), _dtype(logits, "logits"), stride, n, vocab, targets.data_ptr(), tt,
         offsets.data_ptr(), ot, pairs, _per_token(ref_logp, n, "ref_logp"),

@@ -159,7 +159,8 @@ constexpr int kSumX = 128;           // its threads, at most
 constexpr int kJoinGroups = 8;      // k_embed_join: warps of a block, each adding every 16th partial sum
 constexpr int kFew = 1024;           // tokens up to which k_embed_few is taken
 constexpr int kFewX = 256;
-constexpr int kFillRows = 256;       // rows of the table per filling block, at most
+constexpr int kFillX = 256;
+constexpr int kFillBlocks = 4;       // per SM
 
 // The parameter's runs in storage: elements [rel[i], rel[i + 1]) of the
 // parameter start at storage index at[i].
@@ -196,7 +197,6 @@ struct Grad {
   int run;          // tokens per block
   int blocks;       // blocks of tokens
   int slabs;        // blocks of columns
-  int fill_rows;    // rows of the table per filling block (overwrite)
 };
 
 __device__ __forceinline__ int grad_id(const Grad& g, int t) {
@@ -324,32 +324,24 @@ struct __align__(16) Step {
   int act;
 };
 
-// Zeros in the rows of [r0, r1) that are not `named`, neighbours together.
-__device__ void fill_zeros(const Grad& g, const Segments& sg, int r0, int r1, const uint8_t* named) {
-  for (int r = r0; r < r1;) {
-    if (named[r - r0]) {
-      ++r;
-      continue;
-    }
-    int e = r + 1;
-    while (e < r1 && !named[e - r0]) ++e;
-    int64_t i = int64_t(r) * g.cols, left = int64_t(e - r) * g.cols;
-    while (left > 0) {
-      int64_t room;
-      float* p = g.accum + sg.place(i, &room);
-      const int n = static_cast<int>(room < left ? room : left);
-      int head = static_cast<int>((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / 4;
-      head = min(head, n);
-      if (int(threadIdx.x) < head) p[threadIdx.x] = 0.f;
-      const int quads = (n - head) / 4;
-      for (int q = threadIdx.x; q < quads; q += blockDim.x)
-        *reinterpret_cast<float4*>(p + head + 4 * q) = make_float4(0.f, 0.f, 0.f, 0.f);
-      const int tail = head + 4 * quads + threadIdx.x;
-      if (tail < n) p[tail] = 0.f;
-      i += n;
-      left -= n;
-    }
-    r = e;
+// Zeros in the whole parameter (overwrite).  One resident wave of blocks, so
+// that the sort is scheduled beside it and costs no time of its own.  The rows
+// of tokens are written twice.  Zeroing only the other rows beside
+// k_embed_sum, once the sort is done, took 55 us instead of 51 for 5003 tokens
+// of a 50001 x 1001 table, and 183 instead of 202 for 16384 of a 131072 x 2048
+// one, with twice the code.
+__global__ void __launch_bounds__(kFillX) k_embed_fill(float* accum, const __grid_constant__ Segments sg) {
+  tok::allow_next();
+  for (int i = 0; i < sg.n; ++i) {
+    float* p = accum + sg.at[i];
+    const int64_t n = (i + 1 < sg.n ? sg.rel[i + 1] : sg.numel) - sg.rel[i];
+    const int64_t head = min(n, int64_t(((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / 4));
+    const int64_t quads = (n - head) / 4;
+    const int64_t x = int64_t(blockIdx.x) * kFillX + threadIdx.x;
+    if (x < head) p[x] = 0.f;
+    for (int64_t q = x; q < quads; q += int64_t(gridDim.x) * kFillX)
+      __stcs(reinterpret_cast<float4*>(p + head) + q, make_float4(0.f, 0.f, 0.f, 0.f));
+    if (head + 4 * quads + x < n) p[head + 4 * quads + x] = 0.f;
   }
 }
 
@@ -358,7 +350,6 @@ __device__ void fill_zeros(const Grad& g, const Segments& sg, int r0, int r1, co
 // One block per token and block of columns.  The block of an id's first token
 // finds the others (every block reads all the ids: at most 8 KB, from L2),
 // adds them in order of position and writes the row; the others leave.
-// Further blocks zero the rows that no token names (overwrite).
 template <typename T, bool VEC, bool ALIGNED>
 __global__ void __launch_bounds__(kFewX) k_embed_few(const Grad g, const __grid_constant__ Segments sg) {
   constexpr int N = Vec<T>::N;
@@ -366,35 +357,23 @@ __global__ void __launch_bounds__(kFewX) k_embed_few(const Grad g, const __grid_
   constexpr int F = 8;    // ids in flight
   __shared__ unsigned found[kFew / 32];
   __shared__ int list[kFew];
-  __shared__ uint8_t named[kFillRows];
   __shared__ float stage[kFewX * N];
   const int x = threadIdx.x, lane = x % 32, width = blockDim.x;
-  auto each_id = [&](auto use) {   // use(position, id) for all positions up to a multiple of 32
-    for (int j0 = x; j0 - lane < g.n; j0 += F * width) {
-      int id[F];
-#pragma unroll
-      for (int k = 0; k < F; ++k) id[k] = j0 + k * width < g.n ? tok::load_index(g.ids, g.ids64, j0 + k * width) : -1;
-#pragma unroll
-      for (int k = 0; k < F; ++k) use(j0 + k * width, id[k]);
-    }
-  };
-  if (blockIdx.x >= unsigned(g.n) * g.slabs) {
-    const int r0 = (blockIdx.x - g.n * g.slabs) * g.fill_rows, r1 = min(g.rows, r0 + g.fill_rows);
-    for (int r = x; r < r1 - r0; r += width) named[r] = 0;
-    __syncthreads();
-    each_id([&](int, int id) {
-      if (id >= r0 && id < r1) named[id - r0] = 1;
-    });
-    __syncthreads();
-    return fill_zeros(g, sg, r0, r1, named);
-  }
   const int t = blockIdx.x / g.slabs, slab = blockIdx.x % g.slabs;
   const int id = grad_id(g, t);
+  for (int j0 = x; j0 - lane < g.n; j0 += F * width) {
+    int other[F];
+#pragma unroll
+    for (int k = 0; k < F; ++k)
+      other[k] = j0 + k * width < g.n ? tok::load_index(g.ids, g.ids64, j0 + k * width) : -1;
+#pragma unroll
+    for (int k = 0; k < F; ++k) {
+      const unsigned same = __ballot_sync(0xffffffffu, other[k] == id);
+      if (lane == 0 && j0 + k * width < g.n) found[(j0 + k * width) / 32] = same;
+    }
+  }
+  tok::wait_before();   // zeros first (overwrite)
   if (id < 0) return;
-  each_id([&](int j, int other) {
-    const unsigned same = __ballot_sync(0xffffffffu, other == id);
-    if (lane == 0 && j < g.n) found[j / 32] = same;
-  });
   __syncthreads();
   int count = 0;
   for (int w = 0; w < (g.n + 31) / 32; ++w) {
@@ -448,7 +427,8 @@ __global__ void __launch_bounds__(kSortThreads, 1) k_embed_sort(const SortArgs a
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   tok::allow_next();
   if (rank == 0 && threadIdx.x == 0) a.crossing[0] = 0;
-  cl.sync();   // every block has started: total may be written from outside
+  // Every block has to have started before `total` is written from outside.
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   const int share = (a.n + nb * kSortWarps - 1) / (nb * kSortWarps);
   const int64_t from = int64_t(rank * kSortWarps + warp) * share;
   const int lo = static_cast<int>(from < a.n ? from : a.n);
@@ -519,6 +499,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) k_embed_sort(const SortArgs a
       count[w * kSortBins + bin] = run;
       run += c;
     }
+    if (p == 0) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
 #pragma unroll
     for (int b = 0; b < kSortBlocks; ++b)
       if (b < nb) *cl.map_shared_rank(&total[rank][bin], b) = run;
@@ -554,8 +535,9 @@ __global__ void __launch_bounds__(kSortThreads, 1) k_embed_sort(const SortArgs a
         if (t0 + 32 * i + lane < hi)
           dst[rank_in[i] + (once ? mine[bin_of(i)] : 0)] = make_int2(key[i], val[i]);
     }
-    cl.sync();   // dst is complete, and total read everywhere
+    if (p + 1 < a.passes) cl.sync();   // dst is complete, and total read everywhere
   }
+  tok::wait_before();   // k_embed_fill beside it (overwrite): the next kernel waits for this one alone
 }
 
 template <typename T, bool VEC, bool ALIGNED>
@@ -566,27 +548,9 @@ __global__ void __launch_bounds__(kSumX) k_embed_sum(const Grad g, const __grid_
   __shared__ int edge[3];   // ids of the token before, the one before the block before, the one after the next
   __shared__ Step step[2 * kRunMost];
   __shared__ float stage[kSumX * N];
-  __shared__ uint8_t named[kFillRows];
   const int width = blockDim.x;
   tok::wait_before();
   tok::allow_next();
-  if (blockIdx.x >= unsigned(g.blocks) * g.slabs) {
-    const int r0 = (blockIdx.x - g.blocks * g.slabs) * g.fill_rows, r1 = min(g.rows, r0 + g.fill_rows);
-    for (int r = threadIdx.x; r < r1 - r0; r += width) named[r] = 0;
-    int lo = 0, hi = g.n;   // the first sorted token with id >= r0
-    while (lo < hi) {
-      const int mid = lo + (hi - lo) / 2;
-      if (g.sorted[mid].x < r0) lo = mid + 1; else hi = mid;
-    }
-    __syncthreads();
-    for (int t = lo + threadIdx.x; t < g.n; t += width) {
-      const int id = g.sorted[t].x;
-      if (id >= r1) break;
-      named[id - r0] = 1;
-    }
-    __syncthreads();
-    return fill_zeros(g, sg, r0, r1, named);
-  }
   const int block = blockIdx.x / g.slabs, slab = blockIdx.x % g.slabs;
   const int x = threadIdx.x;
   const int64_t t0 = int64_t(block) * g.run;
@@ -786,7 +750,7 @@ int segments_of(const muon_param_t& p, const muon_partition_t* parts, int nparts
   return MUON_OK;
 }
 
-cudaError_t launch_sort(const SortArgs& a, cudaStream_t s) {
+cudaError_t launch_sort(const SortArgs& a, bool early, cudaStream_t s) {
   // 2048 tokens per block (4 per thread), up to a cluster of 16 blocks
   int blocks = 1;
   while (blocks < kSortBlocks && a.n > blocks * 2048) blocks *= 2;
@@ -796,7 +760,7 @@ cudaError_t launch_sort(const SortArgs& a, cudaStream_t s) {
   }
   const cudaError_t e = cudaFuncSetAttribute(k_embed_sort, cudaFuncAttributeMaxDynamicSharedMemorySize, kSortShared);
   if (e != cudaSuccess) return e;
-  return launch(k_embed_sort, blocks, kSortThreads, blocks, false, s, kSortShared, a);
+  return launch(k_embed_sort, blocks, kSortThreads, blocks, early, s, kSortShared, a);
 }
 
 // The gradient's kernels after the sort, or the one for few tokens; *launches
@@ -808,18 +772,16 @@ cudaError_t launch_grad(Grad g, const Segments& sg, bool few, cudaStream_t s, in
                    g.cols % N == 0;
   bool aligned = g.cols % 4 == 0;   // every row of accum (and of partial sums) starts on 16 bytes
   for (int i = 0; i < sg.n && aligned; ++i) aligned = (sg.at[i] - sg.rel[i]) % 4 == 0 && sg.rel[i] % 4 == 0;
-  g.fill_rows = std::min(kFillRows, std::max(1, 16384 / g.cols));
-  const int64_t fills = g.overwrite ? (g.rows + g.fill_rows - 1) / g.fill_rows : 0;
   int width = few ? 64 : 32;   // as many threads as a row has columns for
   while (width < (few ? kFewX : kSumX) && width * N < g.cols) width *= 2;
   g.slabs = static_cast<int>((int64_t(g.cols) + width * N - 1) / (width * N));
-  const int64_t grid = int64_t(few ? g.n : g.blocks) * g.slabs + fills;
+  const int64_t grid = int64_t(few ? g.n : g.blocks) * g.slabs;
   if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
   const unsigned blocks = static_cast<unsigned>(grid);
   ++*launches;
   if (few)
     return launch(!vec ? k_embed_few<T, false, false> : aligned ? k_embed_few<T, true, true> : k_embed_few<T, true, false>,
-                  blocks, width, 1, false, s, 0, g, sg);
+                  blocks, width, 1, g.overwrite, s, 0, g, sg);
   cudaError_t e =
       launch(!vec ? k_embed_sum<T, false, false> : aligned ? k_embed_sum<T, true, true> : k_embed_sum<T, true, false>,
              blocks, width, 1, true, s, 0, g, sg);
@@ -964,9 +926,16 @@ extern "C" int muon_embedding_grad(float* accum, int64_t accum_elems, const void
     so.crossing = reinterpret_cast<int*>(base + w.crossing);
     const bool few = n_tokens <= kFew;
     int launches = 0;
-    if (!few) {
-      const cudaError_t e = launch_sort(so, s);
+    if (overwrite) {
+      const cudaError_t e = launch(k_embed_fill, unsigned(std::min<int64_t>(kFillBlocks * kSms, sg.numel / 1024 + 1)),
+                                   kFillX, 1, false, s, 0, accum, sg);
       if (e != cudaSuccess) return end_call(0, e);
+      ++launches;
+    }
+    if (n_tokens == 0) return end_call(launches, cudaSuccess);
+    if (!few) {
+      const cudaError_t e = launch_sort(so, overwrite, s);
+      if (e != cudaSuccess) return end_call(launches, e);
       ++launches;
     }
     Grad g{};

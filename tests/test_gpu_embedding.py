@@ -145,10 +145,11 @@ def test_gradient_dense(torch, shape, dtype, overwrite):
 @pytest.mark.parametrize("storage,nparts", [("identity", 1), ("identity", 8), ("rank_major", 4),
                                             ("shuffled", 3), ("shuffled", 40)])
 @pytest.mark.parametrize("cols", [37, 64])
-def test_gradient_in_partitions(torch, storage, nparts, cols):
+@pytest.mark.parametrize("T", [900, 3001])
+def test_gradient_in_partitions(torch, storage, nparts, cols, T):
     """The parameter between others of a partitioned buffer: cut anywhere,
     also inside a row; padding and the other parameters untouched."""
-    rows, T = 211, 3001
+    rows = 211
     lay = wl.build_layout([[wl.ParamSpec("w", 17, 13)],
                            [wl.ParamSpec("ln", 1, 33, use_muon=False),
                             wl.ParamSpec("table", rows, cols, use_muon=False),
@@ -172,6 +173,29 @@ def test_gradient_in_partitions(torch, storage, nparts, cols):
         nsg.embedding_grad(dense, dout, ids, (0, rows, cols), scale=0.25, overwrite=overwrite)
         np.testing.assert_array_equal(bits(out[2]), bits(dense.cpu().numpy().reshape(rows, cols)))
     assert nsg.device_error() == 0
+
+
+@pytest.mark.parametrize("T", [700, 5000])
+@pytest.mark.parametrize("cols", [64, 72])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_gradient_of_rows_cut_on_16_bytes(torch, T, cols, dtype):
+    """Rows that start on 16 bytes, some of them cut between partitions: the
+    same bits as without partitions, for few and for many tokens."""
+    rows = 301
+    lay = wl.build_layout([[wl.ParamSpec("table", rows, cols, use_muon=False)]], 16, 7, "rank_major", 3)
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    ids = make_ids(torch, "zipf", T, rows, 5, "int32")
+    dout = torch.randn((T, cols), generator=gen, device="cuda")
+    dout = dout.to(torch.bfloat16) if dtype == "bf16" else dout
+    first = torch.randn(lay.storage_size, generator=gen, device="cuda")
+    for overwrite in (False, True):
+        accum, dense = first.clone(), first.clone()
+        nsg.embedding_grad(accum, dout, ids, lay.params[0], parts=lay.parts, scale=0.5, overwrite=overwrite)
+        nsg.embedding_grad(dense, dout, ids, (0, rows, cols), scale=0.5, overwrite=overwrite)
+        n = rows * cols
+        assert torch.equal(accum[:n], dense[:n]) and torch.equal(accum[n:], first[n:])
+        want, bound, _ = reference_grad(torch, first[:n].view(rows, cols), dout, ids, 0.5, overwrite)
+        assert bool(((accum[:n].view(rows, cols).double() - want).abs() <= bound).all())
 
 
 def test_gradient_of_special_values_and_strides(torch):
