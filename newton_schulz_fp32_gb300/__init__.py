@@ -343,28 +343,34 @@ def newton_schulz(X, Y=None, ns_method="gram", ns_steps: int = 5, operand_mode="
 
 # ------------------------------------------------------------------ the two ends of a model
 
+_KINDS: dict = {}     # torch dtype -> muon_dtype_t, filled on first use (torch is imported late)
+_INDEXES: dict = {}   # torch dtype -> muon_index_t
+
+
+def _torch():
+    import torch
+    if not _KINDS:
+        _INDEXES.update({torch.int32: 0, torch.int64: 1})
+        _KINDS.update({torch.bfloat16: 0, torch.float32: 1})
+    return torch
+
+
 def _dtype(x, name):
     """muon_dtype_t of a tensor."""
-    import torch
-    d = x.dtype
-    if d == torch.bfloat16:
-        return 0
-    if d == torch.float32:
-        return 1
-    raise ValueError(f"{name} must be bfloat16 or float32, not {d}")
+    kind = _KINDS.get(x.dtype)
+    if kind is None:
+        raise ValueError(f"{name} must be bfloat16 or float32, not {x.dtype}")
+    return kind
 
 
 def _index(x, name):
     """muon_index_t of a tensor of token indexes."""
-    import torch
+    kind = _INDEXES.get(x.dtype)
+    if kind is None:
+        raise ValueError(f"{name} must be int32 or int64, not {x.dtype}")
     if not x.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    d = x.dtype
-    if d == torch.int64:
-        return 1
-    if d == torch.int32:
-        return 0
-    raise ValueError(f"{name} must be int32 or int64, not {d}")
+    return kind
 
 
 def _rows(x, name):
@@ -382,10 +388,9 @@ def _rows(x, name):
 
 def _per_token(x, n, name):
     """The address of a contiguous float32 tensor of n elements (or None)."""
-    import torch
     if x is None:
         return None
-    if x.dtype != torch.float32 or x.numel() != n or not x.is_contiguous():
+    if _KINDS.get(x.dtype) != 1 or x.numel() != n or not x.is_contiguous():
         raise ValueError(f"{name} must be a contiguous float32 tensor of {n} elements")
     return x.data_ptr()
 
@@ -431,7 +436,7 @@ def embedding(table, ids, scale: float = 1.0, out=None, out_dtype=None, stream=N
     ids int32 or int64 of any shape, a negative id giving zeros.  Returns a
     tensor of ids' shape plus cols, of out_dtype (default: the table's), or
     fills `out` (2-D with any row stride, or contiguous)."""
-    import torch
+    torch = _torch()
     rows, cols, stride = _rows(table, "table")
     it, device = _index(ids, "ids"), table.get_device()
     _same_device(device, ids, out)
@@ -467,7 +472,7 @@ def embedding_grad(accum, dout, ids, param, parts=None, scale: float = 1.0,
     parts: the buffer's partition table, None where the storage index is the
     flat index; workspace: a CUDA tensor of at least
     embedding_grad_workspace(tokens, cols) bytes (default: a new one)."""
-    import torch
+    torch = _torch()
     if hasattr(param, "dtype"):
         param = (param["offset"], param["rows"], param["cols"])
     offset, rows, cols = param
@@ -529,7 +534,7 @@ def token_logprobs(logits, targets, logit_scale: float = 1.0, out=None, stream=N
     logits tokens x vocab, bf16 or fp32 (leading dimensions are joined);
     targets int32 or int64, a negative one giving 0.  Returns float32 of
     targets' shape."""
-    import torch
+    torch = _torch()
     logits, n, vocab, stride, tt = _logits(logits, targets)
     device = logits.get_device()
     _same_device(device, targets, out)
@@ -572,7 +577,7 @@ def policy_loss(logits, targets, advantages, weights, old_logp=None, ref_logp=No
     buffer), False (loss only), or a tensor to fill -- the logits themselves
     to replace them.  Returns {"stats": float32[4] (loss, policy term, KL,
     clipped weight), "logp": per token, "dlogits"}, all on the device."""
-    import torch
+    torch = _torch()
     logits, n, vocab, stride, tt = _logits(logits, targets)
     device = logits.get_device()
     _same_device(device, targets, advantages, weights, old_logp, ref_logp)
@@ -602,7 +607,7 @@ def preference_loss(logits, targets, offsets, ref_logp=None, beta: float = 0.1,
     pairs + i the other; tokens with a negative target (prompts) are left out.
     Returns {"stats": float32[4] (loss, mean margin, share of positive
     margins, weight), "margins": float32[pairs], "logp", "dlogits"}."""
-    import torch
+    torch = _torch()
     logits, n, vocab, stride, tt = _logits(logits, targets)
     places = offsets.numel()
     if places % 2 != 1:

@@ -13,7 +13,20 @@
 // nothing else has S = 0 and logp NaN.
 //
 // Maxima, sums and e are FP32 whatever the logits' type; sums over tokens are
-// FP64 (a few thousand terms, off the hot path) in a fixed order.
+// kept as two FP32 values, in a fixed order.
+//
+// Which kernel takes a row is a matter of its size, and of whether its gradient
+// is written (launch_rows_of):
+//   k_held    a cluster of blocks holds the row in shared memory: read once,
+//             gradient and all.  Bound by memory: 8192 rows of 131072 bf16 with
+//             their gradient 645 us, 6.5 TB/s of reads and writes.
+//   k_rows    one block streams the row; for long rows without a gradient
+//             (8192 of 131072 bf16: 277 us, 7.0 TB/s) and for rows too long to
+//             be held, whose gradient takes a second pass.
+//   k_given   the gradient from statistics taken before: the preference loss
+//             needs all of a pair's rows before any of their gradients, so it
+//             reads the logits twice (statistics 236 us, gradient 553 us for
+//             8192 rows of 131072 bf16, both at the copy rate).
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
@@ -33,16 +46,16 @@ using tok::Vec;
 __device__ int g_losses_err;
 
 constexpr int kRowThreads = 512;     // k_rows: threads of a row
-constexpr int kSumThreads = 1024;
+constexpr int kSumThreads = 1024;    // k_policy_sum
 constexpr int kHeldThreads = 256;    // k_held: most threads of a block,
 constexpr int kHeldBlocks = 6;       // blocks per SM,
 constexpr int kHeldVecs = 2048;      // 16-byte vectors of a block before a row takes more blocks,
 constexpr int kHeldMost = 13824;     // and at most (216 KB)
 constexpr int kHeldRow = 65536;      // bytes of a row up to which it is held without a gradient too
 constexpr int kSms = 152;
-constexpr int kPairThreads = 256;
-constexpr int kGivenThreads = 256;
-constexpr int kGivenVecs = 8 * kGivenThreads;   // 16-byte vectors of a row per block of k_given
+constexpr int kPairThreads = 1024;   // k_pairs: most threads of a pair
+constexpr int kGivenThreads = 256;   // k_given: most threads of a block
+constexpr int kGivenVecs = 8;        // 16-byte vectors of its threads
 
 int lfail(int code, const std::string& msg) {
   set_last_error(msg.c_str());
@@ -215,8 +228,11 @@ __device__ __forceinline__ void write_zeros(const Rows& a, T* drow) {
     *reinterpret_cast<uint4*>(drow + sh.head + i * Vec<T>::N) = make_uint4(0, 0, 0, 0);
 }
 
-// One block per row: a pass for (m, S), and for the gradient a second one
-// that reads the row again (from L2: the rows in flight are a few tens of MB).
+// One block per row: a pass for (m, S), four loads per thread in flight, and
+// for the gradient a second one that reads the row again.  The second pass
+// comes from L2 (the rows in flight are a few tens of MB) but is not free: the
+// SMs' traffic with L2 is the bound then (8192 rows of 131072 bf16 with their
+// gradient: 887 us).
 template <typename T, int MODE>
 __global__ void __launch_bounds__(kRowThreads) k_rows(const Rows a, const Extra x) {
   constexpr int N = Vec<T>::N;
@@ -377,8 +393,10 @@ __device__ __forceinline__ void sequence(const Rows& a, const Pairs& q, int i, i
 // One block per pair: the two sequences' sums, the margin, and c of every
 // token of the pair.
 __global__ void __launch_bounds__(kPairThreads) k_pairs(const Rows a, const Pairs q) {
+  constexpr int U = 4;   // tokens of a thread under way
   __shared__ tok::Two sh[2][kPairThreads / 32];
   __shared__ float grad;
+  const int width = blockDim.x;
   tok::wait_before();
   tok::allow_next();
   tok::Two sum[2];
@@ -386,11 +404,23 @@ __global__ void __launch_bounds__(kPairThreads) k_pairs(const Rows a, const Pair
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     sequence(a, q, blockIdx.x + j * q.n, b[j], e[j]);
-    for (int64_t t = b[j] + threadIdx.x; t < e[j]; t += kPairThreads) {
-      if (row_target(a, t) < 0) continue;
-      sum[j].add(a.logp[t]);
-      sum[j].lo += q.logp_lo[t];
-      if (q.ref_logp) sum[j].add(-q.ref_logp[t]);
+    for (int64_t t0 = b[j] + threadIdx.x; t0 < e[j]; t0 += U * width) {
+      float hi[U], lo[U], ref[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t t = t0 + u * width;
+        const int y = t < e[j] ? tok::load_index(a.targets, a.targets64, t) : -1;
+        const bool on = y >= 0 && y < a.vocab;
+        hi[u] = on ? a.logp[t] : 0.f;
+        lo[u] = on ? q.logp_lo[t] : 0.f;
+        ref[u] = on && q.ref_logp ? q.ref_logp[t] : 0.f;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        sum[j].add(hi[u]);
+        sum[j].lo += lo[u];
+        sum[j].add(-ref[u]);
+      }
     }
     sum[j].warp_sum();
     if (threadIdx.x % 32 == 0) sh[j][threadIdx.x / 32] = sum[j];
@@ -400,7 +430,7 @@ __global__ void __launch_bounds__(kPairThreads) k_pairs(const Rows a, const Pair
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       sum[j] = sh[j][0];
-      for (int w = 1; w < kPairThreads / 32; ++w) sum[j].add(sh[j][w]);
+      for (int w = 1; w < width / 32; ++w) sum[j].add(sh[j][w]);
     }
     float h;
     if (fabsf(sum[0].hi) <= FLT_MAX && fabsf(sum[1].hi) <= FLT_MAX) {
@@ -421,14 +451,15 @@ __global__ void __launch_bounds__(kPairThreads) k_pairs(const Rows a, const Pair
   const float g = grad;
 #pragma unroll
   for (int j = 0; j < 2; ++j)
-    for (int64_t t = b[j] + threadIdx.x; t < e[j]; t += kPairThreads) q.coef[t] = j ? -g : g;
+    for (int64_t t = b[j] + threadIdx.x; t < e[j]; t += width) q.coef[t] = j ? -g : g;
 }
 
-// The preference loss's statistics from the margins, by one block.
+// The preference loss's statistics from the margins, by the block's first
+// warp: one order of sums, whatever block calls it.
 __device__ __forceinline__ void pair_sum(const Pairs& q, float* stats) {
-  __shared__ tok::Two sh[4][kGivenThreads / 32];
+  if (threadIdx.x >= 32) return;
   tok::Two v[4];   // loss, margin, won, weight
-  for (int i = threadIdx.x; i < q.n; i += kGivenThreads) {
+  for (int i = threadIdx.x; i < q.n; i += 32) {
     const float w = q.weights ? q.weights[i] : 1.f;
     if (w == 0.f) continue;
     const float h = q.margins[i];
@@ -440,24 +471,26 @@ __device__ __forceinline__ void pair_sum(const Pairs& q, float* stats) {
     if (h > 0.f) v[2].add(w);
     v[3].add(w);
   }
-  cluster_sum<kGivenThreads, 4>(v, sh);
-  if (threadIdx.x == 0)
-    for (int k = 0; k < 4; ++k) stats[k] = v[k].value() / (q.weights || q.n == 0 ? 1.f : float(q.n));
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    v[k].warp_sum();
+    if (threadIdx.x == 0) stats[k] = v[k].value() / (q.weights || q.n == 0 ? 1.f : float(q.n));
+  }
 }
 
-__global__ void __launch_bounds__(kGivenThreads) k_pair_sum(const Pairs q, float* stats) {
+__global__ void __launch_bounds__(32) k_pair_sum(const Pairs q, float* stats) {
   tok::wait_before();
   pair_sum(q, stats);
 }
 
 // The gradient from (m, 1/S) and c of every row.  Block 0 sums the
-// statistics; the others take kGivenVecs vectors of a row each, the last rows
-// first: the statistics pass read those last, so some are still in L2.
-template <typename T>
-__global__ void __launch_bounds__(kGivenThreads) k_given(const Rows a, const Extra x, const Pairs q,
+// statistics; the others take kGivenVecs vectors per thread of a row each, the
+// last rows first: the statistics pass read those last, so some are in L2 yet.
+template <typename T, int W>
+__global__ void __launch_bounds__(W) k_given(const Rows a, const Extra x, const Pairs q,
                                                          float* stats, int slices) {
   constexpr int N = Vec<T>::N;
-  constexpr int NV = kGivenVecs / kGivenThreads;
+  constexpr int NV = kGivenVecs;
   tok::wait_before();
   if (blockIdx.x == 0) return pair_sum(q, stats);
   const unsigned task = gridDim.x - 1 - blockIdx.x;
@@ -473,12 +506,12 @@ __global__ void __launch_bounds__(kGivenThreads) k_given(const Rows a, const Ext
   const bool aligned =
       ((reinterpret_cast<uintptr_t>(drow) ^ reinterpret_cast<uintptr_t>(row)) & 15) == 0;
   const RowShape<T> sh(on || aligned ? row : drow, a.vocab);
-  const int i0 = slice * kGivenVecs + threadIdx.x;
+  const int i0 = slice * NV * W + threadIdx.x;
   uint4 v[NV];
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     v[k] = make_uint4(0, 0, 0, 0);
-    const int i = i0 + k * kGivenThreads;
+    const int i = i0 + k * W;
     if (on && i < sh.nvec) v[k] = __ldcs(reinterpret_cast<const uint4*>(row + sh.head + i * N));
   }
   auto one = [&](int u, float z) {
@@ -486,13 +519,13 @@ __global__ void __launch_bounds__(kGivenThreads) k_given(const Rows a, const Ext
     return !on ? 0.f : u == y ? d + g : d;
   };
   if (slice == 0) {   // the elements before and after the vectors
-    const int u = threadIdx.x < sh.head ? threadIdx.x : sh.tail0 + threadIdx.x - 32;
-    if (threadIdx.x < sh.head || (threadIdx.x >= 32 && u < a.vocab))
+    const int u = threadIdx.x < sh.head ? threadIdx.x : sh.tail0 + threadIdx.x - 8;   // fewer than 8 of either
+    if (threadIdx.x < sh.head || (threadIdx.x >= 8 && u < a.vocab))
       drow[u] = tok::from_float<T>(one(u, on ? tok::to_float(row[u]) : 0.f));
   }
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-    const int i = i0 + k * kGivenThreads;
+    const int i = i0 + k * W;
     if (i >= sh.nvec) break;
     const int v0 = sh.head + i * N;
     float f[N];
@@ -508,13 +541,22 @@ __global__ void __launch_bounds__(kGivenThreads) k_given(const Rows a, const Ext
   }
 }
 
+template <typename T>
+cudaError_t launch_given(const Rows& a, const Extra& x, const Pairs& q, float* stats, int width, int slices,
+                         cudaStream_t s) {
+  const unsigned grid = static_cast<unsigned>(a.n * slices + 1);
+  auto go = [&](auto kernel) { return launch(kernel, grid, width, 1, true, s, 0, a, x, q, stats, slices); };
+  return width == 32 ? go(k_given<T, 32>) : width == 64 ? go(k_given<T, 64>)
+         : width == 128 ? go(k_given<T, 128>) : go(k_given<T, 256>);
+}
+
 int sum_blocks(int64_t n) {
   int blocks = 1;
   while (blocks < 8 && n > blocks * int64_t(kSumThreads)) blocks *= 2;
   return blocks;
 }
 
-// ---- a row held in registers
+// ---- a row held on chip
 
 // The blocks of a cluster have started (arrive, then wait before the first
 // write to another's shared memory).  Relaxed: it orders no data.
@@ -523,7 +565,8 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 
 // Sends (m, s) to `slot` in block `rank`, counted in bytes on its barrier
 // there.  A release barrier of the whole cluster instead makes every warp wait
-// for its own earlier loads and stores (the largest stall it measured).
+// for its own earlier memory operations: 798 us instead of 649 for 8192 rows of
+// 131072 bf16 with their gradient.
 __device__ __forceinline__ void send(uint32_t slot, uint32_t bar, int rank, float m, float s) {
   asm volatile(
       "st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];" ::"r"(
@@ -594,12 +637,13 @@ __device__ __forceinline__ void zero_share(const Rows& a, T* drow, int v0, int p
 
 // A row held on chip: one cluster of blocks per row, each with `per_block` of
 // the row's 16-byte vectors in shared memory, brought there by a bulk copy.
-// The row is read from memory exactly
-// once, also where its gradient is written (reading it again from L2 costs as
-// much as from memory: the SMs' traffic with L2 is the bound then), and a row
-// is spread over up to eight SMs, so a call with few rows is short.  Blocks of
+// The row is read from memory exactly once, also where its gradient is
+// written, and a row is spread over up to eight SMs, so a call with few rows is
+// short (one row of 131072 bf16: 3.3 us, 7.3 by one block).  Blocks of
 // different rows on one SM overlap one row's loads with another's arithmetic
-// and writes; holding rows in shared memory leaves registers for six of them.
+// and writes; holding rows in shared memory leaves registers for six of them
+// (in registers, four: 764 us for 8192 rows of 131072 bf16 with their gradient,
+// 645 this way).  Instructions come next: arithmetic on pairs of values.
 template <typename T, int MODE>
 __global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) k_held(const Rows a, const Extra x, int per_block) {
   constexpr int N = Vec<T>::N;
@@ -981,7 +1025,12 @@ extern "C" int muon_preference_loss(const void* logits, int dtype, int64_t strid
     if (!std::isfinite(beta)) return lfail(MUON_ERR_INVALID, "beta must be finite");
     if (!(label_smoothing >= 0.f && label_smoothing <= 1.f))
       return lfail(MUON_ERR_INVALID, "label_smoothing must be in [0, 1]");
-    if (n_tokens * ((int64_t(vocab) + 16383) / 16384 + 1) >= 0x7fffffff)
+    const int vec = dtype == MUON_DTYPE_BF16 ? Vec<__nv_bfloat16>::N : Vec<float>::N;
+    const int nvec = std::max(1, vocab / vec);
+    int given = 32;   // k_given's threads: a short row in one block of them
+    while (given < kGivenThreads && given * kGivenVecs < nvec) given *= 2;
+    const int slices = (nvec + given * kGivenVecs - 1) / (given * kGivenVecs);
+    if (n_tokens * slices >= 0x7fffffff)
       return lfail(MUON_ERR_UNSUPPORTED, "too many tokens of a vocabulary this large for one call");
     if (n_tokens > 0 && (!workspace || misaligned(workspace, 16) || workspace_bytes < preference_bytes(n_tokens)))
       return lfail(MUON_ERR_INVALID, "workspace is NULL, misaligned or too small");
@@ -996,17 +1045,14 @@ extern "C" int muon_preference_loss(const void* logits, int dtype, int64_t strid
     const Pairs q{offsets, offsets_type == MUON_INDEX_INT64, n_pairs, ref_logp, pair_weights, beta,
                   label_smoothing, x.logp_lo, margins, dlogits ? x.coef : nullptr};
     cudaError_t e = launch_rows<kStats>(a, x, dtype, s);
-    if (e == cudaSuccess && n_pairs > 0)
-      e = launch(k_pairs, n_pairs, kPairThreads, 1, n_tokens > 0, s, 0, a, q);
-    const int vec = dtype == MUON_DTYPE_BF16 ? Vec<__nv_bfloat16>::N : Vec<float>::N;
-    const int slices = std::max(1, (vocab / vec + kGivenVecs - 1) / kGivenVecs);
+    int width = 64;   // a pair's mean sequence in one round of its threads
+    while (width < kPairThreads && int64_t(width) * 8 * n_pairs < n_tokens) width *= 2;
+    if (e == cudaSuccess && n_pairs > 0) e = launch(k_pairs, n_pairs, width, 1, n_tokens > 0, s, 0, a, q);
     if (e == cudaSuccess && dlogits && n_tokens > 0) {
-      const unsigned grid = static_cast<unsigned>(n_tokens * slices + 1);
-      e = dtype == MUON_DTYPE_BF16
-              ? launch(k_given<__nv_bfloat16>, grid, kGivenThreads, 1, true, s, 0, a, x, q, stats, slices)
-              : launch(k_given<float>, grid, kGivenThreads, 1, true, s, 0, a, x, q, stats, slices);
+      e = dtype == MUON_DTYPE_BF16 ? launch_given<__nv_bfloat16>(a, x, q, stats, given, slices, s)
+                                   : launch_given<float>(a, x, q, stats, given, slices, s);
     } else if (e == cudaSuccess) {
-      e = launch(k_pair_sum, 1, kGivenThreads, 1, n_tokens > 0 || n_pairs > 0, s, 0, q, stats);
+      e = launch(k_pair_sum, 1, 32, 1, n_tokens > 0 || n_pairs > 0, s, 0, q, stats);
     }
     return end_call((n_tokens > 0) + (n_pairs > 0) + 1, e);
   });
