@@ -152,11 +152,11 @@ constexpr int kSortBlocks = 16;      // most blocks of its cluster
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortBits = 9;
 constexpr int kSortBins = 1 << kSortBits;
-constexpr int kSortItems = 8;        // tokens a thread has in hand
+constexpr int kSortItems = 4;        // tokens a thread has in hand (8 spill at two blocks per SM)
 constexpr int kSortShared = kSortWarps * kSortBins * int(sizeof(int));
 constexpr int kRunMost = 32;         // sorted tokens per block of k_embed_sum, at most
 constexpr int kSumX = 128;           // its threads, at most
-constexpr int kJoinGroups = 8;      // k_embed_join: warps of a block, each adding every 16th partial sum
+constexpr int kJoinGroups = 8;       // k_embed_join: warps of a block, each adding every 8th partial sum
 constexpr int kFew = 1024;           // tokens up to which k_embed_few is taken
 constexpr int kFewX = 256;
 constexpr int kFillX = 256;
@@ -416,9 +416,11 @@ struct SortArgs {
 // bins (equal bins within a warp found by one ballot per bit, so no atomics;
 // match_any took 3 times as long), the counts become offsets, and each warp
 // places its tokens.  A thread fetches kSortItems tokens at a time; up to
-// 65536 tokens they stay in registers, with their ranks, from the count to the
-// placing.
-__global__ void __launch_bounds__(kSortThreads, 1) k_embed_sort(const SortArgs a) {
+// 32768 tokens they stay in registers, with their ranks, from the count to the
+// placing.  Bound by latency (two trips to L2, two scans and a cluster barrier
+// per pass): 14 us for 32768 tokens of 131072 ids, 19 by 8 blocks of twice the
+// threads.
+__global__ void __launch_bounds__(kSortThreads, 2) k_embed_sort(const SortArgs a) {
   extern __shared__ int count[];                  // kSortWarps x kSortBins
   __shared__ int total[kSortBlocks][kSortBins];   // every block's tokens per bin
   __shared__ int scan[kSortBins / 32];
@@ -540,6 +542,13 @@ __global__ void __launch_bounds__(kSortThreads, 1) k_embed_sort(const SortArgs a
   tok::wait_before();   // k_embed_fill beside it (overwrite): the next kernel waits for this one alone
 }
 
+// One block per `run` sorted tokens and block of columns: each thread adds its
+// columns of the tokens, four of them on their way at once, and at the end of a
+// run adds the sum to the row.  Bound by memory: 32768 tokens of 4096 bf16
+// columns, 12000 different ones, move 660 MB in 101 us (6.5 TB/s).  Plain loads
+// and stores of accum are faster than reductions at L2 (102 us against 118),
+// and loading pieces into shared memory by bulk copies is not (120): more of
+// them are under way, but fewer warps are there to add them.
 template <typename T, bool VEC, bool ALIGNED>
 __global__ void __launch_bounds__(kSumX) k_embed_sum(const Grad g, const __grid_constant__ Segments sg) {
   constexpr int N = Vec<T>::N;
