@@ -473,6 +473,7 @@ MUON_API int muon_newton_schulz_noalloc(const void* X, void* Y, int rows, int co
  *     may write until its work on `stream` is done).  All may be captured
  *     into CUDA graphs once each has run on the device.
  *   - n_tokens = 0 is valid (losses then write zero statistics).
+ *   - muon_profile_enable's phases are the step's: these calls are not timed.
  * ------------------------------------------------------------------- */
 typedef enum { MUON_INDEX_INT32 = 0, MUON_INDEX_INT64 = 1 } muon_index_t;
 
