@@ -14,9 +14,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
-import functools
 import os
-import struct
 
 import numpy as np
 
@@ -343,92 +341,56 @@ def newton_schulz(X, Y=None, ns_method="gram", ns_steps: int = 5, operand_mode="
 
 # ------------------------------------------------------------------ the two ends of a model
 
-_KINDS: dict = {}     # torch dtype -> muon_dtype_t, filled on first use (torch is imported late)
-_INDEXES: dict = {}   # torch dtype -> muon_index_t
+# Their arguments are looked at in C (csrc/binding.c); here are signatures and
+# whatever is not on the path of an ordinary call.
+
+_bound = None
 
 
-def _torch():
+def _native():
+    global _bound
+    if _bound is None:
+        import torch
+        L = lib()
+        try:
+            from . import _binding as b
+        except ImportError as e:
+            raise MuonError(MUON_ERR_UNSUPPORTED, f"{e}; build it with newton_schulz_fp32_gb300.build()") from e
+        names = ("muon_last_error", "muon_embedding", "muon_embedding_grad_workspace", "muon_embedding_grad",
+                 "muon_token_logprobs", "muon_policy_loss", "muon_preference_loss_workspace",
+                 "muon_preference_loss")
+        b.init(torch, getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device),
+               getattr(torch._C, "_cuda_getCurrentRawStream", lambda i: torch.cuda.current_stream(i).cuda_stream),
+               MuonError, {n: ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in names})
+        _bound = b
+    return _bound
+
+
+def _elsewhere(x, stream):
+    """A context with x's device current and `stream` (a torch stream, a
+    cudaStream_t or None) torch's current one, so that tensors made inside
+    belong to the stream the kernels run on."""
     import torch
-    if not _KINDS:
-        _INDEXES.update({torch.int32: 0, torch.int64: 1})
-        _KINDS.update({torch.bfloat16: 0, torch.float32: 1})
-    return torch
-
-
-def _dtype(x, name):
-    """muon_dtype_t of a tensor."""
-    kind = _KINDS.get(x.dtype)
-    if kind is None:
-        raise ValueError(f"{name} must be bfloat16 or float32, not {x.dtype}")
-    return kind
-
-
-def _index(x, name):
-    """muon_index_t of a tensor of token indexes."""
-    kind = _INDEXES.get(x.dtype)
-    if kind is None:
-        raise ValueError(f"{name} must be int32 or int64, not {x.dtype}")
-    if not x.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return kind
-
-
-def _rows(x, name):
-    """(rows, columns, elements between rows) of a 2-D tensor whose rows are
-    contiguous."""
-    shape = x.shape
-    if len(shape) != 2:
-        raise ValueError(f"{name} must be 2-D")
-    n, cols = shape
-    across, along = x.stride()
-    if along != 1 and cols > 1:
-        raise ValueError(f"{name}'s rows must be contiguous")
-    return n, cols, across if n > 1 else max(across, cols)
-
-
-def _per_token(x, n, name):
-    """The address of a contiguous float32 tensor of n elements (or None)."""
-    if x is None:
-        return None
-    if _KINDS.get(x.dtype) != 1 or x.numel() != n or not x.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous float32 tensor of {n} elements")
-    return x.data_ptr()
-
-
-def _same_device(index, *others):
-    for o in others:
-        if o is not None and o.get_device() != index:
-            raise ValueError("every tensor must be on one device")
-
-
-def _elsewhere(index, stream):
-    """None where device `index` is torch's current one and no stream is asked
-    for; else a context that makes them current, so that tensors made inside
-    belong to the stream the kernels run on.  Each call enters it and starts
-    again."""
-    import torch
-    if index < 0:
+    if x.device.type != "cuda":
         raise ValueError("tensors must be on a CUDA device")
-    here = torch.cuda.current_device() == index
-    if stream is None and here:
-        return None
     ctx = contextlib.ExitStack()
-    if not here:
-        ctx.enter_context(torch.cuda.device(index))
+    ctx.enter_context(torch.cuda.device(x.device))
     if stream is not None:
         if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream, device=index)
+            stream = torch.cuda.ExternalStream(stream, device=x.device)
         ctx.enter_context(torch.cuda.stream(stream))
     return ctx
 
 
-def _raw_stream(index):
-    """torch's current stream of device `index`, as a cudaStream_t."""
-    import torch
-    try:
-        return torch._C._cuda_getCurrentRawStream(index)
-    except AttributeError:
-        return torch.cuda.current_stream(index).cuda_stream
+def _call(name, first, stream, *args):
+    """A call of the C half; None from it: the device is not the current one."""
+    f = getattr(_native(), name)
+    if stream is None:
+        r = f(*args)
+        if r is not None:
+            return r
+    with _elsewhere(first, stream):
+        return f(*args)
 
 
 def embedding(table, ids, scale: float = 1.0, out=None, out_dtype=None, stream=None):
@@ -436,31 +398,7 @@ def embedding(table, ids, scale: float = 1.0, out=None, out_dtype=None, stream=N
     ids int32 or int64 of any shape, a negative id giving zeros.  Returns a
     tensor of ids' shape plus cols, of out_dtype (default: the table's), or
     fills `out` (2-D with any row stride, or contiguous)."""
-    torch = _torch()
-    rows, cols, stride = _rows(table, "table")
-    it, device = _index(ids, "ids"), table.get_device()
-    _same_device(device, ids, out)
-    ctx = _elsewhere(device, stream)
-    if ctx is not None:
-        with ctx:
-            return embedding(table, ids, scale, out, out_dtype)
-    n = ids.numel()
-    if out is None:
-        out = torch.empty((*ids.shape, cols), dtype=out_dtype or table.dtype, device=table.device)
-        ostride = cols
-    else:
-        if out.shape[-1] != cols or out.numel() != n * cols or out_dtype not in (None, out.dtype):
-            raise ValueError("out must hold ids' shape plus the table's columns")
-        if out.dim() == 2:
-            ostride = _rows(out, "out")[2]
-        elif out.is_contiguous():
-            ostride = cols
-        else:
-            raise ValueError("out must be contiguous or 2-D")
-    _check(lib().muon_embedding(table.data_ptr(), _dtype(table, "table"), stride, rows, cols,
-                                ids.data_ptr(), it, n, scale, out.data_ptr(), _dtype(out, "out"),
-                                ostride, _raw_stream(device)))
-    return out
+    return _call("embedding", table, stream, table, ids, scale, out, out_dtype)
 
 
 def embedding_grad(accum, dout, ids, param, parts=None, scale: float = 1.0,
@@ -472,46 +410,19 @@ def embedding_grad(accum, dout, ids, param, parts=None, scale: float = 1.0,
     parts: the buffer's partition table, None where the storage index is the
     flat index; workspace: a CUDA tensor of at least
     embedding_grad_workspace(tokens, cols) bytes (default: a new one)."""
-    torch = _torch()
     if hasattr(param, "dtype"):
         param = (param["offset"], param["rows"], param["cols"])
     offset, rows, cols = param
-    if accum.dtype != torch.float32 or not accum.is_contiguous():
-        raise ValueError("accum must be a contiguous float32 tensor")
     if dout.dim() != 2:
         dout = dout.reshape(-1, cols)
-    n, it, device = ids.numel(), _index(ids, "ids"), accum.get_device()
-    got, width, stride = _rows(dout, "dout")
-    if got != n or width != cols:
-        raise ValueError("dout must be tokens x cols")
-    if parts is None:
-        table, nparts = None, 0
-        if accum.numel() < offset + rows * cols:
-            raise ValueError(f"accum holds {accum.numel()} elements, the parameter ends at {offset + rows * cols}")
-    else:
+    if parts is not None:
         if getattr(parts, "dtype", None) is not PART_DTYPE:
             parts = _table(parts, PART_DTYPE)[0]
-        table, nparts = parts.tobytes(), len(parts)
-    _same_device(device, dout, ids, workspace)
-    ctx = _elsewhere(device, stream)
-    if ctx is not None:
-        with ctx:
-            return embedding_grad(accum, dout, ids, param, parts, scale, overwrite, workspace)
-    need = embedding_grad_workspace(n, cols)
-    if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=accum.device)
-    have = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(lib().muon_embedding_grad(
-        accum.data_ptr(), accum.numel(), dout.data_ptr(), _dtype(dout, "dout"), stride, ids.data_ptr(), it,
-        n, scale, 1 if overwrite else 0, _PARAM.pack(offset, rows, cols, 0, 0), table, nparts,
-        workspace.data_ptr() if have else None, have, _raw_stream(device)))
-    return accum
+        parts = parts.tobytes()
+    return _call("embedding_grad", accum, stream, accum, dout, ids, offset, rows, cols, parts, scale, overwrite,
+                 workspace)
 
 
-_PARAM = struct.Struct("<qiiii")   # one row of a PARAM_DTYPE table
-
-
-@functools.lru_cache(maxsize=256)
 def embedding_grad_workspace(n_tokens: int, cols: int) -> int:
     """Bytes of scratch embedding_grad needs."""
     b = ctypes.c_size_t()
@@ -519,53 +430,23 @@ def embedding_grad_workspace(n_tokens: int, cols: int) -> int:
     return b.value
 
 
-def _logits(logits, targets):
-    """(2-D logits, tokens, vocabulary, row stride, type of the targets)."""
-    if logits.dim() != 2:
-        logits = logits.view(-1, logits.shape[-1])
-    n, vocab, stride = _rows(logits, "logits")
-    if targets.numel() != n:
-        raise ValueError("one target per row of logits")
-    return logits, n, vocab, stride, _index(targets, "targets")
-
-
 def token_logprobs(logits, targets, logit_scale: float = 1.0, out=None, stream=None):
     """log softmax(logit_scale * logits) at the targets (muon_token_logprobs):
     logits tokens x vocab, bf16 or fp32 (leading dimensions are joined);
     targets int32 or int64, a negative one giving 0.  Returns float32 of
     targets' shape."""
-    torch = _torch()
-    logits, n, vocab, stride, tt = _logits(logits, targets)
-    device = logits.get_device()
-    _same_device(device, targets, out)
-    ctx = _elsewhere(device, stream)
-    if ctx is not None:
-        with ctx:
-            return token_logprobs(logits, targets, logit_scale, out)
-    if out is None:
-        out = torch.empty(targets.shape, dtype=torch.float32, device=logits.device)
-    _check(lib().muon_token_logprobs(logits.data_ptr(), _dtype(logits, "logits"), stride, n, vocab,
-                                     targets.data_ptr(), tt, logit_scale, _per_token(out, n, "out"),
-                                     _raw_stream(device)))
-    return out
+    if logits.dim() != 2:
+        logits = logits.view(-1, logits.shape[-1])
+    return _call("token_logprobs", logits, stream, logits, targets, logit_scale, out)
 
 
-def _dlogits(logits, n, vocab, stride, dlogits):
-    """The gradient's buffer and its row stride: as given, a new one (True;
-    with the logits' row stride, so that its rows are aligned as theirs), or
-    none (False)."""
-    import torch
-    if dlogits is True:
-        d = torch.empty((n, stride), dtype=logits.dtype, device=logits.device)
-        return d if stride == vocab else d[:, :vocab], stride
-    if dlogits is False or dlogits is None:
-        return None, 0
-    if dlogits.dim() != 2:
-        dlogits = dlogits.view(-1, dlogits.shape[-1])
-    if dlogits.dtype != logits.dtype or dlogits.shape != logits.shape:
-        raise ValueError("dlogits must match the logits' shape and type")
-    _same_device(logits.get_device(), dlogits)
-    return dlogits, _rows(dlogits, "dlogits")[2]
+def _flat(logits, dlogits):
+    """Logits, and the gradient's buffer if one is given, as matrices."""
+    if logits.dim() != 2:
+        logits = logits.view(-1, logits.shape[-1])
+        if not (dlogits is None or isinstance(dlogits, bool)):
+            dlogits = dlogits.view(-1, dlogits.shape[-1])
+    return logits, dlogits
 
 
 def policy_loss(logits, targets, advantages, weights, old_logp=None, ref_logp=None,
@@ -577,25 +458,9 @@ def policy_loss(logits, targets, advantages, weights, old_logp=None, ref_logp=No
     buffer), False (loss only), or a tensor to fill -- the logits themselves
     to replace them.  Returns {"stats": float32[4] (loss, policy term, KL,
     clipped weight), "logp": per token, "dlogits"}, all on the device."""
-    torch = _torch()
-    logits, n, vocab, stride, tt = _logits(logits, targets)
-    device = logits.get_device()
-    _same_device(device, targets, advantages, weights, old_logp, ref_logp)
-    ctx = _elsewhere(device, stream)
-    if ctx is not None:
-        with ctx:
-            return policy_loss(logits, targets, advantages, weights, old_logp, ref_logp, clip_low,
-                               clip_high, kl_coef, logit_scale, dlogits)
-    d, dstride = _dlogits(logits, n, vocab, stride, dlogits)
-    logp = torch.empty(targets.shape, dtype=torch.float32, device=logits.device)
-    stats = torch.empty(4, dtype=torch.float32, device=logits.device)
-    _check(lib().muon_policy_loss(
-        logits.data_ptr(), _dtype(logits, "logits"), stride, n, vocab, targets.data_ptr(), tt,
-        _per_token(advantages, n, "advantages"), _per_token(weights, n, "weights"),
-        _per_token(old_logp, n, "old_logp"), _per_token(ref_logp, n, "ref_logp"), clip_low, clip_high,
-        kl_coef, logit_scale, stats.data_ptr(), logp.data_ptr(), None if d is None else d.data_ptr(),
-        dstride, _raw_stream(device)))
-    return {"stats": stats, "logp": logp, "dlogits": d}
+    logits, dlogits = _flat(logits, dlogits)
+    return _call("policy_loss", logits, stream, logits, targets, advantages, weights, old_logp, ref_logp, clip_low,
+                 clip_high, kl_coef, logit_scale, dlogits)
 
 
 def preference_loss(logits, targets, offsets, ref_logp=None, beta: float = 0.1,
@@ -607,34 +472,11 @@ def preference_loss(logits, targets, offsets, ref_logp=None, beta: float = 0.1,
     pairs + i the other; tokens with a negative target (prompts) are left out.
     Returns {"stats": float32[4] (loss, mean margin, share of positive
     margins, weight), "margins": float32[pairs], "logp", "dlogits"}."""
-    torch = _torch()
-    logits, n, vocab, stride, tt = _logits(logits, targets)
-    places = offsets.numel()
-    if places % 2 != 1:
-        raise ValueError("offsets must hold 2 * pairs + 1 positions")
-    pairs, ot, device = places // 2, _index(offsets, "offsets"), logits.get_device()
-    _same_device(device, targets, offsets, ref_logp, pair_weights, workspace)
-    ctx = _elsewhere(device, stream)
-    if ctx is not None:
-        with ctx:
-            return preference_loss(logits, targets, offsets, ref_logp, beta, label_smoothing,
-                                   pair_weights, logit_scale, dlogits, workspace)
-    d, dstride = _dlogits(logits, n, vocab, stride, dlogits)
-    logp = torch.empty(targets.shape, dtype=torch.float32, device=logits.device)
-    stats = torch.empty(4, dtype=torch.float32, device=logits.device)
-    margins = torch.empty(pairs, dtype=torch.float32, device=logits.device)
-    if workspace is None:
-        workspace = torch.empty(preference_loss_workspace(n), dtype=torch.uint8, device=logits.device)
-    _check(lib().muon_preference_loss(
-        logits.data_ptr(), _dtype(logits, "logits"), stride, n, vocab, targets.data_ptr(), tt,
-        offsets.data_ptr(), ot, pairs, _per_token(ref_logp, n, "ref_logp"),
-        _per_token(pair_weights, pairs, "pair_weights"), beta, label_smoothing, logit_scale,
-        stats.data_ptr(), margins.data_ptr(), logp.data_ptr(), None if d is None else d.data_ptr(), dstride,
-        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _raw_stream(device)))
-    return {"stats": stats, "margins": margins, "logp": logp, "dlogits": d}
+    logits, dlogits = _flat(logits, dlogits)
+    return _call("preference_loss", logits, stream, logits, targets, offsets, ref_logp, beta, label_smoothing,
+                 pair_weights, logit_scale, dlogits, workspace)
 
 
-@functools.lru_cache(maxsize=256)
 def preference_loss_workspace(n_tokens: int) -> int:
     """Bytes of scratch preference_loss needs."""
     b = ctypes.c_size_t()

@@ -4,7 +4,8 @@ Each CUDA translation unit is compiled in parallel into ``_build/`` and the
 objects are linked into ``newton_schulz_fp32_gb300/libmuon.so`` (static CUDA
 runtime; the driver API is reached through the runtime's entry-point query,
 so the library links no libcuda).  A rebuild happens only when a source or
-header is newer than the library.
+header is newer than the library.  The C half of the Python binding
+(``csrc/binding.c``) is compiled with gcc into ``_binding.so`` beside it.
 """
 from __future__ import annotations
 
@@ -14,6 +15,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -36,6 +38,20 @@ def nvcc() -> str:
     if not os.path.exists(path):
         raise RuntimeError("nvcc not found: the CUDA 13 toolkit is required to build libmuon")
     return path
+
+
+def _build_binding() -> None:
+    """The C half of the Python binding (_binding.so), against this Python."""
+    src, out = os.path.join(CSRC, "binding.c"), os.path.join(HERE, "_binding.so")
+    deps = [src, os.path.join(ROOT, "include", "muon.h"), __file__]
+    if os.path.exists(out) and all(os.path.getmtime(d) <= os.path.getmtime(out) for d in deps):
+        return
+    cmd = [shutil.which("gcc") or "cc", "-O2", "-std=c11", "-shared", "-fPIC", "-I",
+           sysconfig.get_paths()["include"], src, "-o", out + ".tmp"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"compiling the Python binding failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(out + ".tmp", out)
 
 
 def sources():
@@ -67,6 +83,7 @@ def build(force: bool = False, verbose: bool = False, extra=(), debug: bool = Fa
     """Compile every CUDA source for sm_103a and link libmuon.so (with
     debug: libmuon_debug.so, built with MUON_DEBUG)."""
     lib, build_dir = (LIB_DEBUG, BUILD_DEBUG) if debug else (LIB, BUILD)
+    _build_binding()
     if not force and not _stale(lib):
         return lib
     os.makedirs(build_dir, exist_ok=True)
