@@ -7,10 +7,10 @@
 //     logp = s (z_y - m) - log S
 // and for a loss that depends on the row through logp alone,
 //     dz_v = s c (1[v = y] - e_v / S),   c = d loss / d logp.
-// Subtracting m before scaling keeps rows of the type's lowest value and of
-// minus infinities right without a branch: the running maximum starts at the
-// lowest finite FP32 value, so minus infinity always gives e = 0, and a row of
-// nothing else has S = 0 and logp NaN.
+// (Any m near the maximum serves.)  Subtracting m before scaling keeps rows of
+// the type's lowest value and of minus infinities right without a branch: m
+// starts at the lowest finite FP32 value, so minus infinity always gives e = 0,
+// and a row of nothing else has S = 0 and logp NaN.
 //
 // Maxima, sums and e are FP32 whatever the logits' type; sums over tokens are
 // kept as two FP32 values, in a fixed order.
@@ -45,13 +45,13 @@ using tok::Vec;
 
 __device__ int g_losses_err;
 
-constexpr int kRowThreads = 512;     // k_rows: threads of a row
+constexpr int kRowLoads = 8;         // k_rows: 16-byte loads of a thread in flight
 constexpr int kSumThreads = 1024;    // k_policy_sum
 constexpr int kHeldThreads = 256;    // k_held: most threads of a block,
 constexpr int kHeldBlocks = 6;       // blocks per SM,
 constexpr int kHeldVecs = 2048;      // 16-byte vectors of a block before a row takes more blocks,
 constexpr int kHeldMost = 13824;     // and at most (216 KB)
-constexpr int kHeldRow = 65536;      // bytes of a row up to which it is held without a gradient too
+constexpr int kHeldRow = 8192;       // bytes of a row up to which it is held without a gradient too
 constexpr int kSms = 152;
 constexpr int kPairThreads = 1024;   // k_pairs: most threads of a pair
 constexpr int kGivenThreads = 256;   // k_given: most threads of a block
@@ -78,6 +78,8 @@ struct Rows {
   const void* targets;
   float scale;     // s
   float scale2;    // s log2(e): exp(s x) = 2^(scale2 x)
+  float first, second;   // the same as a product
+  float slack;     // 8 / s
   float* logp;
   void* dlogits;   // NULL: no gradient
   int64_t dstride;
@@ -135,18 +137,20 @@ __device__ __forceinline__ int row_target(const Rows& a, int64_t t) {
   return y < 0 ? -1 : y;
 }
 
-// Joins the softmax statistics (m, s) of two parts of a row.
-__device__ __forceinline__ void join(float& m, float& s, float m2, float s2, float scale2) {
+// Joins the softmax statistics (m, s) of two parts of a row.  Three joins, one
+// in another, end in log S: by expf, since the errors of ex2.approx lie on one
+// side (2e-8 on average).
+__device__ __forceinline__ void join(float& m, float& s, float m2, float s2, float scale) {
   const float top = fmaxf(m, m2);
-  s = s * ex2((m - top) * scale2) + s2 * ex2((m2 - top) * scale2);
+  s = s * expf((m - top) * scale) + s2 * expf((m2 - top) * scale);
   m = top;
 }
 
-__device__ __forceinline__ void warp_join(float& m, float& s, float scale2) {
+__device__ __forceinline__ void warp_join(float& m, float& s, float scale) {
   float top = m;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  s *= ex2((m - top) * scale2);
+  s *= expf((m - top) * scale);
   m = top;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
@@ -162,6 +166,94 @@ struct RowShape {
     if (head > vocab) head = vocab;
     nvec = (vocab - head) / Vec<T>::N;
     tail0 = head + nvec * Vec<T>::N;
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ float vec_max(const uint4& v) {
+  if constexpr (sizeof(T) == 2) {
+    auto pair = [](uint32_t u) { return *reinterpret_cast<__nv_bfloat162*>(&u); };
+    const __nv_bfloat162 m = __hmax2(__hmax2(pair(v.x), pair(v.y)), __hmax2(pair(v.z), pair(v.w)));
+    return fmaxf(__low2float(m), __high2float(m));
+  } else {
+    return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)),
+                 fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+  }
+}
+
+// Two FP32 lanes per instruction.
+__device__ __forceinline__ uint64_t two(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void split(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// e of 16 bytes of logits, in pairs: 2^((z - m) scale2).
+template <typename T>
+__device__ __forceinline__ void vec_exp(const uint4& v, uint64_t minus_m, uint64_t scale2,
+                                        uint64_t (&e)[Vec<T>::N / 2]) {
+  float f[Vec<T>::N];
+  Vec<T>::unpack(v, f);
+#pragma unroll
+  for (int j = 0; j < Vec<T>::N / 2; ++j) {
+    float lo, hi;
+    split(mul2(add2(two(f[2 * j], f[2 * j + 1]), minus_m), scale2), lo, hi);
+    e[j] = two(ex2(lo), ex2(hi));
+  }
+}
+
+// A thread's running sum of e = exp(s (z - m)).  m is not its maximum but one
+// that it reached: it moves when a logit is past it by more than 8 / s, which
+// FP32 has room for, so that most threads take it from their first vector and
+// never rescale (a warp whose lanes follow the maximum rescales at nearly every
+// vector: 279 us became 324 with rescales exact enough to be worth having).
+// Any m serves in the formulas above.  The exponents are formed in two products
+// (Rows::first, second), see make_rows.
+template <typename T>
+struct Softmax {
+  float m = -FLT_MAX;
+  uint64_t s[2] = {0, 0};
+  template <int U>
+  __device__ __forceinline__ void add(const uint4 (&v)[U], const Rows& a) {
+    float top = vec_max<T>(v[0]);
+#pragma unroll
+    for (int u = 1; u < U; ++u) top = fmaxf(top, vec_max<T>(v[u]));
+    if (top - m > a.slack) {
+      const float k = expf((m - top) * a.scale);
+      s[0] = mul2(s[0], two(k, k));
+      s[1] = mul2(s[1], two(k, k));
+      m = top;
+    }
+    const uint64_t mm = two(-m, -m), p = two(a.first, a.first), q = two(a.second, a.second);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float f[Vec<T>::N];
+      Vec<T>::unpack(v[u], f);
+#pragma unroll
+      for (int j = 0; j < Vec<T>::N / 2; ++j) {
+        float lo, hi;
+        split(mul2(mul2(add2(two(f[2 * j], f[2 * j + 1]), mm), p), q), lo, hi);
+        s[j & 1] = add2(s[j & 1], two(ex2(lo), ex2(hi)));
+      }
+    }
+  }
+  __device__ __forceinline__ float sum() const {
+    float lo, hi;
+    split(add2(s[0], s[1]), lo, hi);
+    return lo + hi;
   }
 };
 
@@ -228,15 +320,15 @@ __device__ __forceinline__ void write_zeros(const Rows& a, T* drow) {
     *reinterpret_cast<uint4*>(drow + sh.head + i * Vec<T>::N) = make_uint4(0, 0, 0, 0);
 }
 
-// One block per row: a pass for (m, S), four loads per thread in flight, and
-// for the gradient a second one that reads the row again.  The second pass
+// One block of W threads per row: a pass for (m, S), kRowLoads loads per thread
+// in flight, and for the gradient a second one that reads the row again.  The second pass
 // comes from L2 (the rows in flight are a few tens of MB) but is not free: the
 // SMs' traffic with L2 is the bound then (8192 rows of 131072 bf16 with their
 // gradient: 887 us).
-template <typename T, int MODE>
-__global__ void __launch_bounds__(kRowThreads) k_rows(const Rows a, const Extra x) {
+template <typename T, int MODE, int W>
+__global__ void __launch_bounds__(W) k_rows(const Rows a, const Extra x) {
   constexpr int N = Vec<T>::N;
-  __shared__ float sm[kRowThreads / 32], ss[kRowThreads / 32];
+  __shared__ float sm[W / 32], ss[W / 32];
   tok::allow_next();
   const int64_t t = blockIdx.x;
   const T* row = static_cast<const T*>(a.logits) + t * a.stride;
@@ -254,24 +346,24 @@ __global__ void __launch_bounds__(kRowThreads) k_rows(const Rows a, const Extra 
     return;
   }
   const RowShape<T> sh(row, a.vocab);
-  float m = -FLT_MAX, s = 0.f;
-  auto take = [&](float z) { join(m, s, z, 1.f, a.scale2); };
-  if (threadIdx.x < sh.head) take(tok::to_float(row[threadIdx.x]));
-  for (int v = sh.tail0 + threadIdx.x; v < a.vocab; v += kRowThreads) take(tok::to_float(row[v]));
-#pragma unroll 4
-  for (int i = threadIdx.x; i < sh.nvec; i += kRowThreads) {
-    float f[N];
-    Vec<T>::unpack(*reinterpret_cast<const uint4*>(row + sh.head + i * N), f);
-    float top = m;
+  Softmax<T> part;
+  int i = threadIdx.x;
+  for (; i + (kRowLoads - 1) * W < sh.nvec; i += kRowLoads * W) {
+    uint4 v[kRowLoads];
 #pragma unroll
-    for (int k = 0; k < N; ++k) top = fmaxf(top, f[k]);
-    s *= ex2((m - top) * a.scale2);
-    m = top;
-#pragma unroll
-    for (int k = 0; k < N; ++k) s += ex2((f[k] - m) * a.scale2);
+    for (int u = 0; u < kRowLoads; ++u)
+      v[u] = *reinterpret_cast<const uint4*>(row + sh.head + (i + u * W) * N);
+    part.add(v, a);
   }
+  for (; i < sh.nvec; i += W) {
+    const uint4 v[1] = {*reinterpret_cast<const uint4*>(row + sh.head + i * N)};
+    part.add(v, a);
+  }
+  float m = part.m, s = part.sum();
+  if (threadIdx.x < sh.head) join(m, s, tok::to_float(row[threadIdx.x]), 1.f, a.scale);
+  if (sh.tail0 + int(threadIdx.x) < a.vocab) join(m, s, tok::to_float(row[sh.tail0 + threadIdx.x]), 1.f, a.scale);
   const float zy = tok::to_float(row[y]);
-  warp_join(m, s, a.scale2);
+  warp_join(m, s, a.scale);
   if (threadIdx.x % 32 == 0) {
     sm[threadIdx.x / 32] = m;
     ss[threadIdx.x / 32] = s;
@@ -279,7 +371,7 @@ __global__ void __launch_bounds__(kRowThreads) k_rows(const Rows a, const Extra 
   __syncthreads();
   m = sm[0];
   s = ss[0];
-  for (int w = 1; w < kRowThreads / 32; ++w) join(m, s, sm[w], ss[w], a.scale2);
+  for (int w = 1; w < W / 32; ++w) join(m, s, sm[w], ss[w], a.scale);
   const float logp = a.scale * (zy - m) - logf(s);
   if (threadIdx.x == 0) {
     a.logp[t] = logp;
@@ -575,52 +667,6 @@ __device__ __forceinline__ void send(uint32_t slot, uint32_t bar, int rank, floa
       : "memory");
 }
 
-template <typename T>
-__device__ __forceinline__ float vec_max(const uint4& v) {
-  if constexpr (sizeof(T) == 2) {
-    auto pair = [](uint32_t u) { return *reinterpret_cast<__nv_bfloat162*>(&u); };
-    const __nv_bfloat162 m = __hmax2(__hmax2(pair(v.x), pair(v.y)), __hmax2(pair(v.z), pair(v.w)));
-    return fmaxf(__low2float(m), __high2float(m));
-  } else {
-    return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)),
-                 fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
-  }
-}
-
-// Two FP32 lanes per instruction.
-__device__ __forceinline__ uint64_t two(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ void split(uint64_t v, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
-// e of 16 bytes of logits, in pairs: 2^((z - m) scale2).
-template <typename T>
-__device__ __forceinline__ void vec_exp(const uint4& v, uint64_t minus_m, uint64_t scale2,
-                                        uint64_t (&e)[Vec<T>::N / 2]) {
-  float f[Vec<T>::N];
-  Vec<T>::unpack(v, f);
-#pragma unroll
-  for (int j = 0; j < Vec<T>::N / 2; ++j) {
-    float lo, hi;
-    split(mul2(add2(two(f[2 * j], f[2 * j + 1]), minus_m), scale2), lo, hi);
-    e[j] = two(ex2(lo), ex2(hi));
-  }
-}
-
 // Zeros in vectors [v0, v1) of a row, and around them in block 0.
 template <typename T>
 __device__ __forceinline__ void zero_share(const Rows& a, T* drow, int v0, int per_block, int rank) {
@@ -702,39 +748,23 @@ __global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) k_held(const Rows a
   }
   const float zs = single >= 0 ? tok::to_float(row[single]) : -INFINITY;
   const float zy = warp == 0 ? tok::to_float(row[y]) : 0.f;
-  const uint64_t ss = two(a.scale2, a.scale2);
-  float m = -FLT_MAX, s;
-  {
-    uint64_t acc[2] = {0, 0};
-    tc::mbar_wait(tc::smem_u32(&full), 0, &stopped, &g_losses_err, 1);
+  Softmax<T> share;
+  tc::mbar_wait(tc::smem_u32(&full), 0, &stopped, &g_losses_err, 1);
 #pragma unroll 2
-    for (int i = threadIdx.x; i < mine; i += blockDim.x) {
-      const uint4 v = held[i];
-      const float top = vec_max<T>(v);
-      if (top > m) {
-        const float k = ex2((m - top) * a.scale2);
-        acc[0] = mul2(acc[0], two(k, k));
-        acc[1] = mul2(acc[1], two(k, k));
-        m = top;
-      }
-      uint64_t e[N / 2];
-      vec_exp<T>(v, two(-m, -m), ss, e);
-#pragma unroll
-      for (int j = 0; j < N / 2; ++j) acc[j & 1] = add2(acc[j & 1], e[j]);
-    }
-    float lo, hi;
-    split(add2(acc[0], acc[1]), lo, hi);
-    s = lo + hi;
+  for (int i = threadIdx.x; i < mine; i += blockDim.x) {
+    const uint4 v[1] = {held[i]};
+    share.add(v, a);
   }
-  if (single >= 0) join(m, s, zs, 1.f, a.scale2);
-  warp_join(m, s, a.scale2);
+  float m = share.m, s = share.sum();
+  if (single >= 0) join(m, s, zs, 1.f, a.scale);
+  warp_join(m, s, a.scale);
   if (lane == 0) warp_part[warp] = make_float2(m, s);
   __syncthreads();
   if (warp == 0) {
     const bool on = lane < int(blockDim.x) / 32;
     m = on ? warp_part[lane].x : -FLT_MAX;
     s = on ? warp_part[lane].y : 0.f;
-    warp_join(m, s, a.scale2);
+    warp_join(m, s, a.scale);
   }
   if (c > 1) {
     cluster_wait();
@@ -744,7 +774,7 @@ __global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) k_held(const Rows a
       const float2 p = lane < c ? part[lane] : make_float2(-FLT_MAX, 0.f);
       m = p.x;
       s = p.y;
-      warp_join(m, s, a.scale2);
+      warp_join(m, s, a.scale);
     }
   }
   if (warp == 0 && lane == 0) {
@@ -777,7 +807,7 @@ __global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) k_held(const Rows a
   }
   const bool aligned =
       ((reinterpret_cast<uintptr_t>(drow) ^ reinterpret_cast<uintptr_t>(row)) & 15) == 0;
-  const uint64_t mm = two(-m, -m), gg = two(ga, ga);
+  const uint64_t mm = two(-m, -m), ss = two(a.scale2, a.scale2), gg = two(ga, ga);
 #pragma unroll 2
   for (int i = threadIdx.x; i < mine; i += blockDim.x) {
     const int v0 = sh.head + (base + i) * N;
@@ -837,11 +867,19 @@ template <typename T, int MODE>
 cudaError_t launch_rows_of(const Rows& a, const Extra& x, cudaStream_t s) {
   const Hold h = hold_of(a.n, a.vocab, Vec<T>::N);
   const bool grad = MODE == kPolicy && a.dlogits;
-  // Without a gradient, many long rows are read faster by streams of loads
-  // (8192 rows of 131072 bf16: 279 us, 6.9 TB/s).
-  const bool stream = !grad && a.n >= 2 * kSms && int64_t(a.vocab) * int64_t(sizeof(T)) > kHeldRow;
+  // Without a gradient many rows are read faster by streams of loads, all but
+  // the shortest (8192 rows of 131072 bf16 266 us, held 350; 16384 of 16384 73
+  // us, held 82; 32768 of 2000 39 us, held 37).
+  const int64_t bytes = int64_t(a.vocab) * int64_t(sizeof(T));
+  const bool stream = !grad && a.n >= 2 * kSms && bytes > kHeldRow;
   if (h.c && !stream && a.n * h.c <= 0x7fffffff) return launch_held<T, MODE>(a, x, h, s);
-  return launch(k_rows<T, MODE>, static_cast<unsigned>(a.n), kRowThreads, 1, false, s, 0, a, x);
+  // A thread's loads in flight are to be a small part of its row: for rows of
+  // 8192 / 32768 / 131072 bf16, blocks of 64 threads take 39 / 141 / - us, of 128
+  // 42 / 136 / 284 and of 256 68 / 138 / 266.
+  auto go = [&](auto kernel, int w) { return launch(kernel, static_cast<unsigned>(a.n), w, 1, false, s, 0, a, x); };
+  return bytes <= 16384    ? go(k_rows<T, MODE, 64>, 64)
+         : bytes <= 131072 ? go(k_rows<T, MODE, 128>, 128)
+                           : go(k_rows<T, MODE, 256>, 256);
 }
 
 template <int MODE>
@@ -900,7 +938,23 @@ Rows make_rows(const void* logits, int64_t stride, int64_t n, int vocab, const v
   a.targets64 = targets_type == MUON_INDEX_INT64;
   a.targets = targets;
   a.scale = scale;
-  a.scale2 = static_cast<float>(double(scale) * 1.4426950408889634);
+  const double scale2 = double(scale) * 1.4426950408889634;
+  a.scale2 = static_cast<float>(scale2);
+  a.slack = static_cast<float>(std::min(8.0 / double(scale), 1e38));
+  // Rounded to FP32, s log2(e) makes every exponent too large or too small by
+  // up to 6e-8 of itself, in every row alike, and sums of log-probabilities over
+  // a sequence show it (3e-7 a token at s = 0.8).  Of the factors k / 64 one
+  // leaves a second factor that is exact to about 1e-9.
+  double best = 1.0;
+  for (int k = 64; k < 128; ++k) {
+    const double first = k / 64.0, second = static_cast<float>(scale2 / first);
+    const double off = std::fabs(first * second / scale2 - 1.0);
+    if (off < best) {
+      best = off;
+      a.first = static_cast<float>(first);
+      a.second = static_cast<float>(second);
+    }
+  }
   a.logp = logp;
   a.dlogits = d;
   a.dstride = dstride;
