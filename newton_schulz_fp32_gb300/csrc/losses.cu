@@ -49,6 +49,7 @@ constexpr int kRowLoads = 8;         // k_rows: 16-byte loads of a thread in fli
 constexpr int kSumThreads = 1024;    // k_policy_sum
 constexpr int kHeldThreads = 256;    // k_held: most threads of a block,
 constexpr int kHeldBlocks = 6;       // blocks per SM,
+constexpr int kHeldLoads = 2;        // vectors a thread adds at once,
 constexpr int kHeldVecs = 2048;      // 16-byte vectors of a block before a row takes more blocks,
 constexpr int kHeldMost = 13824;     // and at most (216 KB)
 constexpr int kHeldRow = 8192;       // bytes of a row up to which it is held without a gradient too
@@ -750,9 +751,15 @@ __global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) k_held(const Rows a
   const float zy = warp == 0 ? tok::to_float(row[y]) : 0.f;
   Softmax<T> share;
   tc::mbar_wait(tc::smem_u32(&full), 0, &stopped, &g_losses_err, 1);
-#pragma unroll 2
-  for (int i = threadIdx.x; i < mine; i += blockDim.x) {
-    const uint4 v[1] = {held[i]};
+  int at = threadIdx.x;
+  for (; at + (kHeldLoads - 1) * int(blockDim.x) < mine; at += kHeldLoads * blockDim.x) {
+    uint4 v[kHeldLoads];
+#pragma unroll
+    for (int u = 0; u < kHeldLoads; ++u) v[u] = held[at + u * blockDim.x];
+    share.add(v, a);
+  }
+  for (; at < mine; at += blockDim.x) {
+    const uint4 v[1] = {held[at]};
     share.add(v, a);
   }
   float m = share.m, s = share.sum();
