@@ -327,9 +327,9 @@ struct __align__(16) Step {
 // Zeros in the whole parameter (overwrite).  One resident wave of blocks, so
 // that the sort is scheduled beside it and costs no time of its own.  The rows
 // of tokens are written twice.  Zeroing only the other rows beside
-// k_embed_sum, once the sort is done, took 55 us instead of 51 for 5003 tokens
+// k_embed_sum, once the sort is done, took 55 us instead of 53 for 5003 tokens
 // of a 50001 x 1001 table, and 183 instead of 202 for 16384 of a 131072 x 2048
-// one, with twice the code.
+// one, with twice the code (zeroing alone: 30 us and 165 us).
 __global__ void __launch_bounds__(kFillX) k_embed_fill(float* accum, const __grid_constant__ Segments sg) {
   tok::allow_next();
   for (int i = 0; i < sg.n; ++i) {
@@ -545,7 +545,7 @@ __global__ void __launch_bounds__(kSortThreads, 2) k_embed_sort(const SortArgs a
 // One block per `run` sorted tokens and block of columns: each thread adds its
 // columns of the tokens, four of them on their way at once, and at the end of a
 // run adds the sum to the row.  Bound by memory: 32768 tokens of 4096 bf16
-// columns, 12000 different ones, move 660 MB in 101 us (6.5 TB/s).  Plain loads
+// columns, 12000 different ones, move 660 MB in 99 us (6.6 TB/s).  Plain loads
 // and stores of accum are faster than reductions at L2 (102 us against 118),
 // and loading pieces into shared memory by bulk copies is not (120): more of
 // them are under way, but fewer warps are there to add them.
@@ -687,7 +687,7 @@ struct Workspace {
 
 // Sorted tokens per block of k_embed_sum: 32, so that few runs leave partial
 // sums, or down to 8 where that would leave too few blocks to fill the SMs
-// (5003 tokens of 1001 columns: 36 us at 8, 107 at 32).
+// (20000 tokens of 1001 bf16 columns, the whole call: 81 us at 8, 98 at 16, 158 at 32).
 int run_of(int64_t n, int cols) {
   const int64_t slabs = (int64_t(cols) + 1023) / 1024;
   int run = kRunMost;

@@ -20,12 +20,12 @@
 //   k_held    a cluster of blocks holds the row in shared memory: read once,
 //             gradient and all.  Bound by memory: 8192 rows of 131072 bf16 with
 //             their gradient 645 us, 6.5 TB/s of reads and writes.
-//   k_rows    one block streams the row; for long rows without a gradient
-//             (8192 of 131072 bf16: 277 us, 7.0 TB/s) and for rows too long to
+//   k_rows    one block streams the row; for many rows without a gradient
+//             (8192 of 131072 bf16: 264 us, 7.3 TB/s) and for rows too long to
 //             be held, whose gradient takes a second pass.
 //   k_given   the gradient from statistics taken before: the preference loss
 //             needs all of a pair's rows before any of their gradients, so it
-//             reads the logits twice (statistics 236 us, gradient 553 us for
+//             reads the logits twice (statistics 224 us, gradient 555 us for
 //             8192 rows of 131072 bf16, both at the copy rate).
 #include <algorithm>
 #include <cfloat>
