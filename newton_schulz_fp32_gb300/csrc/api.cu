@@ -19,7 +19,6 @@
 #include <vector>
 
 #include "muon_internal.h"
-#include "token_ops.cuh"
 
 namespace muon {
 namespace {
@@ -1305,10 +1304,6 @@ void count_launches(int n) {
   g_cnt.launches_total += n;
 }
 
-uint64_t g_token_devices = 0;
-void note_token_device(int dev) { g_token_devices |= uint64_t(1) << (dev & 63); }
-uint64_t token_devices() { return g_token_devices; }
-
 int validate_tables(const muon_param_t* params, int nparams, const muon_partition_t* parts,
                     int nparts) {
   Layout L;
@@ -1826,10 +1821,6 @@ extern "C" int muon_device_error(void) {
   for (auto& sp : g_single) check(sp->err);
   const int na = noalloc_take_device_error();
   if (na) worst = na;
-  const int em = embedding_take_device_error();
-  if (em) worst = em;
-  const int lo = losses_take_device_error();
-  if (lo) worst = lo;
   return worst;
 }
 
