@@ -405,8 +405,9 @@ def embedding_grad(accum, dout, ids, param, parts=None, scale: float = 1.0,
                    overwrite: bool = False, workspace=None, stream=None):
     """The lookup's gradient added to (or, with overwrite, put in place of)
     the parameter's elements of the flat FP32 buffer `accum`
-    (muon_embedding_grad).  dout: tokens x cols, bf16 or fp32; ids as given to
-    embedding(); param: (offset, rows, cols) or a row of a PARAM_DTYPE table;
+    (muon_embedding_grad).  dout: tokens x cols, bf16 or fp32 (leading
+    dimensions are joined, by a copy where their layout needs one); ids as
+    given to embedding(); param: (offset, rows, cols) or a row of a PARAM_DTYPE table;
     parts: the buffer's partition table, None where the storage index is the
     flat index; workspace: a CUDA tensor of at least
     embedding_grad_workspace(tokens, cols) bytes (default: a new one)."""
@@ -414,7 +415,11 @@ def embedding_grad(accum, dout, ids, param, parts=None, scale: float = 1.0,
         param = (param["offset"], param["rows"], param["cols"])
     offset, rows, cols = param
     if dout.dim() != 2:
-        dout = dout.reshape(-1, cols)
+        if stream is None:
+            dout = dout.reshape(-1, cols)
+        else:   # reshape may copy: on the stream of the call, which then owns the copy
+            with _elsewhere(dout, stream):
+                dout = dout.reshape(-1, cols)
     if parts is not None:
         if getattr(parts, "dtype", None) is not PART_DTYPE:
             parts = _table(parts, PART_DTYPE)[0]

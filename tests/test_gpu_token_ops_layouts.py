@@ -1,0 +1,84 @@
+"""Embedding and loss calls on tensors as programs have them: batches of
+sequences, slices of them, a workspace of the caller's, other streams."""
+import pytest
+
+import newton_schulz_fp32_gb300 as nsg
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def torch():
+    t = pytest.importorskip("torch")
+    if not t.cuda.is_available():
+        pytest.skip("no CUDA device")
+    nsg.build()
+    return t
+
+
+def batch(torch, B, S, D, V, dtype, seed):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    ids = torch.randint(0, V, (B, S), generator=gen, device="cuda")
+    return ids, torch.randn((B, S + 1, D), generator=gen, device="cuda").to(dtype)
+
+
+@pytest.mark.parametrize("shape", [(3, 5, 8), (4, 300, 33), (2, 2000, 64)])
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+def test_gradient_of_batches_and_slices(torch, shape, dtype):
+    """dout of three dimensions: as it is, without its last step (no matrix in
+    memory), and in the order sequence, batch; the same bits as the matrix."""
+    B, S, D = shape
+    V = 50
+    ids, dx = batch(torch, B, S, D, V, getattr(torch, dtype), S)
+    for part, index in ((dx[:, :-1].contiguous(), ids), (dx[:, :-1], ids),
+                        (dx[:, :-1].transpose(0, 1), ids.t().contiguous())):
+        want, got = torch.zeros(V * D, device="cuda"), torch.zeros(V * D, device="cuda")
+        nsg.embedding_grad(want, part.reshape(-1, D).clone(), index.reshape(-1), (0, V, D))
+        nsg.embedding_grad(got, part, index, (0, V, D))
+        assert torch.equal(got, want)
+    assert nsg.device_error() == 0
+
+
+@pytest.mark.parametrize("S", [300, 2000])
+def test_copied_gradient_on_another_stream(torch, S):
+    """The current stream is kept busy after the side stream has what it needs:
+    a copy made on the current one would be read before it is there."""
+    B, D, V = 2, 64, 50
+    ids, dx = batch(torch, B, S, D, V, torch.float32, S)
+    want = torch.zeros(V * D, device="cuda")
+    nsg.embedding_grad(want, dx[:, :-1].reshape(-1, D).clone(), ids, (0, V, D))
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        got = torch.zeros(V * D, device="cuda")
+        side.wait_stream(torch.cuda.current_stream())
+        busy = torch.randn((4096, 4096), device="cuda")
+        for _ in range(20):
+            busy = busy @ busy * 1e-2
+        nsg.embedding_grad(got, dx[:, :-1], ids, (0, V, D), stream=stream)
+        side.synchronize()
+        assert torch.equal(got, want)
+        torch.cuda.synchronize()
+
+
+def test_logits_of_batches(torch):
+    """Logits and targets of three and two dimensions: the same bits as matrices."""
+    B, S, V = 3, 7, 1001
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    z = torch.randn((B, S, V), generator=gen, device="cuda").to(torch.bfloat16)
+    y = torch.randint(0, V, (B, S), generator=gen, device="cuda")
+    adv, w, old = (torch.rand((B, S), generator=gen, device="cuda") for _ in range(3))
+    flat = z.view(-1, V)
+    lp = nsg.token_logprobs(z, y)
+    assert lp.shape == (B, S) and torch.equal(lp.view(-1), nsg.token_logprobs(flat, y.view(-1)))
+    a = nsg.policy_loss(z, y, adv, w, old - 7)
+    b = nsg.policy_loss(flat, y.view(-1), adv.view(-1), w.view(-1), old.view(-1) - 7)
+    assert a["dlogits"].shape == (B * S, V) and torch.equal(a["dlogits"], b["dlogits"])
+    assert torch.equal(a["stats"], b["stats"])
+    offsets = torch.tensor([0, 7, 21], device="cuda")
+    c, d = nsg.preference_loss(z, y, offsets), nsg.preference_loss(flat, y.view(-1), offsets)
+    assert torch.equal(c["dlogits"], d["dlogits"]) and torch.equal(c["margins"], d["margins"])
+    with pytest.raises(RuntimeError):
+        nsg.token_logprobs(z[:, :-1], y[:, :-1].contiguous())   # no matrix in memory: refused
+    own = z.clone()
+    nsg.policy_loss(own, y, adv, w, old - 7, dlogits=own)
+    assert torch.equal(own.view(-1, V), a["dlogits"])
