@@ -373,13 +373,15 @@ def _elsewhere(x, stream):
     import torch
     if x.device.type != "cuda":
         raise ValueError("tensors must be on a CUDA device")
-    ctx = contextlib.ExitStack()
-    ctx.enter_context(torch.cuda.device(x.device))
-    if stream is not None:
-        if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream, device=x.device)
-        ctx.enter_context(torch.cuda.stream(stream))
-    return ctx
+    with contextlib.ExitStack() as ctx:
+        ctx.enter_context(torch.cuda.device(x.device))
+        if stream is not None:
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream, device=x.device)
+            elif stream.device.index != x.device.index:
+                raise ValueError("the stream is of another device than the tensors")
+            ctx.enter_context(torch.cuda.stream(stream))
+        return ctx.pop_all()
 
 
 def _call(name, first, stream, *args):
@@ -390,7 +392,10 @@ def _call(name, first, stream, *args):
         if r is not None:
             return r
     with _elsewhere(first, stream):
-        return f(*args)
+        r = f(*args)
+    if r is None:
+        raise MuonError(MUON_ERR_CUDA, f"{name}: the tensors' device could not be made the current one")
+    return r
 
 
 def embedding(table, ids, scale: float = 1.0, out=None, out_dtype=None, stream=None):

@@ -41,3 +41,30 @@ def test_a_gradient_that_is_a_matrix_in_memory_is_not_copied(m):
     nsg.embedding_grad(*grad_inputs(m, dx), stream=5)
     (_, call), = m.calls
     assert m.copies == [] and call[2] == dx.data_ptr() and call[-1] == 5
+
+
+def test_a_stream_of_another_device_is_refused(m):
+    """Nothing may be skipped in silence: the call computes, or it raises."""
+    args = grad_inputs(m, torch.zeros(4, 8))
+    z, y = m.tensor(torch.zeros(4, 8)), m.tensor(torch.zeros(4, dtype=torch.int64))
+    a = m.tensor(torch.zeros(4))
+    offsets = m.tensor(torch.zeros(3, dtype=torch.int64))
+    away = m.on_stream(7, 1)
+    for call in (lambda: nsg.embedding_grad(*args, stream=away), lambda: nsg.embedding(z, y, stream=away),
+                 lambda: nsg.token_logprobs(z, y, stream=away), lambda: nsg.policy_loss(z, y, a, a, stream=away),
+                 lambda: nsg.preference_loss(z, y, offsets, stream=away)):
+        with pytest.raises(ValueError, match="another device"):
+            call()
+        assert (m.device, m.stream) == (0, 0)
+    assert m.calls == []
+
+
+def test_tensors_of_another_device_than_the_current_one(m):
+    """The call makes their device current, with its stream or the given one."""
+    accum, dout, ids, param = grad_inputs(m, torch.zeros(4, 8))
+    for t in (accum, dout, ids):
+        t.index, t.device.index = 1, 1
+    assert nsg.embedding_grad(accum, dout, ids, param) is accum
+    assert nsg.embedding_grad(accum, dout, ids, param, stream=m.on_stream(7, 1)) is accum
+    assert nsg.embedding_grad(accum, dout, ids, param, stream=9) is accum
+    assert [c[1][-1] or 0 for c in m.calls] == [0, 7, 9] and m.device == 0
