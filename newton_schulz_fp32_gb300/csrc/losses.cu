@@ -656,15 +656,16 @@ int sum_blocks(int64_t n) {
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
 
-// Sends (m, s) to `slot` in block `rank`, counted in bytes on its barrier
-// there.  A release barrier of the whole cluster instead makes every warp wait
+// Sends (m, s) and z to `slot` in block `rank`, counted in bytes on its
+// barrier there.  A release barrier of the whole cluster instead makes every warp wait
 // for its own earlier memory operations: 798 us instead of 649 for 8192 rows of
 // 131072 bf16 with their gradient.
-__device__ __forceinline__ void send(uint32_t slot, uint32_t bar, int rank, float m, float s) {
+__device__ __forceinline__ void send(uint32_t slot, uint32_t bar, int rank, float m, float s, float z) {
   asm volatile(
-      "st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];" ::"r"(
+      "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
           tc::mapa_shared(slot, rank)),
-      "r"(__float_as_uint(m)), "r"(__float_as_uint(s)), "r"(tc::mapa_shared(bar, rank))
+      "r"(__float_as_uint(m)), "r"(__float_as_uint(s)), "r"(__float_as_uint(z)), "r"(0),
+      "r"(tc::mapa_shared(bar, rank))
       : "memory");
 }
 
@@ -697,7 +698,7 @@ __global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) k_held(const Rows a
   extern __shared__ __align__(128) uint4 held[];
   __shared__ __align__(8) uint64_t full, joined;
   __shared__ float2 warp_part[kHeldThreads / 32];
-  __shared__ __align__(8) float2 part[8];   // (m, s) of every block of the cluster
+  __shared__ __align__(16) float4 part[8];   // (m, s, the target's logit or minus infinity) of every block
   __shared__ float2 out;         // (-g / S, g)
   __shared__ float out_m;
   __shared__ int stopped;
@@ -730,7 +731,7 @@ __global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) k_held(const Rows a
     tc::mbar_init(tc::smem_u32(&full), 1);
     tc::mbar_init(tc::smem_u32(&joined), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    if (c > 1) tc::mbar_expect_tx(tc::smem_u32(&joined), c * 8);
+    if (c > 1) tc::mbar_expect_tx(tc::smem_u32(&joined), c * 16);
     tc::mbar_expect_tx(tc::smem_u32(&full), mine * 16);
     if (mine > 0)
       asm volatile(
@@ -748,7 +749,12 @@ __global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) k_held(const Rows a
     else if (threadIdx.x >= 8 && sh.tail0 + int(threadIdx.x) - 8 < a.vocab) single = sh.tail0 + threadIdx.x - 8;   // fewer than 8 of either
   }
   const float zs = single >= 0 ? tok::to_float(row[single]) : -INFINITY;
-  const float zy = warp == 0 ? tok::to_float(row[y]) : 0.f;
+  // The target's logit is read by the block that writes its gradient alone, and
+  // goes to the others with (m, s): the sums' exchange orders no other load, so
+  // another block's could come after that write where the gradient replaces
+  // the logits.
+  const int owner = y < sh.head || y >= sh.tail0 ? 0 : (y - sh.head) / N / per_block;
+  float zy = warp == 0 && rank == owner ? tok::to_float(row[y]) : -INFINITY;
   Softmax<T> share;
   tc::mbar_wait(tc::smem_u32(&full), 0, &stopped, &g_losses_err, 1);
   int at = threadIdx.x;
@@ -776,12 +782,15 @@ __global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) k_held(const Rows a
   if (c > 1) {
     cluster_wait();
     if (warp == 0) {
-      if (lane < c) send(tc::smem_u32(&part[rank]), tc::smem_u32(&joined), lane, m, s);
+      if (lane < c) send(tc::smem_u32(&part[rank]), tc::smem_u32(&joined), lane, m, s, zy);
       tc::mbar_wait_cluster(tc::smem_u32(&joined), 0, &stopped, &g_losses_err, 4);
-      const float2 p = lane < c ? part[lane] : make_float2(-FLT_MAX, 0.f);
+      const float4 p = lane < c ? part[lane] : make_float4(-FLT_MAX, 0.f, -INFINITY, 0.f);
       m = p.x;
       s = p.y;
+      zy = p.z;   // a NaN is lost here, but is in s as well
       warp_join(m, s, a.scale);
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) zy = fmaxf(zy, __shfl_xor_sync(0xffffffffu, zy, o));
     }
   }
   if (warp == 0 && lane == 0) {

@@ -82,3 +82,26 @@ def test_logits_of_batches(torch):
     own = z.clone()
     nsg.policy_loss(own, y, adv, w, old - 7, dlogits=own)
     assert torch.equal(own.view(-1, V), a["dlogits"])
+
+
+@pytest.mark.parametrize("V", [131072, 50001, 33000])
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("T", [1, 64, 700])
+def test_policy_gradient_in_place_of_rows_over_several_blocks(torch, V, dtype, T):
+    """The target anywhere in a row that several blocks hold, the gradient in
+    place of the logits: the same bits as beside them."""
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    z = torch.randn((T, V), generator=gen, device="cuda").to(getattr(torch, dtype))
+    borders = [0, 1, 7, 8, V - 1, V - 2, V - 9] + [k * V // 8 + d for k in range(1, 8) for d in (-9, -1, 0, 1, 8)]
+    y = torch.tensor([borders[t % len(borders)] for t in range(T)], device="cuda")
+    adv, w = torch.randn(T, generator=gen, device="cuda"), torch.rand(T, generator=gen, device="cuda")
+    w[T // 3] = 0 if T > 1 else 1
+    lp = nsg.token_logprobs(z, y)
+    old = lp - 0.1 * torch.randn(T, generator=gen, device="cuda")
+    want = nsg.policy_loss(z, y, adv, w, old, lp, kl_coef=0.1)
+    for _ in range(3):
+        own = z.clone()
+        got = nsg.policy_loss(own, y, adv, w, old, lp, kl_coef=0.1, dlogits=own)
+        assert torch.equal(own, want["dlogits"])
+        assert torch.equal(got["logp"], want["logp"]) and torch.equal(got["stats"], want["stats"])
+    assert nsg.device_error() == 0
