@@ -414,7 +414,7 @@ def embedding_grad(accum, dout, ids, param, parts=None, scale: float = 1.0,
     dimensions are joined, by a copy where their layout needs one); ids as
     given to embedding(); param: (offset, rows, cols) or a row of a PARAM_DTYPE table;
     parts: the buffer's partition table, None where the storage index is the
-    flat index; workspace: a CUDA tensor of at least
+    flat index; workspace: a contiguous CUDA tensor of at least
     embedding_grad_workspace(tokens, cols) bytes (default: a new one)."""
     if hasattr(param, "dtype"):
         param = (param["offset"], param["rows"], param["cols"])
@@ -480,6 +480,8 @@ def preference_loss(logits, targets, offsets, ref_logp=None, beta: float = 0.1,
     (muon_preference_loss).  offsets: 2 * pairs + 1 positions (int32 or int64,
     on the device); sequence i < pairs is pair i's preferred answer, sequence
     pairs + i the other; tokens with a negative target (prompts) are left out.
+    workspace: a contiguous CUDA tensor of at least
+    preference_loss_workspace(tokens) bytes (default: a new one).
     Returns {"stats": float32[4] (loss, mean margin, share of positive
     margins, weight), "margins": float32[pairs], "logp", "dlogits"}."""
     logits, dlogits = _flat(logits, dlogits)

@@ -133,6 +133,15 @@ static int per_token(PyObject* t, long long n, int optional, const char* name, v
   return contiguous(t, name) ? -1 : address(t, out);
 }
 
+/* Where a caller's scratch lies and how many bytes it has. */
+static int scratch(PyObject* t, void** out, long long* bytes) {
+  long long n, size;
+  if (contiguous(t, "workspace") || ask(t, g.s_numel, &n) || ask(t, g.s_element_size, &size) || address(t, out))
+    return -1;
+  *bytes = n * size;
+  return 0;
+}
+
 /* 1: all on torch's current device, 0: all on another one, -1: an error.  *device: that device. */
 static int placed(PyObject* const* tensors, int n, long long* device) {
   if (ask(tensors[0], g.s_get_device, device)) return -1;
@@ -326,16 +335,15 @@ static PyObject* py_embedding_grad(PyObject* self, PyObject* const* a, Py_ssize_
   size_t need;
   if (done(g.embedding_grad_workspace(n, (int)cols, &need))) return NULL;
   if (work) {
-    long long size;
-    if (ask(work, g.s_numel, &bytes) || ask(work, g.s_element_size, &size)) return NULL;
-    bytes *= size;
+    if (scratch(work, &pw, &bytes)) return NULL;
     Py_INCREF(work);
   } else if (need > 0) {
     work = make_flat((long long)need, g.uint8, accum);
     if (!work) return NULL;
     bytes = (long long)need;
+    if (address(work, &pw)) goto fail;
   }
-  if ((work && address(work, &pw)) || address(dout, &pd) || address(ids, &pi) || stream_of(device, &stream)) goto fail;
+  if (address(dout, &pd) || address(ids, &pi) || stream_of(device, &stream)) goto fail;
   int rc;
   Py_BEGIN_ALLOW_THREADS
   rc = g.embedding_grad(pa, elems, pd, dk, d.stride, pi, ik, n, scale, overwrite, &param,
@@ -502,17 +510,15 @@ static PyObject* py_preference_loss(PyObject* self, PyObject* const* a, Py_ssize
   if (here == 0) Py_RETURN_NONE;
   if (done(g.preference_loss_workspace(r.n, &need)) || gradient(a[8], a[0], &r, &d, &pd, &dstride)) return NULL;
   if (work) {
-    long long size;
     Py_INCREF(work);
-    if (ask(work, g.s_numel, &bytes) || ask(work, g.s_element_size, &size)) goto end;
-    bytes *= size;
+    if (scratch(work, &pk, &bytes)) goto end;
   } else {
-    if (!(work = make_flat((long long)need, g.uint8, a[0]))) goto end;
+    if (!(work = make_flat((long long)need, g.uint8, a[0])) || address(work, &pk)) goto end;
     bytes = (long long)need;
   }
   if (!(logp = make_like(a[1], g.fp32, a[0])) || !(stats = make_flat(4, g.fp32, a[0])) ||
       !(margins = make_flat(pairs, g.fp32, a[0])) || address(logp, &pl) || address(stats, &ps) ||
-      address(margins, &pm) || address(work, &pk) || stream_of(device, &stream))
+      address(margins, &pm) || stream_of(device, &stream))
     goto end;
   int rc;
   Py_BEGIN_ALLOW_THREADS

@@ -105,3 +105,34 @@ def test_policy_gradient_in_place_of_rows_over_several_blocks(torch, V, dtype, T
         assert torch.equal(own, want["dlogits"])
         assert torch.equal(got["logp"], want["logp"]) and torch.equal(got["stats"], want["stats"])
     assert nsg.device_error() == 0
+
+
+@pytest.mark.parametrize("T", [1025, 5000, 40000])
+def test_workspace_of_the_callers(torch, T):
+    """A workspace of exactly the bytes asked for: the same bits as with a new
+    one, and nothing written past it; a byte less is refused."""
+    D, V = 24, 700
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    ids = (700 ** torch.rand(T, generator=gen, device="cuda") - 1).long()
+    dout = torch.randn((T, D), generator=gen, device="cuda")
+    z = torch.randn((T, 65), generator=gen, device="cuda")
+    offsets = torch.tensor([0, T // 3, T // 2, T - 5, T], device="cuda")
+    y = torch.randint(-9, 65, (T,), generator=gen, device="cuda")
+    want = torch.zeros(V * D, device="cuda")
+    nsg.embedding_grad(want, dout, ids, (0, V, D))
+    loss = nsg.preference_loss(z, y, offsets)
+    for need, call in ((nsg.embedding_grad_workspace(T, D), "grad"), (nsg.preference_loss_workspace(T), "loss")):
+        whole = torch.full((need + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+        got = torch.zeros(V * D, device="cuda")
+        if call == "grad":
+            nsg.embedding_grad(got, dout, ids, (0, V, D), workspace=whole[:need])
+            assert torch.equal(got, want)
+            with pytest.raises(nsg.MuonError, match="workspace"):
+                nsg.embedding_grad(got, dout, ids, (0, V, D), workspace=whole[:need - 1])
+        else:
+            again = nsg.preference_loss(z, y, offsets, workspace=whole[:need])
+            assert all(torch.equal(again[k], loss[k]) for k in loss)
+            with pytest.raises(nsg.MuonError, match="workspace"):
+                nsg.preference_loss(z, y, offsets, workspace=whole[:need - 1])
+        assert bool((whole[need:] == 0xA5).all())
+    assert nsg.device_error() == 0

@@ -68,3 +68,25 @@ def test_tensors_of_another_device_than_the_current_one(m):
     assert nsg.embedding_grad(accum, dout, ids, param, stream=m.on_stream(7, 1)) is accum
     assert nsg.embedding_grad(accum, dout, ids, param, stream=9) is accum
     assert [c[1][-1] or 0 for c in m.calls] == [0, 7, 9] and m.device == 0
+
+
+def test_a_workspace_has_to_be_contiguous(m):
+    """An expanded tensor has less memory than elements; between the elements
+    of a slice lies what is somebody else's."""
+    args = grad_inputs(m, torch.zeros(2000, 8))
+    z, y = m.tensor(torch.zeros(4, 8)), m.tensor(torch.zeros(4, dtype=torch.int64))
+    offsets = m.tensor(torch.zeros(3, dtype=torch.int64))
+    need = max(nsg.embedding_grad_workspace(2000, 8), nsg.preference_loss_workspace(4))
+    whole = torch.empty(2 * need, dtype=torch.uint8)
+    for bad in (torch.empty(1, dtype=torch.uint8).expand(need), whole[::2]):
+        work = m.tensor(bad)
+        with pytest.raises(ValueError, match="workspace must be contiguous"):
+            nsg.embedding_grad(*args, workspace=work)
+        with pytest.raises(ValueError, match="workspace must be contiguous"):
+            nsg.preference_loss(z, y, offsets, workspace=work)
+    assert m.calls == []
+    work = m.tensor(whole[:need].view(torch.int32) if need % 4 == 0 else whole[:need])
+    nsg.embedding_grad(*args, workspace=work)
+    nsg.preference_loss(z, y, offsets, workspace=work)
+    (_, g), (_, p) = m.calls
+    assert g[-3] == p[-3] == whole.data_ptr() and g[-2] == p[-2] == need
