@@ -323,9 +323,9 @@ static PyObject* py_embedding_grad(PyObject* self, PyObject* const* a, Py_ssize_
   char* table = NULL;
   Py_ssize_t table_bytes = 0;
   if (a[6] != Py_None && PyBytes_AsStringAndSize(a[6], &table, &table_bytes)) return NULL;
-  if (!table && param.offset >= 0 && rows >= 0 && elems < param.offset + rows * cols) {
-    PyErr_Format(PyExc_ValueError, "accum holds %lld elements, the parameter ends at %lld", elems,
-                 (long long)param.offset + rows * cols);
+  if (!table && param.offset >= 0 && rows >= 0 && elems - rows * cols < param.offset) {
+    PyErr_Format(PyExc_ValueError, "accum holds %lld elements, the parameter begins at %lld and has %lld", elems,
+                 (long long)param.offset, rows * cols);
     return NULL;
   }
   PyObject* tensors[4] = {accum, dout, ids, work};

@@ -15,6 +15,7 @@
 // So every sum has one fixed order, and the work is balanced whatever the ids.
 #include <algorithm>
 #include <cmath>
+#include <limits>
 #include <string>
 #include <vector>
 
@@ -721,6 +722,8 @@ Workspace workspace_of(int64_t n, int cols) {
 int segments_of(const muon_param_t& p, const muon_partition_t* parts, int nparts, Segments* out) {
   const int64_t numel = int64_t(p.rows) * p.cols;
   out->numel = numel;
+  if (p.offset > std::numeric_limits<int64_t>::max() - numel)
+    return efail(MUON_ERR_INVALID, "the parameter's end is past the range of an index");
   if (nparts == 0) {
     out->n = 1;
     out->rel[0] = 0;
@@ -730,7 +733,8 @@ int segments_of(const muon_param_t& p, const muon_partition_t* parts, int nparts
   std::vector<std::pair<int64_t, int64_t>> st;
   for (int i = 0; i < nparts; ++i) {
     const muon_partition_t& q = parts[i];
-    if (q.flat_begin < 0 || q.flat_end < q.flat_begin || q.storage_offset < 0)
+    if (q.flat_begin < 0 || q.flat_end < q.flat_begin || q.storage_offset < 0 ||
+        q.storage_offset > std::numeric_limits<int64_t>::max() - (q.flat_end - q.flat_begin))
       return efail(MUON_ERR_INVALID, "partition " + std::to_string(i) + " has a bad range");
     if (i > 0 && parts[i - 1].flat_end > q.flat_begin)
       return efail(MUON_ERR_INVALID, "partitions must be sorted by flat_begin and must not overlap (at " +
