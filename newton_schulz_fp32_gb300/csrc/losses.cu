@@ -168,6 +168,13 @@ struct RowShape {
     nvec = (vocab - head) / Vec<T>::N;
     tail0 = head + nvec * Vec<T>::N;
   }
+  // This thread's element before or after the vectors, or -1: fewer than 8 of
+  // either.  (A vocabulary may end at the last int: tail0 + a thread's number
+  // need not fit in one.)
+  __device__ __forceinline__ int single(int vocab) const {
+    const int k = int(threadIdx.x) - 8;
+    return int(threadIdx.x) < head ? int(threadIdx.x) : k >= 0 && k < vocab - tail0 ? tail0 + k : -1;
+  }
 };
 
 template <typename T>
@@ -292,10 +299,8 @@ __device__ __forceinline__ void write_grad(const Rows& a, const T* row, T* drow,
   };
   const bool aligned =
       ((reinterpret_cast<uintptr_t>(drow) ^ reinterpret_cast<uintptr_t>(row)) & 15) == 0;
-  if (threadIdx.x < sh.head)
-    drow[threadIdx.x] = tok::from_float<T>(one(threadIdx.x, tok::to_float(row[threadIdx.x])));
-  for (int v = sh.tail0 + threadIdx.x; v < a.vocab; v += blockDim.x)
-    drow[v] = tok::from_float<T>(one(v, tok::to_float(row[v])));
+  const int u = sh.single(a.vocab);
+  if (u >= 0) drow[u] = tok::from_float<T>(one(u, tok::to_float(row[u])));
   for (int i = threadIdx.x; i < sh.nvec; i += blockDim.x) {
     const int v0 = sh.head + i * N;
     float f[N];
@@ -314,9 +319,8 @@ __device__ __forceinline__ void write_grad(const Rows& a, const T* row, T* drow,
 template <typename T>
 __device__ __forceinline__ void write_zeros(const Rows& a, T* drow) {
   const RowShape<T> sh(drow, a.vocab);
-  const T zero = tok::from_float<T>(0.f);
-  if (threadIdx.x < sh.head) drow[threadIdx.x] = zero;
-  for (int v = sh.tail0 + threadIdx.x; v < a.vocab; v += blockDim.x) drow[v] = zero;
+  const int u = sh.single(a.vocab);
+  if (u >= 0) drow[u] = tok::from_float<T>(0.f);
   for (int i = threadIdx.x; i < sh.nvec; i += blockDim.x)
     *reinterpret_cast<uint4*>(drow + sh.head + i * Vec<T>::N) = make_uint4(0, 0, 0, 0);
 }
@@ -362,7 +366,7 @@ __global__ void __launch_bounds__(W) k_rows(const Rows a, const Extra x) {
   }
   float m = part.m, s = part.sum();
   if (threadIdx.x < sh.head) join(m, s, tok::to_float(row[threadIdx.x]), 1.f, a.scale);
-  if (sh.tail0 + int(threadIdx.x) < a.vocab) join(m, s, tok::to_float(row[sh.tail0 + threadIdx.x]), 1.f, a.scale);
+  if (int(threadIdx.x) < a.vocab - sh.tail0) join(m, s, tok::to_float(row[sh.tail0 + threadIdx.x]), 1.f, a.scale);
   const float zy = tok::to_float(row[y]);
   warp_join(m, s, a.scale);
   if (threadIdx.x % 32 == 0) {
@@ -612,9 +616,8 @@ __global__ void __launch_bounds__(W) k_given(const Rows a, const Extra x, const 
     return !on ? 0.f : u == y ? d + g : d;
   };
   if (slice == 0) {   // the elements before and after the vectors
-    const int u = threadIdx.x < sh.head ? threadIdx.x : sh.tail0 + threadIdx.x - 8;   // fewer than 8 of either
-    if (threadIdx.x < sh.head || (threadIdx.x >= 8 && u < a.vocab))
-      drow[u] = tok::from_float<T>(one(u, on ? tok::to_float(row[u]) : 0.f));
+    const int u = sh.single(a.vocab);
+    if (u >= 0) drow[u] = tok::from_float<T>(one(u, on ? tok::to_float(row[u]) : 0.f));
   }
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
@@ -673,11 +676,8 @@ __device__ __forceinline__ void send(uint32_t slot, uint32_t bar, int rank, floa
 template <typename T>
 __device__ __forceinline__ void zero_share(const Rows& a, T* drow, int v0, int per_block, int rank) {
   const RowShape<T> sh(drow, a.vocab);
-  const T zero = tok::from_float<T>(0.f);
-  if (rank == 0) {
-    if (threadIdx.x < sh.head) drow[threadIdx.x] = zero;
-    else if (threadIdx.x >= 8 && sh.tail0 + int(threadIdx.x) - 8 < a.vocab) drow[sh.tail0 + threadIdx.x - 8] = zero;
-  }
+  const int u = rank == 0 ? sh.single(a.vocab) : -1;
+  if (u >= 0) drow[u] = tok::from_float<T>(0.f);
   const int v1 = min(sh.nvec, v0 + per_block);
   for (int i = v0 + threadIdx.x; i < v1; i += blockDim.x)
     __stcs(reinterpret_cast<uint4*>(drow + sh.head + i * Vec<T>::N), make_uint4(0, 0, 0, 0));
@@ -743,11 +743,7 @@ __global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) k_held(const Rows a
   __syncthreads();
   if (c > 1) cluster_arrive();   // waited for before the first write to another block
   // elements before and after the vectors: one per thread of the first block
-  int single = -1;
-  if (rank == 0) {
-    if (threadIdx.x < sh.head) single = threadIdx.x;
-    else if (threadIdx.x >= 8 && sh.tail0 + int(threadIdx.x) - 8 < a.vocab) single = sh.tail0 + threadIdx.x - 8;   // fewer than 8 of either
-  }
+  const int single = rank == 0 ? sh.single(a.vocab) : -1;
   const float zs = single >= 0 ? tok::to_float(row[single]) : -INFINITY;
   // The target's logit is read by the block that writes its gradient alone, and
   // goes to the others with (m, s): the sums' exchange orders no other load, so
