@@ -672,6 +672,14 @@ __device__ __forceinline__ void send(uint32_t slot, uint32_t bar, int rank, floa
       : "memory");
 }
 
+// After a wait that ran out, once more and for longer than any other block's
+// waits before its stores: no copy or remote store may find its block gone.
+__device__ __noinline__ void wait_again(uint32_t bar) {
+  const unsigned long long t0 = tc::globaltimer();
+  while (!tc::mbar_try_wait(bar, 0) && tc::globaltimer() - t0 < 2 * tc::kTimeoutNs) {
+  }
+}
+
 // Zeros in vectors [v0, v1) of a row, and around them in block 0.
 template <typename T>
 __device__ __forceinline__ void zero_share(const Rows& a, T* drow, int v0, int per_block, int rank) {
@@ -779,7 +787,8 @@ __global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) k_held(const Rows a
     cluster_wait();
     if (warp == 0) {
       if (lane < c) send(tc::smem_u32(&part[rank]), tc::smem_u32(&joined), lane, m, s, zy);
-      tc::mbar_wait_cluster(tc::smem_u32(&joined), 0, &stopped, &g_losses_err, 4);
+      if (!tc::mbar_wait_cluster(tc::smem_u32(&joined), 0, &stopped, &g_losses_err, 4))
+        wait_again(tc::smem_u32(&joined));
       const float4 p = lane < c ? part[lane] : make_float4(-FLT_MAX, 0.f, -INFINITY, 0.f);
       m = p.x;
       s = p.y;
@@ -805,11 +814,9 @@ __global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) k_held(const Rows a
       out_m = m;
     }
   }
-  if (MODE != kPolicy || !drow) {
-    __syncthreads();   // no thread leaves while the others' values are still on their way here
-    return;
-  }
-  __syncthreads();
+  __syncthreads();   // no thread leaves while the others' values are still on their way here
+  if (stopped) return wait_again(tc::smem_u32(&full));
+  if (MODE != kPolicy || !drow) return;
   const float ga = out.x, g = out.y;
   m = out_m;
   if (g == 0.f) return zero_share<T>(a, drow, base, per_block, rank);
