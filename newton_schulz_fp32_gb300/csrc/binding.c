@@ -379,17 +379,19 @@ static int loss_rows(PyObject* logits, PyObject* targets, Rows* r) {
 }
 
 /* The gradient's buffer (a new reference or NULL): as given, a new one (True;
- * with the logits' row stride, so that its rows are aligned as theirs), or
- * none (False, None). */
+ * its rows lie against 16 bytes as the logits' do, without what lies between
+ * those), or none (False, None). */
 static int gradient(PyObject* asked, PyObject* logits, const Rows* r, PyObject** out, void** p, long long* stride) {
   *out = NULL;
   *p = NULL;
   *stride = 0;
   if (asked == Py_False || asked == Py_None) return 0;
   if (asked == Py_True) {
-    PyObject* d = make(Py_BuildValue("(LL)", r->z.rows, r->z.stride), r->kind ? g.fp32 : g.bf16, logits);
-    if (d && r->z.stride != r->z.cols) {
-      PyObject* part = PyObject_CallMethod(d, "narrow", "iiL", 1, 0, r->z.cols);
+    const long long cols = r->z.cols, gap = r->z.rows > 1 && r->z.stride > cols ? r->z.stride - cols : 0;
+    const long long wide = cols + gap % (r->kind ? 4 : 8);
+    PyObject* d = make(Py_BuildValue("(LL)", r->z.rows, wide), r->kind ? g.fp32 : g.bf16, logits);
+    if (d && wide != cols) {
+      PyObject* part = PyObject_CallMethod(d, "narrow", "iiL", 1, 0, cols);
       Py_DECREF(d);
       d = part;
     }
@@ -398,7 +400,7 @@ static int gradient(PyObject* asked, PyObject* logits, const Rows* r, PyObject**
       return -1;
     }
     *out = d;
-    *stride = r->z.stride;
+    *stride = wide;
     return 0;
   }
   Shape s;

@@ -136,3 +136,23 @@ def test_workspace_of_the_callers(torch, T):
                 nsg.preference_loss(z, y, offsets, workspace=whole[:need - 1])
         assert bool((whole[need:] == 0xA5).all())
     assert nsg.device_error() == 0
+
+
+@pytest.mark.parametrize("V", [1000, 1001, 40003])
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+def test_logits_of_the_last_step(torch, V, dtype):
+    """logits[:, -1] of a batch of sequences: the new gradient takes its own
+    rows' memory, and has the bits of a contiguous copy's."""
+    B, S = 5, 9
+    gen = torch.Generator(device="cuda").manual_seed(V)
+    z = torch.randn((B, S, V), generator=gen, device="cuda").to(getattr(torch, dtype))[:, -1]
+    y = torch.randint(0, V, (B,), generator=gen, device="cuda")
+    adv, w = (torch.rand(B, generator=gen, device="cuda") for _ in range(2))
+    offsets = torch.tensor([0, 2, 5], device="cuda")
+    for call in (lambda x: nsg.policy_loss(x, y, adv, w), lambda x: nsg.preference_loss(x, y, offsets)):
+        got = call(z)["dlogits"]
+        assert got.untyped_storage().nbytes() < B * (V + 8) * got.element_size()
+        laid = torch.empty_strided((B, V), got.stride(), dtype=z.dtype, device="cuda").copy_(z)
+        if z.data_ptr() % 16 == 0:
+            assert torch.equal(got, call(laid)["dlogits"])
+    assert nsg.device_error() == 0

@@ -90,3 +90,29 @@ def test_a_workspace_has_to_be_contiguous(m):
     nsg.preference_loss(z, y, offsets, workspace=work)
     (_, g), (_, p) = m.calls
     assert g[-3] == p[-3] == whole.data_ptr() and g[-2] == p[-2] == need
+
+
+@pytest.mark.parametrize("dtype,per", [(torch.bfloat16, 8), (torch.float32, 4)])
+@pytest.mark.parametrize("loss", ["policy", "preference"])
+def test_a_new_gradient_is_no_larger_than_its_rows(m, dtype, per, loss):
+    """logits[:, -1] of a batch of sequences: the new gradient's rows lie as the
+    logits' do against 16 bytes, without the sequences between them."""
+    for rows, vocab, stride in ((3, 1000, 40 * 1000), (1, 1000, 40 * 1000), (3, 1001, 40 * 1001), (1, 7, 7 * 9),
+                                (3, 1000, 1000), (3, 1000, 1024), (3, 1001, 1002), (5, 1001, 1001), (2, 1, 1), (3, 1, 77)):
+        z = m.tensor(torch.zeros(rows * stride, dtype=dtype).view(rows, stride)[:, :vocab])
+        y = m.tensor(torch.zeros(rows, dtype=torch.int64))
+        a = m.tensor(torch.zeros(rows))
+        m.calls.clear()
+        m.made.clear()
+        if loss == "policy":
+            d = nsg.policy_loss(z, y, a, a)["dlogits"]
+        else:
+            d = nsg.preference_loss(z, y, m.tensor(torch.zeros(3, dtype=torch.int64)))["dlogits"]
+        made = m.made[0]   # the buffer behind it
+        (_, call), = m.calls
+        given = call[2], call[-2 if loss == "policy" else -4]
+        assert d.shape == (rows, vocab) and d.dtype == dtype and d.data_ptr() == made.data_ptr()
+        assert given[1] == made.shape[1] and vocab <= given[1] < vocab + per
+        assert rows == 1 or (given[0] == stride and given[1] % per == stride % per and d.stride()[0] == given[1])
+        if stride == vocab:
+            assert d.is_contiguous() and made.shape == (rows, vocab)
