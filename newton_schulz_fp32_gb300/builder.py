@@ -5,7 +5,9 @@ objects are linked into ``newton_schulz_fp32_gb300/libmuon.so`` (static CUDA
 runtime; the driver API is reached through the runtime's entry-point query,
 so the library links no libcuda).  A rebuild happens only when a source or
 header is newer than the library.  The C half of the Python binding
-(``csrc/binding.c``) is compiled with gcc into ``_binding.so`` beside it.
+(``csrc/binding.c``) is compiled with gcc into ``_binding`` plus the interpreter's suffix
+beside it, where Python's headers are there; without them the embedding and
+loss calls raise and everything else works.
 """
 from __future__ import annotations
 
@@ -16,6 +18,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -41,13 +44,20 @@ def nvcc() -> str:
 
 
 def _build_binding() -> None:
-    """The C half of the Python binding (_binding.so), against this Python."""
-    src, out = os.path.join(CSRC, "binding.c"), os.path.join(HERE, "_binding.so")
+    """The C half of the Python binding, against this Python (its suffix keeps
+    another one from loading it)."""
+    src = os.path.join(CSRC, "binding.c")
+    out = os.path.join(HERE, "_binding" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
     deps = [src, os.path.join(ROOT, "include", "muon.h"), __file__]
     if os.path.exists(out) and all(os.path.getmtime(d) <= os.path.getmtime(out) for d in deps):
         return
-    cmd = [shutil.which("gcc") or "cc", "-O2", "-std=c11", "-shared", "-fPIC", "-I",
-           sysconfig.get_paths()["include"], src, "-o", out + ".tmp"]
+    include = sysconfig.get_paths()["include"]
+    if not os.path.exists(os.path.join(include, "Python.h")):
+        warnings.warn(f"no Python.h in {include}: the embedding and loss calls are not built for Python",
+                      RuntimeWarning)
+        return
+    cmd = [shutil.which("gcc") or "cc", "-O2", "-std=c11", "-shared", "-fPIC", "-I", include, src,
+           "-o", out + ".tmp"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"compiling the Python binding failed:\n{r.stdout}\n{r.stderr}")
@@ -83,9 +93,13 @@ def build(force: bool = False, verbose: bool = False, extra=(), debug: bool = Fa
     """Compile every CUDA source for sm_103a and link libmuon.so (with
     debug: libmuon_debug.so, built with MUON_DEBUG)."""
     lib, build_dir = (LIB_DEBUG, BUILD_DEBUG) if debug else (LIB, BUILD)
+    if force or _stale(lib):
+        _build_library(lib, build_dir, verbose, extra, debug)
     _build_binding()
-    if not force and not _stale(lib):
-        return lib
+    return lib
+
+
+def _build_library(lib, build_dir, verbose, extra, debug) -> None:
     os.makedirs(build_dir, exist_ok=True)
     extra = list(extra) + (["-DMUON_DEBUG"] if debug else [])
     if verbose:
@@ -98,7 +112,6 @@ def build(force: bool = False, verbose: bool = False, extra=(), debug: bool = Fa
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, lib)
-    return lib
 
 
 if __name__ == "__main__":
