@@ -466,7 +466,9 @@ MUON_API int muon_newton_schulz_noalloc(const void* X, void* Y, int rows, int co
  *     fastest.
  *   - Sums, maxima and statistics are FP32 or wider; results are rounded
  *     once, when they are written.  Every sum has a fixed order: the same
- *     inputs give the same bits.
+ *     call on the same inputs gives the same bits.  Another number of tokens,
+ *     other alignment or strides, or a loss without its gradient may sum a row
+ *     in another order, and differ in the last bits.
  *   - No call allocates, synchronises or keeps state: scratch, where a call
  *     needs any, is the caller's `workspace` (16-byte aligned device memory
  *     of at least the bytes its *_workspace function returns, which the call
