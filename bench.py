@@ -42,13 +42,13 @@ FALLBACK = {"hbm_gbs": 6800.0, "bf16_tflops": 1900.0, "bf16_tflops_sustained": 1
 # sources they were taken on (hash below: the kernel, and for Llama-3-8B
 # also the planner whose task order sets the L2 reuse).  GPT-2: the full
 # step.  Llama-3-8B: the full step is too large to capture, so one layer
-# (the same seven shapes) was captured, 13.136 GB per launch, and scaled by
+# (the same seven shapes) was captured, 13.184 GB per launch, and scaled by
 # the 32 layers.
 GEMM_TRAFFIC = {
     "gpt2": {"bytes_per_launch": 3.8480e9, "sources_sha256_16": "7179c2b5092211c5",
              "files": ["newton_schulz_fp32_gb300/csrc/gemm_tc2.cu",
                        "newton_schulz_fp32_gb300/csrc/tc_common.cuh"]},
-    "llama": {"bytes_per_launch": 32 * 13.1362e9, "sources_sha256_16": "932fe30ce6969503",
+    "llama": {"bytes_per_launch": 32 * 13.1845e9, "sources_sha256_16": "1906d6a60342276a",
               "files": ["newton_schulz_fp32_gb300/csrc/gemm_tc2.cu",
                         "newton_schulz_fp32_gb300/csrc/tc_common.cuh",
                         "newton_schulz_fp32_gb300/csrc/api.cu"]},
@@ -59,7 +59,7 @@ GEMM_TRAFFIC = {
 # of the split-3 m x m recurrence, Y), summed from one ncu capture of the
 # full 8192-matrix step (dram__bytes_read.sum + dram__bytes_write.sum,
 # one pass), valid for the sources hashed.
-RAGGED_NS_TRAFFIC = {"bytes_per_step": 46.476e9, "sources_sha256_16": "5bd3eca0ff84a1f3",
+RAGGED_NS_TRAFFIC = {"bytes_per_step": 46.474e9, "sources_sha256_16": "d90598d6f955b834",
                      "files": ["newton_schulz_fp32_gb300/csrc/gemm_tc3.cu",
                                "newton_schulz_fp32_gb300/csrc/gemm_tc.cu",
                                "newton_schulz_fp32_gb300/csrc/tc_common.cuh",

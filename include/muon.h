@@ -652,12 +652,16 @@ MUON_API const char* muon_last_error(void);
 MUON_API void muon_release_workspace(void);
 
 /* Synchronises the device and returns the first error code a kernel
- * recorded since the last query (0 = none), clearing it.  The tensor-core
+ * recorded since the last query (0 = none), clearing it.  The step's codes
+ * come first, then those of muon_newton_schulz_noalloc, of the embedding and
+ * of the loss calls, one a query: ask until it returns 0.  The tensor-core
  * kernels bound every wait; a wait that runs out records a positive code
  * here instead of hanging (1 = TMA producer, 2 = MMA issuer, 3 = epilogue,
  * 4 = a dependency of the SM-pair kernel).  A library built with MUON_DEBUG
  * also checks every streaming-kernel tile against the extents its tables
  * describe and records 16 for a tile that would leave them (and skips it).
+ * A loss call's rows wait for their own copy (1) and for the row's other
+ * blocks (4) in the same way.
  * 17 and 18 are bad token indexes and sequence offsets (see "The two ends of a
  * language model").
  * A step whose products hit such an error also reports applied = -1. */

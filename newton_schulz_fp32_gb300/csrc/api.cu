@@ -19,6 +19,7 @@
 #include <vector>
 
 #include "muon_internal.h"
+#include "token_ops.cuh"
 
 namespace muon {
 namespace {
@@ -1304,6 +1305,10 @@ void count_launches(int n) {
   g_cnt.launches_total += n;
 }
 
+uint64_t g_token_devices = 0;
+void note_token_device(int dev) { g_token_devices |= uint64_t(1) << (dev & 63); }
+uint64_t token_devices() { return g_token_devices; }
+
 int validate_tables(const muon_param_t* params, int nparams, const muon_partition_t* parts,
                     int nparts) {
   Layout L;
@@ -1819,8 +1824,10 @@ extern "C" int muon_device_error(void) {
   };
   for (auto& tp : g_plans) check(tp->d_err);
   for (auto& sp : g_single) check(sp->err);
-  const int na = noalloc_take_device_error();
-  if (na) worst = na;
+  // the other operators' codes, one a query: none is cleared unreported
+  if (!worst) worst = noalloc_take_device_error();
+  if (!worst) worst = embedding_take_device_error();
+  if (!worst) worst = losses_take_device_error();
   return worst;
 }
 

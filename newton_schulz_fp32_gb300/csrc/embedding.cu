@@ -849,11 +849,6 @@ int end_call(int launches, cudaError_t e) {
 
 int embedding_take_device_error() { return take_flag(g_embedding_err); }
 
-// Devices that ran an embedding or loss call (the callers hold the library lock).
-static uint64_t g_token_devices = 0;
-void note_token_device(int dev) { g_token_devices |= uint64_t(1) << (dev & 63); }
-uint64_t token_devices() { return g_token_devices; }
-
 }  // namespace muon
 
 using namespace muon;

@@ -34,7 +34,6 @@
 #include <cstring>
 
 #include "muon_internal.h"
-#include "token_ops.cuh"
 
 namespace muon {
 namespace {
@@ -115,9 +114,7 @@ int muon::noalloc_take_device_error() {   // the caller holds the library lock
       cudaMemset(g_scratch_addr[dev], 0, sizeof(int));
     }
   }
-  // the embedding and loss calls, which allocate nothing either
-  const int embedding = embedding_take_device_error(), losses = losses_take_device_error();
-  return worst ? worst : embedding ? embedding : losses;
+  return worst;
 }
 
 extern "C" int muon_newton_schulz_noalloc(const void* X, void* Y, int rows, int cols, int io_dtype,

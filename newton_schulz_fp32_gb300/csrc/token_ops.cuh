@@ -142,29 +142,27 @@ int entry(F&& body) {
 // Host side.  Which devices have run these operators (bit per device; the
 // caller holds the library lock), so that muon_device_error reads their flags.
 void note_token_device(int dev);
-// The flags' first nonzero code on every device noted, cleared once read.
+// The first nonzero code among the devices noted, cleared once read; the
+// others' wait for the next query.
 int embedding_take_device_error();
 int losses_take_device_error();
 uint64_t token_devices();
 
-// Reads and clears a TU's flag on every noted device.  `symbol` is the TU's
-// own __device__ int.
+// `symbol`: the TU's own __device__ int.
 template <typename S>
 int take_flag(S& symbol) {
-  int worst = 0, now = 0;
+  int v = 0, now = 0;
   if (!token_devices() || cudaGetDevice(&now) != cudaSuccess) return 0;
-  for (int d = 0; d < 64; ++d) {
+  for (int d = 0; d < 64 && !v; ++d) {
     if (!(token_devices() >> d & 1)) continue;
-    int v = 0;
     const int zero = 0;
-    if (cudaSetDevice(d) == cudaSuccess &&
-        cudaMemcpyFromSymbol(&v, symbol, sizeof(int)) == cudaSuccess && v) {
-      if (!worst) worst = v;
-      cudaMemcpyToSymbol(symbol, &zero, sizeof(int));
-    }
+    if (cudaSetDevice(d) != cudaSuccess || (d != now && cudaDeviceSynchronize() != cudaSuccess) ||
+        cudaMemcpyFromSymbol(&v, symbol, sizeof(int)) != cudaSuccess)
+      v = 0;
+    if (v) cudaMemcpyToSymbol(symbol, &zero, sizeof(int));
   }
   cudaSetDevice(now);
-  return worst;
+  return v;
 }
 
 }  // namespace muon
