@@ -510,7 +510,9 @@ MUON_API int muon_embedding(const void* table, int table_dtype, int64_t table_st
  *   workspace : muon_embedding_grad_workspace(n_tokens, cols) bytes
  * Errors: MUON_ERR_INVALID as muon_embedding, for a bad table (as muon_step),
  * a short or misaligned workspace; MUON_ERR_UNSUPPORTED if the parameter lies
- * in more than MUON_EMBEDDING_MAX_SEGMENTS partitions. */
+ * in more than MUON_EMBEDDING_MAX_SEGMENTS partitions, or for more tokens than
+ * one launch takes at this cols (2^44 elements of dout and more).  Nothing is
+ * written then. */
 #define MUON_EMBEDDING_MAX_SEGMENTS 128
 MUON_API int muon_embedding_grad_workspace(int64_t n_tokens, int cols, size_t* bytes);
 MUON_API int muon_embedding_grad(float* accum, int64_t accum_elems, const void* dout,

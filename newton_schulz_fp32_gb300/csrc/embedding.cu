@@ -776,21 +776,25 @@ cudaError_t launch_sort(const SortArgs& a, bool early, cudaStream_t s) {
   return launch(k_embed_sort, blocks, kSortThreads, blocks, early, s, kSortShared, a);
 }
 
+// Threads along a row of k_embed_few or k_embed_sum, `per` columns each: as
+// many as it has columns for.
+int row_threads(bool few, int cols, int per) {
+  int width = few ? 64 : 32;
+  while (width < (few ? kFewX : kSumX) && width * per < cols) width *= 2;
+  return width;
+}
+
 // The gradient's kernels after the sort, or the one for few tokens; *launches
 // counts them.
 template <typename T>
-cudaError_t launch_grad(Grad g, const Segments& sg, bool few, cudaStream_t s, int* launches) {
+cudaError_t launch_grad(const Grad& g, const Segments& sg, bool few, cudaStream_t s, int* launches) {
   constexpr int N = Vec<T>::N;
   const bool vec = reinterpret_cast<uintptr_t>(g.dout) % 16 == 0 && g.dstride * sizeof(T) % 16 == 0 &&
                    g.cols % N == 0;
   bool aligned = g.cols % 4 == 0;   // every row of accum (and of partial sums) starts on 16 bytes
   for (int i = 0; i < sg.n && aligned; ++i) aligned = (sg.at[i] - sg.rel[i]) % 4 == 0 && sg.rel[i] % 4 == 0;
-  int width = few ? 64 : 32;   // as many threads as a row has columns for
-  while (width < (few ? kFewX : kSumX) && width * N < g.cols) width *= 2;
-  g.slabs = static_cast<int>((int64_t(g.cols) + width * N - 1) / (width * N));
-  const int64_t grid = int64_t(few ? g.n : g.blocks) * g.slabs;
-  if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  const unsigned blocks = static_cast<unsigned>(grid);
+  const int width = row_threads(few, g.cols, N);
+  const unsigned blocks = static_cast<unsigned>((few ? g.n : g.blocks) * g.slabs);
   ++*launches;
   if (few)
     return launch(!vec ? k_embed_few<T, false, false> : aligned ? k_embed_few<T, true, true> : k_embed_few<T, true, false>,
@@ -921,6 +925,13 @@ extern "C" int muon_embedding_grad(float* accum, int64_t accum_elems, const void
     const Workspace w = workspace_of(n_tokens, param->cols);
     if (w.bytes > 0 && (!workspace || misaligned(workspace, 16) || workspace_bytes < w.bytes))
       return efail(MUON_ERR_INVALID, "workspace is NULL, misaligned or too small");
+    const bool few = n_tokens <= kFew;
+    const int64_t blocks = token_blocks(n_tokens, param->cols);
+    const int per = dout_dtype == MUON_DTYPE_BF16 ? Vec<__nv_bfloat16>::N : Vec<float>::N;
+    const int slab = per * row_threads(few, param->cols, per);
+    const int64_t slabs = (int64_t(param->cols) + slab - 1) / slab;
+    if ((few ? n_tokens : blocks) * slabs > 0x7fffffff)
+      return efail(MUON_ERR_UNSUPPORTED, "too many tokens of rows this long for one call");
     if (n_tokens == 0 && !overwrite) return MUON_OK;
     if ((rc = begin_call()) != MUON_OK) return rc;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -937,7 +948,6 @@ extern "C" int muon_embedding_grad(float* accum, int64_t accum_elems, const void
     so.sorted = reinterpret_cast<int2*>(base + w.sorted);
     so.other = reinterpret_cast<int2*>(base + w.other);
     so.crossing = reinterpret_cast<int*>(base + w.crossing);
-    const bool few = n_tokens <= kFew;
     int launches = 0;
     if (overwrite) {
       const cudaError_t e = launch(k_embed_fill, unsigned(std::min<int64_t>(kFillBlocks * kSms, sg.numel / 1024 + 1)),
@@ -966,12 +976,11 @@ extern "C" int muon_embedding_grad(float* accum, int64_t accum_elems, const void
     g.partial = reinterpret_cast<float*>(base + w.partial);
     g.crossing = so.crossing;
     g.run = run_of(n_tokens, param->cols);
-    g.blocks = static_cast<int>(token_blocks(n_tokens, param->cols));
+    g.blocks = static_cast<int>(blocks);
+    g.slabs = static_cast<int>(slabs);
     const cudaError_t e = dout_dtype == MUON_DTYPE_BF16
                               ? launch_grad<__nv_bfloat16>(g, sg, few, s, &launches)
                               : launch_grad<float>(g, sg, few, s, &launches);
-    if (e == cudaErrorInvalidConfiguration)
-      return efail(MUON_ERR_UNSUPPORTED, "too many tokens, rows and columns for one launch");
     return end_call(launches, e);
   });
 }

@@ -37,3 +37,12 @@ def test_a_parameter_that_ends_past_the_index_range_is_refused(lib, param, parts
     for overwrite in (0, 1):
         assert gradient(lib, param, parts, overwrite=overwrite) == nsg.MUON_ERR_INVALID
         assert "range" in lib.muon_last_error().decode() or "accum_elems" in lib.muon_last_error().decode()
+
+
+@pytest.mark.parametrize("overwrite", [0, 1])
+@pytest.mark.parametrize("n,cols", [(1 << 30, 1 << 17), (1 << 28, 1 << 20), (1 << 30, 1 << 30)])
+def test_a_gradient_of_too_many_blocks_is_refused_before_anything_is_written(lib, overwrite, n, cols):
+    """A grid past 2^31 - 1 blocks is known from the sizes, before the table is
+    zeroed (overwrite) or the tokens are sorted."""
+    rc = gradient(lib, (0, 1, cols, 0, 0), n=n, accum_elems=MOST, workspace_bytes=1 << 62, overwrite=overwrite)
+    assert rc == nsg.MUON_ERR_UNSUPPORTED and "too many" in lib.muon_last_error().decode()
