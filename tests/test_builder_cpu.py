@@ -1,8 +1,10 @@
 """The builder where the Python binding's C half cannot be compiled, or was
-compiled for another interpreter."""
+compiled for another interpreter; and which tests run beside a GPU."""
 import os
+import pathlib
 import sys
 import sysconfig
+import types
 
 import pytest
 
@@ -30,6 +32,21 @@ def test_the_binding_is_this_interpreters(monkeypatch, tmp_path):
     built = os.path.getmtime(tmp_path / os.listdir(tmp_path)[0])
     builder.build()
     assert os.path.getmtime(tmp_path / os.listdir(tmp_path)[0]) == built
+
+
+def test_made_up_addresses_stay_away_from_a_gpu(monkeypatch):
+    """Beside a GPU's device node the refusal tests are skipped, torch or not."""
+    import conftest
+    marks = []
+    items = [types.SimpleNamespace(path=pathlib.Path("tests") / name, add_marker=lambda m, n=name: marks.append((n, m.name)))
+             for name in (conftest.MADE_UP_ADDRESSES, "test_library_cpu.py")]
+    assert (pathlib.Path(conftest.__file__).parent / conftest.MADE_UP_ADDRESSES).exists()
+    monkeypatch.setattr(conftest, "gpu_nodes", lambda: [])
+    conftest.pytest_collection_modifyitems(items)
+    assert marks == []
+    monkeypatch.setattr(conftest, "gpu_nodes", lambda: ["/dev/nvidia0"])
+    conftest.pytest_collection_modifyitems(items)
+    assert marks == [(conftest.MADE_UP_ADDRESSES, "skip")]
 
 
 def test_calls_without_the_binding_say_so(monkeypatch):
