@@ -757,8 +757,8 @@ __global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) k_held(const Rows a
   // goes to the others with (m, s): the sums' exchange orders no other load, so
   // another block's could come after that write where the gradient replaces
   // the logits.
-  const int owner = y < sh.head || y >= sh.tail0 ? 0 : (y - sh.head) / N / per_block;
-  float zy = warp == 0 && rank == owner ? tok::to_float(row[y]) : -INFINITY;
+  const bool ours = y < sh.head || y >= sh.tail0 ? rank == 0 : unsigned((y - sh.head) / N - base) < unsigned(mine);
+  float zy = warp == 0 && ours ? tok::to_float(row[y]) : -INFINITY;
   Softmax<T> share;
   tc::mbar_wait(tc::smem_u32(&full), 0, &stopped, &g_losses_err, 1);
   int at = threadIdx.x;
