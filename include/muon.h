@@ -537,13 +537,17 @@ MUON_API int muon_token_logprobs(const void* logits, int dtype, int64_t stride, 
 
 /* The clipped policy loss with a KL term, and its gradient.  For each token t
  * with a target >= 0 and weights[t] != 0 (the others take no part: their
- * logits and inputs are not read, their logp is 0 and their gradient row 0):
+ * logits are not read, their inputs may hold anything, their logp is 0 and
+ * their gradient row 0):
  *     r  = exp(logp - old_logp[t])           (1 if old_logp is NULL)
  *     p  = -min(r A, clamp(r, 1 - clip_low, 1 + clip_high) A),  A = advantages[t]
  *     k  = exp(ref_logp[t] - logp) - (ref_logp[t] - logp) - 1   (0 if NULL)
  *     loss = sum_t weights[t] (p + kl_coef k)
  * The gradient takes p as -r A where r A <= clamp(r) A, else as constant
- * (old_logp, NULL or not, is a constant).  weights carry the mask and the
+ * (old_logp, NULL or not, is a constant).  With old_logp and ref_logp NULL and
+ * advantages of 1 it is that of the weighted cross entropy -sum w logp (whose
+ * value is in logp; stats then hold -sum w).  r A is 0 for A = 0 also where r
+ * is past FP32's range.  weights carry the mask and the
  * normalisation (1 / active tokens, 1 / (sequences * length), over the whole
  * step when micro-batches are accumulated).
  *   stats   : device float[4]: loss, sum w p, sum w k, sum of the weights of

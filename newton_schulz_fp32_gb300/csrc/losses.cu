@@ -113,7 +113,7 @@ __device__ __forceinline__ Token load_token(const Policy& p, int64_t t) {
 __device__ __forceinline__ PolicyTerms policy_terms(const Token& k, const Policy& p, float logp) {
   PolicyTerms o;
   const float r = p.old_logp ? expf(logp - k.old) : (logp == logp ? 1.f : logp);
-  const float free = r * k.a;
+  const float free = k.a == 0.f && r > FLT_MAX ? 0.f : r * k.a;   // an r past the range is a number all the same
   const float held = fminf(fmaxf(r, 1.f - p.clip_low), 1.f + p.clip_high) * k.a;
   o.cut = free > held;
   o.term = o.cut ? -held : -free;
@@ -122,7 +122,7 @@ __device__ __forceinline__ PolicyTerms policy_terms(const Token& k, const Policy
   if (p.ref_logp) {
     const float q = k.ref - logp;
     const float g = expm1f(q);
-    o.kl = g - q;
+    o.kl = q > FLT_MAX ? q : g - q;
     if (p.kl_coef != 0.f) o.coef -= p.kl_coef * g;   // 0 times infinity would spoil the gradient
   }
   return o;
