@@ -616,8 +616,13 @@ __global__ void __launch_bounds__(W) k_given(const Rows a, const Extra x, const 
     return !on ? 0.f : u == y ? d + g : d;
   };
   if (slice == 0) {   // the elements before and after the vectors
-    const int u = sh.single(a.vocab);
-    if (u >= 0) drow[u] = tok::from_float<T>(one(u, on ? tok::to_float(row[u]) : 0.f));
+    // RowShape::single, written out: 48 registers and five blocks per SM, 56 and four by the call
+    const int k = int(threadIdx.x) - 8;
+    const bool before = int(threadIdx.x) < sh.head;
+    if (before || (k >= 0 && k < a.vocab - sh.tail0)) {
+      const int u = before ? int(threadIdx.x) : sh.tail0 + k;
+      drow[u] = tok::from_float<T>(one(u, on ? tok::to_float(row[u]) : 0.f));
+    }
   }
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
