@@ -73,9 +73,9 @@ class Model:
         _, g_hidden, g_head = self.views(self.dense)
         g_hidden.copy_(da.T @ x)
         g_head.copy_(d.T @ h)
-        nsg.accumulate(self.accum, self.dense, 1.0, overwrite=True, params=self.params, parts=self.parts)
+        nsg.accumulate(self.accum, self.dense, 1.0, overwrite=True, params=self.params[1:], parts=self.parts)
         nsg.embedding_grad(self.accum, da @ self.hidden, tokens, self.params[0], parts=self.parts,
-                           scale=math.sqrt(DIM))
+                           scale=math.sqrt(DIM), overwrite=True)
         self.steps += 1
         nsg.step_ex(self.accum, self.momentum, self.master, self.params, self.parts, beta=0.9, lr=lr,
                     ns_method="standard", clip=1.0, operand_mode="bf16",
