@@ -501,6 +501,10 @@ MUON_API int muon_embedding(const void* table, int table_dtype, int64_t table_st
  * once.  Without overwrite only rows of
  * tokens that occur are read and written; with overwrite every row is written
  * (zeros where no token occurs).  Nothing outside the parameter is touched.
+ * A micro-batch that overwrites accum, by muon_accumulate or folded into the
+ * step (muon_step_options_t), takes this gradient with it: call
+ * muon_accumulate first, or leave this parameter out of its table, and fold
+ * without overwrite.
  *   accum : device float storage buffer, 16-byte aligned
  *   accum_elems : its elements; a table that leaves it is refused
  *   dout  : device, n_tokens x cols of dout_dtype, dout_stride >= cols

@@ -18,10 +18,11 @@
 // Which kernel takes a row is a matter of its size, and of whether its gradient
 // is written (launch_rows_of):
 //   k_held    a cluster of blocks holds the row in shared memory: read once,
-//             gradient and all.  Bound by memory: 8192 rows of 131072 bf16 with
-//             their gradient 645 us, 6.5 TB/s of reads and writes.
+//             gradient and all.  Bound by memory: 8192 rows of 131072 bf16, 5%
+//             of them masked, with their gradient 660 us the whole call, 6.35
+//             TB/s of reads and writes.
 //   k_rows    one block streams the row; for many rows without a gradient
-//             (8192 of 131072 bf16: 264 us, 7.3 TB/s) and for rows too long to
+//             (8192 of 131072 bf16, 10% left out: 265 us, 7.3 TB/s) and for rows too long to
 //             be held, whose gradient takes a second pass.
 //   k_given   the gradient from statistics taken before: the preference loss
 //             needs all of a pair's rows before any of their gradients, so it
@@ -666,8 +667,8 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 
 // Sends (m, s) and z to `slot` in block `rank`, counted in bytes on its
 // barrier there.  A release barrier of the whole cluster instead makes every warp wait
-// for its own earlier memory operations: 798 us instead of 649 for 8192 rows of
-// 131072 bf16 with their gradient.
+// for its own earlier memory operations: 23% longer for 8192 rows of 131072
+// bf16 with their gradient.
 __device__ __forceinline__ void send(uint32_t slot, uint32_t bar, int rank, float m, float s, float z) {
   asm volatile(
       "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
@@ -703,8 +704,8 @@ __device__ __forceinline__ void zero_share(const Rows& a, T* drow, int v0, int p
 // short (one row of 131072 bf16: 3.3 us, 7.3 by one block).  Blocks of
 // different rows on one SM overlap one row's loads with another's arithmetic
 // and writes; holding rows in shared memory leaves registers for six of them
-// (in registers, four: 764 us for 8192 rows of 131072 bf16 with their gradient,
-// 645 this way).  Instructions come next: arithmetic on pairs of values.
+// (in registers, four: 18% longer for 8192 rows of 131072 bf16 with their
+// gradient).  Instructions come next: arithmetic on pairs of values.
 template <typename T, int MODE>
 __global__ void __launch_bounds__(kHeldThreads, kHeldBlocks) k_held(const Rows a, const Extra x, int per_block) {
   constexpr int N = Vec<T>::N;
@@ -869,7 +870,7 @@ Hold hold_of(int64_t n, int vocab, int per_vec) {
   // Few rows: as many threads as help.  Many rows: 16 vectors per thread, so that
   // an SM has blocks of more rows to turn to (16384 rows of 8192 bf16: 41 us, 57
   // at 4 vectors); 8 where shared memory limits the blocks (8192 rows of
-  // 131072 bf16 with their gradient: 654 us, 693 at 16).
+  // 131072 bf16 with their gradient: 6% longer at 16).
   const int per_thread = n * c < 4 * kSms ? 2 : vecs * 7 > kHeldMost ? 8 : 16;
   int threads = 32;
   while (threads < kHeldThreads && threads * per_thread < vecs) threads *= 2;
@@ -892,7 +893,7 @@ cudaError_t launch_rows_of(const Rows& a, const Extra& x, cudaStream_t s) {
   const Hold h = hold_of(a.n, a.vocab, Vec<T>::N);
   const bool grad = MODE == kPolicy && a.dlogits;
   // Without a gradient many rows are read faster by streams of loads, all but
-  // the shortest (8192 rows of 131072 bf16 266 us, held 350; 16384 of 16384 73
+  // the shortest (8192 rows of 131072 bf16 265 us, held 350; 16384 of 16384 73
   // us, held 82; 32768 of 2000 39 us, held 37).
   const int64_t bytes = int64_t(a.vocab) * int64_t(sizeof(T));
   const bool stream = !grad && a.n >= 2 * kSms && bytes > kHeldRow;
