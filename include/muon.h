@@ -601,6 +601,221 @@ MUON_API int muon_preference_loss(const void* logits, int dtype, int64_t stride,
                                   int64_t dlogits_stride, void* workspace,
                                   size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------------
+ * The layers of a language model.
+ *
+ * What lies between the two ends: dense layers, whose weights are the
+ * matrices a step orthogonalises, dropout, and the norm and rotation of query
+ * and key heads.  Gradients of parameters are summed in FP32 straight into
+ * the flat accumulation buffer, as muon_embedding_grad does it.
+ *
+ * The conventions of "The two ends of a language model" hold, in particular:
+ * strides in elements, any stride >= the row's length, any base aligned to
+ * its type; FP32 sums in a fixed order; no allocation, no synchronisation, no
+ * state; scratch is the caller's, and two calls that may run at the same time
+ * need scratch of their own; capturable once each has run on the device;
+ * n_tokens = 0 is valid (gradients with overwrite are then zeroed).  "May not
+ * overlap" is checked for the spans of memory, first to last element.  A
+ * parameter may lie in up to MUON_EMBEDDING_MAX_SEGMENTS partitions.
+ * ------------------------------------------------------------------- */
+
+/* The activation of a dense layer: u, max(u, 0), max(u, 0)^2,
+ * u (1 + tanh(sqrt(2 / pi) (u + 0.044715 u^3))) / 2, u / (1 + exp(-u)).
+ * Their slopes at 0 are 1, 0, 0, 1/2, 1/2. */
+typedef enum {
+  MUON_ACT_NONE = 0,
+  MUON_ACT_RELU = 1,
+  MUON_ACT_RELU2 = 2,
+  MUON_ACT_GELU = 3,
+  MUON_ACT_SILU = 4
+} muon_activation_t;
+
+/* Dropout.  An element is left out where its draw, 16 bits, is below
+ * round(65536 rate); the others are multiplied by 65536 / (65536 -
+ * round(65536 rate)), so that the mean is kept exactly.  The draws are those of
+ * Philox4x32-10 (Salmon et al., "Parallel random numbers: as easy as 1, 2, 3",
+ * 2011) with the counter (col / 8, row, site, step) and the key seed, low word
+ * first: element (row, col) takes bits [16 (col % 2), + 16) of word
+ * (col % 8) / 2.  `rng` is device memory, 8-byte aligned, holding two int64:
+ * seed, step (its low 32 bits), so that a captured call draws anew when the
+ * program has changed the step.  `site` tells layers apart.  No mask is
+ * stored: the gradient's mask is drawn again. */
+
+/* u = x weight^T + bias;  pre = u;  out = residual + dropout(activation(u)),
+ * each rounded once from FP32.
+ *   x, weight : device, bf16, n_tokens x in_features and out_features x
+ *               in_features
+ *   bias      : device, out_features of bias_dtype, or NULL
+ *   pre       : device, bf16, n_tokens x out_features, or NULL: u, which the
+ *               gradient of the activation needs
+ *   dropout   : the rate, in [0, 1) and less than 1 - 2^-17; rng is looked at
+ *               if round(65536 dropout) > 0
+ *   residual  : device, n_tokens x out_features of out_dtype, or NULL.  It may
+ *               be `out` itself (same address and stride)
+ *   out       : device, n_tokens x out_features of out_dtype
+ * out and pre may overlap nothing else the call is given.
+ * workspace: operands whose rows do not all start on 16 bytes are copied there
+ * first; muon_linear_workspace says how many bytes that takes (0: none).
+ * Errors: MUON_ERR_INVALID for a wrong struct_size, NULL or misaligned
+ * pointers, unknown types, sizes < 1 or > 2^24 (features), n_tokens < 0 or >
+ * 2^30, short strides, overlaps, a short or misaligned workspace;
+ * MUON_ERR_UNSUPPORTED for products too large for one launch. */
+typedef struct muon_linear_args {
+  int32_t struct_size;   /* sizeof(muon_linear_args_t) */
+  int32_t activation;    /* muon_activation_t */
+  int64_t n_tokens;
+  int32_t in_features, out_features;
+  const void* x;
+  int64_t x_stride;
+  const void* weight;
+  int64_t weight_stride;
+  const void* bias;
+  void* pre;
+  int64_t pre_stride;
+  const void* residual;
+  int64_t residual_stride;
+  void* out;
+  int64_t out_stride;
+  const int64_t* rng;
+  int32_t bias_dtype, out_dtype;
+  float dropout;
+  uint32_t site;
+} muon_linear_args_t;
+MUON_API int muon_linear_workspace(const muon_linear_args_t* args, size_t* bytes);
+MUON_API int muon_linear(const muon_linear_args_t* args, void* workspace, size_t workspace_bytes,
+                         void* stream);
+
+/* The gradients of u = x weight^T + bias for dout = d loss / d u:
+ *     dx            = (dout weight) * activation'(pre)
+ *     accum[param]  = (overwrite ? 0 : accum[param]) + scale * dout^T x
+ *     accum[bias]   = (overwrite ? 0 : accum[bias]) + scale * sum over t of dout
+ * The activation is the one BEFORE this layer (x = activation(pre), so dx is
+ * the gradient with respect to pre, which is what the layer before it takes
+ * as its dout); MUON_ACT_NONE: pre is not looked at.  With dropout after the
+ * layer, dout is muon_dropout of the gradient behind it.
+ *   dout   : device, bf16, n_tokens x out_features
+ *   x      : device, bf16, n_tokens x in_features; may be NULL if param is
+ *   weight : device, bf16, out_features x in_features; may be NULL if dx is
+ *   pre    : device, bf16, n_tokens x in_features
+ *   dx     : device, bf16, n_tokens x in_features, or NULL; may overlap
+ *            nothing else the call is given
+ *   param  : host, rows = out_features, cols = in_features, or NULL: no
+ *            gradient of the weight
+ *   bias   : host, rows * cols = out_features, or NULL
+ *   accum, accum_elems, parts, nparts, scale, overwrite : as
+ *            muon_embedding_grad; not looked at if param and bias are NULL.
+ *            The two parameters may not overlap.
+ * Errors: as muon_linear and muon_embedding_grad. */
+typedef struct muon_linear_grad_args {
+  int32_t struct_size;   /* sizeof(muon_linear_grad_args_t) */
+  int32_t activation;
+  int64_t n_tokens;
+  int32_t in_features, out_features;
+  const void* dout;
+  int64_t dout_stride;
+  const void* x;
+  int64_t x_stride;
+  const void* weight;
+  int64_t weight_stride;
+  const void* pre;
+  int64_t pre_stride;
+  void* dx;
+  int64_t dx_stride;
+  float* accum;
+  int64_t accum_elems;
+  const muon_param_t* param;
+  const muon_param_t* bias;
+  const muon_partition_t* parts;
+  int32_t nparts, overwrite;
+  float scale;
+  int32_t reserved;      /* 0 */
+} muon_linear_grad_args_t;
+MUON_API int muon_linear_grad_workspace(const muon_linear_grad_args_t* args, size_t* bytes);
+MUON_API int muon_linear_grad(const muon_linear_grad_args_t* args, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/* out = residual + dropout(x), rounded once.  The gradient with respect to x
+ * is the same call on the gradient of out, without a residual.
+ *   x, residual, out : device, rows x cols of dtype; residual may be NULL; out
+ *              may be x or the residual itself (same address and stride), and
+ *              overlap them in no other way
+ * Errors: MUON_ERR_INVALID. */
+MUON_API int muon_dropout(const void* x, int64_t x_stride, const void* residual,
+                          int64_t residual_stride, void* out, int64_t out_stride, int dtype,
+                          int64_t rows, int cols, float rate, const int64_t* rng, uint32_t site,
+                          void* stream);
+
+/* Norm and rotation of heads, in one pass over queries and keys.  For each
+ * token t and head h of each group, with x the head's head_dim elements:
+ *     n   = x / sqrt(mean of x^2 + eps) * weight    (norm = 0: n = x;
+ *                                                    weight NULL: 1)
+ *     out = n with pair i, of 2 * pairs <= head_dim leading elements, turned by
+ *           the angle positions[t][axis[i]] * inv_freq[i]:
+ *           (a, b) -> (a cos - b sin, b cos + a sin)
+ * Pair i is elements (i, pairs + i), or (2 i, 2 i + 1) if interleaved; the
+ * elements behind the pairs are not turned.  Angles are formed as whole turns
+ * in 64-bit fixed point, so far positions lose nothing but the 2^-53 of
+ * inv_freq itself.  A token with a NEGATIVE position on any axis is no token:
+ * its heads are not read and its rows of out are zeros.
+ *   groups    : host, n_groups = 1 or 2 (queries, keys): x and out device, of
+ *               dtype, element d of head h of token t at t * stride +
+ *               h * head_stride + d; weight device, head_dim of dtype, or NULL.
+ *               out may be x itself (same address and strides), and overlap
+ *               nothing else.  Rows of different tokens or heads of an out may
+ *               not overlap: head_stride >= head_dim and either stride >=
+ *               heads' span or head_stride >= tokens' span
+ *   positions : device, n_tokens x axes of positions_type, contiguous; NULL if
+ *               pairs = 0
+ *   inv_freq  : host, pairs finite doubles (radians per position)
+ *   axis      : host, pairs of [0, axes), or NULL: 0
+ * Errors: MUON_ERR_INVALID; head_dim is in [1, 256], axes in [1, 8]. */
+#define MUON_MAX_HEAD_DIM 256
+#define MUON_MAX_AXES 8
+typedef struct muon_heads {
+  const void* x;
+  int64_t x_stride, x_head_stride;
+  const void* weight;
+  void* out;
+  int64_t out_stride, out_head_stride;
+  int32_t heads;
+  int32_t reserved; /* 0 */
+} muon_heads_t;
+MUON_API int muon_norm_rotary(const muon_heads_t* groups, int n_groups, int dtype,
+                              int64_t n_tokens, int head_dim, int norm, float eps,
+                              const void* positions, int positions_type, int axes,
+                              const double* inv_freq, const int32_t* axis, int pairs,
+                              int interleaved, void* stream);
+
+/* Its gradients.  For each group: dx of the heads, and with norm and a param
+ *     accum[param] = (overwrite ? 0 : accum[param]) + scale * d loss / d weight
+ * (param: rows * cols = head_dim).  x is the heads before the norm; it is not
+ * looked at if norm = 0.  Tokens with a negative position take no part: their
+ * rows of dx are zeros.  dx may be dout itself, or x itself (same address and
+ * strides).
+ *   workspace : muon_norm_rotary_grad_workspace bytes, needed for a param
+ * Errors: as muon_norm_rotary and muon_embedding_grad. */
+typedef struct muon_heads_grad {
+  const void* dout;
+  int64_t dout_stride, dout_head_stride;
+  const void* x;
+  int64_t x_stride, x_head_stride;
+  const void* weight;
+  void* dx;
+  int64_t dx_stride, dx_head_stride;
+  const muon_param_t* param; /* host, or NULL */
+  int32_t heads;
+  int32_t reserved; /* 0 */
+} muon_heads_grad_t;
+MUON_API int muon_norm_rotary_grad_workspace(int64_t n_tokens, int head_dim, size_t* bytes);
+MUON_API int muon_norm_rotary_grad(const muon_heads_grad_t* groups, int n_groups, int dtype,
+                                   int64_t n_tokens, int head_dim, int norm, float eps,
+                                   const void* positions, int positions_type, int axes,
+                                   const double* inv_freq, const int32_t* axis, int pairs,
+                                   int interleaved, float* accum, int64_t accum_elems,
+                                   const muon_partition_t* parts, int nparts, float scale,
+                                   int overwrite, void* workspace, size_t workspace_bytes,
+                                   void* stream);
+
 /* Host-side counters (no GPU work).  Returns MUON_OK. */
 MUON_API int muon_get_stats(muon_stats_t* out);
 
@@ -674,6 +889,8 @@ MUON_API void muon_release_workspace(void);
  * blocks (4) in the same way.
  * 17 and 18 are bad token indexes and sequence offsets (see "The two ends of a
  * language model").
+ * The products of muon_linear and muon_linear_grad record 1, 2 and 3 as the
+ * step's do; they are asked last.
  * A step whose products hit such an error also reports applied = -1. */
 MUON_API int muon_device_error(void);
 

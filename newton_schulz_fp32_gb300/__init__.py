@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import math
 import os
 
 import numpy as np
@@ -42,7 +43,10 @@ EXPORTED = ["muon_accumulate", "muon_accumulate_n", "muon_step", "muon_newton_sc
             "muon_dp_plan_sizes", "muon_dp_plan_tables", "muon_dp_pack", "muon_dp_unpack",
             "muon_dp_finish", "muon_embedding", "muon_embedding_grad",
             "muon_embedding_grad_workspace", "muon_token_logprobs", "muon_policy_loss",
-            "muon_preference_loss", "muon_preference_loss_workspace"]
+            "muon_preference_loss", "muon_preference_loss_workspace", "muon_linear",
+            "muon_linear_workspace", "muon_linear_grad", "muon_linear_grad_workspace", "muon_dropout",
+            "muon_norm_rotary", "muon_norm_rotary_grad", "muon_norm_rotary_grad_workspace"]
+ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "relu2": 2, "gelu": 3, "silu": 4}
 CLIP_MODES = {"update": 0, "grad": 1}
 
 
@@ -83,6 +87,45 @@ class TableInfo(ctypes.Structure):
                 ("stack_rows", ctypes.c_int32), ("muon_elements", ctypes.c_int64),
                 ("aux_elements", ctypes.c_int64), ("padding_elements", ctypes.c_int64),
                 ("segments", ctypes.c_int64), ("workspace_bytes", ctypes.c_uint64)]
+
+
+class LinearArgs(ctypes.Structure):
+    """muon_linear_args_t."""
+    _fields_ = [("struct_size", ctypes.c_int32), ("activation", ctypes.c_int32), ("n_tokens", ctypes.c_int64),
+                ("in_features", ctypes.c_int32), ("out_features", ctypes.c_int32), ("x", ctypes.c_void_p),
+                ("x_stride", ctypes.c_int64), ("weight", ctypes.c_void_p), ("weight_stride", ctypes.c_int64),
+                ("bias", ctypes.c_void_p), ("pre", ctypes.c_void_p), ("pre_stride", ctypes.c_int64),
+                ("residual", ctypes.c_void_p), ("residual_stride", ctypes.c_int64), ("out", ctypes.c_void_p),
+                ("out_stride", ctypes.c_int64), ("rng", ctypes.c_void_p), ("bias_dtype", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32), ("dropout", ctypes.c_float), ("site", ctypes.c_uint32)]
+
+
+class LinearGradArgs(ctypes.Structure):
+    """muon_linear_grad_args_t."""
+    _fields_ = [("struct_size", ctypes.c_int32), ("activation", ctypes.c_int32), ("n_tokens", ctypes.c_int64),
+                ("in_features", ctypes.c_int32), ("out_features", ctypes.c_int32), ("dout", ctypes.c_void_p),
+                ("dout_stride", ctypes.c_int64), ("x", ctypes.c_void_p), ("x_stride", ctypes.c_int64),
+                ("weight", ctypes.c_void_p), ("weight_stride", ctypes.c_int64), ("pre", ctypes.c_void_p),
+                ("pre_stride", ctypes.c_int64), ("dx", ctypes.c_void_p), ("dx_stride", ctypes.c_int64),
+                ("accum", ctypes.c_void_p), ("accum_elems", ctypes.c_int64), ("param", ctypes.c_void_p),
+                ("bias", ctypes.c_void_p), ("parts", ctypes.c_void_p), ("nparts", ctypes.c_int32),
+                ("overwrite", ctypes.c_int32), ("scale", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+class Heads(ctypes.Structure):
+    """muon_heads_t."""
+    _fields_ = [("x", ctypes.c_void_p), ("x_stride", ctypes.c_int64), ("x_head_stride", ctypes.c_int64),
+                ("weight", ctypes.c_void_p), ("out", ctypes.c_void_p), ("out_stride", ctypes.c_int64),
+                ("out_head_stride", ctypes.c_int64), ("heads", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class HeadsGrad(ctypes.Structure):
+    """muon_heads_grad_t."""
+    _fields_ = [("dout", ctypes.c_void_p), ("dout_stride", ctypes.c_int64), ("dout_head_stride", ctypes.c_int64),
+                ("x", ctypes.c_void_p), ("x_stride", ctypes.c_int64), ("x_head_stride", ctypes.c_int64),
+                ("weight", ctypes.c_void_p), ("dx", ctypes.c_void_p), ("dx_stride", ctypes.c_int64),
+                ("dx_head_stride", ctypes.c_int64), ("param", ctypes.c_void_p), ("heads", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
 
 
 class PhaseTime(ctypes.Structure):
@@ -142,6 +185,16 @@ def lib():
         L.muon_preference_loss_workspace.argtypes = [I64, S]
         L.muon_preference_loss.argtypes = [P, I, I64, I64, I, P, I, P, I, I, P, P, F, F, F, P, P,
                                            P, P, I64, P, ctypes.c_size_t, P]
+        Z, U = ctypes.c_size_t, ctypes.c_uint32
+        L.muon_linear_workspace.argtypes = [ctypes.POINTER(LinearArgs), S]
+        L.muon_linear.argtypes = [ctypes.POINTER(LinearArgs), P, Z, P]
+        L.muon_linear_grad_workspace.argtypes = [ctypes.POINTER(LinearGradArgs), S]
+        L.muon_linear_grad.argtypes = [ctypes.POINTER(LinearGradArgs), P, Z, P]
+        L.muon_dropout.argtypes = [P, I64, P, I64, P, I64, I, I64, I, F, P, U, P]
+        L.muon_norm_rotary.argtypes = [ctypes.POINTER(Heads), I, I, I64, I, I, F, P, I, I, P, P, I, I, P]
+        L.muon_norm_rotary_grad_workspace.argtypes = [I64, I, S]
+        L.muon_norm_rotary_grad.argtypes = [ctypes.POINTER(HeadsGrad), I, I, I64, I, I, F, P, I, I, P, P, I, I, P,
+                                            I64, P, I, F, I, P, Z, P]
         for name in ("muon_accumulate", "muon_accumulate_n", "muon_step", "muon_step_ex",
                      "muon_newton_schulz", "muon_newton_schulz_noalloc", "muon_get_stats",
                      "muon_device_error", "muon_profile_enable", "muon_profile_read",
@@ -149,7 +202,9 @@ def lib():
                      "muon_testing_set", "muon_embedding", "muon_embedding_grad",
                      "muon_embedding_grad_workspace", "muon_token_logprobs",
                      "muon_policy_loss", "muon_preference_loss",
-                     "muon_preference_loss_workspace"):
+                     "muon_preference_loss_workspace", "muon_linear", "muon_linear_workspace",
+                     "muon_linear_grad", "muon_linear_grad_workspace", "muon_dropout",
+                     "muon_norm_rotary", "muon_norm_rotary_grad", "muon_norm_rotary_grad_workspace"):
             getattr(L, name).restype = I
         _lib = L
     return _lib
@@ -362,6 +417,8 @@ def _native():
         b.init(torch, getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device),
                getattr(torch._C, "_cuda_getCurrentRawStream", lambda i: torch.cuda.current_stream(i).cuda_stream),
                MuonError, {n: ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in names})
+        b.init_layers({n: ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in EXPORTED
+                       if n.startswith(("muon_linear", "muon_dropout", "muon_norm_rotary"))})
         _bound = b
     return _bound
 
@@ -493,6 +550,192 @@ def preference_loss_workspace(n_tokens: int) -> int:
     """Bytes of scratch preference_loss needs."""
     b = ctypes.c_size_t()
     _check(lib().muon_preference_loss_workspace(n_tokens, ctypes.byref(b)))
+    return b.value
+
+
+# ------------------------------------------------------------------ the layers of a model
+
+def _joined(x, keep: int, stream):
+    """x with all but its last `keep` dimensions joined; where its layout needs
+    a copy for that, one on the stream of the call, which then owns it."""
+    if x is None or x.dim() == keep + 1:
+        return x
+    shape = (-1, *x.shape[x.dim() - keep:])
+    if 0 in x.shape:
+        shape = (math.prod(x.shape[:x.dim() - keep]), *shape[1:])
+    if stream is None:
+        return x.reshape(shape)
+    with _elsewhere(x, stream):
+        return x.reshape(shape)
+
+
+def _joined_out(x, keep: int):
+    """The same for a tensor that is written (or a bool or None): no copy."""
+    if x is None or isinstance(x, bool) or x.dim() == keep + 1:
+        return x
+    lead = math.prod(x.shape[:x.dim() - keep])
+    return x.view(lead, *x.shape[x.dim() - keep:])
+
+
+def _activation(name):
+    try:
+        return ACTIVATIONS[name]
+    except (KeyError, TypeError):
+        raise ValueError(f"unknown activation {name!r}: one of {sorted(k for k in ACTIVATIONS if k)}") from None
+
+
+def _param(p):
+    if p is None:
+        return None
+    if hasattr(p, "dtype"):
+        p = (p["offset"], p["rows"], p["cols"])
+    return tuple(int(v) for v in p)
+
+
+def _parts(parts):
+    if parts is None:
+        return None
+    if getattr(parts, "dtype", None) is not PART_DTYPE:
+        parts = _table(parts, PART_DTYPE)[0]
+    return parts.tobytes()
+
+
+def linear(x, weight, bias=None, activation=None, residual=None, dropout: float = 0.0, rng=None,
+           site: int = 0, out=None, out_dtype=None, pre=False, workspace=None, stream=None):
+    """residual + dropout(activation(x weight^T + bias)) (muon_linear): x
+    tokens x in_features (leading dimensions are joined, by a copy where their
+    layout needs one), weight out_features x in_features, both bf16; bias bf16
+    or fp32; activation one of ACTIVATIONS.  out_dtype: bf16 or fp32 (default:
+    out's, the residual's or bf16).  rng: an int64 CUDA tensor (seed, step),
+    site: which of the model's dropouts this is.  pre: True or a bf16 tensor to
+    fill: x weight^T + bias is kept too, for the gradient.  out may be the
+    residual.  workspace: a contiguous CUDA tensor of at least the bytes
+    muon_linear_workspace says (default: a new one, if operands' rows do not
+    start on 16 bytes).  Returns out, or (out, pre)."""
+    lead = None if x.dim() == 2 else x.shape[:-1]
+    keep = pre is not False and pre is not None
+    given = out
+    r = _call("linear", x, stream, _joined(x, 1, stream), weight, bias, _activation(activation),
+              _joined(residual, 1, stream) if residual is not out else _joined_out(residual, 1), dropout, rng, site,
+              _joined_out(out, 1), out_dtype, _joined_out(pre, 1), workspace)
+    if lead is None and given is None and not keep:
+        return r
+    y, u = r if keep else (r, None)
+    if given is not None:
+        y = given
+    elif lead is not None:
+        y = y.view(*lead, y.shape[-1])
+    if not keep:
+        return y
+    if not isinstance(pre, bool):
+        u = pre
+    elif lead is not None:
+        u = u.view(*lead, u.shape[-1])
+    return y, u
+
+
+def linear_grad(accum, dout, x, weight, param=None, bias_param=None, parts=None, scale: float = 1.0,
+                overwrite: bool = False, activation=None, pre=None, dx=True, workspace=None, stream=None):
+    """The gradients of x weight^T + bias for dout (muon_linear_grad): returns
+    dx = (dout weight) * activation'(pre), where `activation` is the one before
+    this layer (x = activation(pre)); adds scale * dout^T x to the parameter
+    `param` of the flat FP32 buffer accum, and scale times dout's sum over the
+    tokens to `bias_param` (overwrite: puts them there).  param, parts: as
+    embedding_grad; None: that gradient is not taken (accum and x, which it
+    needs, may then be None).  dx: True (a new tensor), False (none; weight may
+    then be None) or a tensor to fill."""
+    lead = None if dout.dim() == 2 else dout.shape[:-1]
+    r = _call("linear_grad", dout, stream, accum, _joined(dout, 1, stream), _joined(x, 1, stream), weight,
+              _param(param), _param(bias_param), _parts(parts), scale, overwrite, _activation(activation),
+              _joined(pre, 1, stream), _joined_out(dx, 1), workspace)[0]
+    if not isinstance(dx, bool) and dx is not None:
+        return dx
+    return r if r is None or lead is None else r.view(*lead, r.shape[-1])
+
+
+def dropout(x, rate: float, rng, site: int = 0, residual=None, out=None, stream=None):
+    """residual + dropout(x) (muon_dropout), bf16 or fp32; the gradient is
+    dropout(dout, rate, rng, site) with the same generator (rng: an int64 CUDA
+    tensor (seed, step)).  The draws go by row (leading dimensions joined) and
+    column.  out may be x or the residual."""
+    shape = x.shape
+    flat_out = _joined_out(out, 1)
+    flat = lambda t: _joined_out(t, 1) if t is out else _joined(t, 1, stream)  # noqa: E731
+    r = _call("dropout", x, stream, flat(x), rate, rng, site, flat(residual), flat_out)
+    if out is not None:
+        return out
+    return r if len(shape) == 2 else r.view(shape)
+
+
+def rotary_frequencies(dims: int, base: float = 10000.0, sections=None, own_ladder: bool = False):
+    """(inv_freq, axis) of a rotation of the first `dims` elements of each head:
+    pair i turns base^(-2 i / dims) radians a position.  sections: how many
+    pairs follow each position axis (time, height, width, ...), in order;
+    own_ladder: the frequencies start anew in each section, base^(-j / section)."""
+    if dims % 2:
+        raise ValueError("dims must be even")
+    pairs = dims // 2
+    sections = [pairs] if sections is None else [int(n) for n in sections]
+    if sum(sections) != pairs or min(sections, default=0) < 0:
+        raise ValueError("sections must add up to dims / 2")
+    axis = np.repeat(np.arange(len(sections), dtype=np.int32), sections)
+    if own_ladder:
+        power = np.concatenate([np.arange(n) / max(n, 1) for n in sections])
+    else:
+        power = np.arange(pairs) / max(pairs, 1)
+    return np.float64(base) ** -power.astype(np.float64), axis
+
+
+def norm_rotary(q, k=None, positions=None, inv_freq=None, axis=None, interleaved: bool = False,
+                norm: bool = True, q_weight=None, k_weight=None, eps: float = 1e-6, q_out=None,
+                k_out=None, stream=None):
+    """Heads normalised and turned by their positions (muon_norm_rotary), queries
+    and keys in one pass: q and k tokens x heads x head_dim (leading dimensions
+    are joined), bf16 or fp32, of any strides whose heads are contiguous, such
+    as parts of one packed projection.  positions: int32 or int64, one per
+    token or tokens x axes, a negative one meaning "no token" (zeros);
+    inv_freq, axis: numpy float64 and int32, as rotary_frequencies gives them,
+    None: no rotation; norm: divide by the root mean square, times the weight
+    if there is one.  q_out, k_out: tensors to fill, q and k themselves too.
+    Returns (q, k), k None where none was given."""
+    lead = None if q.dim() == 3 else q.shape[:-2]
+    flat = lambda t, o: _joined_out(t, 2) if t is o else _joined(t, 2, stream)  # noqa: E731
+    a, b = _call("norm_rotary", q, stream, flat(q, q_out), flat(k, k_out), positions, inv_freq, axis, interleaved, norm,
+                 q_weight, k_weight, eps, _joined_out(q_out, 2), _joined_out(k_out, 2))
+    return _heads_back(a, q_out, lead), _heads_back(b, k_out, lead)
+
+
+def _heads_back(t, given, lead):
+    if given is not None:
+        return given
+    return t if t is None or lead is None else t.view(*lead, *t.shape[1:])
+
+
+def norm_rotary_grad(dq, q, dk=None, k=None, positions=None, inv_freq=None, axis=None,
+                     interleaved: bool = False, norm: bool = True, q_weight=None, k_weight=None,
+                     eps: float = 1e-6, accum=None, q_param=None, k_param=None, parts=None,
+                     scale: float = 1.0, overwrite: bool = False, dq_out=None, dk_out=None,
+                     workspace=None, stream=None):
+    """The gradients of norm_rotary (muon_norm_rotary_grad) for dq and dk: returns
+    those of q and k (q and k: the heads before the norm, not needed without
+    it), and adds scale times those of the weights to q_param and k_param of
+    accum (overwrite: puts them there; None: they are not taken).  dq_out,
+    dk_out: tensors to fill, dq and dk themselves too.  workspace: a contiguous
+    CUDA tensor of at least norm_rotary_grad_workspace(tokens, head_dim) bytes
+    (default: a new one)."""
+    lead = None if dq.dim() == 3 else dq.shape[:-2]
+    flat = lambda t, o: _joined_out(t, 2) if t is o else _joined(t, 2, stream)  # noqa: E731
+    a, b = _call("norm_rotary_grad", dq, stream, flat(dq, dq_out), flat(q, dq_out), flat(dk, dk_out), flat(k, dk_out),
+                 positions, inv_freq, axis, interleaved, norm, q_weight, k_weight, eps, accum, _param(q_param),
+                 _param(k_param), _parts(parts), scale, overwrite, _joined_out(dq_out, 2), _joined_out(dk_out, 2),
+                 workspace)
+    return _heads_back(a, dq_out, lead), _heads_back(b, dk_out, lead)
+
+
+def norm_rotary_grad_workspace(n_tokens: int, head_dim: int) -> int:
+    """Bytes of scratch norm_rotary_grad needs for the weights' gradients."""
+    b = ctypes.c_size_t()
+    _check(lib().muon_norm_rotary_grad_workspace(n_tokens, head_dim, ctypes.byref(b)))
     return b.value
 
 

@@ -1,4 +1,4 @@
-/* Argument marshalling of the embedding and loss calls, in C.
+/* Argument marshalling of the embedding, loss and layer calls, in C.
  *
  * A call on a few tokens is a few microseconds of GPU time; looking at a dozen
  * tensors' types, shapes and addresses in Python took two to five times that.
@@ -10,6 +10,7 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 #include <limits.h>
+#include <string.h>
 
 #include "../../include/muon.h"
 
@@ -33,6 +34,18 @@ static struct {
   int (*preference_loss)(const void*, int, int64_t, int64_t, int, const void*, int, const void*, int, int,
                          const float*, const float*, float, float, float, float*, float*, float*, void*, int64_t,
                          void*, size_t, void*);
+  int (*linear_workspace)(const muon_linear_args_t*, size_t*);
+  int (*linear)(const muon_linear_args_t*, void*, size_t, void*);
+  int (*linear_grad_workspace)(const muon_linear_grad_args_t*, size_t*);
+  int (*linear_grad)(const muon_linear_grad_args_t*, void*, size_t, void*);
+  int (*dropout)(const void*, int64_t, const void*, int64_t, void*, int64_t, int, int64_t, int, float,
+                 const int64_t*, uint32_t, void*);
+  int (*norm_rotary)(const muon_heads_t*, int, int, int64_t, int, int, float, const void*, int, int, const double*,
+                     const int32_t*, int, int, void*);
+  int (*norm_rotary_grad_workspace)(int64_t, int, size_t*);
+  int (*norm_rotary_grad)(const muon_heads_grad_t*, int, int, int64_t, int, int, float, const void*, int, int,
+                          const double*, const int32_t*, int, int, float*, int64_t, const muon_partition_t*, int,
+                          float, int, void*, size_t, void*);
 } g;
 
 /* ------------------------------------------------------------------ tensors */
@@ -538,6 +551,604 @@ end:
   return answer;
 }
 
+/* ------------------------------------------------------------------ layers */
+
+/* Scratch of `need` bytes: the caller's (checked by the library) or a new one.
+ * *work: a new reference, or NULL where none is needed. */
+static int provide(PyObject* given, size_t need, PyObject* like, PyObject** work, void** p, size_t* bytes) {
+  *work = NULL;
+  *p = NULL;
+  *bytes = 0;
+  if (given != Py_None) {
+    long long have;
+    if (scratch(given, p, &have)) return -1;
+    *bytes = (size_t)have;
+    Py_INCREF(given);
+    *work = given;
+  } else if (need > 0) {
+    if (!(*work = make_flat((long long)need, g.uint8, like))) return -1;
+    if (address(*work, p)) {
+      Py_CLEAR(*work);
+      return -1;
+    }
+    *bytes = need;
+  }
+  return 0;
+}
+
+/* A bfloat16 matrix. */
+static int bf16_rows(PyObject* t, const char* name, Shape* s, void** p) {
+  int kind;
+  if (rows_of(t, name, s) || element_kind(t, name, &kind)) return -1;
+  if (kind) return refuse("%s must be bfloat16", name);
+  return address(t, p);
+}
+
+/* A matrix of the given shape, and of the given kind if that is not -1. */
+static int matrix(PyObject* t, const char* name, long long rows, long long cols, int kind, Shape* s, void** p) {
+  int k;
+  if (rows_of(t, name, s) || element_kind(t, name, &k)) return -1;
+  if (s->rows != rows || s->cols != cols || (kind >= 0 && k != kind)) {
+    PyErr_Format(PyExc_ValueError, "%s must be %lld x %lld%s", name, rows, cols,
+                 kind < 0 ? "" : kind ? ", float32" : ", bfloat16");
+    return -1;
+  }
+  return address(t, p);
+}
+
+/* Two int64: seed and step. */
+static int generator(PyObject* t, void** p) {
+  *p = NULL;
+  if (t == Py_None) return 0;
+  PyObject* d = PyObject_GetAttr(t, g.s_dtype);
+  if (!d) return -1;
+  const int fits = d == g.int64;
+  Py_DECREF(d);
+  long long n;
+  if (ask(t, g.s_numel, &n)) return -1;
+  if (!fits || n != 2) return refuse("%s must be a contiguous int64 tensor of 2 elements (seed, step)", "rng");
+  return contiguous(t, "rng") ? -1 : address(t, p);
+}
+
+static int site_of(PyObject* o, uint32_t* out) {
+  const long long v = PyLong_AsLongLong(o);
+  if (v == -1 && PyErr_Occurred()) return -1;
+  *out = (uint32_t)v;
+  return v >= 0 && v <= 0xffffffffll ? 0 : refuse("%s must be in [0, 2^32)", "site");
+}
+
+/* A tensor's shape with another last dimension, as a new matrix's size. */
+static PyObject* make_rows(long long rows, long long cols, PyObject* dtype, PyObject* like) {
+  return make(Py_BuildValue("(LL)", rows, cols), dtype, like);
+}
+
+/* linear(x, weight, bias, activation, residual, rate, rng, site, out, out_dtype, pre, workspace); x, residual, out and
+ * pre are matrices.  Returns out, or (out, pre). */
+static PyObject* py_linear(PyObject* self, PyObject* const* a, Py_ssize_t na) {
+  (void)self;
+  if (arity(na, 12)) return NULL;
+  muon_linear_args_t l = {0};
+  Shape x, w, s;
+  void *p, *pw, *stream;
+  long long n, device;
+  PyObject *out = NULL, *pre = NULL, *work = NULL, *answer = NULL;
+  const int keep_pre = PyBool_Check(a[10]) ? a[10] == Py_True : a[10] != Py_None;
+  const long act = PyLong_AsLong(a[3]);
+  if (act == -1 && PyErr_Occurred()) return NULL;
+  if (bf16_rows(a[0], "x", &x, &p)) return NULL;
+  l.x = p;
+  if (bf16_rows(a[1], "weight", &w, &p)) return NULL;
+  l.weight = p;
+  if (w.cols != x.cols) return refuse("%s must be out_features x in_features", "weight"), NULL;
+  if (w.rows > INT_MAX) return refuse("%s has too many rows", "weight"), NULL;
+  int kind = a[9] == Py_None ? 0 : a[9] == g.fp32 ? 1 : a[9] == g.bf16 ? 0 : -1;
+  if (kind < 0) return refuse("%s must be bfloat16 or float32", "out_dtype"), NULL;
+  if (a[8] != Py_None) {
+    int ok;
+    if (element_kind(a[8], "out", &ok)) return NULL;
+    if (a[9] != Py_None && ok != kind) return refuse("%s is not of out_dtype", "out"), NULL;
+    kind = ok;
+  } else if (a[9] == Py_None && a[4] != Py_None && element_kind(a[4], "residual", &kind)) {
+    return NULL;
+  }
+  if (a[2] != Py_None) {
+    if (element_kind(a[2], "bias", &l.bias_dtype) || ask(a[2], g.s_numel, &n)) return NULL;
+    if (n != w.rows) return refuse("%s must have out_features elements", "bias"), NULL;
+    if (contiguous(a[2], "bias") || address(a[2], &p)) return NULL;
+    l.bias = p;
+  }
+  if (a[4] != Py_None) {
+    if (matrix(a[4], "residual", x.rows, w.rows, kind, &s, &p)) return NULL;
+    l.residual = p;
+    l.residual_stride = s.stride;
+  }
+  if (real(a[5], &l.dropout) || generator(a[6], &p) || site_of(a[7], &l.site)) return NULL;
+  l.rng = p;
+  PyObject* tensors[8] = {a[0], a[1], a[2], a[4], a[6], a[8], PyBool_Check(a[10]) ? NULL : a[10], a[11]};
+  const int here = placed(tensors, 8, &device);
+  if (here < 0) return NULL;
+  if (here == 0) Py_RETURN_NONE;
+  if (a[8] != Py_None) {
+    if (matrix(a[8], "out", x.rows, w.rows, kind, &s, &p)) return NULL;
+    Py_INCREF(a[8]);
+    out = a[8];
+    l.out_stride = s.stride;
+  } else {
+    if (!(out = make_rows(x.rows, w.rows, kind ? g.fp32 : g.bf16, a[0])) || address(out, &p)) goto end;
+    l.out_stride = w.rows;
+  }
+  l.out = p;
+  if (keep_pre) {
+    if (!PyBool_Check(a[10])) {
+      if (matrix(a[10], "pre", x.rows, w.rows, 0, &s, &p)) goto end;
+      Py_INCREF(a[10]);
+      pre = a[10];
+      l.pre_stride = s.stride;
+    } else {
+      if (!(pre = make_rows(x.rows, w.rows, g.bf16, a[0])) || address(pre, &p)) goto end;
+      l.pre_stride = w.rows;
+    }
+    l.pre = x.rows ? p : NULL;
+  }
+  l.struct_size = (int32_t)sizeof(l);
+  l.activation = (int32_t)act;
+  l.n_tokens = x.rows;
+  l.in_features = (int32_t)x.cols;
+  l.out_features = (int32_t)w.rows;
+  l.x_stride = x.stride;
+  l.weight_stride = w.stride;
+  l.out_dtype = kind;
+  size_t need, bytes;
+  if (done(g.linear_workspace(&l, &need)) || provide(a[11], need, a[0], &work, &pw, &bytes) ||
+      stream_of(device, &stream))
+    goto end;
+  int rc;
+  Py_BEGIN_ALLOW_THREADS
+  rc = g.linear(&l, pw, bytes, stream);
+  Py_END_ALLOW_THREADS
+  if (done(rc)) goto end;
+  if (keep_pre) {
+    answer = PyTuple_Pack(2, out, pre);
+  } else {
+    Py_INCREF(out);
+    answer = out;
+  }
+end:
+  Py_XDECREF(out);
+  Py_XDECREF(pre);
+  Py_XDECREF(work);
+  return answer;
+}
+
+/* A parameter as a tuple (offset, rows, cols), or None. */
+static int param_of(PyObject* o, const char* name, muon_param_t* p, const muon_param_t** out) {
+  *out = NULL;
+  if (o == Py_None) return 0;
+  long long offset, rows, cols;
+  if (!PyTuple_Check(o) || !PyArg_ParseTuple(o, "LLL", &offset, &rows, &cols)) {
+    if (!PyErr_Occurred()) refuse("%s must be (offset, rows, cols)", name);
+    return -1;
+  }
+  if (rows > INT_MAX || rows < INT_MIN || cols > INT_MAX || cols < INT_MIN)
+    return refuse("%s has too many rows or columns", name);
+  p->offset = offset;
+  p->rows = (int32_t)rows;
+  p->cols = (int32_t)cols;
+  p->num_heads = p->use_muon = 0;
+  *out = p;
+  return 0;
+}
+
+/* accum and the partition table (bytes or None) a gradient is put in. */
+typedef struct {
+  void* accum;
+  long long elems;
+  char* table;
+  Py_ssize_t bytes;
+  float scale;
+  int overwrite;
+} Sums;
+
+static int sums_of(PyObject* accum, PyObject* parts, PyObject* scale, PyObject* overwrite, int wanted, Sums* s) {
+  *s = (Sums){0};
+  if (real(scale, &s->scale)) return -1;
+  s->overwrite = PyObject_IsTrue(overwrite);
+  if (s->overwrite < 0) return -1;
+  if (parts != Py_None && PyBytes_AsStringAndSize(parts, &s->table, &s->bytes)) return -1;
+  if (accum == Py_None) return wanted ? refuse("%s is needed for the gradient of a parameter", "accum") : 0;
+  return ask(accum, g.s_numel, &s->elems) || per_token(accum, s->elems, 0, "accum", &s->accum) ? -1 : 0;
+}
+
+/* linear_grad(accum, dout, x, weight, param, bias_param, partition table, scale, overwrite, activation, pre, dx,
+ *             workspace); dout, x, pre and dx are matrices.  Returns dx or None, in a tuple (None means another
+ *             device here). */
+static PyObject* py_linear_grad(PyObject* self, PyObject* const* a, Py_ssize_t na) {
+  (void)self;
+  if (arity(na, 13)) return NULL;
+  muon_linear_grad_args_t l = {0};
+  muon_param_t param, bias;
+  Shape d, x, s;
+  Sums sums;
+  void *p, *pw, *stream;
+  long long device;
+  PyObject *dx = NULL, *work = NULL, *answer = NULL;
+  const int want_dx = PyBool_Check(a[11]) ? a[11] == Py_True : a[11] != Py_None;
+  const long act = PyLong_AsLong(a[9]);
+  if (act == -1 && PyErr_Occurred()) return NULL;
+  if (bf16_rows(a[1], "dout", &d, &p)) return NULL;
+  l.dout = p;
+  if (param_of(a[4], "param", &param, &l.param) || param_of(a[5], "bias_param", &bias, &l.bias)) return NULL;
+  if (d.cols > INT_MAX) return refuse("%s has too many columns", "dout"), NULL;
+  long long in = -1;
+  if (a[2] != Py_None) {
+    if (bf16_rows(a[2], "x", &x, &p)) return NULL;
+    if (x.rows != d.rows) return refuse("%s must have dout's tokens", "x"), NULL;
+    l.x = p;
+    l.x_stride = x.stride;
+    in = x.cols;
+  } else if (l.param && d.rows) {
+    return refuse("%s is needed for the weight's gradient", "x"), NULL;
+  }
+  if (a[3] != Py_None) {
+    if (bf16_rows(a[3], "weight", &s, &p)) return NULL;
+    if (s.rows != d.cols || (in >= 0 && s.cols != in))
+      return refuse("%s must be out_features x in_features", "weight"), NULL;
+    l.weight = p;
+    l.weight_stride = s.stride;
+    in = s.cols;
+  } else if (want_dx) {
+    return refuse("%s is needed for dx", "weight"), NULL;
+  }
+  if (in < 0) in = l.param ? l.param->cols : 1;
+  if (sums_of(a[0], a[6], a[7], a[8], l.param || l.bias, &sums)) return NULL;
+  if (a[10] != Py_None) {
+    if (matrix(a[10], "pre", d.rows, in, 0, &s, &p)) return NULL;
+    l.pre = p;
+    l.pre_stride = s.stride;
+  } else if (want_dx && act != MUON_ACT_NONE && d.rows) {
+    return refuse("%s is needed for the activation's slope", "pre"), NULL;
+  }
+  PyObject* tensors[7] = {a[1], a[0], a[2], a[3], a[10], PyBool_Check(a[11]) ? NULL : a[11], a[12]};
+  const int here = placed(tensors, 7, &device);
+  if (here < 0) return NULL;
+  if (here == 0) Py_RETURN_NONE;
+  if (want_dx) {
+    if (!PyBool_Check(a[11])) {
+      if (matrix(a[11], "dx", d.rows, in, 0, &s, &p)) return NULL;
+      Py_INCREF(a[11]);
+      dx = a[11];
+      l.dx_stride = s.stride;
+    } else {
+      if (!(dx = make_rows(d.rows, in, g.bf16, a[1])) || address(dx, &p)) goto end;
+      l.dx_stride = in;
+    }
+    l.dx = p;
+  }
+  l.struct_size = (int32_t)sizeof(l);
+  l.activation = (int32_t)act;
+  l.n_tokens = d.rows;
+  l.in_features = (int32_t)in;
+  l.out_features = (int32_t)d.cols;
+  l.dout_stride = d.stride;
+  l.accum = sums.accum;
+  l.accum_elems = sums.elems;
+  l.parts = (const muon_partition_t*)sums.table;
+  l.nparts = (int32_t)(sums.bytes / (Py_ssize_t)sizeof(muon_partition_t));
+  l.scale = sums.scale;
+  l.overwrite = sums.overwrite;
+  size_t need, bytes;
+  if (done(g.linear_grad_workspace(&l, &need)) || provide(a[12], need, a[1], &work, &pw, &bytes) ||
+      stream_of(device, &stream))
+    goto end;
+  int rc;
+  Py_BEGIN_ALLOW_THREADS
+  rc = g.linear_grad(&l, pw, bytes, stream);
+  Py_END_ALLOW_THREADS
+  if (done(rc)) goto end;
+  answer = PyTuple_Pack(1, dx ? dx : Py_None);
+end:
+  Py_XDECREF(dx);
+  Py_XDECREF(work);
+  return answer;
+}
+
+/* dropout(x, rate, rng, site, residual, out); matrices. */
+static PyObject* py_dropout(PyObject* self, PyObject* const* a, Py_ssize_t na) {
+  (void)self;
+  if (arity(na, 6)) return NULL;
+  Shape x, r = {0}, o;
+  int kind;
+  float rate;
+  uint32_t site;
+  long long device;
+  void *px, *pr = NULL, *po, *rng, *stream;
+  PyObject* out;
+  if (rows_of(a[0], "x", &x) || element_kind(a[0], "x", &kind) || address(a[0], &px) || real(a[1], &rate) ||
+      generator(a[2], &rng) || site_of(a[3], &site) ||
+      (a[4] != Py_None && matrix(a[4], "residual", x.rows, x.cols, kind, &r, &pr)))
+    return NULL;
+  PyObject* tensors[4] = {a[0], a[2], a[4], a[5]};
+  const int here = placed(tensors, 4, &device);
+  if (here < 0) return NULL;
+  if (here == 0) Py_RETURN_NONE;
+  if (a[5] != Py_None) {
+    if (matrix(a[5], "out", x.rows, x.cols, kind, &o, &po)) return NULL;
+    Py_INCREF(a[5]);
+    out = a[5];
+  } else {
+    if (!(out = make_rows(x.rows, x.cols, kind ? g.fp32 : g.bf16, a[0]))) return NULL;
+    o.stride = x.cols;
+    if (address(out, &po)) goto fail;
+  }
+  if (stream_of(device, &stream)) goto fail;
+  int rc;
+  Py_BEGIN_ALLOW_THREADS
+  rc = g.dropout(px, x.stride, pr, r.stride, po, o.stride, kind, x.rows, (int)x.cols, rate, rng, site, stream);
+  Py_END_ALLOW_THREADS
+  if (done(rc)) goto fail;
+  return out;
+fail:
+  Py_DECREF(out);
+  return NULL;
+}
+
+/* A tensor of heads: tokens x heads x head_dim, elements of a head contiguous. */
+typedef struct {
+  long long n, heads, dim, stride, head;
+} HeadShape;
+
+static int heads_of(PyObject* t, const char* name, HeadShape* out) {
+  PyObject* shape = PyObject_GetAttr(t, g.s_shape);
+  if (!shape) return -1;
+  PyObject* stride = PyObject_CallMethodNoArgs(t, g.s_stride);
+  if (!stride) {
+    Py_DECREF(shape);
+    return -1;
+  }
+  const int three = PyTuple_Check(shape) && PyTuple_GET_SIZE(shape) == 3 && PyTuple_Check(stride) &&
+                    PyTuple_GET_SIZE(stride) == 3;
+  long long along = 1;
+  if (three) {
+    out->n = PyLong_AsLongLong(PyTuple_GET_ITEM(shape, 0));
+    out->heads = PyLong_AsLongLong(PyTuple_GET_ITEM(shape, 1));
+    out->dim = PyLong_AsLongLong(PyTuple_GET_ITEM(shape, 2));
+    out->stride = PyLong_AsLongLong(PyTuple_GET_ITEM(stride, 0));
+    out->head = PyLong_AsLongLong(PyTuple_GET_ITEM(stride, 1));
+    along = PyLong_AsLongLong(PyTuple_GET_ITEM(stride, 2));
+  }
+  Py_DECREF(shape);
+  Py_DECREF(stride);
+  if (PyErr_Occurred()) return -1;
+  if (!three) return refuse("%s must be tokens x heads x head_dim", name);
+  if (along != 1 && out->dim > 1) return refuse("%s's heads must be contiguous", name);
+  if (out->heads > INT_MAX || out->dim > INT_MAX) return refuse("%s is too large", name);
+  /* strides of dimensions with one element say nothing */
+  if (out->heads == 1) out->head = out->dim;
+  if (out->n == 1) out->stride = (out->heads - 1) * out->head + out->dim;
+  return 0;
+}
+
+static int same_heads(PyObject* t, const char* name, const HeadShape* want, int kind, HeadShape* s, void** p) {
+  int k;
+  if (heads_of(t, name, s) || element_kind(t, name, &k)) return -1;
+  if (k != kind || s->n != want->n || s->heads != want->heads || s->dim != want->dim)
+    return refuse("%s must have the heads' shape and type", name);
+  return address(t, p);
+}
+
+static int head_weight(PyObject* t, const char* name, long long dim, int kind, const void** out) {
+  *out = NULL;
+  if (t == Py_None) return 0;
+  int k;
+  long long n;
+  void* p;
+  if (element_kind(t, name, &k) || ask(t, g.s_numel, &n)) return -1;
+  if (k != kind || n != dim) return refuse("%s must have head_dim elements of the heads' type", name);
+  if (contiguous(t, name) || address(t, &p)) return -1;
+  *out = p;
+  return 0;
+}
+
+/* positions (tensor or None), inv_freq and axis (buffers of float64 and int32, or None). */
+typedef struct {
+  void* positions;
+  int type, axes, pairs, interleaved, norm;
+  float eps;
+  Py_buffer freq, axis;
+} Turns;
+
+static void turns_gone(Turns* t) {
+  if (t->freq.obj) PyBuffer_Release(&t->freq);
+  if (t->axis.obj) PyBuffer_Release(&t->axis);
+}
+
+static int turns_of(PyObject* positions, PyObject* freq, PyObject* axis, PyObject* interleaved, PyObject* norm,
+                    PyObject* eps, long long n, Turns* t) {
+  *t = (Turns){0};
+  t->axes = 1;
+  t->interleaved = PyObject_IsTrue(interleaved);
+  t->norm = PyObject_IsTrue(norm);
+  if (t->interleaved < 0 || t->norm < 0 || real(eps, &t->eps)) return -1;
+  if (freq == Py_None) return 0;
+  if (PyObject_GetBuffer(freq, &t->freq, PyBUF_ND | PyBUF_FORMAT)) return -1;
+  if (t->freq.ndim != 1 || t->freq.itemsize != 8 || !t->freq.format || t->freq.format[strlen(t->freq.format) - 1] != 'd')
+    return refuse("%s must be a 1-D float64 array", "inv_freq");
+  if (t->freq.len / 8 > INT_MAX) return refuse("%s is too long", "inv_freq");
+  t->pairs = (int)(t->freq.len / 8);
+  if (axis != Py_None) {
+    if (PyObject_GetBuffer(axis, &t->axis, PyBUF_ND | PyBUF_FORMAT)) return -1;
+    if (t->axis.ndim != 1 || t->axis.itemsize != 4 || !t->axis.format ||
+        t->axis.format[strlen(t->axis.format) - 1] != 'i' || t->axis.len / 4 != t->pairs)
+      return refuse("%s must be a 1-D int32 array of inv_freq's length", "axis");
+  }
+  if (positions == Py_None) return t->pairs ? refuse("%s are needed for a rotation", "positions") : 0;
+  long long count;
+  if (index_kind(positions, "positions", &t->type) || ask(positions, g.s_numel, &count) ||
+      address(positions, &t->positions))
+    return -1;
+  PyObject* shape = PyObject_GetAttr(positions, g.s_shape);
+  if (!shape) return -1;
+  long long axes = 1;
+  if (count != n) {
+    const Py_ssize_t dims = PyTuple_GET_SIZE(shape);
+    axes = dims ? PyLong_AsLongLong(PyTuple_GET_ITEM(shape, dims - 1)) : -1;
+  }
+  Py_DECREF(shape);
+  if (axes < 1 || axes > INT_MAX || count != n * axes)
+    return refuse("%s must be one per token, or tokens x axes", "positions");
+  t->axes = (int)axes;
+  return 0;
+}
+
+static PyObject* new_heads(const HeadShape* s, int kind, PyObject* like) {
+  return make(Py_BuildValue("(LLL)", s->n, s->heads, s->dim), kind ? g.fp32 : g.bf16, like);
+}
+
+/* norm_rotary(q, k, positions, inv_freq, axis, interleaved, norm, q_weight, k_weight, eps, q_out, k_out); returns
+ * (q, k or None). */
+static PyObject* py_norm_rotary(PyObject* self, PyObject* const* a, Py_ssize_t na) {
+  (void)self;
+  if (arity(na, 12)) return NULL;
+  muon_heads_t h[2] = {{0}, {0}};
+  HeadShape s[2], o;
+  Turns t = {0};
+  int kind, rc = 0;
+  long long device;
+  void *p, *stream;
+  PyObject *outs[2] = {NULL, NULL}, *answer = NULL;
+  static const char* const names[2][3] = {{"q", "q_weight", "q_out"}, {"k", "k_weight", "k_out"}};
+  const int groups = a[1] == Py_None ? 1 : 2;
+  if (element_kind(a[0], "q", &kind)) return NULL;
+  for (int i = 0; i < groups; ++i) {
+    int other;
+    if (heads_of(a[i], names[i][0], &s[i]) || element_kind(a[i], names[i][0], &other) || address(a[i], &p)) return NULL;
+    if (other != kind || s[i].n != s[0].n || s[i].dim != s[0].dim)
+      return refuse("%s must have q's tokens, head_dim and type", names[i][0]), NULL;
+    h[i].x = p;
+    h[i].x_stride = s[i].stride;
+    h[i].x_head_stride = s[i].head;
+    h[i].heads = (int32_t)s[i].heads;
+    if (head_weight(a[7 + i], names[i][1], s[0].dim, kind, &h[i].weight)) return NULL;
+  }
+  if (turns_of(a[2], a[3], a[4], a[5], a[6], a[9], s[0].n, &t)) goto end;
+  PyObject* tensors[7] = {a[0], a[1], a[2], a[7], a[8], a[10], a[11]};
+  const int here = placed(tensors, 7, &device);
+  if (here < 0) goto end;
+  if (here == 0) {
+    turns_gone(&t);
+    Py_RETURN_NONE;
+  }
+  for (int i = 0; i < groups; ++i) {
+    if (a[10 + i] != Py_None) {
+      if (same_heads(a[10 + i], names[i][2], &s[i], kind, &o, &p)) goto end;
+      Py_INCREF(a[10 + i]);
+      outs[i] = a[10 + i];
+    } else {
+      if (!(outs[i] = new_heads(&s[i], kind, a[0])) || address(outs[i], &p)) goto end;
+      o.head = s[i].dim;
+      o.stride = s[i].heads * s[i].dim;
+    }
+    h[i].out = p;
+    h[i].out_stride = o.stride;
+    h[i].out_head_stride = o.head;
+  }
+  if (stream_of(device, &stream)) goto end;
+  Py_BEGIN_ALLOW_THREADS
+  rc = g.norm_rotary(h, groups, kind, s[0].n, (int)s[0].dim, t.norm, t.eps, t.positions, t.type, t.axes, t.freq.buf,
+                     t.axis.buf, t.pairs, t.interleaved, stream);
+  Py_END_ALLOW_THREADS
+  if (done(rc)) goto end;
+  answer = PyTuple_Pack(2, outs[0], outs[1] ? outs[1] : Py_None);
+end:
+  turns_gone(&t);
+  Py_XDECREF(outs[0]);
+  Py_XDECREF(outs[1]);
+  return answer;
+}
+
+/* norm_rotary_grad(dq, q, dk, k, positions, inv_freq, axis, interleaved, norm, q_weight, k_weight, eps, accum, q_param,
+ *                  k_param, partition table, scale, overwrite, dq_out, dk_out, workspace); returns (dq, dk or None). */
+static PyObject* py_norm_rotary_grad(PyObject* self, PyObject* const* a, Py_ssize_t na) {
+  (void)self;
+  if (arity(na, 21)) return NULL;
+  muon_heads_grad_t h[2] = {{0}, {0}};
+  muon_param_t params[2];
+  HeadShape s[2], o;
+  Turns t = {0};
+  Sums sums;
+  int kind, rc = 0;
+  long long device;
+  size_t need = 0, bytes;
+  void *p, *pw, *stream;
+  PyObject *outs[2] = {NULL, NULL}, *work = NULL, *answer = NULL;
+  static const char* const names[2][5] = {{"dq", "q", "q_weight", "q_param", "dq_out"},
+                                          {"dk", "k", "k_weight", "k_param", "dk_out"}};
+  const int groups = a[2] == Py_None ? 1 : 2;
+  if (element_kind(a[0], "dq", &kind)) return NULL;
+  for (int i = 0; i < groups; ++i) {
+    int other;
+    if (heads_of(a[2 * i], names[i][0], &s[i]) || element_kind(a[2 * i], names[i][0], &other) ||
+        address(a[2 * i], &p))
+      return NULL;
+    if (other != kind || s[i].n != s[0].n || s[i].dim != s[0].dim)
+      return refuse("%s must have dq's tokens, head_dim and type", names[i][0]), NULL;
+    h[i].dout = p;
+    h[i].dout_stride = s[i].stride;
+    h[i].dout_head_stride = s[i].head;
+    h[i].heads = (int32_t)s[i].heads;
+    if (a[2 * i + 1] != Py_None) {
+      if (same_heads(a[2 * i + 1], names[i][1], &s[i], kind, &o, &p)) return NULL;
+      h[i].x = p;
+      h[i].x_stride = o.stride;
+      h[i].x_head_stride = o.head;
+    }
+    if (head_weight(a[9 + i], names[i][2], s[0].dim, kind, &h[i].weight) ||
+        param_of(a[13 + i], names[i][3], &params[i], &h[i].param))
+      return NULL;
+  }
+  if (sums_of(a[12], a[15], a[16], a[17], h[0].param || h[1].param, &sums)) return NULL;
+  if (turns_of(a[4], a[5], a[6], a[7], a[8], a[11], s[0].n, &t)) goto end;
+  PyObject* tensors[11] = {a[0], a[1], a[2], a[3], a[4], a[9], a[10], a[12], a[18], a[19], a[20]};
+  const int here = placed(tensors, 11, &device);
+  if (here < 0) goto end;
+  if (here == 0) {
+    turns_gone(&t);
+    Py_RETURN_NONE;
+  }
+  for (int i = 0; i < groups; ++i) {
+    if (a[18 + i] != Py_None) {
+      if (same_heads(a[18 + i], names[i][4], &s[i], kind, &o, &p)) goto end;
+      Py_INCREF(a[18 + i]);
+      outs[i] = a[18 + i];
+    } else {
+      if (!(outs[i] = new_heads(&s[i], kind, a[0])) || address(outs[i], &p)) goto end;
+      o.head = s[i].dim;
+      o.stride = s[i].heads * s[i].dim;
+    }
+    h[i].dx = p;
+    h[i].dx_stride = o.stride;
+    h[i].dx_head_stride = o.head;
+  }
+  if (((h[0].param || h[1].param) && done(g.norm_rotary_grad_workspace(s[0].n, (int)s[0].dim, &need))) ||
+      provide(a[20], need, a[0], &work, &pw, &bytes) || stream_of(device, &stream))
+    goto end;
+  Py_BEGIN_ALLOW_THREADS
+  rc = g.norm_rotary_grad(h, groups, kind, s[0].n, (int)s[0].dim, t.norm, t.eps, t.positions, t.type, t.axes,
+                          t.freq.buf, t.axis.buf, t.pairs, t.interleaved, sums.accum, sums.elems,
+                          (const muon_partition_t*)sums.table,
+                          (int)(sums.bytes / (Py_ssize_t)sizeof(muon_partition_t)), sums.scale, sums.overwrite, pw,
+                          bytes, stream);
+  Py_END_ALLOW_THREADS
+  if (done(rc)) goto end;
+  answer = PyTuple_Pack(2, outs[0], outs[1] ? outs[1] : Py_None);
+end:
+  turns_gone(&t);
+  Py_XDECREF(outs[0]);
+  Py_XDECREF(outs[1]);
+  Py_XDECREF(work);
+  return answer;
+}
+
 /* ------------------------------------------------------------------ set-up */
 
 static int keep(PyObject** slot, PyObject* from, const char* name) {
@@ -578,6 +1189,18 @@ static PyObject* py_init(PyObject* self, PyObject* const* a, Py_ssize_t na) {
       ENTRY(policy_loss, "muon_policy_loss") || ENTRY(preference_loss_workspace, "muon_preference_loss_workspace") ||
       ENTRY(preference_loss, "muon_preference_loss"))
     return NULL;
+  Py_RETURN_NONE;
+}
+
+/* init_layers({name: address of the library's function}), after init */
+static PyObject* py_init_layers(PyObject* self, PyObject* const* a, Py_ssize_t na) {
+  (void)self;
+  if (arity(na, 1)) return NULL;
+#undef ENTRY
+#define ENTRY(slot) entry(a[0], "muon_" #slot, (void**)&g.slot)
+  if (ENTRY(linear_workspace) || ENTRY(linear) || ENTRY(linear_grad_workspace) || ENTRY(linear_grad) ||
+      ENTRY(dropout) || ENTRY(norm_rotary) || ENTRY(norm_rotary_grad_workspace) || ENTRY(norm_rotary_grad))
+    return NULL;
 #undef ENTRY
   Py_RETURN_NONE;
 }
@@ -589,6 +1212,12 @@ static PyMethodDef methods[] = {
     {"token_logprobs", (PyCFunction)(void (*)(void))py_token_logprobs, METH_FASTCALL, NULL},
     {"policy_loss", (PyCFunction)(void (*)(void))py_policy_loss, METH_FASTCALL, NULL},
     {"preference_loss", (PyCFunction)(void (*)(void))py_preference_loss, METH_FASTCALL, NULL},
+    {"init_layers", (PyCFunction)(void (*)(void))py_init_layers, METH_FASTCALL, NULL},
+    {"linear", (PyCFunction)(void (*)(void))py_linear, METH_FASTCALL, NULL},
+    {"linear_grad", (PyCFunction)(void (*)(void))py_linear_grad, METH_FASTCALL, NULL},
+    {"dropout", (PyCFunction)(void (*)(void))py_dropout, METH_FASTCALL, NULL},
+    {"norm_rotary", (PyCFunction)(void (*)(void))py_norm_rotary, METH_FASTCALL, NULL},
+    {"norm_rotary_grad", (PyCFunction)(void (*)(void))py_norm_rotary_grad, METH_FASTCALL, NULL},
     {NULL, NULL, 0, NULL}};
 
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", NULL, -1, methods, NULL, NULL, NULL, NULL};

@@ -15,9 +15,7 @@
 // So every sum has one fixed order, and the work is balanced whatever the ids.
 #include <algorithm>
 #include <cmath>
-#include <limits>
 #include <string>
-#include <vector>
 
 #include <cooperative_groups.h>
 
@@ -162,26 +160,6 @@ constexpr int kFew = 1024;           // tokens up to which k_embed_few is taken
 constexpr int kFewX = 256;
 constexpr int kFillX = 256;
 constexpr int kFillBlocks = 4;       // per SM
-
-// The parameter's runs in storage: elements [rel[i], rel[i + 1]) of the
-// parameter start at storage index at[i].
-struct Segments {
-  int n;
-  int64_t rel[MUON_EMBEDDING_MAX_SEGMENTS];
-  int64_t at[MUON_EMBEDDING_MAX_SEGMENTS];
-  int64_t numel;
-
-  // storage index of element i, and how many elements follow in one piece
-  __device__ __forceinline__ int64_t place(int64_t i, int64_t* room) const {
-    int lo = 0, hi = n - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) / 2;
-      if (rel[mid] <= i) lo = mid; else hi = mid - 1;
-    }
-    *room = (lo + 1 < n ? rel[lo + 1] : numel) - i;
-    return at[lo] + (i - rel[lo]);
-  }
-};
 
 struct Grad {
   float* accum;
@@ -718,51 +696,6 @@ Workspace workspace_of(int64_t n, int cols) {
   return w;
 }
 
-// The parameter's pieces in storage, in flat order.
-int segments_of(const muon_param_t& p, const muon_partition_t* parts, int nparts, Segments* out) {
-  const int64_t numel = int64_t(p.rows) * p.cols;
-  out->numel = numel;
-  if (p.offset > std::numeric_limits<int64_t>::max() - numel)
-    return efail(MUON_ERR_INVALID, "the parameter's end is past the range of an index");
-  if (nparts == 0) {
-    out->n = 1;
-    out->rel[0] = 0;
-    out->at[0] = p.offset;
-    return MUON_OK;
-  }
-  std::vector<std::pair<int64_t, int64_t>> st;
-  for (int i = 0; i < nparts; ++i) {
-    const muon_partition_t& q = parts[i];
-    if (q.flat_begin < 0 || q.flat_end < q.flat_begin || q.storage_offset < 0 ||
-        q.storage_offset > std::numeric_limits<int64_t>::max() - (q.flat_end - q.flat_begin))
-      return efail(MUON_ERR_INVALID, "partition " + std::to_string(i) + " has a bad range");
-    if (i > 0 && parts[i - 1].flat_end > q.flat_begin)
-      return efail(MUON_ERR_INVALID, "partitions must be sorted by flat_begin and must not overlap (at " +
-                                         std::to_string(i) + ")");
-    if (q.flat_end > q.flat_begin)
-      st.push_back({q.storage_offset, q.storage_offset + q.flat_end - q.flat_begin});
-  }
-  std::sort(st.begin(), st.end());
-  for (size_t i = 1; i < st.size(); ++i)
-    if (st[i - 1].second > st[i].first) return efail(MUON_ERR_INVALID, "partitions overlap in storage");
-  int64_t cursor = 0;
-  out->n = 0;
-  for (int i = 0; i < nparts && cursor < numel; ++i) {
-    const muon_partition_t& q = parts[i];
-    const int64_t lo = std::max(p.offset, q.flat_begin) - p.offset;
-    const int64_t hi = std::min(p.offset + numel, q.flat_end) - p.offset;
-    if (lo >= hi) continue;
-    if (lo != cursor) break;
-    if (out->n == MUON_EMBEDDING_MAX_SEGMENTS)
-      return efail(MUON_ERR_UNSUPPORTED, "the parameter lies in more than MUON_EMBEDDING_MAX_SEGMENTS partitions");
-    out->rel[out->n] = lo;
-    out->at[out->n++] = q.storage_offset + (p.offset + lo - q.flat_begin);
-    cursor = hi;
-  }
-  if (cursor != numel) return efail(MUON_ERR_INVALID, "the parameter is not covered by the partitions");
-  return MUON_OK;
-}
-
 cudaError_t launch_sort(const SortArgs& a, bool early, cudaStream_t s) {
   // 2048 tokens per block (4 per thread), up to a cluster of 16 blocks
   int blocks = 1;
@@ -807,12 +740,6 @@ cudaError_t launch_grad(const Grad& g, const Segments& sg, bool few, cudaStream_
   const int slabs = static_cast<int>((int64_t(g.cols) + 127) / 128);
   const unsigned join = static_cast<unsigned>(std::min<int64_t>(int64_t(g.blocks) * slabs, 8 * kSms));
   return launch(aligned ? k_embed_join<true> : k_embed_join<false>, join, 32 * kJoinGroups, 1, true, s, 0, g, sg, slabs);
-}
-
-bool misaligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
-
-size_t dtype_bytes(int dtype) {
-  return dtype == MUON_DTYPE_BF16 ? 2 : dtype == MUON_DTYPE_FP32 ? 4 : 0;
 }
 
 // The checks the lookup and its gradient share.  x: the rows of `cols`

@@ -916,8 +916,6 @@ cudaError_t launch_rows(const Rows& a, const Extra& x, int dtype, cudaStream_t s
 
 // ------------------------------------------------------------------ arguments
 
-bool misaligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
-
 int check_rows(const void* logits, int dtype, int64_t stride, int64_t n, int vocab,
                const void* targets, int targets_type, float scale, const float* logp) {
   if (dtype != MUON_DTYPE_BF16 && dtype != MUON_DTYPE_FP32)
@@ -1006,7 +1004,11 @@ size_t preference_bytes(int64_t n) { return (size_t(n) * (sizeof(float2) + 2 * s
 
 }  // namespace
 
-int losses_take_device_error() { return take_flag(g_losses_err); }
+// The last of the chain muon_device_error asks: the products' codes behind the losses'.
+int losses_take_device_error() {
+  const int v = take_flag(g_losses_err);
+  return v ? v : linear_take_device_error();
+}
 
 }  // namespace muon
 

@@ -1,6 +1,12 @@
 // Shared by the operators at the two ends of a language model (embedding.cu,
-// losses.cu): element types, token indexes, the device error flag.
+// losses.cu) and of its layers (linear.cu, layers.cu): element types, token
+// indexes, where a parameter lies in storage, the device error flag.
 #pragma once
+
+#include <algorithm>
+#include <limits>
+#include <string>
+#include <vector>
 
 #include <cuda_bf16.h>
 
@@ -100,6 +106,26 @@ __device__ __forceinline__ void allow_next() { asm volatile("griddepcontrol.laun
 
 }  // namespace tok
 
+// The parameter's runs in storage: elements [rel[i], rel[i + 1]) of the
+// parameter start at storage index at[i].
+struct Segments {
+  int n;
+  int64_t rel[MUON_EMBEDDING_MAX_SEGMENTS];
+  int64_t at[MUON_EMBEDDING_MAX_SEGMENTS];
+  int64_t numel;
+
+  // storage index of element i, and how many elements follow in one piece
+  __device__ __forceinline__ int64_t place(int64_t i, int64_t* room) const {
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (rel[mid] <= i) lo = mid; else hi = mid - 1;
+    }
+    *room = (lo + 1 < n ? rel[lo + 1] : numel) - i;
+    return at[lo] + (i - rel[lo]);
+  }
+};
+
 // Launches `kernel` in clusters of `cluster` blocks; early: it may be
 // scheduled while the kernel before it drains (it then calls wait_before).
 template <typename... A, typename... B>
@@ -139,6 +165,62 @@ int entry(F&& body) {
   }
 }
 
+inline bool misaligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
+
+inline size_t dtype_bytes(int dtype) {
+  return dtype == MUON_DTYPE_BF16 ? 2 : dtype == MUON_DTYPE_FP32 ? 4 : 0;
+}
+
+inline int fail_with(int code, const std::string& msg) {
+  set_last_error(msg.c_str());
+  return code;
+}
+
+// The parameter's pieces in storage, in flat order.
+inline int segments_of(const muon_param_t& p, const muon_partition_t* parts, int nparts, Segments* out) {
+  const int64_t numel = int64_t(p.rows) * p.cols;
+  out->numel = numel;
+  if (p.offset > std::numeric_limits<int64_t>::max() - numel)
+    return fail_with(MUON_ERR_INVALID, "the parameter's end is past the range of an index");
+  if (nparts == 0) {
+    out->n = 1;
+    out->rel[0] = 0;
+    out->at[0] = p.offset;
+    return MUON_OK;
+  }
+  std::vector<std::pair<int64_t, int64_t>> st;
+  for (int i = 0; i < nparts; ++i) {
+    const muon_partition_t& q = parts[i];
+    if (q.flat_begin < 0 || q.flat_end < q.flat_begin || q.storage_offset < 0 ||
+        q.storage_offset > std::numeric_limits<int64_t>::max() - (q.flat_end - q.flat_begin))
+      return fail_with(MUON_ERR_INVALID, "partition " + std::to_string(i) + " has a bad range");
+    if (i > 0 && parts[i - 1].flat_end > q.flat_begin)
+      return fail_with(MUON_ERR_INVALID, "partitions must be sorted by flat_begin and must not overlap (at " +
+                                         std::to_string(i) + ")");
+    if (q.flat_end > q.flat_begin)
+      st.push_back({q.storage_offset, q.storage_offset + q.flat_end - q.flat_begin});
+  }
+  std::sort(st.begin(), st.end());
+  for (size_t i = 1; i < st.size(); ++i)
+    if (st[i - 1].second > st[i].first) return fail_with(MUON_ERR_INVALID, "partitions overlap in storage");
+  int64_t cursor = 0;
+  out->n = 0;
+  for (int i = 0; i < nparts && cursor < numel; ++i) {
+    const muon_partition_t& q = parts[i];
+    const int64_t lo = std::max(p.offset, q.flat_begin) - p.offset;
+    const int64_t hi = std::min(p.offset + numel, q.flat_end) - p.offset;
+    if (lo >= hi) continue;
+    if (lo != cursor) break;
+    if (out->n == MUON_EMBEDDING_MAX_SEGMENTS)
+      return fail_with(MUON_ERR_UNSUPPORTED, "the parameter lies in more than MUON_EMBEDDING_MAX_SEGMENTS partitions");
+    out->rel[out->n] = lo;
+    out->at[out->n++] = q.storage_offset + (p.offset + lo - q.flat_begin);
+    cursor = hi;
+  }
+  if (cursor != numel) return fail_with(MUON_ERR_INVALID, "the parameter is not covered by the partitions");
+  return MUON_OK;
+}
+
 // Host side.  Which devices have run these operators (bit per device; the
 // caller holds the library lock), so that muon_device_error reads their flags.
 void note_token_device(int dev);
@@ -146,6 +228,7 @@ void note_token_device(int dev);
 // others' wait for the next query.
 int embedding_take_device_error();
 int losses_take_device_error();
+int linear_take_device_error();
 uint64_t token_devices();
 
 // `symbol`: the TU's own __device__ int.
