@@ -705,6 +705,7 @@ MUON_API int muon_linear(const muon_linear_args_t* args, void* workspace, size_t
  *   accum, accum_elems, parts, nparts, scale, overwrite : as
  *            muon_embedding_grad; not looked at if param and bias are NULL.
  *            The two parameters may not overlap.
+ * Which of the gradients are asked for may change the order of a sum.
  * Errors: as muon_linear and muon_embedding_grad. */
 typedef struct muon_linear_grad_args {
   int32_t struct_size;   /* sizeof(muon_linear_grad_args_t) */

@@ -2,7 +2,10 @@
 // dropout and residual, and its gradients: dx through the activation before the
 // layer, and the weight's and bias's summed straight into the flat,
 // partitioned FP32 accumulation buffer.
+#include <type_traits>
+
 #include "layers.cuh"
+#include "tc_common.cuh"
 
 namespace muon {
 namespace {
@@ -14,114 +17,808 @@ using lay::Span;
 __device__ int g_linear_err;
 
 // ------------------------------------------------------------------ epilogues
+//
+// A warp takes a chunk of 32 rows x 32 columns of the result.  Its lane has, in
+// turn, eight consecutive columns of row 8 i + lane / 4, i = 0 .. 3: 16 bytes of
+// bf16 and the eight elements that one draw of dropout serves.  What is added to
+// the chunk or multiplies it (residual, argument of the activation, old sums)
+// is fetched ahead by asynchronous copies into slots of the lane's own.
+
+constexpr int kSlotBytes = 4096;    // a warp's slots: a chunk of FP32, or two of bf16
+constexpr int kChunkBytes = 4096;   // a chunk of FP32 sums
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+__device__ __forceinline__ uint4 slot16(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+  return v;
+}
+
+// A matrix that is read or written beside the sums.
+struct Matrix {
+  void* p;
+  int64_t stride;
+  int fp32;
+  int wide;   // every row starts on 16 bytes
+
+  __device__ __forceinline__ void* at(int64_t r, int64_t c) const {
+    return static_cast<char*>(p) + (r * stride + c) * (fp32 ? 4 : 2);
+  }
+  // The lane's eight elements of a row, `left` of them inside.
+  __device__ __forceinline__ void load(int64_t r, int64_t c, int left, float* f) const {
+    if (fp32) {
+      const float* q = static_cast<const float*>(p) + r * stride + c;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = j < left ? q[j] : 0.f;
+    } else {
+      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p) + r * stride + c;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = j < left ? tok::to_float(q[j]) : 0.f;
+    }
+  }
+  __device__ __forceinline__ void store(int64_t r, int64_t c, int left, const float* f) const {
+    if (wide && left >= 8) {
+      uint4* q = static_cast<uint4*>(at(r, c));
+      if (fp32) {
+        q[0] = tok::Vec<float>::pack(f);
+        q[1] = tok::Vec<float>::pack(f + 4);
+      } else {
+        q[0] = tok::Vec<__nv_bfloat16>::pack(f);
+      }
+    } else if (fp32) {
+      float* q = static_cast<float*>(p) + r * stride + c;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < left) q[j] = f[j];
+    } else {
+      __nv_bfloat16* q = static_cast<__nv_bfloat16*>(p) + r * stride + c;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < left) q[j] = __float2bfloat16_rn(f[j]);
+    }
+  }
+  // Fetches the lane's part of a chunk into its slots; bf16 chunks alternate
+  // between two halves.
+  __device__ __forceinline__ void fetch(uint32_t slots, int half, int64_t r0, int64_t c0, int64_t rows, int64_t cols,
+                                        int lane) const {
+    const int64_t c = c0 + (lane & 3) * 8;
+    if (!wide || cols - c < 8) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t r = r0 + 8 * i + (lane >> 2);
+      if (r >= rows) break;
+      const char* q = static_cast<const char*>(at(r, c));
+      if (fp32) {
+        copy16(slots + (2 * i) * 512 + lane * 16, q);
+        copy16(slots + (2 * i + 1) * 512 + lane * 16, q + 16);
+      } else {
+        copy16(slots + half * 2048 + i * 512 + lane * 16, q);
+      }
+    }
+  }
+  __device__ __forceinline__ void fetched(uint32_t slots, int half, int i, int64_t r, int64_t c, int left, int lane,
+                                          float* f) const {
+    if (!wide || left < 8) return load(r, c, left, f);
+    if (fp32) {
+      tok::Vec<float>::unpack(slot16(slots + (2 * i) * 512 + lane * 16), f);
+      tok::Vec<float>::unpack(slot16(slots + (2 * i + 1) * 512 + lane * 16), f + 4);
+    } else {
+      tok::Vec<__nv_bfloat16>::unpack(slot16(slots + half * 2048 + i * 512 + lane * 16), f);
+    }
+  }
+};
+
+template <int KIND>
+__device__ __forceinline__ void act8(float* v) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = lay::activation(v[j], KIND);
+}
+
+template <int KIND>
+__device__ __forceinline__ void slope8(float* v, const float* u) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] *= lay::slope(u[j], KIND);
+}
 
 // out = residual + dropout(activation(acc + bias)), pre = acc + bias.
 struct Forward {
   const void* bias;
-  __nv_bfloat16* pre;
-  const void* residual;
-  void* out;
-  int64_t pre_stride, res_stride, out_stride;
-  int bias32, out32, act;
+  Matrix out, pre, residual;   // p = NULL: none
+  int64_t rows;                // tokens
+  int cols, bias32, act;
   Dropout drop;
 
-  __device__ __forceinline__ void put(float v, int64_t t, int64_t n, const Draw& draw) const {
-    if (bias) v += bias32 ? static_cast<const float*>(bias)[n]
-                          : tok::to_float(static_cast<const __nv_bfloat16*>(bias)[n]);
-    if (pre) pre[t * pre_stride + n] = __float2bfloat16_rn(v);
-    v = lay::activation(v, act);
-    if (drop.least)
-      v = lay::dropped(v, lay::draw_of(draw.at(uint32_t(t), uint32_t(n / 8), drop.site), int(n % 8)), drop);
-    if (out32) {
-      if (residual) v += static_cast<const float*>(residual)[t * res_stride + n];
-      static_cast<float*>(out)[t * out_stride + n] = v;
-    } else {
-      if (residual) v += tok::to_float(static_cast<const __nv_bfloat16*>(residual)[t * res_stride + n]);
-      static_cast<__nv_bfloat16*>(out)[t * out_stride + n] = __float2bfloat16_rn(v);
+  __device__ __forceinline__ bool halves() const { return !residual.fp32; }
+  __device__ __forceinline__ void fetch(uint32_t slots, int half, int64_t t0, int64_t n0, int lane) const {
+    if (residual.p) residual.fetch(slots, half, t0, n0, rows, cols, lane);
+  }
+  template <typename Read>
+  __device__ __forceinline__ void chunk(const Read& read, uint32_t slots, int half, int64_t t0, int64_t n0, int lane,
+                                        const Draw& draw) const {
+    const int64_t n = n0 + (lane & 3) * 8;
+    const int left = int(min(int64_t(8), cols - n));
+    if (left <= 0) return;
+    float b[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      b[j] = !bias || j >= left ? 0.f
+             : bias32           ? static_cast<const float*>(bias)[n + j]
+                                : tok::to_float(static_cast<const __nv_bfloat16*>(bias)[n + j]);
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+      const int64_t t = t0 + 8 * i + (lane >> 2);
+      if (t >= rows) break;
+      float v[8];
+      read(8 * i + (lane >> 2), lane & 3, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] += b[j];
+      if (pre.p) pre.store(t, n, left, v);
+      switch (act) {
+        case MUON_ACT_RELU: act8<MUON_ACT_RELU>(v); break;
+        case MUON_ACT_RELU2: act8<MUON_ACT_RELU2>(v); break;
+        case MUON_ACT_GELU: act8<MUON_ACT_GELU>(v); break;
+        case MUON_ACT_SILU: act8<MUON_ACT_SILU>(v); break;
+        default: break;
+      }
+      if (drop.least) {
+        const uint4 w = draw.at(uint32_t(t), uint32_t(n / 8), drop.site);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = lay::dropped(v[j], lay::draw_of(w, j), drop);
+      }
+      if (residual.p) {
+        float r[8];
+        residual.fetched(slots, half, i, t, n, left, lane, r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] += r[j];
+      }
+      out.store(t, n, left, v);
     }
   }
 };
 
 // dx = acc * activation'(pre).
 struct InputGrad {
-  const __nv_bfloat16* pre;
-  __nv_bfloat16* dx;
-  int64_t pre_stride, dx_stride;
-  int act;
+  Matrix dx, pre;
+  int64_t rows;
+  int cols, act;
+  Dropout drop;   // none
 
-  __device__ __forceinline__ void put(float v, int64_t t, int64_t k, const Draw&) const {
-    if (act != MUON_ACT_NONE) v *= lay::slope(tok::to_float(pre[t * pre_stride + k]), act);
-    dx[t * dx_stride + k] = __float2bfloat16_rn(v);
+  __device__ __forceinline__ bool halves() const { return true; }
+  __device__ __forceinline__ void fetch(uint32_t slots, int half, int64_t t0, int64_t n0, int lane) const {
+    if (act != MUON_ACT_NONE) pre.fetch(slots, half, t0, n0, rows, cols, lane);
+  }
+  template <typename Read>
+  __device__ __forceinline__ void chunk(const Read& read, uint32_t slots, int half, int64_t t0, int64_t n0, int lane,
+                                        const Draw&) const {
+    const int64_t n = n0 + (lane & 3) * 8;
+    const int left = int(min(int64_t(8), cols - n));
+    if (left <= 0) return;
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+      const int64_t t = t0 + 8 * i + (lane >> 2);
+      if (t >= rows) break;
+      float v[8];
+      read(8 * i + (lane >> 2), lane & 3, v);
+      if (act != MUON_ACT_NONE) {
+        float u[8];
+        pre.fetched(slots, half, i, t, n, left, lane, u);
+        switch (act) {
+          case MUON_ACT_RELU: slope8<MUON_ACT_RELU>(v, u); break;
+          case MUON_ACT_RELU2: slope8<MUON_ACT_RELU2>(v, u); break;
+          case MUON_ACT_GELU: slope8<MUON_ACT_GELU>(v, u); break;
+          default: slope8<MUON_ACT_SILU>(v, u); break;
+        }
+      }
+      dx.store(t, n, left, v);
+    }
   }
 };
 
 // accum = (overwrite ? 0 : accum) + scale * acc, at the parameter's place.
 struct WeightGrad {
   float* accum;
-  int64_t cols;
+  int64_t rows;
+  int cols, overwrite;
   float scale;
-  int overwrite;
+  Dropout drop;   // none
   Segments sg;
 
-  __device__ __forceinline__ void put(float v, int64_t n, int64_t k, const Draw&) const {
+  __device__ __forceinline__ bool halves() const { return false; }
+  // The lane's eight elements lie in one piece, on 16 bytes.
+  __device__ __forceinline__ float* whole(int64_t r, int64_t c, int left) const {
     int64_t room;
-    float* p = accum + sg.place(n * cols + k, &room);
-    *p = (overwrite ? 0.f : *p) + scale * v;
+    float* p = accum + sg.place(r * cols + c, &room);
+    return left >= 8 && room >= 8 && (reinterpret_cast<uintptr_t>(p) & 15) == 0 ? p : nullptr;
+  }
+  __device__ __forceinline__ void fetch(uint32_t slots, int, int64_t r0, int64_t c0, int lane) const {
+    if (overwrite) return;
+    const int64_t c = c0 + (lane & 3) * 8;
+    const int left = int(min(int64_t(8), cols - c));
+    if (left < 8) return;
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+      const int64_t r = r0 + 8 * i + (lane >> 2);
+      if (r >= rows) break;
+      const float* p = whole(r, c, left);
+      if (!p) continue;
+      copy16(slots + (2 * i) * 512 + lane * 16, p);
+      copy16(slots + (2 * i + 1) * 512 + lane * 16, p + 4);
+    }
+  }
+  template <typename Read>
+  __device__ __forceinline__ void chunk(const Read& read, uint32_t slots, int, int64_t r0, int64_t c0, int lane,
+                                        const Draw&) const {
+    const int64_t c = c0 + (lane & 3) * 8;
+    const int left = int(min(int64_t(8), cols - c));
+    if (left <= 0) return;
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+      const int64_t r = r0 + 8 * i + (lane >> 2);
+      if (r >= rows) break;
+      float v[8];
+      read(8 * i + (lane >> 2), lane & 3, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] *= scale;
+      if (float* p = whole(r, c, left)) {
+        if (!overwrite) {
+          float o[8];
+          tok::Vec<float>::unpack(slot16(slots + (2 * i) * 512 + lane * 16), o);
+          tok::Vec<float>::unpack(slot16(slots + (2 * i + 1) * 512 + lane * 16), o + 4);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] += o[j];
+        }
+        reinterpret_cast<uint4*>(p)[0] = tok::Vec<float>::pack(v);
+        reinterpret_cast<uint4*>(p)[1] = tok::Vec<float>::pack(v + 4);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (j >= left) break;
+          int64_t room;
+          float* q = accum + sg.place(r * cols + c + j, &room);
+          *q = (overwrite ? 0.f : *q) + v[j];
+        }
+      }
+    }
   }
 };
 
-// ------------------------------------------------------------------ product
-
-// acc[m][n] = sum over k of A(m, k) B(n, k); element (r, k) of an operand lies at
-// r * row + k * col.
-struct Operands {
-  const __nv_bfloat16* a;
-  const __nv_bfloat16* b;
-  int64_t arow, acol, brow, bcol;
-  int64_t m, n, k;
+struct NoProduct {
+  Dropout drop;
+  __device__ __forceinline__ bool halves() const { return true; }
+  __device__ __forceinline__ void fetch(uint32_t, int, int64_t, int64_t, int) const {}
+  template <typename Read>
+  __device__ __forceinline__ void chunk(const Read&, uint32_t, int, int64_t, int64_t, int, const Draw&) const {}
 };
 
-constexpr int kTile = 64, kDepth = 16;
-
-template <typename Epilogue>
-__global__ void __launch_bounds__(256) k_product(const Operands p, const __grid_constant__ Epilogue e,
-                                                 const Dropout drop) {
-  __shared__ float sa[kDepth][kTile], sb[kDepth][kTile];
-  const int64_t tiles_n = (p.n + kTile - 1) / kTile;
-  const int64_t m0 = blockIdx.x / tiles_n * kTile, n0 = blockIdx.x % tiles_n * kTile;
-  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-  float acc[4][4] = {};
-  for (int64_t k0 = 0; k0 < p.k; k0 += kDepth) {
-    for (int i = threadIdx.x; i < kTile * kDepth; i += 256) {
-      const int r = i / kDepth, k = i % kDepth;
-      const bool in = k0 + k < p.k;
-      sa[k][r] = in && m0 + r < p.m ? tok::to_float(p.a[(m0 + r) * p.arow + (k0 + k) * p.acol]) : 0.f;
-      sb[k][r] = in && n0 + r < p.n ? tok::to_float(p.b[(n0 + r) * p.brow + (k0 + k) * p.bcol]) : 0.f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < kDepth; ++k)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] += sa[k][ty * 4 + i] * sb[k][tx * 4 + j];
-    __syncthreads();
-  }
-  Draw draw;
-  draw.init(drop);
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t m = m0 + ty * 4 + i, n = n0 + tx * 4 + j;
-      if (m < p.m && n < p.n) e.put(acc[i][j], m, n, draw);
-    }
+// A chunk of sums in shared memory: 32 rows of 128 bytes, their 16-byte pieces
+// exchanged by the row's low bits, so that neither a lane's row nor eight lanes'
+// pieces meet in a bank.
+__device__ __forceinline__ uint32_t piece(int row, int granule) {
+  return uint32_t(row) * 128u + (uint32_t(granule ^ (row & 7)) << 4);
 }
 
-template <typename Epilogue>
-cudaError_t launch_product(const Operands& p, const Epilogue& e, const Dropout& drop, cudaStream_t s) {
-  const int64_t blocks = ((p.m + kTile - 1) / kTile) * ((p.n + kTile - 1) / kTile);
-  return launch(k_product<Epilogue>, unsigned(blocks), 256, 1, false, s, 0, p, e, drop);
+__device__ __forceinline__ void stage_rows(uint32_t at, int lane, const float* x) {   // lane: the row
+#pragma unroll
+  for (int g = 0; g < 8; ++g)
+    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at + piece(lane, g)), "f"(x[4 * g]),
+                 "f"(x[4 * g + 1]), "f"(x[4 * g + 2]), "f"(x[4 * g + 3])
+                 : "memory");
+}
+
+__device__ __forceinline__ void stage_columns(uint32_t at, int lane, const float* x) {   // lane: the column
+#pragma unroll
+  for (int r = 0; r < 32; ++r)
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + piece(r, lane >> 2) + (lane & 3) * 4), "f"(x[r]) : "memory");
+}
+
+struct ReadOwn {
+  uint32_t at;
+  __device__ __forceinline__ void operator()(int row, int quarter, float* v) const {
+    tok::Vec<float>::unpack(slot16(at + piece(row, 2 * quarter)), v);
+    tok::Vec<float>::unpack(slot16(at + piece(row, 2 * quarter + 1)), v + 4);
+  }
+};
+
+// The same chunk's sums from every block of the cluster, added in their order.
+struct ReadAll {
+  uint32_t at;
+  int blocks;
+  __device__ __forceinline__ void operator()(int row, int quarter, float* v) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = 0.f;
+#pragma unroll 4
+    for (int b = 0; b < blocks; ++b) {
+      const uint32_t far = tc::mapa_shared(at, b);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float x, y, z, w;
+        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(x), "=f"(y), "=f"(z), "=f"(w)
+                     : "r"(far + piece(row, 2 * quarter + h)));
+        v[4 * h] += x;
+        v[4 * h + 1] += y;
+        v[4 * h + 2] += z;
+        v[4 * h + 3] += w;
+      }
+    }
+  }
+};
+
+// ------------------------------------------------------------------ products
+
+using namespace tc;
+
+// D[m][n] = sum over k of A[m][k] B[n][k].  An operand lies with its k
+// contiguous, or (mn) with its rows contiguous, k rows apart.
+struct Product {
+  CUtensorMap a, b;
+  int64_t m, n;
+  int k;                  // blocks of 64
+  int tiles_m, tiles_n;
+  int a_mn, b_mn;
+};
+
+template <class E0, class E1>
+struct Work {
+  Product p[2];
+  int tiles0, tiles;      // tiles of p[0], and of both
+  E0 e0;
+  E1 e1;
+};
+
+constexpr int BK = 64;
+
+// Sums of so many K blocks (1024 terms) are formed in tensor memory, whose
+// additions cut off instead of rounding; FP32 registers add those.  Without
+// that a sum of 32768 terms loses 6e-5 of its size (half a unit of 2^-23 every 16
+// terms, all in one direction); with it 2e-6.
+constexpr int kDepth = 16;
+
+__device__ __forceinline__ uint32_t idesc_of(const Product& p, int m, int n) {
+  return make_idesc(p.b_mn != 0, m, n) | (p.a_mn ? 1u << 15 : 0u);
+}
+
+// K block `kb` of `rows` (64 or 128) rows of an operand from row0.
+template <int ROWS, bool PAIR>
+__device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* map, int mn, int kb, int row0,
+                                             uint32_t bar) {
+  auto one = [&](uint32_t d, int x, int y) {
+    if constexpr (PAIR) tma_load_2d_pair(d, map, x, y, bar);
+    else tma_load_2d(d, map, x, y, bar);
+  };
+  if (!mn) {
+    one(dst, kb * BK, row0);
+  } else {
+    constexpr int W = ROWS < 64 ? ROWS : 64;
+#pragma unroll
+    for (int j = 0; j < ROWS / W; ++j) one(dst + j * (W * BK * 2), row0 + j * W, kb * BK);
+  }
+}
+
+// Descriptor of its 16 terms from k * 16.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t at, int mn, int k, int rows) {
+  return mn ? make_desc(at + k * 16 * 128, 64 * BK * 2, 1024, kSwizzle128)
+            : make_desc(at + k * 32, 16, 1024, kSwizzle128);
+}
+
+// Tiles in groups of eight rows of tiles, column by column: what is under way
+// at one time shares its operands in L2.
+__device__ __forceinline__ void tile_of(const Product& p, int i, int* tm, int* tn) {
+  const int per = 8 * p.tiles_n, g = i / per, first = g * 8, rows = min(8, p.tiles_m - first), r = i - g * per;
+  *tm = first + r % rows;
+  *tn = r / rows;
+}
+
+constexpr int kPairThreads = 320;
+constexpr int kPairWarps = 8;   // of the epilogue
+
+template <int BN>
+struct PairShape {
+  static constexpr int kA = 128 * BK * 2, kB = BN / 2 * BK * 2, kStage = kA + kB;
+  static constexpr int kStages = BN == 256 ? 5 : 6;
+  static constexpr int kBars = 2 * kStages + 4;
+  static constexpr int kShared = 1024 + kStages * kStage + kPairWarps * (kChunkBytes + kSlotBytes) + 8 * kBars + 16;
+};
+
+// Tiles of 256 x BN on pairs of SMs (tcgen05 cta_group::2): each block of the
+// pair loads its half of either operand and holds 128 rows of the result.
+// Warp 0 loads, warp 1 of the even block issues the products, eight warps of
+// each block add up the partial sums and write the results of one tile while
+// the next one's are formed.
+template <int BN, class E0, class E1>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+k_linear_pair(const __grid_constant__ Work<E0, E1> w, int* err) {
+  using S = PairShape<BN>;
+  extern __shared__ uint8_t raw_shared[];
+  const uint32_t base = (smem_u32(raw_shared) + 1023u) & ~1023u;
+  const uint32_t epi = base + S::kStages * S::kStage;
+  const uint32_t bars = epi + kPairWarps * (kChunkBytes + kSlotBytes);
+  auto full = [&](int s) { return bars + 8u * s; };
+  auto empty = [&](int s) { return bars + 8u * (S::kStages + s); };
+  auto tfull = [&](int i) { return bars + 8u * (2 * S::kStages + i); };
+  auto tempty = [&](int i) { return bars + 8u * (2 * S::kStages + 2 + i); };
+  uint8_t* tail = raw_shared + (bars + 8u * S::kBars - smem_u32(raw_shared));
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tail);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail) + 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int first = blockIdx.x / 2, step = gridDim.x / 2;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S::kStages; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(tfull(i), 1);
+      mbar_init(tempty(i), 2 * kPairWarps);
+    }
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                 "r"(2 * BN)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int s = 0;
+      uint32_t ph = 0;
+      for (int tile = first; tile < w.tiles && !*abort_flag; tile += step) {
+        const int which = tile >= w.tiles0;
+        const Product& p = w.p[which];
+        int tm, tn;
+        tile_of(p, which ? tile - w.tiles0 : tile, &tm, &tn);
+        const int row0 = tm * 256 + int(rank) * 128, col0 = tn * BN + int(rank) * (BN / 2);
+        for (int kb = 0; kb < p.k; ++kb) {
+          if (!mbar_wait(empty(s), ph ^ 1u, abort_flag, err, ERR_TIMEOUT_PRODUCER)) break;
+          const uint32_t sa = base + s * S::kStage, fb = mapa_shared(full(s), 0);
+          if (rank == 0) mbar_expect_tx(full(s), 2 * S::kStage);
+          load_operand<128, true>(sa, &p.a, p.a_mn, kb, row0, fb);
+          load_operand<BN / 2, true>(sa + S::kA, &p.b, p.b_mn, kb, col0, fb);
+          if (++s == S::kStages) { s = 0; ph ^= 1u; }
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      int s = 0, acc = 0;
+      uint32_t ph = 0, acc_ph = 0;
+      bool ok = true;
+      for (int tile = first; ok && tile < w.tiles; tile += step) {
+        const Product& p = w.p[tile >= w.tiles0];
+        const uint32_t idesc = idesc_of(p, 256, BN);
+        const int a_mn = p.a_mn, b_mn = p.b_mn;
+        for (int k0 = 0; ok && k0 < p.k; k0 += kDepth) {
+          if (!mbar_wait(tempty(acc), acc_ph ^ 1u, abort_flag, err, ERR_TIMEOUT_MMA)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t d = tmem + uint32_t(acc * BN);
+          const int k1 = min(p.k, k0 + kDepth);
+          for (int kb = k0; kb < k1; ++kb) {
+            if (!mbar_wait(full(s), ph, abort_flag, err, ERR_TIMEOUT_MMA)) { ok = false; break; }
+            tc_fence_after();
+            const uint32_t sa = base + s * S::kStage;
+#pragma unroll
+            for (int k = 0; k < BK / 16; ++k)
+              umma_bf16_pair(d, operand_desc(sa, a_mn, k, 128), operand_desc(sa + S::kA, b_mn, k, BN / 2), idesc,
+                             kb > k0 || k > 0);
+            umma_commit_pair(empty(s), 0x3);
+            if (++s == S::kStages) { s = 0; ph ^= 1u; }
+          }
+          if (!ok) break;
+          umma_commit_pair(tfull(acc), 0x3);
+          acc ^= 1;
+          if (acc == 0) acc_ph ^= 1u;
+        }
+      }
+    }
+  } else {
+    const int ew = warp - 2, q = warp & 3, side = ew >> 2;
+    const uint32_t stage = epi + ew * (kChunkBytes + kSlotBytes), slots = stage + kChunkBytes;
+    constexpr int N = BN / 64;   // chunks of a warp
+    Draw draw;
+    draw.init(w.e0.drop);
+    int acc = 0;
+    uint32_t acc_ph = 0;
+    bool ok = true;
+    for (int tile = first; ok && tile < w.tiles; tile += step) {
+      const int which = tile >= w.tiles0;
+      const Product& p = w.p[which];
+      int tm, tn;
+      tile_of(p, which ? tile - w.tiles0 : tile, &tm, &tn);
+      const int64_t m0 = int64_t(tm) * 256 + rank * 128 + q * 32, n0 = int64_t(tn) * BN + side * (BN / 2);
+      const bool here = m0 < p.m;
+      auto fetch = [&](int c) {
+        if (which) w.e1.fetch(slots, c & 1, m0, n0 + 32 * c, lane);
+        else w.e0.fetch(slots, c & 1, m0, n0 + 32 * c, lane);
+      };
+      if (here && n0 < p.n) fetch(0);
+      float sum[N][32];
+#pragma unroll
+      for (int c = 0; c < N; ++c)
+#pragma unroll
+        for (int j = 0; j < 32; ++j) sum[c][j] = 0.f;
+      for (int k0 = 0; k0 < p.k; k0 += kDepth) {
+        if (!mbar_wait(tfull(acc), acc_ph, abort_flag, err, ERR_TIMEOUT_EPILOGUE)) { ok = false; break; }
+        __syncwarp();
+        tc_fence_after();
+        if (here) {
+#pragma unroll
+          for (int c = 0; c < N; ++c) {
+            float x[32];
+            tmem_ld32(tmem + uint32_t(acc * BN + side * (BN / 2) + c * 32) + (uint32_t(q * 32) << 16), x);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) sum[c][j] += x[j];
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(mapa_shared(tempty(acc), 0));
+        acc ^= 1;
+        if (acc == 0) acc_ph ^= 1u;
+      }
+      if (!ok || !here) continue;
+#pragma unroll
+      for (int c = 0; c < N; ++c) {
+        if (n0 + 32 * c >= p.n) continue;
+        stage_rows(stage, lane, sum[c]);
+        copies_done();
+        __syncwarp();
+        // the other half is free; FP32 slots are refilled once this chunk has read them
+        const bool ahead = c + 1 < N && n0 + 32 * (c + 1) < p.n;
+        const bool halves = which ? w.e1.halves() : w.e0.halves();
+        if (ahead && halves) fetch(c + 1);
+        if (which) w.e1.chunk(ReadOwn{stage}, slots, c & 1, m0, n0 + 32 * c, lane, draw);
+        else w.e0.chunk(ReadOwn{stage}, slots, c & 1, m0, n0 + 32 * c, lane, draw);
+        if (ahead && !halves) fetch(c + 1);
+        __syncwarp();
+      }
+    }
+  }
+  if (*abort_flag) {
+    const unsigned long long t0 = globaltimer();
+    while (globaltimer() - t0 < 20000000ull) __nanosleep(100000);
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  if (warp == 1)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * BN) : "memory");
+}
+
+constexpr int kSplitThreads = 192;
+constexpr int kSplitWarps = 4;   // of the epilogue
+constexpr int kMostSplits = 8;   // blocks of a portable cluster
+
+template <int BN>
+struct SplitShape {
+  static constexpr int kA = 128 * BK * 2, kB = BN * BK * 2, kStage = kA + kB;
+  static constexpr int kStages = BN == 128 ? 6 : 8;
+  static constexpr int kBars = 2 * kStages + 4;
+  static constexpr int kChunks = kSplitWarps * (BN / 32);
+  static constexpr int kShared = 1024 + kStages * kStage + kSplitWarps * kSlotBytes + 8 * kBars + 16;
+  static_assert(kChunks * kChunkBytes <= kStages * kStage, "the sums take the operands' place");
+};
+
+// One tile of 128 x BN per cluster, whose blocks share out the K blocks and add
+// their sums through distributed shared memory, in the order of the blocks.
+// SWAP: the rows of the product are the result's columns (features, of which
+// there are many) and its columns the result's rows (few tokens), so that few
+// tokens leave no part of a tile's 128 rows empty.
+template <int BN, bool SWAP, class E0, class E1>
+__global__ void __launch_bounds__(kSplitThreads, 1)
+k_linear_split(const __grid_constant__ Work<E0, E1> w, int splits, int* err) {
+  using S = SplitShape<BN>;
+  extern __shared__ uint8_t raw_shared[];
+  const uint32_t base = (smem_u32(raw_shared) + 1023u) & ~1023u;
+  const uint32_t slot_base = base + S::kStages * S::kStage;
+  const uint32_t bars = slot_base + kSplitWarps * kSlotBytes;
+  auto full = [&](int s) { return bars + 8u * s; };
+  auto empty = [&](int s) { return bars + 8u * (S::kStages + s); };
+  auto tfull = [&](int i) { return bars + 8u * (2 * S::kStages + i); };
+  auto tempty = [&](int i) { return bars + 8u * (2 * S::kStages + 2 + i); };
+  uint8_t* tail = raw_shared + (bars + 8u * S::kBars - smem_u32(raw_shared));
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tail);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail) + 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tile = blockIdx.x / splits, rank = blockIdx.x % splits;   // clusters are consecutive blocks
+  const int which = tile >= w.tiles0;
+  const Product& p = w.p[which];
+  int tm, tn;
+  tile_of(p, which ? tile - w.tiles0 : tile, &tm, &tn);
+  const int kb0 = int(int64_t(p.k) * rank / splits), kb1 = int(int64_t(p.k) * (rank + 1) / splits);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S::kStages; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(tfull(i), 1);
+      mbar_init(tempty(i), kSplitWarps);
+    }
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                 "r"(2 * BN)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  const int ew = warp - 2, q = warp & 3;
+  const uint32_t slots = slot_base + ew * kSlotBytes;
+  constexpr int N = BN / 32;
+  // where chunk (quarter of the rows, 32 columns) lies in the result
+  auto row_of = [&](int quarter, int c) { return SWAP ? int64_t(tn) * BN + 32 * c : int64_t(tm) * 128 + 32 * quarter; };
+  auto col_of = [&](int quarter, int c) { return SWAP ? int64_t(tm) * 128 + 32 * quarter : int64_t(tn) * BN + 32 * c; };
+  auto inside = [&](int quarter, int c) {
+    return int64_t(tm) * 128 + 32 * quarter < p.m && int64_t(tn) * BN + 32 * c < p.n;
+  };
+  bool ok = true;
+  if (warp == 0) {
+    if (lane == 0) {
+      int s = 0;
+      uint32_t ph = 0;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!mbar_wait(empty(s), ph ^ 1u, abort_flag, err, ERR_TIMEOUT_PRODUCER)) break;
+        const uint32_t sa = base + s * S::kStage;
+        mbar_expect_tx(full(s), S::kStage);
+        load_operand<128, false>(sa, &p.a, p.a_mn, kb, tm * 128, full(s));
+        load_operand<BN, false>(sa + S::kA, &p.b, p.b_mn, kb, tn * BN, full(s));
+        if (++s == S::kStages) { s = 0; ph ^= 1u; }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      int s = 0, acc = 0;
+      uint32_t ph = 0, acc_ph = 0;
+      const uint32_t idesc = idesc_of(p, 128, BN);
+      for (int k0 = kb0; ok && k0 < kb1; k0 += kDepth) {
+        if (!mbar_wait(tempty(acc), acc_ph ^ 1u, abort_flag, err, ERR_TIMEOUT_MMA)) break;
+        tc_fence_after();
+        const uint32_t d = tmem + uint32_t(acc * BN);
+        const int k1 = min(kb1, k0 + kDepth);
+        for (int kb = k0; kb < k1; ++kb) {
+          if (!mbar_wait(full(s), ph, abort_flag, err, ERR_TIMEOUT_MMA)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t sa = base + s * S::kStage;
+#pragma unroll
+          for (int k = 0; k < BK / 16; ++k)
+            umma_bf16(d, operand_desc(sa, p.a_mn, k, 128), operand_desc(sa + S::kA, p.b_mn, k, BN), idesc,
+                      kb > k0 || k > 0);
+          umma_commit(empty(s));
+          if (++s == S::kStages) { s = 0; ph ^= 1u; }
+        }
+        if (!ok) break;
+        umma_commit(tfull(acc));
+        acc ^= 1;
+        if (acc == 0) acc_ph ^= 1u;
+      }
+    }
+  } else {
+    int acc = 0;
+    uint32_t acc_ph = 0;
+    float sum[N][32];
+#pragma unroll
+    for (int c = 0; c < N; ++c)
+#pragma unroll
+      for (int j = 0; j < 32; ++j) sum[c][j] = 0.f;
+    for (int k0 = kb0; k0 < kb1; k0 += kDepth) {
+      if (!mbar_wait(tfull(acc), acc_ph, abort_flag, err, ERR_TIMEOUT_EPILOGUE)) { ok = false; break; }
+      __syncwarp();
+      tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < N; ++c) {
+        float x[32];
+        tmem_ld32(tmem + uint32_t(acc * BN + c * 32) + (uint32_t(q * 32) << 16), x);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) sum[c][j] += x[j];
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(tempty(acc));
+      acc ^= 1;
+      if (acc == 0) acc_ph ^= 1u;
+    }
+    // Every product has read its operands: the sums take their place.  (All of
+    // a block's loads have landed, since its products waited for them.)
+    if (ok) {
+#pragma unroll
+      for (int c = 0; c < N; ++c) {
+        const uint32_t at = base + uint32_t((q * N + c) * kChunkBytes);
+        if (SWAP) stage_columns(at, lane, sum[c]);
+        else stage_rows(at, lane, sum[c]);
+      }
+    }
+  }
+  __syncwarp();
+  if (splits > 1) cluster_sync();
+  else __syncthreads();
+  // every block's status: a block that gave up has staged nothing
+  bool good = !*abort_flag;
+  if (splits > 1)
+    for (int b = 0; b < splits; ++b) {
+      uint32_t v;
+      asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(mapa_shared(smem_u32(tail), b)));
+      good = good && v == 0;
+    }
+  if (warp >= 2 && good) {
+    Draw draw;
+    draw.init(w.e0.drop);
+    // the cluster's blocks, and their warps, take chunks in turn
+    for (int i = rank + splits * ew; i < S::kChunks; i += splits * kSplitWarps) {
+      const int quarter = i / N, c = i % N;
+      if (!inside(quarter, c)) continue;
+      const uint32_t at = base + uint32_t(i * kChunkBytes);
+      const int64_t r = row_of(quarter, c), n = col_of(quarter, c);
+      if (which) w.e1.fetch(slots, 0, r, n, lane);
+      else w.e0.fetch(slots, 0, r, n, lane);
+      copies_done();
+      if (splits > 1) {
+        if (which) w.e1.chunk(ReadAll{at, splits}, slots, 0, r, n, lane, draw);
+        else w.e0.chunk(ReadAll{at, splits}, slots, 0, r, n, lane, draw);
+      } else {
+        if (which) w.e1.chunk(ReadOwn{at}, slots, 0, r, n, lane, draw);
+        else w.e0.chunk(ReadOwn{at}, slots, 0, r, n, lane, draw);
+      }
+    }
+  }
+  if (*abort_flag) {
+    const unsigned long long t0 = globaltimer();
+    while (globaltimer() - t0 < 20000000ull) __nanosleep(100000);
+  }
+  __syncwarp();
+  tc_fence_before();
+  if (splits > 1) cluster_sync();   // nobody leaves while its sums may be read
+  else __syncthreads();
+  tc_fence_after();
+  if (warp == 1)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * BN) : "memory");
+}
+
+// ------------------------------------------------------------------ operands that are copied first
+
+constexpr int kPackThreads = 256;
+
+// Rows of `cols` elements at any stride to rows that start on 16 bytes; eight
+// elements per thread.  What a row's last piece holds beyond cols is not read.
+__global__ void __launch_bounds__(kPackThreads)
+k_linear_pack(const __nv_bfloat16* in, int64_t stride, __nv_bfloat16* out, int64_t out_stride, int64_t rows, int cols) {
+  const int pieces = (cols + 7) / 8;
+  const int64_t all = rows * pieces;
+  for (int64_t i = int64_t(blockIdx.x) * kPackThreads + threadIdx.x; i < all; i += int64_t(gridDim.x) * kPackThreads) {
+    const int64_t r = i / pieces;
+    const int c = int(i - r * pieces) * 8;
+    const unsigned short* q = reinterpret_cast<const unsigned short*>(in) + r * stride + c;
+    uint32_t v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t lo = c + 2 * j < cols ? q[2 * j] : 0u, hi = c + 2 * j + 1 < cols ? q[2 * j + 1] : 0u;
+      v[j] = lo | hi << 16;
+    }
+    *reinterpret_cast<uint4*>(out + r * out_stride + c) = make_uint4(v[0], v[1], v[2], v[3]);
+  }
 }
 
 // ------------------------------------------------------------------ bias
@@ -154,14 +851,201 @@ __global__ void __launch_bounds__(1024) k_bias_grad(const BiasGrad a, const __gr
 // ------------------------------------------------------------------ host
 
 constexpr int kMostFeatures = 1 << 24;
+constexpr int kSms = 152, kPairs = kSms / 2;
 
+// An operand of a product: rows x cols, bf16.
+struct Operand {
+  const void* p = nullptr;
+  int64_t rows = 0, cols = 0, stride = 0;
+  size_t packed = 0;   // bytes of its copy in the workspace; 0: read where it lies
+
+  Operand() = default;
+  Operand(const void* q, int64_t r, int64_t c, int64_t s) : p(q), rows(r), cols(c), stride(s) {
+    if (r <= 1) stride = (c + 7) / 8 * 8;   // a single row's stride says nothing
+    // what the copies of tiles take: rows that start on 16 bytes, strides below 2^40 bytes
+    if (q && (misaligned(q, 16) || stride % 8 || stride >= (int64_t(1) << 39)))
+      packed = (size_t(r) * ((c + 7) / 8 * 16) + 255) & ~size_t(255);
+  }
+  // Copies it where that is needed; *at moves behind the copy.
+  cudaError_t pack(char** at, cudaStream_t s, int* launches) {
+    if (!packed) return cudaSuccess;
+    const int64_t to = (cols + 7) / 8 * 8, pieces = rows * (to / 8);
+    __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(*at);
+    const unsigned grid = unsigned(std::min<int64_t>((pieces + kPackThreads - 1) / kPackThreads, 16 * kSms));
+    const cudaError_t e = launch(k_linear_pack, grid, kPackThreads, 1, false, s, 0,
+                                 static_cast<const __nv_bfloat16*>(p), stride, out, to, rows, int(cols));
+    *at += packed;
+    p = out;
+    stride = to;
+    ++*launches;
+    return e;
+  }
+};
+
+// How a product, or two at once, is run: pairs of SMs and tiles of 256 x bn, or
+// single ones, 128 x bn, with the K blocks shared out to `splits` blocks.
+struct Plan {
+  bool pairs = false, swap = false;
+  int bn = 0, splits = 1;
+};
+
+struct Extent {
+  int64_t m, n, k;   // of the product as in D[m][n], k in elements
+};
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// The plan of least estimated time.
+// A K block takes a pair 0.30 us at 256 columns and 0.18 at 128, a single SM
+// 0.17 us (bound by the loads of its operands), a tile's results 2 us behind the
+// last one; a cluster's sums 1.5 us.
+Plan plan_of(const Extent* x, int count) {
+  Plan best;
+  double least = 0;
+  auto offer = [&](const Plan& p, double us) {
+    if (!best.bn || us < least) {
+      best = p;
+      least = us;
+    }
+  };
+  for (int bn : {256, 128}) {
+    double work = 0, longest = 0;
+    int64_t tiles = 0;
+    for (int i = 0; i < count; ++i) {
+      const int64_t t = ceil_div(x[i].m, 256) * ceil_div(x[i].n, bn);
+      const double one = double(ceil_div(x[i].k, 64)) * (bn == 256 ? 0.30 : 0.18) + 1.0;
+      tiles += t;
+      work += double(t) * one;
+      longest = std::max(longest, one);
+    }
+    const double waves = std::ceil(double(tiles) / kPairs);
+    Plan p;
+    p.pairs = true;
+    p.bn = bn;
+    offer(p, std::max(waves * work / double(tiles), longest) + 3.0);
+  }
+  for (int s = 1; s <= kMostSplits; ++s) {
+    double work = 0, longest = 0;
+    int64_t blocks = 0, k = 1 << 30;
+    for (int i = 0; i < count; ++i) {
+      const int64_t t = ceil_div(x[i].m, 128) * ceil_div(x[i].n, 128) * s, kb = ceil_div(x[i].k, 64);
+      const double one = double(ceil_div(kb, s)) * 0.17 + (s > 1 ? 2.5 : 2.0);
+      blocks += t;
+      work += double(t) * one;
+      longest = std::max(longest, one);
+      k = std::min(k, kb);
+    }
+    if (s > 1 && k < 2 * s) break;
+    const double waves = std::ceil(double(blocks) / kSms);
+    Plan p;
+    p.bn = 128;
+    p.splits = s;
+    offer(p, std::max(waves * work / double(blocks), longest) + 1.0);
+  }
+  return best;
+}
+
+// Few tokens: features are the rows of the tiles, and the K blocks are shared out
+// until the SMs are full.
+Plan plan_few(int64_t tokens, int64_t features, int64_t k) {
+  Plan p;
+  p.swap = true;
+  p.bn = tokens <= 32 ? 32 : 64;
+  const int64_t tiles = ceil_div(features, 128) * ceil_div(tokens, p.bn), kb = ceil_div(k, 64);
+  double least = 0;
+  for (int s = 1; s <= kMostSplits && (s == 1 || kb >= 2 * s); ++s) {
+    const double us = std::ceil(double(tiles * s) / kSms) * double(ceil_div(kb, s)) * 0.17 + (s > 1 ? 1.5 : 0.0);
+    if (s == 1 || us < least) {
+      least = us;
+      p.splits = s;
+    }
+  }
+  return p;
+}
+
+constexpr int kFewTokens = 64;
+
+// The product of a and b, whose k lies along their columns (or, mn, along their
+// rows), as the plan's tiles.  False: the driver refuses a map.
+bool make_product(const Plan& plan, const Operand& a, bool a_mn, const Operand& b, bool b_mn, Product* p) {
+  p->m = a_mn ? a.cols : a.rows;
+  p->n = b_mn ? b.cols : b.rows;
+  const int64_t k = a_mn ? a.rows : a.cols;
+  p->k = int(ceil_div(k, BK));
+  p->a_mn = a_mn;
+  p->b_mn = b_mn;
+  p->tiles_m = int(ceil_div(p->m, plan.pairs ? 256 : 128));
+  p->tiles_n = int(ceil_div(p->n, plan.bn));
+  if (k == 0) return true;   // nothing is loaded
+  auto map = [](CUtensorMap* m, const Operand& o, bool mn, int rows) {
+    return encode_2d(m, o.p, 2, o.cols, o.rows, o.stride, mn ? uint32_t(std::min(rows, 64)) : BK,
+                     mn ? BK : uint32_t(rows), CU_TENSOR_MAP_SWIZZLE_128B);
+  };
+  return map(&p->a, a, a_mn, 128) && map(&p->b, b, b_mn, plan.pairs ? plan.bn / 2 : plan.bn);
+}
+
+template <auto KERNEL, class W>
+cudaError_t launch_shared(unsigned grid, unsigned block, int cluster, int bytes, cudaStream_t s, const W& w,
+                          int splits, int* err) {
+  static uint64_t done = 0;   // devices that know how much shared memory this kernel takes
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (!(done >> (dev & 63) & 1)) {
+    e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    done |= uint64_t(1) << (dev & 63);
+  }
+  if constexpr (std::is_invocable_v<decltype(KERNEL), W, int*>)
+    return launch(KERNEL, grid, block, 1, false, s, bytes, w, err);
+  else
+    return launch(KERNEL, grid, block, cluster, false, s, bytes, w, splits, err);
+}
+
+template <class E0, class E1>
+cudaError_t launch_work(const Plan& plan, const Work<E0, E1>& w, cudaStream_t s) {
+  void* err = nullptr;
+  const cudaError_t e = cudaGetSymbolAddress(&err, g_linear_err);
+  if (e != cudaSuccess) return e;
+  int* flag = static_cast<int*>(err);
+  if (plan.pairs) {
+    const unsigned grid = 2 * unsigned(std::min(w.tiles, kPairs));
+    if (plan.bn == 256)
+      return launch_shared<k_linear_pair<256, E0, E1>>(grid, kPairThreads, 2, PairShape<256>::kShared, s, w, 1, flag);
+    return launch_shared<k_linear_pair<128, E0, E1>>(grid, kPairThreads, 2, PairShape<128>::kShared, s, w, 1, flag);
+  }
+  const unsigned grid = unsigned(w.tiles) * plan.splits;
+  if constexpr (std::is_same_v<E1, NoProduct> && !std::is_same_v<E0, WeightGrad>) {
+    if (plan.swap && plan.bn == 32)
+      return launch_shared<k_linear_split<32, true, E0, E1>>(grid, kSplitThreads, plan.splits, SplitShape<32>::kShared, s,
+                                                           w, plan.splits, flag);
+    if (plan.swap)
+      return launch_shared<k_linear_split<64, true, E0, E1>>(grid, kSplitThreads, plan.splits, SplitShape<64>::kShared, s,
+                                                           w, plan.splits, flag);
+  }
+  return launch_shared<k_linear_split<128, false, E0, E1>>(grid, kSplitThreads, plan.splits, SplitShape<128>::kShared, s,
+                                                         w, plan.splits, flag);
+}
+
+// One product.
+template <class E>
+cudaError_t run_one(const Plan& plan, const Operand& a, bool a_mn, const Operand& b, bool b_mn, const E& e,
+                    cudaStream_t s) {
+  static Work<E, NoProduct> w;   // large; the caller holds the library lock
+  w.e0 = e;
+  if (!make_product(plan, a, a_mn, b, b_mn, &w.p[0])) return cudaErrorInvalidValue;
+  w.tiles0 = w.tiles = w.p[0].tiles_m * w.p[0].tiles_n;
+  return launch_work(plan, w, s);
+}
+
+// The sum of launches' tiles stays below 2^31 (each plan has no more than this).
 int check_sizes(int64_t tokens, int in, int out, int act) {
   if (tokens < 0 || tokens > (int64_t(1) << 30)) return fail_with(MUON_ERR_INVALID, "n_tokens must be in [0, 2^30]");
   if (in < 1 || out < 1 || in > kMostFeatures || out > kMostFeatures)
     return fail_with(MUON_ERR_INVALID, "in_features and out_features must be in [1, 2^24]");
   if (act < MUON_ACT_NONE || act > MUON_ACT_SILU) return fail_with(MUON_ERR_INVALID, "unknown activation");
-  auto tiles = [](int64_t a, int64_t b) { return ((a + kTile - 1) / kTile) * ((b + kTile - 1) / kTile); };
-  if (tiles(tokens, out) > 0x7fffffff || tiles(tokens, in) > 0x7fffffff || tiles(in, out) > 0x7fffffff)
+  auto tiles = [](int64_t a, int64_t b) { return ceil_div(a, 128) * ceil_div(b, 128) * kMostSplits; };
+  if (tiles(tokens, out) + tiles(tokens, in) + tiles(in, out) > 0x7fffffff)
     return fail_with(MUON_ERR_UNSUPPORTED, "too many tokens and features for one launch");
   return MUON_OK;
 }
@@ -200,15 +1084,16 @@ int check_forward(const muon_linear_args_t* a, Forward* f) {
   if (out.meets(pre) || pre.meets(res) ||
       (out.meets(res) && !lay::same(a->residual, a->residual_stride, a->out, a->out_stride)))
     return fail_with(MUON_ERR_INVALID, "out, pre and the residual overlap");
+  auto matrix = [&](const void* p, int64_t stride, size_t size) {
+    return Matrix{const_cast<void*>(p), stride, size == 4, !misaligned(p, 16) && (T <= 1 || stride * int64_t(size) % 16 == 0)};
+  };
   f->bias = a->bias;
   f->bias32 = a->bias_dtype == MUON_DTYPE_FP32;
-  f->pre = static_cast<__nv_bfloat16*>(a->pre);
-  f->pre_stride = a->pre_stride;
-  f->residual = a->residual;
-  f->res_stride = a->residual_stride;
-  f->out = a->out;
-  f->out_stride = a->out_stride;
-  f->out32 = es == 4;
+  f->out = matrix(a->out, a->out_stride, es);
+  f->pre = matrix(a->pre, a->pre_stride, 2);
+  f->residual = matrix(a->residual, a->residual_stride, es);
+  f->rows = T;
+  f->cols = N;
   f->act = a->activation;
   return MUON_OK;
 }
@@ -255,6 +1140,25 @@ int check_grad(const muon_linear_grad_args_t* a, GradPlaces* at) {
   return MUON_OK;
 }
 
+// The operands of the gradients' products.
+struct GradOperands {
+  Operand dout, weight, x;
+  size_t bytes() const { return dout.packed + weight.packed + x.packed; }
+};
+
+GradOperands grad_operands(const muon_linear_grad_args_t& a) {
+  GradOperands o;
+  if (a.n_tokens == 0) {   // sums of nothing: extents only
+    o.dout = Operand(nullptr, 0, a.out_features, a.out_features);
+    o.x = Operand(nullptr, 0, a.in_features, a.in_features);
+    return o;
+  }
+  if (a.dx || a.param) o.dout = Operand(a.dout, a.n_tokens, a.out_features, a.dout_stride);
+  if (a.dx) o.weight = Operand(a.weight, a.out_features, a.in_features, a.weight_stride);
+  if (a.param) o.x = Operand(a.x, a.n_tokens, a.in_features, a.x_stride);
+  return o;
+}
+
 }  // namespace
 
 int linear_take_device_error() { return take_flag(g_linear_err); }
@@ -262,6 +1166,21 @@ int linear_take_device_error() { return take_flag(g_linear_err); }
 }  // namespace muon
 
 using namespace muon;
+
+namespace {
+
+// Where the workspace is too small for `need` bytes.
+int check_workspace(const void* workspace, size_t bytes, size_t need, std::initializer_list<Span> others) {
+  if (!need) return MUON_OK;
+  if (!workspace || misaligned(workspace, 16) || bytes < need)
+    return fail_with(MUON_ERR_INVALID, "workspace is NULL, misaligned or too small");
+  const Span work(workspace, 1, int64_t(need), int64_t(need), 1);
+  for (const Span& v : others)
+    if (v.meets(work)) return fail_with(MUON_ERR_INVALID, "workspace overlaps another tensor");
+  return MUON_OK;
+}
+
+}  // namespace
 
 extern "C" int muon_linear_workspace(const muon_linear_args_t* args, size_t* bytes) {
   return entry([&]() -> int {
@@ -271,7 +1190,9 @@ extern "C" int muon_linear_workspace(const muon_linear_args_t* args, size_t* byt
     const int rc = check_forward(args, &f);
     if (rc != MUON_OK) return rc;
     if (!bytes) return fail_with(MUON_ERR_INVALID, "bytes is NULL");
-    *bytes = 0;
+    const Operand x(args->x, args->n_tokens, args->in_features, args->x_stride),
+        w(args->weight, args->out_features, args->in_features, args->weight_stride);
+    *bytes = args->n_tokens ? x.packed + w.packed : 0;
     return MUON_OK;
   });
 }
@@ -284,12 +1205,33 @@ extern "C" int muon_linear(const muon_linear_args_t* args, void* workspace, size
     Forward f{};
     int rc = check_forward(args, &f);
     if (rc != MUON_OK) return rc;
-    if (args->n_tokens == 0) return MUON_OK;
-    if ((rc = lay::begin_call()) != MUON_OK) return rc;
-    const Operands p{static_cast<const __nv_bfloat16*>(args->x), static_cast<const __nv_bfloat16*>(args->weight),
-                     args->x_stride, 1, args->weight_stride, 1, args->n_tokens, args->out_features,
-                     args->in_features};
-    return lay::end_call(1, launch_product(p, f, f.drop, static_cast<cudaStream_t>(stream)));
+    const muon_linear_args_t& a = *args;
+    const int64_t T = a.n_tokens;
+    const int K = a.in_features, N = a.out_features;
+    if (T == 0) return MUON_OK;
+    Operand x(a.x, T, K, a.x_stride), w(a.weight, N, K, a.weight_stride);
+    const size_t es = dtype_bytes(a.out_dtype);
+    if ((rc = check_workspace(workspace, workspace_bytes, x.packed + w.packed,
+                              {Span(a.x, T, a.x_stride, K, 2), Span(a.weight, N, a.weight_stride, K, 2),
+                               Span(a.bias, 1, N, N, dtype_bytes(a.bias_dtype)),
+                               Span(a.residual, T, a.residual_stride, N, es), Span(a.out, T, a.out_stride, N, es),
+                               Span(a.pre, T, a.pre_stride, N, 2),
+                               Span(f.drop.least ? a.rng : nullptr, 1, 2, 2, 8)})) != MUON_OK ||
+        (rc = lay::begin_call()) != MUON_OK)
+      return rc;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    char* at = static_cast<char*>(workspace);
+    int launches = 0;
+    cudaError_t e = x.pack(&at, s, &launches);
+    if (e == cudaSuccess) e = w.pack(&at, s, &launches);
+    if (e != cudaSuccess) return lay::end_call(launches, e);
+    if (T <= kFewTokens) {
+      e = run_one(plan_few(T, N, K), w, false, x, false, f, s);
+    } else {
+      const Extent size{T, N, K};
+      e = run_one(plan_of(&size, 1), x, false, w, false, f, s);
+    }
+    return lay::end_call(launches + 1, e);
   });
 }
 
@@ -301,7 +1243,7 @@ extern "C" int muon_linear_grad_workspace(const muon_linear_grad_args_t* args, s
     const int rc = check_grad(args, &at);
     if (rc != MUON_OK) return rc;
     if (!bytes) return fail_with(MUON_ERR_INVALID, "bytes is NULL");
-    *bytes = 0;
+    *bytes = grad_operands(*args).bytes();
     return MUON_OK;
   });
 }
@@ -312,37 +1254,78 @@ extern "C" int muon_linear_grad(const muon_linear_grad_args_t* args, void* works
     NvtxRange nvtx_("muon_linear_grad");
     std::lock_guard<std::mutex> lk(library_mutex());
     set_last_error(nullptr);
-    GradPlaces at;
-    int rc = check_grad(args, &at);
+    GradPlaces places;
+    int rc = check_grad(args, &places);
     if (rc != MUON_OK) return rc;
     const muon_linear_grad_args_t& a = *args;
-    const bool sums = a.param || a.bias;
-    if (a.n_tokens == 0 && !(sums && a.overwrite)) return MUON_OK;
-    if ((rc = lay::begin_call()) != MUON_OK) return rc;
+    const int64_t T = a.n_tokens;
+    const int K = a.in_features, N = a.out_features;
+    const bool sums = a.param || a.bias, slope = a.dx && a.activation != MUON_ACT_NONE;
+    if (T == 0 && !(sums && a.overwrite)) return MUON_OK;
+    GradOperands o = grad_operands(a);
+    if ((rc = check_workspace(workspace, workspace_bytes, o.bytes(),
+                              {Span(a.dout, T, a.dout_stride, N, 2), Span(a.param ? a.x : nullptr, T, a.x_stride, K, 2),
+                               Span(a.dx ? a.weight : nullptr, N, a.weight_stride, K, 2),
+                               Span(slope ? a.pre : nullptr, T, a.pre_stride, K, 2), Span(a.dx, T, a.dx_stride, K, 2),
+                               Span(sums ? a.accum : nullptr, 1, a.accum_elems, a.accum_elems, 4)})) != MUON_OK ||
+        (rc = lay::begin_call()) != MUON_OK)
+      return rc;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const __nv_bfloat16 *d = static_cast<const __nv_bfloat16*>(a.dout), *x = static_cast<const __nv_bfloat16*>(a.x),
-                        *w = static_cast<const __nv_bfloat16*>(a.weight);
+    char* at = static_cast<char*>(workspace);
     int launches = 0;
-    cudaError_t e = cudaSuccess;
-    if (a.dx && a.n_tokens) {
-      const InputGrad f{static_cast<const __nv_bfloat16*>(a.pre), static_cast<__nv_bfloat16*>(a.dx), a.pre_stride,
-                        a.dx_stride, a.activation};
-      const Operands p{d, w, a.dout_stride, 1, 1, a.weight_stride, a.n_tokens, a.in_features, a.out_features};
-      if ((e = launch_product(p, f, Dropout{}, s)) != cudaSuccess) return lay::end_call(launches, e);
+    cudaError_t e = o.dout.pack(&at, s, &launches);
+    if (e == cudaSuccess) e = o.weight.pack(&at, s, &launches);
+    if (e == cudaSuccess) e = o.x.pack(&at, s, &launches);
+    if (e != cudaSuccess) return lay::end_call(launches, e);
+    InputGrad f{};
+    auto matrix = [&](const void* p, int64_t stride) {
+      return Matrix{const_cast<void*>(p), stride, 0, !misaligned(p, 16) && (T <= 1 || stride % 8 == 0)};
+    };
+    f.dx = matrix(a.dx, a.dx_stride);
+    f.pre = matrix(a.pre, a.pre_stride);
+    f.rows = T;
+    f.cols = K;
+    f.act = a.activation;
+    WeightGrad g{};
+    g.accum = a.accum;
+    g.rows = N;
+    g.cols = K;
+    g.overwrite = a.overwrite;
+    g.scale = a.scale;
+    if (a.param) g.sg = places.weight;
+    const bool dx = a.dx && T, dw = a.param, few = T <= kFewTokens;
+    const Extent size[2] = {{T, K, N}, {N, K, T}};   // of dx and of the weight's gradient
+    if (dx && dw && !few) {
+      // both at once: the tiles of one fill the SMs behind those of the other
+      static Work<InputGrad, WeightGrad> w;   // large; this call holds the library lock
+      const Plan plan = plan_of(size, 2);
+      w.e0 = f;
+      w.e1 = g;
+      e = make_product(plan, o.dout, false, o.weight, true, &w.p[0]) &&
+                  make_product(plan, o.dout, true, o.x, true, &w.p[1])
+              ? cudaSuccess
+              : cudaErrorInvalidValue;
+      w.tiles0 = w.p[0].tiles_m * w.p[0].tiles_n;
+      w.tiles = w.tiles0 + w.p[1].tiles_m * w.p[1].tiles_n;
+      if (e == cudaSuccess) e = launch_work(plan, w, s);
       ++launches;
+    } else {
+      if (dx) {
+        e = few ? run_one(plan_few(T, K, N), o.weight, true, o.dout, false, f, s)
+                : run_one(plan_of(&size[0], 1), o.dout, false, o.weight, true, f, s);
+        ++launches;
+      }
+      if (dw && e == cudaSuccess) {
+        e = run_one(plan_of(&size[1], 1), o.dout, true, o.x, true, g, s);
+        ++launches;
+      }
     }
-    if (a.param) {
-      const WeightGrad f{a.accum, a.in_features, a.scale, a.overwrite, at.weight};
-      const Operands p{d, x, 1, a.dout_stride, 1, a.x_stride, a.out_features, a.in_features, a.n_tokens};
-      if ((e = launch_product(p, f, Dropout{}, s)) != cudaSuccess) return lay::end_call(launches, e);
-      ++launches;
-    }
+    if (e != cudaSuccess) return lay::end_call(launches, e);
     if (a.bias) {
-      const BiasGrad b{d, a.dout_stride, a.n_tokens, a.out_features, a.accum, a.scale, a.overwrite};
-      e = launch(k_bias_grad, unsigned((a.out_features + 31) / 32), 1024, 1, false, s, 0, b, at.bias);
-      if (e != cudaSuccess) return lay::end_call(launches, e);
+      const BiasGrad b{static_cast<const __nv_bfloat16*>(a.dout), a.dout_stride, T, N, a.accum, a.scale, a.overwrite};
+      e = launch(k_bias_grad, unsigned((N + 31) / 32), 1024, 1, false, s, 0, b, places.bias);
       ++launches;
     }
-    return lay::end_call(launches, cudaSuccess);
+    return lay::end_call(launches, e);
   });
 }
