@@ -45,53 +45,51 @@ struct Matrix {
   int fp32;
   int wide;   // every row starts on 16 bytes
 
-  __device__ __forceinline__ void* at(int64_t r, int64_t c) const {
+  __device__ __forceinline__ char* at(int64_t r, int64_t c) const {
     return static_cast<char*>(p) + (r * stride + c) * (fp32 ? 4 : 2);
   }
-  // The lane's eight elements of a row, `left` of them inside.
-  __device__ __forceinline__ void load(int64_t r, int64_t c, int left, float* f) const {
+  __device__ __forceinline__ int64_t step() const { return 8 * stride * (fp32 ? 4 : 2); }   // bytes between the lane's rows
+  // The lane's eight elements at q, `left` of them inside the row.
+  __device__ __forceinline__ void load(const char* q, int left, float* f) const {
     if (fp32) {
-      const float* q = static_cast<const float*>(p) + r * stride + c;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = j < left ? q[j] : 0.f;
+      for (int j = 0; j < 8; ++j) f[j] = j < left ? reinterpret_cast<const float*>(q)[j] : 0.f;
     } else {
-      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p) + r * stride + c;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = j < left ? tok::to_float(q[j]) : 0.f;
+      for (int j = 0; j < 8; ++j)
+        f[j] = j < left ? tok::to_float(reinterpret_cast<const __nv_bfloat16*>(q)[j]) : 0.f;
     }
   }
-  __device__ __forceinline__ void store(int64_t r, int64_t c, int left, const float* f) const {
+  __device__ __forceinline__ void store(char* q, int left, const float* f) const {
     if (wide && left >= 8) {
-      uint4* q = static_cast<uint4*>(at(r, c));
+      uint4* u = reinterpret_cast<uint4*>(q);
       if (fp32) {
-        q[0] = tok::Vec<float>::pack(f);
-        q[1] = tok::Vec<float>::pack(f + 4);
+        u[0] = tok::Vec<float>::pack(f);
+        u[1] = tok::Vec<float>::pack(f + 4);
       } else {
-        q[0] = tok::Vec<__nv_bfloat16>::pack(f);
+        u[0] = tok::Vec<__nv_bfloat16>::pack(f);
       }
     } else if (fp32) {
-      float* q = static_cast<float*>(p) + r * stride + c;
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (j < left) q[j] = f[j];
+        if (j < left) reinterpret_cast<float*>(q)[j] = f[j];
     } else {
-      __nv_bfloat16* q = static_cast<__nv_bfloat16*>(p) + r * stride + c;
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (j < left) q[j] = __float2bfloat16_rn(f[j]);
+        if (j < left) reinterpret_cast<__nv_bfloat16*>(q)[j] = __float2bfloat16_rn(f[j]);
     }
   }
   // Fetches the lane's part of a chunk into its slots; bf16 chunks alternate
   // between two halves.
   __device__ __forceinline__ void fetch(uint32_t slots, int half, int64_t r0, int64_t c0, int64_t rows, int64_t cols,
                                         int lane) const {
-    const int64_t c = c0 + (lane & 3) * 8;
+    const int64_t c = c0 + (lane & 3) * 8, r = r0 + (lane >> 2);
     if (!wide || cols - c < 8) return;
+    const char* q = at(r, c);
+    const int64_t by = step();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t r = r0 + 8 * i + (lane >> 2);
-      if (r >= rows) break;
-      const char* q = static_cast<const char*>(at(r, c));
+    for (int i = 0; i < 4; ++i, q += by) {
+      if (r + 8 * i >= rows) break;
       if (fp32) {
         copy16(slots + (2 * i) * 512 + lane * 16, q);
         copy16(slots + (2 * i + 1) * 512 + lane * 16, q + 16);
@@ -100,9 +98,9 @@ struct Matrix {
       }
     }
   }
-  __device__ __forceinline__ void fetched(uint32_t slots, int half, int i, int64_t r, int64_t c, int left, int lane,
+  __device__ __forceinline__ void fetched(uint32_t slots, int half, int i, const char* q, int left, int lane,
                                           float* f) const {
-    if (!wide || left < 8) return load(r, c, left, f);
+    if (!wide || left < 8) return load(q, left, f);
     if (fp32) {
       tok::Vec<float>::unpack(slot16(slots + (2 * i) * 512 + lane * 16), f);
       tok::Vec<float>::unpack(slot16(slots + (2 * i + 1) * 512 + lane * 16), f + 4);
@@ -113,16 +111,25 @@ struct Matrix {
 };
 
 template <int KIND>
-__device__ __forceinline__ void act8(float* v) {
+__device__ __forceinline__ void act32(float (&v)[4][8]) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = lay::activation(v[j], KIND);
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[i][j] = lay::activation(v[i][j], KIND);
 }
 
 template <int KIND>
-__device__ __forceinline__ void slope8(float* v, const float* u) {
+__device__ __forceinline__ void slope32(float (&v)[4][8], const float (&u)[4][8]) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] *= lay::slope(u[j], KIND);
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[i][j] *= lay::slope(u[i][j], KIND);
 }
+
+// A lane's four rows of a chunk go through each step together: four independent
+// chains hide the latency that one warp has nothing else to hide behind (one
+// row at a time, the results of a 256 x 256 tile took 12 us, longer than the
+// sums of 4096 terms; now 3 us).
 
 // out = residual + dropout(activation(acc + bias)), pre = acc + bias.
 struct Forward {
@@ -132,6 +139,8 @@ struct Forward {
   int cols, bias32, act;
   Dropout drop;
 
+  // Sums of a result in FP32 are added up in registers, see kDepth.
+  __device__ __forceinline__ bool exact() const { return out.fp32; }
   __device__ __forceinline__ bool halves() const { return !residual.fp32; }
   __device__ __forceinline__ void fetch(uint32_t slots, int half, int64_t t0, int64_t n0, int lane) const {
     if (residual.p) residual.fetch(slots, half, t0, n0, rows, cols, lane);
@@ -139,44 +148,67 @@ struct Forward {
   template <typename Read>
   __device__ __forceinline__ void chunk(const Read& read, uint32_t slots, int half, int64_t t0, int64_t n0, int lane,
                                         const Draw& draw) const {
-    const int64_t n = n0 + (lane & 3) * 8;
+    const int64_t n = n0 + (lane & 3) * 8, t = t0 + (lane >> 2);
     const int left = int(min(int64_t(8), cols - n));
-    if (left <= 0) return;
-    float b[8];
+    const int live = int(min(int64_t(4), (rows - t + 7) >> 3));   // of the lane's rows
+    if (left <= 0 || live <= 0) return;
+    float v[4][8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      b[j] = !bias || j >= left ? 0.f
-             : bias32           ? static_cast<const float*>(bias)[n + j]
-                                : tok::to_float(static_cast<const __nv_bfloat16*>(bias)[n + j]);
-#pragma unroll 1
-    for (int i = 0; i < 4; ++i) {
-      const int64_t t = t0 + 8 * i + (lane >> 2);
-      if (t >= rows) break;
-      float v[8];
-      read(8 * i + (lane >> 2), lane & 3, v);
+    for (int i = 0; i < 4; ++i) read(8 * i + (lane >> 2), lane & 3, v[i]);
+    if (bias) {
+      float b[8];
+      if (bias32) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] += b[j];
-      if (pre.p) pre.store(t, n, left, v);
-      switch (act) {
-        case MUON_ACT_RELU: act8<MUON_ACT_RELU>(v); break;
-        case MUON_ACT_RELU2: act8<MUON_ACT_RELU2>(v); break;
-        case MUON_ACT_GELU: act8<MUON_ACT_GELU>(v); break;
-        case MUON_ACT_SILU: act8<MUON_ACT_SILU>(v); break;
-        default: break;
+        for (int j = 0; j < 8; ++j) b[j] = j < left ? static_cast<const float*>(bias)[n + j] : 0.f;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          b[j] = j < left ? tok::to_float(static_cast<const __nv_bfloat16*>(bias)[n + j]) : 0.f;
       }
-      if (drop.least) {
-        const uint4 w = draw.at(uint32_t(t), uint32_t(n / 8), drop.site);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = lay::dropped(v[j], lay::draw_of(w, j), drop);
-      }
-      if (residual.p) {
-        float r[8];
-        residual.fetched(slots, half, i, t, n, left, lane, r);
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] += r[j];
-      }
-      out.store(t, n, left, v);
+        for (int j = 0; j < 8; ++j) v[i][j] += b[j];
     }
+    if (pre.p) {
+      char* q = pre.at(t, n);
+      const int64_t by = pre.step();
+#pragma unroll
+      for (int i = 0; i < 4; ++i, q += by)
+        if (i < live) pre.store(q, left, v[i]);
+    }
+    switch (act) {
+      case MUON_ACT_RELU: act32<MUON_ACT_RELU>(v); break;
+      case MUON_ACT_RELU2: act32<MUON_ACT_RELU2>(v); break;
+      case MUON_ACT_GELU: act32<MUON_ACT_GELU>(v); break;
+      case MUON_ACT_SILU: act32<MUON_ACT_SILU>(v); break;
+      default: break;
+    }
+    if (drop.least) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint4 w = draw.at(uint32_t(t + 8 * i), uint32_t(n / 8), drop.site);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] = lay::dropped(v[i][j], lay::draw_of(w, j), drop);
+      }
+    }
+    if (residual.p) {
+      const char* q = residual.at(t, n);
+      const int64_t by = residual.step();
+#pragma unroll
+      for (int i = 0; i < 4; ++i, q += by) {
+        if (i >= live) break;
+        float r[8];
+        residual.fetched(slots, half, i, q, left, lane, r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] += r[j];
+      }
+    }
+    char* q = out.at(t, n);
+    const int64_t by = out.step();
+#pragma unroll
+    for (int i = 0; i < 4; ++i, q += by)
+      if (i < live) out.store(q, left, v[i]);
   }
 };
 
@@ -187,6 +219,7 @@ struct InputGrad {
   int cols, act;
   Dropout drop;   // none
 
+  __device__ __forceinline__ bool exact() const { return false; }
   __device__ __forceinline__ bool halves() const { return true; }
   __device__ __forceinline__ void fetch(uint32_t slots, int half, int64_t t0, int64_t n0, int lane) const {
     if (act != MUON_ACT_NONE) pre.fetch(slots, half, t0, n0, rows, cols, lane);
@@ -194,27 +227,32 @@ struct InputGrad {
   template <typename Read>
   __device__ __forceinline__ void chunk(const Read& read, uint32_t slots, int half, int64_t t0, int64_t n0, int lane,
                                         const Draw&) const {
-    const int64_t n = n0 + (lane & 3) * 8;
+    const int64_t n = n0 + (lane & 3) * 8, t = t0 + (lane >> 2);
     const int left = int(min(int64_t(8), cols - n));
-    if (left <= 0) return;
-#pragma unroll 1
-    for (int i = 0; i < 4; ++i) {
-      const int64_t t = t0 + 8 * i + (lane >> 2);
-      if (t >= rows) break;
-      float v[8];
-      read(8 * i + (lane >> 2), lane & 3, v);
-      if (act != MUON_ACT_NONE) {
-        float u[8];
-        pre.fetched(slots, half, i, t, n, left, lane, u);
-        switch (act) {
-          case MUON_ACT_RELU: slope8<MUON_ACT_RELU>(v, u); break;
-          case MUON_ACT_RELU2: slope8<MUON_ACT_RELU2>(v, u); break;
-          case MUON_ACT_GELU: slope8<MUON_ACT_GELU>(v, u); break;
-          default: slope8<MUON_ACT_SILU>(v, u); break;
-        }
+    const int live = int(min(int64_t(4), (rows - t + 7) >> 3));
+    if (left <= 0 || live <= 0) return;
+    float v[4][8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) read(8 * i + (lane >> 2), lane & 3, v[i]);
+    if (act != MUON_ACT_NONE) {
+      float u[4][8];
+      const char* q = pre.at(t, n);
+      const int64_t by = pre.step();
+#pragma unroll
+      for (int i = 0; i < 4; ++i, q += by)
+        if (i < live) pre.fetched(slots, half, i, q, left, lane, u[i]);
+      switch (act) {
+        case MUON_ACT_RELU: slope32<MUON_ACT_RELU>(v, u); break;
+        case MUON_ACT_RELU2: slope32<MUON_ACT_RELU2>(v, u); break;
+        case MUON_ACT_GELU: slope32<MUON_ACT_GELU>(v, u); break;
+        default: slope32<MUON_ACT_SILU>(v, u); break;
       }
-      dx.store(t, n, left, v);
     }
+    char* q = dx.at(t, n);
+    const int64_t by = dx.step();
+#pragma unroll
+    for (int i = 0; i < 4; ++i, q += by)
+      if (i < live) dx.store(q, left, v[i]);
   }
 };
 
@@ -227,6 +265,7 @@ struct WeightGrad {
   Dropout drop;   // none
   Segments sg;
 
+  __device__ __forceinline__ bool exact() const { return true; }
   __device__ __forceinline__ bool halves() const { return false; }
   // The lane's eight elements lie in one piece, on 16 bytes.
   __device__ __forceinline__ float* whole(int64_t r, int64_t c, int left) const {
@@ -236,14 +275,13 @@ struct WeightGrad {
   }
   __device__ __forceinline__ void fetch(uint32_t slots, int, int64_t r0, int64_t c0, int lane) const {
     if (overwrite) return;
-    const int64_t c = c0 + (lane & 3) * 8;
+    const int64_t c = c0 + (lane & 3) * 8, r = r0 + (lane >> 2);
     const int left = int(min(int64_t(8), cols - c));
     if (left < 8) return;
-#pragma unroll 1
+#pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int64_t r = r0 + 8 * i + (lane >> 2);
-      if (r >= rows) break;
-      const float* p = whole(r, c, left);
+      if (r + 8 * i >= rows) break;
+      const float* p = whole(r + 8 * i, c, left);
       if (!p) continue;
       copy16(slots + (2 * i) * 512 + lane * 16, p);
       copy16(slots + (2 * i + 1) * 512 + lane * 16, p + 4);
@@ -252,34 +290,37 @@ struct WeightGrad {
   template <typename Read>
   __device__ __forceinline__ void chunk(const Read& read, uint32_t slots, int, int64_t r0, int64_t c0, int lane,
                                         const Draw&) const {
-    const int64_t c = c0 + (lane & 3) * 8;
+    const int64_t c = c0 + (lane & 3) * 8, r = r0 + (lane >> 2);
     const int left = int(min(int64_t(8), cols - c));
-    if (left <= 0) return;
-#pragma unroll 1
-    for (int i = 0; i < 4; ++i) {
-      const int64_t r = r0 + 8 * i + (lane >> 2);
-      if (r >= rows) break;
-      float v[8];
-      read(8 * i + (lane >> 2), lane & 3, v);
+    const int live = int(min(int64_t(4), (rows - r + 7) >> 3));
+    if (left <= 0 || live <= 0) return;
+    float v[4][8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] *= scale;
-      if (float* p = whole(r, c, left)) {
+    for (int i = 0; i < 4; ++i) {
+      read(8 * i + (lane >> 2), lane & 3, v[i]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] *= scale;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i >= live) break;
+      if (float* p = whole(r + 8 * i, c, left)) {
         if (!overwrite) {
           float o[8];
           tok::Vec<float>::unpack(slot16(slots + (2 * i) * 512 + lane * 16), o);
           tok::Vec<float>::unpack(slot16(slots + (2 * i + 1) * 512 + lane * 16), o + 4);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] += o[j];
+          for (int j = 0; j < 8; ++j) v[i][j] += o[j];
         }
-        reinterpret_cast<uint4*>(p)[0] = tok::Vec<float>::pack(v);
-        reinterpret_cast<uint4*>(p)[1] = tok::Vec<float>::pack(v + 4);
+        reinterpret_cast<uint4*>(p)[0] = tok::Vec<float>::pack(v[i]);
+        reinterpret_cast<uint4*>(p)[1] = tok::Vec<float>::pack(v[i] + 4);
       } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           if (j >= left) break;
           int64_t room;
-          float* q = accum + sg.place(r * cols + c + j, &room);
-          *q = (overwrite ? 0.f : *q) + v[j];
+          float* q = accum + sg.place((r + 8 * i) * cols + c + j, &room);
+          *q = (overwrite ? 0.f : *q) + v[i][j];
         }
       }
     }
@@ -288,6 +329,7 @@ struct WeightGrad {
 
 struct NoProduct {
   Dropout drop;
+  __device__ __forceinline__ bool exact() const { return false; }
   __device__ __forceinline__ bool halves() const { return true; }
   __device__ __forceinline__ void fetch(uint32_t, int, int64_t, int64_t, int) const {}
   template <typename Read>
@@ -352,6 +394,33 @@ struct ReadAll {
 
 using namespace tc;
 
+// One lane of a converged warp.  The compiler knows that elect.sync leaves one
+// thread: behind `lane == 0` it issued each copy and each product through a loop
+// over the lanes that might be there, 125 cycles apiece, and a K block took 0.45
+// us instead of 0.28 at 256 x 256, 0.3 instead of 0.1 at 128 x 32.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
+  return one != 0;
+}
+
+// Bounded wait, timed by the SM's own clock.
+constexpr long long kMostCycles = 4000000000ll;   // about 2 s
+
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err, int code) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (true) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if (clock64() - t0 > kMostCycles) {
+      *abort_flag = 1;
+      atomicExch(err, code);
+      return false;
+    }
+  }
+}
+
 // D[m][n] = sum over k of A[m][k] B[n][k].  An operand lies with its k
 // contiguous, or (mn) with its rows contiguous, k rows apart.
 struct Product {
@@ -372,11 +441,12 @@ struct Work {
 
 constexpr int BK = 64;
 
-// Sums of so many K blocks (1024 terms) are formed in tensor memory, whose
-// additions cut off instead of rounding; FP32 registers add those.  Without
-// that a sum of 32768 terms loses 6e-5 of its size (half a unit of 2^-23 every 16
-// terms, all in one direction); with it 2e-6.
-constexpr int kDepth = 16;
+// Tensor memory's additions cut off instead of rounding, all in one direction: half
+// a unit of 2^-23 every 16 terms.  For a result in FP32 so many K blocks (512
+// terms) are summed there and FP32 registers add those (a sum of 32768 terms is then
+// off by 1e-6 of its size, where one pass would leave 6e-5).  What is rounded to bf16
+// is not: 2^24 terms would have to come together before that showed.
+constexpr int kDepth = 8;
 
 __device__ __forceinline__ uint32_t idesc_of(const Product& p, int m, int n) {
   return make_idesc(p.b_mn != 0, m, n) | (p.a_mn ? 1u << 15 : 0u);
@@ -399,11 +469,14 @@ __device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* ma
   }
 }
 
-// Descriptor of its 16 terms from k * 16.
-__device__ __forceinline__ uint64_t operand_desc(uint32_t at, int mn, int k, int rows) {
-  return mn ? make_desc(at + k * 16 * 128, 64 * BK * 2, 1024, kSwizzle128)
-            : make_desc(at + k * 32, 16, 1024, kSwizzle128);
+// Descriptor of the first 16 of its terms, and what the next 16 and the next
+// stage add to it (its low bits are the address / 16, below 2^14).  One thread
+// issues every product: building descriptors anew for each took it 0.45 us a K
+// block, where the tensor cores take 0.28.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t at, int mn) {
+  return mn ? make_desc(at, 64 * BK * 2, 1024, kSwizzle128) : make_desc(at, 16, 1024, kSwizzle128);
 }
+__device__ __forceinline__ uint32_t operand_step(int mn) { return mn ? 16 * 128 / 16 : 32 / 16; }
 
 // Tiles in groups of eight rows of tiles, column by column: what is under way
 // at one time shares its operands in L2.
@@ -474,7 +547,7 @@ k_linear_pair(const __grid_constant__ Work<E0, E1> w, int* err) {
   const uint32_t tmem = *tmem_slot;
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       int s = 0;
       uint32_t ph = 0;
       for (int tile = first; tile < w.tiles && !*abort_flag; tile += step) {
@@ -483,38 +556,41 @@ k_linear_pair(const __grid_constant__ Work<E0, E1> w, int* err) {
         int tm, tn;
         tile_of(p, which ? tile - w.tiles0 : tile, &tm, &tn);
         const int row0 = tm * 256 + int(rank) * 128, col0 = tn * BN + int(rank) * (BN / 2);
-        for (int kb = 0; kb < p.k; ++kb) {
-          if (!mbar_wait(empty(s), ph ^ 1u, abort_flag, err, ERR_TIMEOUT_PRODUCER)) break;
+        const int nk = p.k, a_mn = p.a_mn, b_mn = p.b_mn;
+        const CUtensorMap *ma = &p.a, *mb = &p.b;
+        for (int kb = 0; kb < nk; ++kb) {
+          if (!wait(empty(s), ph ^ 1u, abort_flag, err, ERR_TIMEOUT_PRODUCER)) break;
           const uint32_t sa = base + s * S::kStage, fb = mapa_shared(full(s), 0);
           if (rank == 0) mbar_expect_tx(full(s), 2 * S::kStage);
-          load_operand<128, true>(sa, &p.a, p.a_mn, kb, row0, fb);
-          load_operand<BN / 2, true>(sa + S::kA, &p.b, p.b_mn, kb, col0, fb);
+          load_operand<128, true>(sa, ma, a_mn, kb, row0, fb);
+          load_operand<BN / 2, true>(sa + S::kA, mb, b_mn, kb, col0, fb);
           if (++s == S::kStages) { s = 0; ph ^= 1u; }
         }
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0 && elect_one()) {
       int s = 0, acc = 0;
       uint32_t ph = 0, acc_ph = 0;
       bool ok = true;
       for (int tile = first; ok && tile < w.tiles; tile += step) {
         const Product& p = w.p[tile >= w.tiles0];
         const uint32_t idesc = idesc_of(p, 256, BN);
-        const int a_mn = p.a_mn, b_mn = p.b_mn;
-        for (int k0 = 0; ok && k0 < p.k; k0 += kDepth) {
-          if (!mbar_wait(tempty(acc), acc_ph ^ 1u, abort_flag, err, ERR_TIMEOUT_MMA)) { ok = false; break; }
+        const uint64_t a0 = operand_desc(base, p.a_mn), b0 = operand_desc(base + S::kA, p.b_mn);
+        const uint32_t a_step = operand_step(p.a_mn), b_step = operand_step(p.b_mn);
+        const int nk = p.k, depth = (tile >= w.tiles0 ? w.e1.exact() : w.e0.exact()) ? kDepth : nk;
+        for (int k0 = 0; ok && k0 < nk; k0 += depth) {
+          if (!wait(tempty(acc), acc_ph ^ 1u, abort_flag, err, ERR_TIMEOUT_MMA)) { ok = false; break; }
           tc_fence_after();
           const uint32_t d = tmem + uint32_t(acc * BN);
-          const int k1 = min(p.k, k0 + kDepth);
+          const int k1 = min(nk, k0 + depth);
           for (int kb = k0; kb < k1; ++kb) {
-            if (!mbar_wait(full(s), ph, abort_flag, err, ERR_TIMEOUT_MMA)) { ok = false; break; }
+            if (!wait(full(s), ph, abort_flag, err, ERR_TIMEOUT_MMA)) { ok = false; break; }
             tc_fence_after();
-            const uint32_t sa = base + s * S::kStage;
+            uint64_t ad = a0 + uint32_t(s * (S::kStage / 16)), bd = b0 + uint32_t(s * (S::kStage / 16));
 #pragma unroll
-            for (int k = 0; k < BK / 16; ++k)
-              umma_bf16_pair(d, operand_desc(sa, a_mn, k, 128), operand_desc(sa + S::kA, b_mn, k, BN / 2), idesc,
-                             kb > k0 || k > 0);
+            for (int k = 0; k < BK / 16; ++k, ad += a_step, bd += b_step)
+              umma_bf16_pair(d, ad, bd, idesc, kb > k0 || k > 0);
             umma_commit_pair(empty(s), 0x3);
             if (++s == S::kStages) { s = 0; ph ^= 1u; }
           }
@@ -546,45 +622,70 @@ k_linear_pair(const __grid_constant__ Work<E0, E1> w, int* err) {
         else w.e0.fetch(slots, c & 1, m0, n0 + 32 * c, lane);
       };
       if (here && n0 < p.n) fetch(0);
+      // the chunk in `stage`; the other half of bf16 slots is refilled before it is
+      // read, FP32 slots behind that
+      auto finish = [&](int c) {
+        copies_done();
+        __syncwarp();
+        const bool ahead = c + 1 < N && n0 + 32 * (c + 1) < p.n, halves = which ? w.e1.halves() : w.e0.halves();
+        if (ahead && halves) fetch(c + 1);
+        if (which) w.e1.chunk(ReadOwn{stage}, slots, c & 1, m0, n0 + 32 * c, lane, draw);
+        else w.e0.chunk(ReadOwn{stage}, slots, c & 1, m0, n0 + 32 * c, lane, draw);
+        if (ahead && !halves) fetch(c + 1);
+        __syncwarp();
+      };
+      auto next = [&] {   // hands the accumulator back
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(mapa_shared(tempty(acc), 0));
+        acc ^= 1;
+        if (acc == 0) acc_ph ^= 1u;
+      };
+      const uint32_t mine = tmem + uint32_t(side * (BN / 2)) + (uint32_t(q * 32) << 16);
+      if (!(which ? w.e1.exact() : w.e0.exact())) {
+        if (p.k == 0) continue;   // no such product: results in bf16 have terms
+        if (!wait(tfull(acc), acc_ph, abort_flag, err, ERR_TIMEOUT_EPILOGUE)) { ok = false; break; }
+        __syncwarp();
+        tc_fence_after();
+        if (here) {
+#pragma unroll 1
+          for (int c = 0; c < N; ++c) {
+            if (n0 + 32 * c >= p.n) break;
+            float x[32];
+            tmem_ld32(mine + uint32_t(acc * BN + c * 32), x);
+            stage_rows(stage, lane, x);
+            finish(c);
+          }
+        }
+        next();
+        continue;
+      }
       float sum[N][32];
 #pragma unroll
       for (int c = 0; c < N; ++c)
 #pragma unroll
         for (int j = 0; j < 32; ++j) sum[c][j] = 0.f;
       for (int k0 = 0; k0 < p.k; k0 += kDepth) {
-        if (!mbar_wait(tfull(acc), acc_ph, abort_flag, err, ERR_TIMEOUT_EPILOGUE)) { ok = false; break; }
+        if (!wait(tfull(acc), acc_ph, abort_flag, err, ERR_TIMEOUT_EPILOGUE)) { ok = false; break; }
         __syncwarp();
         tc_fence_after();
         if (here) {
 #pragma unroll
           for (int c = 0; c < N; ++c) {
             float x[32];
-            tmem_ld32(tmem + uint32_t(acc * BN + side * (BN / 2) + c * 32) + (uint32_t(q * 32) << 16), x);
+            tmem_ld32(mine + uint32_t(acc * BN + c * 32), x);
 #pragma unroll
             for (int j = 0; j < 32; ++j) sum[c][j] += x[j];
           }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(mapa_shared(tempty(acc), 0));
-        acc ^= 1;
-        if (acc == 0) acc_ph ^= 1u;
+        next();
       }
       if (!ok || !here) continue;
 #pragma unroll
       for (int c = 0; c < N; ++c) {
         if (n0 + 32 * c >= p.n) continue;
         stage_rows(stage, lane, sum[c]);
-        copies_done();
-        __syncwarp();
-        // the other half is free; FP32 slots are refilled once this chunk has read them
-        const bool ahead = c + 1 < N && n0 + 32 * (c + 1) < p.n;
-        const bool halves = which ? w.e1.halves() : w.e0.halves();
-        if (ahead && halves) fetch(c + 1);
-        if (which) w.e1.chunk(ReadOwn{stage}, slots, c & 1, m0, n0 + 32 * c, lane, draw);
-        else w.e0.chunk(ReadOwn{stage}, slots, c & 1, m0, n0 + 32 * c, lane, draw);
-        if (ahead && !halves) fetch(c + 1);
-        __syncwarp();
+        finish(c);
       }
     }
   }
@@ -607,11 +708,13 @@ constexpr int kMostSplits = 8;   // blocks of a portable cluster
 template <int BN>
 struct SplitShape {
   static constexpr int kA = 128 * BK * 2, kB = BN * BK * 2, kStage = kA + kB;
-  static constexpr int kStages = BN == 128 ? 6 : 8;
+  static constexpr int kBlocks = BN == 128 ? 1 : 2;   // per SM
+  static constexpr int kStages = BN == 128 ? 6 : BN == 64 ? 4 : 5;
   static constexpr int kBars = 2 * kStages + 4;
   static constexpr int kChunks = kSplitWarps * (BN / 32);
-  static constexpr int kShared = 1024 + kStages * kStage + kSplitWarps * kSlotBytes + 8 * kBars + 16;
-  static_assert(kChunks * kChunkBytes <= kStages * kStage, "the sums take the operands' place");
+  static constexpr int kShared = 1024 + kStages * kStage + 8 * kBars + 16;
+  static_assert(kChunks * kChunkBytes + kSplitWarps * kSlotBytes <= kStages * kStage,
+                "sums and slots take the operands' place");
 };
 
 // One tile of 128 x BN per cluster, whose blocks share out the K blocks and add
@@ -620,13 +723,12 @@ struct SplitShape {
 // there are many) and its columns the result's rows (few tokens), so that few
 // tokens leave no part of a tile's 128 rows empty.
 template <int BN, bool SWAP, class E0, class E1>
-__global__ void __launch_bounds__(kSplitThreads, 1)
+__global__ void __launch_bounds__(kSplitThreads, SplitShape<BN>::kBlocks)
 k_linear_split(const __grid_constant__ Work<E0, E1> w, int splits, int* err) {
   using S = SplitShape<BN>;
   extern __shared__ uint8_t raw_shared[];
   const uint32_t base = (smem_u32(raw_shared) + 1023u) & ~1023u;
-  const uint32_t slot_base = base + S::kStages * S::kStage;
-  const uint32_t bars = slot_base + kSplitWarps * kSlotBytes;
+  const uint32_t bars = base + S::kStages * S::kStage;
   auto full = [&](int s) { return bars + 8u * s; };
   auto empty = [&](int s) { return bars + 8u * (S::kStages + s); };
   auto tfull = [&](int i) { return bars + 8u * (2 * S::kStages + i); };
@@ -667,7 +769,7 @@ k_linear_split(const __grid_constant__ Work<E0, E1> w, int splits, int* err) {
   const uint32_t tmem = *tmem_slot;
 
   const int ew = warp - 2, q = warp & 3;
-  const uint32_t slots = slot_base + ew * kSlotBytes;
+  const uint32_t slots = base + S::kChunks * kChunkBytes + ew * kSlotBytes;   // once the operands are read
   constexpr int N = BN / 32;
   // where chunk (quarter of the rows, 32 columns) lies in the result
   auto row_of = [&](int quarter, int c) { return SWAP ? int64_t(tn) * BN + 32 * c : int64_t(tm) * 128 + 32 * quarter; };
@@ -677,36 +779,39 @@ k_linear_split(const __grid_constant__ Work<E0, E1> w, int splits, int* err) {
   };
   bool ok = true;
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       int s = 0;
       uint32_t ph = 0;
+      const int a_mn = p.a_mn, b_mn = p.b_mn;
+      const CUtensorMap *ma = &p.a, *mb = &p.b;
       for (int kb = kb0; kb < kb1; ++kb) {
-        if (!mbar_wait(empty(s), ph ^ 1u, abort_flag, err, ERR_TIMEOUT_PRODUCER)) break;
+        if (!wait(empty(s), ph ^ 1u, abort_flag, err, ERR_TIMEOUT_PRODUCER)) break;
         const uint32_t sa = base + s * S::kStage;
         mbar_expect_tx(full(s), S::kStage);
-        load_operand<128, false>(sa, &p.a, p.a_mn, kb, tm * 128, full(s));
-        load_operand<BN, false>(sa + S::kA, &p.b, p.b_mn, kb, tn * BN, full(s));
+        load_operand<128, false>(sa, ma, a_mn, kb, tm * 128, full(s));
+        load_operand<BN, false>(sa + S::kA, mb, b_mn, kb, tn * BN, full(s));
         if (++s == S::kStages) { s = 0; ph ^= 1u; }
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (elect_one()) {
       int s = 0, acc = 0;
       uint32_t ph = 0, acc_ph = 0;
       const uint32_t idesc = idesc_of(p, 128, BN);
+      const uint64_t a0 = operand_desc(base, p.a_mn), b0 = operand_desc(base + S::kA, p.b_mn);
+      const uint32_t a_step = operand_step(p.a_mn), b_step = operand_step(p.b_mn);
       for (int k0 = kb0; ok && k0 < kb1; k0 += kDepth) {
-        if (!mbar_wait(tempty(acc), acc_ph ^ 1u, abort_flag, err, ERR_TIMEOUT_MMA)) break;
+        if (!wait(tempty(acc), acc_ph ^ 1u, abort_flag, err, ERR_TIMEOUT_MMA)) break;
         tc_fence_after();
         const uint32_t d = tmem + uint32_t(acc * BN);
         const int k1 = min(kb1, k0 + kDepth);
         for (int kb = k0; kb < k1; ++kb) {
-          if (!mbar_wait(full(s), ph, abort_flag, err, ERR_TIMEOUT_MMA)) { ok = false; break; }
+          if (!wait(full(s), ph, abort_flag, err, ERR_TIMEOUT_MMA)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t sa = base + s * S::kStage;
+          uint64_t ad = a0 + uint32_t(s * (S::kStage / 16)), bd = b0 + uint32_t(s * (S::kStage / 16));
 #pragma unroll
-          for (int k = 0; k < BK / 16; ++k)
-            umma_bf16(d, operand_desc(sa, p.a_mn, k, 128), operand_desc(sa + S::kA, p.b_mn, k, BN), idesc,
-                      kb > k0 || k > 0);
+          for (int k = 0; k < BK / 16; ++k, ad += a_step, bd += b_step)
+            umma_bf16(d, ad, bd, idesc, kb > k0 || k > 0);
           umma_commit(empty(s));
           if (++s == S::kStages) { s = 0; ph ^= 1u; }
         }
@@ -725,7 +830,7 @@ k_linear_split(const __grid_constant__ Work<E0, E1> w, int splits, int* err) {
 #pragma unroll
       for (int j = 0; j < 32; ++j) sum[c][j] = 0.f;
     for (int k0 = kb0; k0 < kb1; k0 += kDepth) {
-      if (!mbar_wait(tfull(acc), acc_ph, abort_flag, err, ERR_TIMEOUT_EPILOGUE)) { ok = false; break; }
+      if (!wait(tfull(acc), acc_ph, abort_flag, err, ERR_TIMEOUT_EPILOGUE)) { ok = false; break; }
       __syncwarp();
       tc_fence_after();
 #pragma unroll
@@ -946,20 +1051,14 @@ Plan plan_of(const Extent* x, int count) {
 }
 
 // Few tokens: features are the rows of the tiles, and the K blocks are shared out
-// until the SMs are full.
+// until there are two blocks per SM: what counts is how many bytes of the weight
+// are on their way (14 MB with 1.5 us of latency under load).
 Plan plan_few(int64_t tokens, int64_t features, int64_t k) {
   Plan p;
   p.swap = true;
   p.bn = tokens <= 32 ? 32 : 64;
   const int64_t tiles = ceil_div(features, 128) * ceil_div(tokens, p.bn), kb = ceil_div(k, 64);
-  double least = 0;
-  for (int s = 1; s <= kMostSplits && (s == 1 || kb >= 2 * s); ++s) {
-    const double us = std::ceil(double(tiles * s) / kSms) * double(ceil_div(kb, s)) * 0.17 + (s > 1 ? 1.5 : 0.0);
-    if (s == 1 || us < least) {
-      least = us;
-      p.splits = s;
-    }
-  }
+  while (p.splits < kMostSplits && tiles * (p.splits + 1) <= 2 * kSms && kb >= 2 * (p.splits + 1)) ++p.splits;
   return p;
 }
 
