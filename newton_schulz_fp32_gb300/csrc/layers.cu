@@ -1,6 +1,8 @@
 // Dropout from a counter, and the norm and rotation of query and key heads
 // with its gradients.  Both are bound by memory: every element is read once
 // and written once.
+#include <type_traits>
+
 #include "layers.cuh"
 
 namespace muon {
@@ -15,8 +17,8 @@ constexpr int kSms = 152;
 
 // ------------------------------------------------------------------ dropout
 
-constexpr int kDropThreads = 256;
-constexpr int kDropRows = 2;   // rows a thread has under way
+constexpr int kDropThreads = 128;
+constexpr int kDropRows = 1;   // rows a thread has under way
 
 struct DropArgs {
   const void* x;
@@ -108,7 +110,7 @@ cudaError_t launch_dropout(const DropArgs& a, cudaStream_t s) {
 
 constexpr int kMaxPairs = MUON_MAX_HEAD_DIM / 2;
 constexpr int kRotWarps = 8;
-constexpr int kGradBlocks = 4 * kSms;   // blocks of the gradient, each with its own partial sums
+constexpr int kGradBlocks = 2 * kSms;   // most blocks of the gradient, each with its own partial sums
 
 // One of the tensors of a group: element d of head h of token t at
 // t * stride + h * head + d.
@@ -125,16 +127,27 @@ struct Group {
   int heads;
 };
 
+// How a head is laid over lanes.  A unit is P pairs (elements of both halves, or
+// 2 P neighbours if interleaved), or 2 P elements behind the pairs; a lane has NU
+// units.  P = 4 and 2 need accesses of P and 2 P elements aligned (see wide()).
+template <int P_, int NU_, bool FIXED_, bool NORM_, bool INTER_>
+struct Shape {
+  static constexpr int P = P_, NU = NU_;
+  static constexpr bool kFixed = FIXED_;   // norm and order of pairs known when compiled
+  static __device__ __forceinline__ bool norm(int n) { return kFixed ? NORM_ : n != 0; }
+  static __device__ __forceinline__ bool inter(int i) { return kFixed ? INTER_ : i != 0; }
+};
+
 struct RotArgs {
   Group group[2];
   int groups;
   int64_t n;
-  int dim, pairs, axes, interleaved, pos64;
-  float eps;
+  int dim, pairs, axes, norm, interleaved, pos64;
+  float eps, inv_dim;
   const void* positions;
   float* partial;              // the gradient: [block][group][dim]
   int want[2];                 // groups whose weight's gradient is wanted
-  int split[2], share[2];      // pieces a token's heads are cut into, and heads in a piece
+  int split, share;            // pieces a token's heads (of both groups, one after the other) are cut into, and heads in a piece
   uint64_t turns[kMaxPairs];   // turns per position, in units of 2^-64
   uint8_t axis[kMaxPairs];
 };
@@ -145,170 +158,288 @@ __device__ __forceinline__ int64_t position(const RotArgs& a, int64_t t, int axi
                  : reinterpret_cast<const int32_t*>(a.positions)[i];
 }
 
-// cos and sin of pair i: position * turns wraps at whole turns by itself; its
-// upper 32 bits, as a signed fraction, are the angle in half turns / 2^31.
-__device__ __forceinline__ void angle(const RotArgs& a, int64_t t, int i, float* c, float* s) {
-  const uint64_t whole = uint64_t(position(a, t, a.axis[i])) * a.turns[i];
+// Whether token t is one: no position is negative.
+__device__ __forceinline__ bool is_token(const RotArgs& a, int64_t t) {
+  bool on = true;
+  if (a.pairs)
+    for (int x = 0; x < a.axes; ++x) on = on && position(a, t, x) >= 0;
+  return on;
+}
+
+// cos and sin of a pair's angle: position * turns wraps at whole turns by itself;
+// its upper 32 bits, as a signed fraction, are the angle in half turns / 2^31.
+__device__ __forceinline__ void angle(int64_t pos, uint64_t turns, float* c, float* s) {
+  const uint64_t whole = uint64_t(pos) * turns;
   const float half_turns = float(int32_t((whole + 0x80000000u) >> 32)) * 4.656612873077393e-10f;
   sincospif(half_turns, s, c);
 }
 
-// A lane's share of a head: NU units of 2 * P elements.  Rotated units hold P
-// pairs: P elements and their P partners; the rest holds 2 * P consecutive ones.
-template <int P>
-struct Place {
-  int a, b;      // first element of either half
-  int na, nb;    // how many of them there are
-  int pair;      // first pair; -1: not turned
-  __device__ __forceinline__ void of(const RotArgs& r, int unit) {
-    const int turned = r.pairs / P;
-    pair = -1;
-    if (unit < turned) {
-      pair = unit * P;
-      a = r.interleaved ? unit * 2 * P : unit * P;
-      b = r.interleaved ? a + P : r.pairs + unit * P;
-      na = nb = P;
+// P elements (0 beyond n) as they lie in memory; P > 1: one access, all or nothing.
+template <typename T, int P>
+struct Part {
+  static constexpr int kBytes = P * int(sizeof(T));
+  using Raw = std::conditional_t<kBytes == 16, uint4, std::conditional_t<kBytes == 8, uint2, std::conditional_t<kBytes == 4, uint32_t, uint16_t>>>;
+  Raw raw;
+  __device__ __forceinline__ void load(const T* p, int n) {
+    raw = Raw{};
+    if (n) raw = *reinterpret_cast<const Raw*>(p);
+  }
+  __device__ __forceinline__ void to(float* f) const {
+    if constexpr (sizeof(T) == 4) {
+      const uint32_t* u = reinterpret_cast<const uint32_t*>(&raw);
+#pragma unroll
+      for (int i = 0; i < P; ++i) f[i] = __uint_as_float(u[i]);
+    } else if constexpr (P == 1) {
+      f[0] = __uint_as_float(uint32_t(raw) << 16);
     } else {
-      a = 2 * r.pairs + (unit - turned) * 2 * P;
-      b = a + P;
-      na = max(0, min(P, r.dim - a));
-      nb = max(0, min(P, r.dim - b));
+      const uint32_t* u = reinterpret_cast<const uint32_t*>(&raw);
+#pragma unroll
+      for (int i = 0; i < P / 2; ++i) Vec<T>::unpack2(u[i], f + 2 * i);
+    }
+  }
+  __device__ __forceinline__ void from(const float* f) {
+    if constexpr (sizeof(T) == 4) {
+      uint32_t* u = reinterpret_cast<uint32_t*>(&raw);
+#pragma unroll
+      for (int i = 0; i < P; ++i) u[i] = __float_as_uint(f[i]);
+    } else if constexpr (P == 1) {
+      const __nv_bfloat16 h = __float2bfloat16_rn(f[0]);
+      raw = *reinterpret_cast<const uint16_t*>(&h);
+    } else {
+      uint32_t* u = reinterpret_cast<uint32_t*>(&raw);
+#pragma unroll
+      for (int i = 0; i < P / 2; ++i) u[i] = Vec<T>::pack2(f[2 * i], f[2 * i + 1]);
+    }
+  }
+  __device__ __forceinline__ void store(T* p, int n) const {
+    if (n) *reinterpret_cast<Raw*>(p) = raw;
+  }
+};
+
+// A lane's units of a head as pairs: f[2 k] and f[2 k + 1] are pair k's two
+// elements (of what is not turned, any two).
+template <typename T, class S>
+__device__ __forceinline__ void to_pairs(const Part<T, S::P>& a, const Part<T, S::P>& b, bool inter, float* f) {
+  constexpr int P = S::P;
+  float x[2 * P];
+  a.to(x);
+  b.to(x + P);
+#pragma unroll
+  for (int k = 0; k < P; ++k) {
+    f[2 * k] = inter ? x[2 * k] : x[k];
+    f[2 * k + 1] = inter ? x[2 * k + 1] : x[P + k];
+  }
+}
+
+template <typename T, class S>
+__device__ __forceinline__ void from_pairs(Part<T, S::P>& a, Part<T, S::P>& b, bool inter, const float* f) {
+  constexpr int P = S::P;
+  float x[2 * P];
+#pragma unroll
+  for (int k = 0; k < P; ++k) {
+    x[inter ? 2 * k : k] = f[2 * k];
+    x[inter ? 2 * k + 1 : P + k] = f[2 * k + 1];
+  }
+  a.from(x);
+  b.from(x + P);
+}
+
+// How fast pairs turn and by which axis, in shared memory (lanes that read
+// different kernel arguments wait for one another).
+struct Turns {
+  uint64_t turns[kMaxPairs];
+  uint8_t axis[kMaxPairs];
+  __device__ __forceinline__ void init(const RotArgs& a) {
+    for (int i = threadIdx.x; i < a.pairs; i += blockDim.x) {
+      turns[i] = a.turns[i];
+      axis[i] = a.axis[i];
+    }
+    __syncthreads();
+  }
+};
+
+// What a lane keeps over all tokens: where its units lie.
+template <class S>
+struct Units {
+  static constexpr int P = S::P, NU = S::NU;
+  int at[NU], gap[NU];     // first element, and how far behind it the other P are
+  int na[NU], nb[NU];      // how many there are of either
+  bool turned[NU];
+  int pair[NU];            // the first
+
+  __device__ __forceinline__ void init(const RotArgs& a, int in_head, int lanes) {
+    const int whole = a.pairs / P;
+    const bool inter = S::inter(a.interleaved);
+#pragma unroll
+    for (int u = 0; u < NU; ++u) {
+      const int unit = in_head + u * lanes;
+      turned[u] = unit < whole;
+      if (turned[u]) {
+        at[u] = inter ? unit * 2 * P : unit * P;
+        gap[u] = inter ? P : a.pairs;
+        na[u] = nb[u] = P;
+      } else {
+        at[u] = 2 * a.pairs + (unit - whole) * 2 * P;
+        gap[u] = P;
+        na[u] = max(0, min(P, a.dim - at[u]));
+        nb[u] = max(0, min(P, a.dim - at[u] - P));
+      }
+      pair[u] = unit * P;
+    }
+  }
+  __device__ __forceinline__ void turn_by(const RotArgs& a, const Turns& q, int64_t t, bool on, float (&c)[NU][P],
+                                          float (&s)[NU][P]) const {
+#pragma unroll
+    for (int u = 0; u < NU; ++u)
+#pragma unroll
+      for (int k = 0; k < P; ++k) {
+        c[u][k] = 1.f;
+        s[u][k] = 0.f;
+        if (turned[u] && on) angle(position(a, t, q.axis[pair[u] + k]), q.turns[pair[u] + k], &c[u][k], &s[u][k]);
+      }
+  }
+  // The weight's elements, as pairs.
+  template <typename T>
+  __device__ __forceinline__ void weights(const RotArgs& a, const void* p, float (&w)[NU][2 * P]) const {
+#pragma unroll
+    for (int u = 0; u < NU; ++u) {
+#pragma unroll
+      for (int k = 0; k < 2 * P; ++k) w[u][k] = 1.f;
+      if (!p) continue;
+      Part<T, P> x, y;
+      x.load(static_cast<const T*>(p) + at[u], na[u]);
+      y.load(static_cast<const T*>(p) + at[u] + gap[u], nb[u]);
+      to_pairs<T, S>(x, y, turned[u] && S::inter(a.interleaved), w[u]);
     }
   }
 };
 
-// P elements as floats (0 beyond n).  P = 4: one access of 8 or 16 bytes, all
-// or nothing.
-template <typename T, int P>
-__device__ __forceinline__ void load_part(const T* p, int n, float* f) {
-  if constexpr (P == 4) {
-    if constexpr (sizeof(T) == 2) {
-      uint2 v = make_uint2(0, 0);
-      if (n) v = *reinterpret_cast<const uint2*>(p);
-      Vec<T>::unpack2(v.x, f);
-      Vec<T>::unpack2(v.y, f + 2);
-    } else {
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (n) v = *reinterpret_cast<const uint4*>(p);
-      Vec<T>::unpack(v, f);
-    }
-  } else {
-    static_assert(P == 1, "one pair or four");
-    f[0] = n ? tok::to_float(*p) : 0.f;
-  }
+// Sums over the `lanes` lanes that hold a head, of several heads at once.
+template <int U>
+__device__ __forceinline__ void head_sums(float (&v)[U], int lanes) {
+  for (int o = lanes / 2; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < U; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
 }
 
-template <typename T, int P>
-__device__ __forceinline__ void store_part(T* p, int n, const float* f) {
-  if (!n) return;
-  if constexpr (P == 4) {
-    if constexpr (sizeof(T) == 2)
-      *reinterpret_cast<uint2*>(p) = make_uint2(Vec<T>::pack2(f[0], f[1]), Vec<T>::pack2(f[2], f[3]));
-    else
-      *reinterpret_cast<uint4*>(p) = Vec<T>::pack(f);
-  } else {
-    *p = tok::from_float<T>(f[0]);
-  }
-}
-
-// Pairs of a unit turned in place: (a, b) -> (a c - b s, b c + a s).  f: the
-// unit's 2 * P elements, those at `a` first.
-template <int P>
-__device__ __forceinline__ void turn(float* f, const float* c, const float* s, bool interleaved) {
-#pragma unroll
-  for (int k = 0; k < P; ++k) {
-    if (interleaved && P > 1) {
-      const float x = f[2 * k], y = f[2 * k + 1];
-      f[2 * k] = x * c[k] - y * s[k];
-      f[2 * k + 1] = y * c[k] + x * s[k];
-    } else {
-      const float x = f[k], y = f[P + k];
-      f[k] = x * c[k] - y * s[k];
-      f[P + k] = y * c[k] + x * s[k];
-    }
-  }
-}
-
-// Sum over the `lanes` lanes that hold a head.
-__device__ __forceinline__ float head_sum(float v, int lanes) {
-  for (int o = lanes / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-
-// A warp takes a token's heads of one group, or a piece of them where tokens
-// are few; `lanes` lanes hold a head, 32 / lanes heads go at once.  The
-// token's cosines and sines stay in registers over its heads.
-template <typename T, int P, int NU, bool NORM>
-__global__ void __launch_bounds__(32 * kRotWarps) k_norm_rotary(const __grid_constant__ RotArgs a, int lanes) {
-  const int lane = threadIdx.x % 32, in_head = lane % lanes, first = lane / lanes, step = 32 / lanes;
-  const int tasks = a.split[0] + a.split[1];
-  const int64_t task = int64_t(blockIdx.x) * kRotWarps + threadIdx.x / 32;
-  const int64_t t = task / tasks;
-  if (t >= a.n) return;
-  int piece = static_cast<int>(task % tasks);
-  const int which = piece >= a.split[0];
-  if (which) piece -= a.split[0];
-  const Group& g = a.group[which];
-  const int h0 = piece * a.share[which], h1 = min(g.heads, h0 + a.share[which]);
-  bool on = true;
-  if (a.pairs)
-    for (int x = 0; x < a.axes; ++x) on = on && position(a, t, x) >= 0;
-  Place<P> at[NU];
-  float c[NU][P], s[NU][P], w[NU][2 * P];
-#pragma unroll
-  for (int u = 0; u < NU; ++u) {
-    at[u].of(a, in_head + u * lanes);
-#pragma unroll
-    for (int k = 0; k < P; ++k) {
-      c[u][k] = 1.f;
-      s[u][k] = 0.f;
-      if (at[u].pair >= 0 && on) angle(a, t, at[u].pair + k, &c[u][k], &s[u][k]);
-    }
-    if constexpr (NORM) {
-#pragma unroll
-      for (int k = 0; k < 2 * P; ++k) w[u][k] = 1.f;
-      if (g.weight) {
-        load_part<T, P>(static_cast<const T*>(g.weight) + at[u].a, at[u].na, w[u]);
-        load_part<T, P>(static_cast<const T*>(g.weight) + at[u].b, at[u].nb, w[u] + P);
-      }
-    }
-  }
-  const T* in = static_cast<const T*>(g.in.p) + t * g.in.stride;
-  T* out = static_cast<T*>(const_cast<void*>(g.out.p)) + t * g.out.stride;
-  constexpr int U = NU == 1 ? 2 : 1;   // heads a lane has under way
-  for (int b = h0; b < h1; b += U * step) {
-    float f[U][NU][2 * P];
-#pragma unroll
-    for (int v = 0; v < U; ++v) {
-      const int h = b + v * step + first;
-      const bool here = on && h < h1;
-#pragma unroll
-      for (int u = 0; u < NU; ++u) {
-        load_part<T, P>(in + h * g.in.head + at[u].a, here ? at[u].na : 0, f[v][u]);
-        load_part<T, P>(in + h * g.in.head + at[u].b, here ? at[u].nb : 0, f[v][u] + P);
-      }
-    }
-#pragma unroll
-    for (int v = 0; v < U; ++v) {
-      const int h = b + v * step + first;
-      if constexpr (NORM) {
-        float sum = 0.f;
+// A warp takes a token's heads, both groups', or a piece of them where tokens are
+// few; `lanes` lanes hold a head, 32 / lanes heads go at once and U of those are
+// under way.  What a token's pairs are multiplied by, cosines and sines with the
+// weight in them, stays in registers over its heads.
+template <typename T, class S>
+__global__ void __launch_bounds__(32 * kRotWarps, 2) k_norm_rotary(const __grid_constant__ RotArgs a, int lanes) {
+  constexpr int P = S::P, NU = S::NU, U = NU > 1 ? 1 : P == 4 ? 4 : 2;
+  const int lane = threadIdx.x % 32, first = lane / lanes, step = 32 / lanes;
+  const bool inter = S::inter(a.interleaved);
+  __shared__ Turns turns;
+  turns.init(a);
+  Units<S> units;
+  units.init(a, lane % lanes, lanes);
+  const int64_t tasks = a.n * a.split;
+  for (int64_t task = int64_t(blockIdx.x) * kRotWarps + threadIdx.x / 32; task < tasks;
+       task += int64_t(gridDim.x) * kRotWarps) {
+    const int64_t t = a.split == 1 ? task : task / a.split;
+    const int piece = a.split == 1 ? 0 : static_cast<int>(task - t * a.split);
+    const bool on = is_token(a, t);
+    float c[NU][P], s[NU][P];
+    units.turn_by(a, turns, t, on, c, s);
+    int before = 0;   // heads of the groups before this one
+#pragma unroll 1
+    for (int which = 0; which < a.groups; ++which) {
+      const Group& g = a.group[which];
+      const int h0 = max(0, piece * a.share - before), h1 = min(g.heads, (piece + 1) * a.share - before);
+      before += g.heads;
+      if (h0 >= h1) continue;
+      // (a, b) -> r (a ac - b bs, b bc + a as)
+      float ac[NU][P], bs[NU][P], bc[NU][P], as[NU][P];
+      {
+        float w[NU][2 * P];
+        units.template weights<T>(a, g.weight, w);
 #pragma unroll
         for (int u = 0; u < NU; ++u)
 #pragma unroll
-          for (int k = 0; k < 2 * P; ++k) sum += f[v][u][k] * f[v][u][k];
-        const float r = rsqrtf(head_sum(sum, lanes) / float(a.dim) + a.eps);
-#pragma unroll
-        for (int u = 0; u < NU; ++u)
-#pragma unroll
-          for (int k = 0; k < 2 * P; ++k) f[v][u][k] = on ? f[v][u][k] * r * w[u][k] : 0.f;
+          for (int k = 0; k < P; ++k) {
+            ac[u][k] = w[u][2 * k] * c[u][k];
+            as[u][k] = w[u][2 * k] * s[u][k];
+            bc[u][k] = w[u][2 * k + 1] * c[u][k];
+            bs[u][k] = w[u][2 * k + 1] * s[u][k];
+          }
       }
-      if (h >= h1) continue;
+      const int64_t iby = g.in.head * step, oby = g.out.head * step;
+      const T* in = static_cast<const T*>(g.in.p) + t * g.in.stride + (h0 + first) * g.in.head;
+      T* out = static_cast<T*>(const_cast<void*>(g.out.p)) + t * g.out.stride + (h0 + first) * g.out.head;
+      Part<T, P> x[U][NU], y[U][NU], nx[U][NU], ny[U][NU];   // these heads, and the next ones on their way
+      auto fetch = [&](int left) {
 #pragma unroll
-      for (int u = 0; u < NU; ++u) {
-        turn<P>(f[v][u], c[u], s[u], a.interleaved);
-        store_part<T, P>(out + h * g.out.head + at[u].a, at[u].na, f[v][u]);
-        store_part<T, P>(out + h * g.out.head + at[u].b, at[u].nb, f[v][u] + P);
+        for (int v = 0; v < U; ++v, in += iby) {
+          const bool here = on && v * step < left;
+#pragma unroll
+          for (int u = 0; u < NU; ++u) {
+            const T* q = in + units.at[u];
+            nx[v][u].load(q, here ? units.na[u] : 0);
+            ny[v][u].load(q + units.gap[u], here ? units.nb[u] : 0);
+          }
+        }
+      };
+      fetch(h1 - h0 - first);
+#pragma unroll 1
+      for (int left = h1 - h0 - first; left + first > 0; left -= U * step) {
+#pragma unroll
+        for (int v = 0; v < U; ++v)
+#pragma unroll
+          for (int u = 0; u < NU; ++u) {
+            x[v][u] = nx[v][u];
+            y[v][u] = ny[v][u];
+          }
+        fetch(left - U * step);
+        float r[U];
+        if (S::norm(a.norm)) {
+#pragma unroll
+          for (int v = 0; v < U; ++v) {
+            r[v] = 0.f;
+#pragma unroll
+            for (int u = 0; u < NU; ++u) {
+              float f[2 * P];
+              x[v][u].to(f);
+              y[v][u].to(f + P);
+#pragma unroll
+              for (int k = 0; k < 2 * P; ++k) r[v] += f[k] * f[k];
+            }
+          }
+          head_sums<U>(r, lanes);
+#pragma unroll
+          for (int v = 0; v < U; ++v) r[v] = on ? rsqrtf(r[v] * a.inv_dim + a.eps) : 0.f;
+        } else {
+#pragma unroll
+          for (int v = 0; v < U; ++v) r[v] = 1.f;
+        }
+#pragma unroll
+        for (int v = 0; v < U; ++v, out += oby) {
+          if (v * step >= left) continue;
+#pragma unroll
+          for (int u = 0; u < NU; ++u) {
+            const bool in_pairs = units.turned[u] && inter;
+            float f[2 * P], o[2 * P];
+            to_pairs<T, S>(x[v][u], y[v][u], in_pairs, f);
+#pragma unroll
+            for (int k = 0; k < P; ++k) {
+              o[2 * k] = r[v] * (f[2 * k] * ac[u][k] - f[2 * k + 1] * bs[u][k]);
+              o[2 * k + 1] = r[v] * (f[2 * k + 1] * bc[u][k] + f[2 * k] * as[u][k]);
+            }
+            if (!units.turned[u]) {   // neighbours, not a pair: an infinite one leaves the other alone
+#pragma unroll
+              for (int k = 0; k < P; ++k) {
+                o[2 * k] = r[v] * (f[2 * k] * ac[u][k]);
+                o[2 * k + 1] = r[v] * (f[2 * k + 1] * bc[u][k]);
+              }
+            }
+            Part<T, P> p, q;
+            from_pairs<T, S>(p, q, in_pairs, o);
+            T* to = out + units.at[u];
+            p.store(to, units.na[u]);
+            q.store(to + units.gap[u], units.nb[u]);
+          }
+        }
       }
     }
   }
@@ -318,108 +449,143 @@ __global__ void __launch_bounds__(32 * kRotWarps) k_norm_rotary(const __grid_con
 //     dw += g n,   dx = r (g w - n mean(g w n)).
 // A lane keeps its columns' dw over all tokens of its warp; blocks leave
 // partial sums, which k_norm_join adds in order.
-template <typename T, int P, int NU, bool NORM>
-__global__ void __launch_bounds__(32 * kRotWarps) k_norm_rotary_grad(const __grid_constant__ RotArgs a, int lanes) {
+template <typename T, class S>
+__global__ void __launch_bounds__(32 * kRotWarps, 2) k_norm_rotary_grad(const __grid_constant__ RotArgs a, int lanes) {
+  constexpr int P = S::P, NU = S::NU, U = NU > 1 ? 1 : 2;
   __shared__ float sums[kRotWarps][MUON_MAX_HEAD_DIM];
   const int warp = threadIdx.x / 32;
-  const int lane = threadIdx.x % 32, in_head = lane % lanes, first = lane / lanes, step = 32 / lanes;
-  Place<P> at[NU];
+  const int lane = threadIdx.x % 32, first = lane / lanes, step = 32 / lanes;
+  const bool inter = S::inter(a.interleaved);
+  __shared__ Turns turns;
+  turns.init(a);
+  Units<S> units;
+  units.init(a, lane % lanes, lanes);
+  float dw[2][NU][2 * P] = {};
+  const int64_t tasks = a.n * a.split;
+  for (int64_t task = int64_t(blockIdx.x) * kRotWarps + warp; task < tasks; task += int64_t(gridDim.x) * kRotWarps) {
+    const int64_t t = a.split == 1 ? task : task / a.split;
+    const int piece = a.split == 1 ? 0 : static_cast<int>(task - t * a.split);
+    const bool on = is_token(a, t);
+    float c[NU][P], s[NU][P];
+    units.turn_by(a, turns, t, on, c, s);
 #pragma unroll
-  for (int u = 0; u < NU; ++u) at[u].of(a, in_head + u * lanes);
-  for (int which = 0; which < a.groups; ++which) {
-    const Group& g = a.group[which];
-    float w[NU][2 * P], dw[NU][2 * P];
+    for (int which = 0; which < 2; ++which) {   // unrolled: dw stays in registers
+      const Group& g = a.group[which];
+      const int before = which ? a.group[0].heads : 0;
+      const int h0 = max(0, piece * a.share - before), h1 = min(g.heads, (piece + 1) * a.share - before);
+      if (which >= a.groups || h0 >= h1) continue;
+      float w[NU][2 * P];
+      units.template weights<T>(a, g.weight, w);
+      const int64_t dby = g.in.head * step, xby = g.x.head * step, oby = g.out.head * step;
+      const T* din = static_cast<const T*>(g.in.p) + t * g.in.stride + (h0 + first) * g.in.head;
+      const T* xin = static_cast<const T*>(g.x.p) + t * g.x.stride + (h0 + first) * g.x.head;
+      T* out = static_cast<T*>(const_cast<void*>(g.out.p)) + t * g.out.stride + (h0 + first) * g.out.head;
+      Part<T, P> p[U][NU], q[U][NU], y[U][NU], z[U][NU];   // heads on their way
+      auto fetch = [&](int left) {
 #pragma unroll
-    for (int u = 0; u < NU; ++u) {
+        for (int v = 0; v < U; ++v, din += dby, xin += xby) {
+          const bool here = on && v * step < left;
 #pragma unroll
-      for (int k = 0; k < 2 * P; ++k) w[u][k] = 1.f, dw[u][k] = 0.f;
-      if (NORM && g.weight) {
-        load_part<T, P>(static_cast<const T*>(g.weight) + at[u].a, at[u].na, w[u]);
-        load_part<T, P>(static_cast<const T*>(g.weight) + at[u].b, at[u].nb, w[u] + P);
-      }
-    }
-    const int split = a.split[which], share = a.share[which];
-    for (int64_t task = int64_t(blockIdx.x) * kRotWarps + warp; task < a.n * split;
-         task += int64_t(gridDim.x) * kRotWarps) {
-      const int64_t t = task / split;
-      const int h0 = static_cast<int>(task % split) * share, h1 = min(g.heads, h0 + share);
-      bool on = true;
-      if (a.pairs)
-        for (int x = 0; x < a.axes; ++x) on = on && position(a, t, x) >= 0;
-      float c[NU][P], s[NU][P];
-#pragma unroll
-      for (int u = 0; u < NU; ++u)
-#pragma unroll
-        for (int k = 0; k < P; ++k) {
-          c[u][k] = 1.f;
-          s[u][k] = 0.f;
-          if (at[u].pair >= 0 && on) angle(a, t, at[u].pair + k, &c[u][k], &s[u][k]);
-          s[u][k] = -s[u][k];
+          for (int u = 0; u < NU; ++u) {
+            const T* i = din + units.at[u];
+            p[v][u].load(i, here ? units.na[u] : 0);
+            q[v][u].load(i + units.gap[u], here ? units.nb[u] : 0);
+            if (S::norm(a.norm)) {
+              i = xin + units.at[u];
+              y[v][u].load(i, here ? units.na[u] : 0);
+              z[v][u].load(i + units.gap[u], here ? units.nb[u] : 0);
+            }
+          }
         }
-      for (int b = h0; b < h1; b += step) {
-        const int h = b + first;
-        const bool here = on && h < h1;
-        float d[NU][2 * P], x[NU][2 * P];
-        const T* din = static_cast<const T*>(g.in.p) + t * g.in.stride + h * g.in.head;
-        const T* xin = static_cast<const T*>(g.x.p) + t * g.x.stride + h * g.x.head;
+      };
+      fetch(h1 - h0 - first);
+#pragma unroll 1
+      for (int left = h1 - h0 - first; left + first > 0; left -= U * step) {
+        float d[U][NU][2 * P], x[U][NU][2 * P];
+        {
 #pragma unroll
-        for (int u = 0; u < NU; ++u) {
-          load_part<T, P>(din + at[u].a, here ? at[u].na : 0, d[u]);
-          load_part<T, P>(din + at[u].b, here ? at[u].nb : 0, d[u] + P);
-          if constexpr (NORM) {
-            load_part<T, P>(xin + at[u].a, here ? at[u].na : 0, x[u]);
-            load_part<T, P>(xin + at[u].b, here ? at[u].nb : 0, x[u] + P);
+          for (int v = 0; v < U; ++v)
+#pragma unroll
+            for (int u = 0; u < NU; ++u) {
+              const bool in_pairs = units.turned[u] && inter;
+              float f[2 * P];
+              to_pairs<T, S>(p[v][u], q[v][u], in_pairs, f);
+#pragma unroll
+              for (int k = 0; k < P; ++k) {
+                d[v][u][2 * k] = f[2 * k] * c[u][k] + f[2 * k + 1] * s[u][k];
+                d[v][u][2 * k + 1] = f[2 * k + 1] * c[u][k] - f[2 * k] * s[u][k];
+              }
+              if (!units.turned[u]) {
+#pragma unroll
+                for (int k = 0; k < 2 * P; ++k) d[v][u][k] = f[k];
+              }
+              if (S::norm(a.norm)) to_pairs<T, S>(y[v][u], z[v][u], in_pairs, x[v][u]);
+            }
+        }
+        fetch(left - U * step);
+        if (S::norm(a.norm)) {
+          float r[U], m[U];
+#pragma unroll
+          for (int v = 0; v < U; ++v) {
+            r[v] = m[v] = 0.f;
+#pragma unroll
+            for (int u = 0; u < NU; ++u)
+#pragma unroll
+              for (int k = 0; k < 2 * P; ++k) {
+                r[v] += x[v][u][k] * x[v][u][k];
+                m[v] += x[v][u][k] * (d[v][u][k] * w[u][k]);
+              }
+          }
+          head_sums<U>(r, lanes);
+          head_sums<U>(m, lanes);
+#pragma unroll
+          for (int v = 0; v < U; ++v) {
+            r[v] = on ? rsqrtf(r[v] * a.inv_dim + a.eps) : 0.f;
+            m[v] = m[v] * r[v] * a.inv_dim;   // mean of g w n
+#pragma unroll
+            for (int u = 0; u < NU; ++u)
+#pragma unroll
+              for (int k = 0; k < 2 * P; ++k) {
+                const float n = x[v][u][k] * r[v];
+                if (v * step < left) dw[which][u][k] += d[v][u][k] * n;
+                d[v][u][k] = r[v] * (d[v][u][k] * w[u][k] - n * m[v]);
+              }
           }
         }
 #pragma unroll
-        for (int u = 0; u < NU; ++u) turn<P>(d[u], c[u], s[u], a.interleaved);
-        if constexpr (NORM) {
-          float sq = 0.f, dot = 0.f;
+        for (int v = 0; v < U; ++v, out += oby) {
+          if (v * step >= left) continue;
 #pragma unroll
-          for (int u = 0; u < NU; ++u)
-#pragma unroll
-            for (int k = 0; k < 2 * P; ++k) {
-              sq += x[u][k] * x[u][k];
-              dot += x[u][k] * (d[u][k] * w[u][k]);
-            }
-          const float inv = 1.f / float(a.dim);
-          const float r = rsqrtf(head_sum(sq, lanes) * inv + a.eps);
-          const float m = head_sum(dot, lanes) * r * inv;   // mean of g w n
-#pragma unroll
-          for (int u = 0; u < NU; ++u)
-#pragma unroll
-            for (int k = 0; k < 2 * P; ++k) {
-              const float n = x[u][k] * r;
-              if (here) dw[u][k] += d[u][k] * n;
-              d[u][k] = r * (d[u][k] * w[u][k] - n * m);
-            }
-        }
-        if (h >= h1) continue;
-        T* out = static_cast<T*>(const_cast<void*>(g.out.p)) + t * g.out.stride + h * g.out.head;
-#pragma unroll
-        for (int u = 0; u < NU; ++u) {
-          if (!on) {
-#pragma unroll
-            for (int k = 0; k < 2 * P; ++k) d[u][k] = 0.f;
+          for (int u = 0; u < NU; ++u) {
+            Part<T, P> p, q;
+            from_pairs<T, S>(p, q, units.turned[u] && inter, d[v][u]);
+            T* to = out + units.at[u];
+            p.store(to, units.na[u]);
+            q.store(to + units.gap[u], units.nb[u]);
           }
-          store_part<T, P>(out + at[u].a, at[u].na, d[u]);
-          store_part<T, P>(out + at[u].b, at[u].nb, d[u] + P);
         }
       }
     }
-    if (!NORM || !a.want[which]) continue;
+  }
+  if (!S::norm(a.norm)) return;
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    if (!a.want[which]) continue;
     // lanes of the same columns, then the block's warps
     __syncthreads();
 #pragma unroll
-    for (int u = 0; u < NU; ++u)
+    for (int u = 0; u < NU; ++u) {
+      const bool in_pairs = units.turned[u] && inter;
 #pragma unroll
       for (int k = 0; k < 2 * P; ++k) {
-        float v = dw[u][k];
+        float v = dw[which][u][k];
         for (int o = lanes; o < 32; o *= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
-        const int i = k < P ? at[u].a + k : at[u].b + (k - P);
-        const bool there = k < P ? k < at[u].na : k - P < at[u].nb;
+        // the k-th of the lane's values is one of pair k / 2
+        const int j = in_pairs ? k : k % 2 * P + k / 2, i = units.at[u] + (j < P ? j : units.gap[u] + (j - P));
+        const bool there = j < P ? j < units.na[u] : j - P < units.nb[u];
         if (first == 0 && there) sums[warp][i] = v;
       }
+    }
     __syncthreads();
     for (int i = threadIdx.x; i < a.dim; i += 32 * kRotWarps) {
       float v = 0.f;
@@ -462,9 +628,8 @@ k_norm_join(const JoinArgs a, const __grid_constant__ Segments s0, const __grid_
 
 // ---- host
 
-int grad_blocks(int64_t n) {
-  return static_cast<int>(std::min<int64_t>(kGradBlocks, std::max<int64_t>(1, (n + kRotWarps - 1) / kRotWarps)));
-}
+// Blocks of the gradient: all of them from 64 tokens on (a token's heads are then cut into pieces).
+int grad_blocks(int64_t n) { return static_cast<int>(std::min<int64_t>(kGradBlocks, 5 * n)); }
 
 // Whether element d of any head of two tensors can share memory: apart as
 // spans, or interleaved rows of one stride whose windows are apart (queries and
@@ -521,7 +686,9 @@ int make_rotation(RotArgs* a, int n_groups, int dtype, int64_t n_tokens, int hea
   a->n = n_tokens;
   a->dim = head_dim;
   a->pairs = pairs;
+  a->norm = norm;
   a->eps = eps;
+  a->inv_dim = 1.f / float(head_dim);
   a->interleaved = interleaved;
   if (!pairs) return MUON_OK;
   if (positions_type != MUON_INDEX_INT32 && positions_type != MUON_INDEX_INT64)
@@ -545,17 +712,17 @@ int make_rotation(RotArgs* a, int n_groups, int dtype, int64_t n_tokens, int hea
   return MUON_OK;
 }
 
-bool on16(const Heads& h, size_t es) {
-  return !h.p || (!misaligned(h.p, 16) && h.stride * int64_t(es) % 16 == 0 && h.head * int64_t(es) % 16 == 0);
-}
-
-// Four pairs to a unit where every access is then aligned: rows of 16 bytes,
-// and neither the pairs nor what is behind them ends inside a unit.
-bool wide(const RotArgs& a, size_t es) {
-  if (a.pairs % 4 || (a.dim - 2 * a.pairs) % 8) return false;
+// Whether units of `per` pairs fit: every access of a unit aligned (neighbours go
+// as two accesses, so rows on `per` elements are enough), and neither the
+// pairs nor what is behind them ending inside a unit.
+bool fits(const RotArgs& a, int per, size_t es) {
+  const int64_t unit = per * int64_t(es);
+  auto on = [&](const Heads& h) {
+    return !h.p || (!misaligned(h.p, unit) && h.stride * int64_t(es) % unit == 0 && h.head * int64_t(es) % unit == 0);
+  };
+  if (a.pairs % per || (a.dim - 2 * a.pairs) % (2 * per)) return false;
   for (int i = 0; i < a.groups; ++i)
-    if (!on16(a.group[i].in, es) || !on16(a.group[i].x, es) || !on16(a.group[i].out, es) ||
-        misaligned(a.group[i].weight, 16))
+    if (!on(a.group[i].in) || !on(a.group[i].x) || !on(a.group[i].out) || misaligned(a.group[i].weight, unit))
       return false;
   return true;
 }
@@ -569,39 +736,41 @@ int lanes_of(const RotArgs& a, int per) {
 }
 
 // A token's heads in one piece, or in more where tokens are too few to fill the
-// SMs with a warp each.
-void split_heads(RotArgs* a, int lanes) {
-  const int step = 32 / lanes;
+// SMs with a warp each (pieces of at least `least` heads).
+void split_heads(RotArgs* a, int least) {
   int64_t total = 0;
   for (int i = 0; i < a->groups; ++i) total += a->group[i].heads;
-  int share = int(std::max<int64_t>(step, std::min<int64_t>(total * a->n / (32 * kSms), 1 << 20)));
-  share = (share + step - 1) / step * step;
-  for (int i = 0; i < 2; ++i) {
-    a->share[i] = share;
-    a->split[i] = i < a->groups ? (a->group[i].heads + share - 1) / share : 0;
-  }
+  int64_t share = std::max<int64_t>(least, std::min<int64_t>(total, total * a->n / (24 * kSms)));
+  share = (share + least - 1) / least * least;
+  a->share = static_cast<int>(share);
+  a->split = static_cast<int>((total + share - 1) / share);
 }
 
-template <typename T>
-cudaError_t launch_rotary(RotArgs& a, bool norm, cudaStream_t s) {
-  const bool v = wide(a, sizeof(T));
-  const int lanes = lanes_of(a, v ? 4 : 1);
-  split_heads(&a, lanes);
-  const int64_t tasks = a.n * (a.split[0] + a.split[1]);
-  auto k = v ? (norm ? k_norm_rotary<T, 4, 1, true> : k_norm_rotary<T, 4, 1, false>)
-             : (norm ? k_norm_rotary<T, 1, 4, true> : k_norm_rotary<T, 1, 4, false>);
-  return launch(k, unsigned((tasks + kRotWarps - 1) / kRotWarps), 32 * kRotWarps, 1, false, s, 0, a, lanes);
-}
-
-template <typename T>
-cudaError_t launch_rotary_grad(RotArgs& a, bool norm, int blocks, cudaStream_t s) {
-  const bool v = wide(a, sizeof(T));
-  const int lanes = lanes_of(a, v ? 4 : 1);
-  split_heads(&a, lanes);
-  auto k = v ? (norm ? k_norm_rotary_grad<T, 4, 1, true> : k_norm_rotary_grad<T, 4, 1, false>)
-             : (norm ? k_norm_rotary_grad<T, 1, 4, true> : k_norm_rotary_grad<T, 1, 4, false>);
+// Four pairs to a unit, two where four do not fit (heads of up to 128 elements: 32
+// lanes), else one.
+template <typename T, template <typename, class> class KERNEL>
+cudaError_t launch_heads(RotArgs& a, int blocks, cudaStream_t s) {
+  const int per = fits(a, 4, sizeof(T)) ? 4 : fits(a, 2, sizeof(T)) && a.dim <= 128 ? 2 : 1;
+  const int lanes = lanes_of(a, per);
+  split_heads(&a, 32 / lanes);
+  void (*k)(RotArgs, int) = KERNEL<T, Shape<1, 4, false, false, false>>::kernel;
+  if (per == 2) k = KERNEL<T, Shape<2, 1, false, false, false>>::kernel;
+  else if (per == 4 && a.norm && a.interleaved) k = KERNEL<T, Shape<4, 1, true, true, true>>::kernel;
+  else if (per == 4 && a.norm) k = KERNEL<T, Shape<4, 1, true, true, false>>::kernel;
+  else if (per == 4) k = KERNEL<T, Shape<4, 1, false, false, false>>::kernel;
+  if (!blocks) blocks = int(std::min<int64_t>((a.n * a.split + kRotWarps - 1) / kRotWarps, 2 * kSms));
   return launch(k, unsigned(blocks), 32 * kRotWarps, 1, false, s, 0, a, lanes);
 }
+
+template <typename T, class S>
+struct There {
+  static constexpr auto kernel = k_norm_rotary<T, S>;
+};
+
+template <typename T, class S>
+struct Back {
+  static constexpr auto kernel = k_norm_rotary_grad<T, S>;
+};
 
 }  // namespace
 }  // namespace muon
@@ -697,7 +866,7 @@ extern "C" int muon_norm_rotary(const muon_heads_t* groups, int n_groups, int dt
     }
     if ((rc = lay::begin_call()) != MUON_OK) return rc;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return lay::end_call(1, es == 2 ? launch_rotary<__nv_bfloat16>(a, norm, s) : launch_rotary<float>(a, norm, s));
+    return lay::end_call(1, es == 2 ? launch_heads<__nv_bfloat16, There>(a, 0, s) : launch_heads<float, There>(a, 0, s));
   });
 }
 
@@ -802,8 +971,7 @@ extern "C" int muon_norm_rotary_grad(const muon_heads_grad_t* groups, int n_grou
     cudaError_t e = cudaSuccess;
     if (n_tokens) {
       a.partial = static_cast<float*>(workspace);
-      e = es == 2 ? launch_rotary_grad<__nv_bfloat16>(a, norm, blocks, s)
-                  : launch_rotary_grad<float>(a, norm, blocks, s);
+      e = es == 2 ? launch_heads<__nv_bfloat16, Back>(a, blocks, s) : launch_heads<float, Back>(a, blocks, s);
       if (e != cudaSuccess) return lay::end_call(launches, e);
       ++launches;
     }

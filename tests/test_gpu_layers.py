@@ -320,6 +320,24 @@ def test_tokens_that_are_none_may_hold_anything():
     assert not bool(b.any()) and not bool(two.any())
 
 
+def test_elements_behind_the_pairs_stay_apart():
+    """An infinite or NaN element that is not turned changes no other."""
+    freq, axis = nsg.rotary_frequencies(64)
+    for dtype, dim in ((BF16, 96), (FP32, 80), (BF16, 67)):
+        pos = positions_of(1, 6, 1)
+        x = normal(2, (6, 3, dim), 1.0, dtype)
+        clean = nsg.norm_rotary(x, None, pos, freq, axis, norm=False)[0]
+        back = nsg.norm_rotary_grad(x, None, None, None, pos, freq, axis, norm=False)[0]
+        bad = x.clone()
+        bad[:, :, 65] = float("inf")
+        bad[:, :, dim - 1] = float("nan")
+        keep = [i for i in range(dim) if i not in (65, dim - 1)]
+        for got, want in ((nsg.norm_rotary(bad, None, pos, freq, axis, norm=False)[0], clean),
+                          (nsg.norm_rotary_grad(bad, None, None, None, pos, freq, axis, norm=False)[0], back)):
+            assert torch.equal(got[..., keep], want[..., keep]) and bool(torch.isnan(got[..., dim - 1]).all())
+            assert bool(torch.isinf(got[..., 65]).all())
+
+
 def test_streams_and_graphs():
     freq, axis = nsg.rotary_frequencies(64)
     x, d, pos = normal(1, (50, 4, 64)), normal(2, (50, 4, 64), 0.1), positions_of(3, 50, 1)
