@@ -59,6 +59,8 @@ __device__ __forceinline__ void store8(T* p, int left, const float* f) {
 // blockDim.x threads along a row, eight columns (one draw of 128 bits) each.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kDropThreads) k_dropout(const DropArgs a) {
+  tok::wait_before();
+  tok::allow_next();
   Draw draw;
   draw.init(a.d);
   const int64_t r0 = (int64_t(blockIdx.x) * blockDim.y + threadIdx.y) * kDropRows;
@@ -101,9 +103,7 @@ cudaError_t launch_dropout(const DropArgs& a, cudaStream_t s) {
   while (tx < groups && tx < kDropThreads) tx *= 2;
   const dim3 block(tx, kDropThreads / tx);
   const unsigned grid = unsigned((a.rows + int64_t(block.y) * kDropRows - 1) / (int64_t(block.y) * kDropRows));
-  if (vec) k_dropout<T, true><<<grid, block, 0, s>>>(a);
-  else k_dropout<T, false><<<grid, block, 0, s>>>(a);
-  return cudaSuccess;
+  return launch(vec ? k_dropout<T, true> : k_dropout<T, false>, grid, block, 1, true, s, 0, a);
 }
 
 // ------------------------------------------------------------------ norm and rotation
@@ -335,6 +335,8 @@ __global__ void __launch_bounds__(32 * kRotWarps, 2) k_norm_rotary(const __grid_
   turns.init(a);
   Units<S> units;
   units.init(a, lane % lanes, lanes);
+  tok::wait_before();
+  tok::allow_next();
   const int64_t tasks = a.n * a.split;
   for (int64_t task = int64_t(blockIdx.x) * kRotWarps + threadIdx.x / 32; task < tasks;
        task += int64_t(gridDim.x) * kRotWarps) {
@@ -460,6 +462,8 @@ __global__ void __launch_bounds__(32 * kRotWarps, 2) k_norm_rotary_grad(const __
   turns.init(a);
   Units<S> units;
   units.init(a, lane % lanes, lanes);
+  tok::wait_before();
+  tok::allow_next();
   float dw[2][NU][2 * P] = {};
   const int64_t tasks = a.n * a.split;
   for (int64_t task = int64_t(blockIdx.x) * kRotWarps + warp; task < tasks; task += int64_t(gridDim.x) * kRotWarps) {
@@ -613,6 +617,8 @@ k_norm_join(const JoinArgs a, const __grid_constant__ Segments s0, const __grid_
   const int slabs = (a.dim + 31) / 32;
   const int which = blockIdx.x / slabs, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int i = blockIdx.x % slabs * 32 + lane;
+  tok::wait_before();
+  tok::allow_next();
   if (!a.want[which]) return;
   float v = 0.f;
   if (i < a.dim)
@@ -759,7 +765,7 @@ cudaError_t launch_heads(RotArgs& a, int blocks, cudaStream_t s) {
   else if (per == 4 && a.norm) k = KERNEL<T, Shape<4, 1, true, true, false>>::kernel;
   else if (per == 4) k = KERNEL<T, Shape<4, 1, false, false, false>>::kernel;
   if (!blocks) blocks = int(std::min<int64_t>((a.n * a.split + kRotWarps - 1) / kRotWarps, 2 * kSms));
-  return launch(k, unsigned(blocks), 32 * kRotWarps, 1, false, s, 0, a, lanes);
+  return launch(k, unsigned(blocks), 32 * kRotWarps, 1, true, s, 0, a, lanes);
 }
 
 template <typename T, class S>
@@ -982,7 +988,7 @@ extern "C" int muon_norm_rotary_grad(const muon_heads_grad_t* groups, int n_grou
       j.accum = accum;
       j.scale = scale;
       j.overwrite = overwrite;
-      e = launch(k_norm_join, unsigned(2 * ((head_dim + 31) / 32)), 32 * kJoinWarps, 1, false, s, 0, j, sg[0], sg[1]);
+      e = launch(k_norm_join, unsigned(2 * ((head_dim + 31) / 32)), 32 * kJoinWarps, 1, true, s, 0, j, sg[0], sg[1]);
       ++launches;
     }
     return lay::end_call(launches, e);

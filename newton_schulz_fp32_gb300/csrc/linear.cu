@@ -13,8 +13,22 @@ namespace {
 using lay::Draw;
 using lay::Dropout;
 using lay::Span;
+using namespace tc;
 
 __device__ int g_linear_err;
+
+// The kernels of one call follow one another by programmatic launch.  The first
+// waits for what was in the stream before it, and lets the next one start; one
+// that needs nothing of the kernels before it in the call (late) runs beside them
+// and waits for them only at its end, so that what comes after the call waits for
+// all of it.
+__device__ __forceinline__ void begin_kernel(int late) {
+  if (!late) tok::wait_before();
+  tok::allow_next();
+}
+__device__ __forceinline__ void end_kernel(int late) {
+  if (late) tok::wait_before();
+}
 
 // ------------------------------------------------------------------ epilogues
 //
@@ -266,7 +280,6 @@ struct WeightGrad {
   Segments sg;
 
   __device__ __forceinline__ bool exact() const { return true; }
-  __device__ __forceinline__ bool halves() const { return false; }
   // The lane's eight elements lie in one piece, on 16 bytes.
   __device__ __forceinline__ float* whole(int64_t r, int64_t c, int left) const {
     int64_t room;
@@ -327,14 +340,79 @@ struct WeightGrad {
   }
 };
 
-struct NoProduct {
-  Dropout drop;
-  __device__ __forceinline__ bool exact() const { return false; }
-  __device__ __forceinline__ bool halves() const { return true; }
-  __device__ __forceinline__ void fetch(uint32_t, int, int64_t, int64_t, int) const {}
-  template <typename Read>
-  __device__ __forceinline__ void chunk(const Read&, uint32_t, int, int64_t, int64_t, int, const Draw&) const {}
-};
+// A warp's 32 rows x 64 columns of sums, as the pair kernel hands them to accum:
+// a lane's row lies in shared memory, 272 bytes from the next (so that eight lanes'
+// stores meet in no bank), and goes out as one bulk copy of 256 bytes, added at L2
+// or put in place; a warp so needs no load of the old sums and waits for nothing.
+// Rows that do not start on 16 bytes, and pieces that end inside (columns,
+// partitions), go element by element, 32 columns at once.
+constexpr int kSumColumns = 32;
+constexpr int kRowBytes = kSumColumns * 4 + 16;
+
+__device__ __forceinline__ void bulk_add(float* dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.reduce.async.bulk.global.shared::cta.bulk_group.add.f32 [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_put(float* dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
+}
+
+// x: the lane's row, kSumColumns columns from c0.
+__device__ __forceinline__ void put_rows(const WeightGrad& w, uint32_t stage, int64_t r0, int64_t c0, int lane,
+                                         const float (*x)[32]) {
+  const uint32_t mine = stage + uint32_t(lane * kRowBytes);
+  tma_store_wait_read();   // this lane's row before
+  const float scale = w.scale;
+#pragma unroll
+  for (int g = 0; g < kSumColumns / 4; ++g)
+    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(mine + g * 16), "f"(scale * x[g / 8][g % 8 * 4]),
+                 "f"(scale * x[g / 8][g % 8 * 4 + 1]), "f"(scale * x[g / 8][g % 8 * 4 + 2]),
+                 "f"(scale * x[g / 8][g % 8 * 4 + 3])
+                 : "memory");
+  const int64_t r = r0 + lane;
+  const int width = int(min(int64_t(kSumColumns), w.cols - c0));
+  int64_t room = 0;
+  float* p = r < w.rows ? w.accum + w.sg.place(r * w.cols + c0, &room) : nullptr;
+  const bool whole = p && room >= width && (reinterpret_cast<uintptr_t>(p) & 15) == 0 && width % 4 == 0;
+  if (whole) {
+    fence_async_smem();
+    if (w.overwrite) bulk_put(p, mine, width * 4);
+    else bulk_add(p, mine, width * 4);
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  }
+  uint32_t rest = __ballot_sync(0xffffffffu, p && !whole);
+  if (!rest) return;
+  __syncwarp();
+  while (rest) {
+    constexpr int U = 4;   // rows under way
+    constexpr int H = kSumColumns / 32;
+    float old[U][H], sum[U][H];
+    float* q[U][H];
+    uint32_t now = rest;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int row = now ? __ffs(now) - 1 : -1;
+      now &= now - 1;
+#pragma unroll
+      for (int h = 0; h < H; ++h) {
+        q[u][h] = nullptr;
+        const int c = lane + 32 * h;
+        if (row < 0 || c >= width) continue;
+        int64_t left;
+        q[u][h] = w.accum + w.sg.place((r0 + row) * w.cols + c0 + c, &left);
+        old[u][h] = w.overwrite ? 0.f : *q[u][h];
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(sum[u][h]) : "r"(stage + uint32_t(row * kRowBytes + c * 4)));
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int h = 0; h < H; ++h)
+        if (q[u][h]) *q[u][h] = old[u][h] + sum[u][h];
+    rest = now;
+  }
+  __syncwarp();   // rows are read before they are written again
+}
 
 // A chunk of sums in shared memory: 32 rows of 128 bytes, their 16-byte pieces
 // exchanged by the row's low bits, so that neither a lane's row nor eight lanes'
@@ -392,8 +470,6 @@ struct ReadAll {
 
 // ------------------------------------------------------------------ products
 
-using namespace tc;
-
 // One lane of a converged warp.  The compiler knows that elect.sync leaves one
 // thread: behind `lane == 0` it issued each copy and each product through a loop
 // over the lanes that might be there, 125 cycles apiece, and a K block took 0.45
@@ -431,22 +507,22 @@ struct Product {
   int a_mn, b_mn;
 };
 
-template <class E0, class E1>
-struct Work {
-  Product p[2];
-  int tiles0, tiles;      // tiles of p[0], and of both
-  E0 e0;
-  E1 e1;
+template <class E>
+struct One {
+  Product p;
+  int tiles;
+  E e;
 };
 
 constexpr int BK = 64;
 
 // Tensor memory's additions cut off instead of rounding, all in one direction: half
-// a unit of 2^-23 every 16 terms.  For a result in FP32 so many K blocks (512
-// terms) are summed there and FP32 registers add those (a sum of 32768 terms is then
-// off by 1e-6 of its size, where one pass would leave 6e-5).  What is rounded to bf16
-// is not: 2^24 terms would have to come together before that showed.
-constexpr int kDepth = 8;
+// a unit of 2^-23 every 16 terms.  For a result in FP32 so many K blocks of 64 terms
+// are summed there and FP32 registers add those (a sum of 32768 terms is then off by
+// 1e-6 of its size, where one pass would leave 6e-5).  What is rounded to bf16 is
+// not: 2^24 terms would have to come together before that showed.
+constexpr int kDepth = 16;      // pairs of SMs
+constexpr int kDepthFew = 4;    // single SMs: sums of few terms, which are nearer to begin with
 
 __device__ __forceinline__ uint32_t idesc_of(const Product& p, int m, int n) {
   return make_idesc(p.b_mn != 0, m, n) | (p.a_mn ? 1u << 15 : 0u);
@@ -478,6 +554,19 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t at, int mn) {
 }
 __device__ __forceinline__ uint32_t operand_step(int mn) { return mn ? 16 * 128 / 16 : 32 / 16; }
 
+// 32 lanes x 16 columns of FP32 from tensor memory.
+__device__ __forceinline__ void tmem_ld16(uint32_t at, float* v) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(at));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
 // Tiles in groups of eight rows of tiles, column by column: what is under way
 // at one time shares its operands in L2.
 __device__ __forceinline__ void tile_of(const Product& p, int i, int* tm, int* tn) {
@@ -489,12 +578,14 @@ __device__ __forceinline__ void tile_of(const Product& p, int i, int* tm, int* t
 constexpr int kPairThreads = 320;
 constexpr int kPairWarps = 8;   // of the epilogue
 
-template <int BN>
+template <int BN, class E>
 struct PairShape {
+  static constexpr bool kSums = std::is_same_v<E, WeightGrad>;
   static constexpr int kA = 128 * BK * 2, kB = BN / 2 * BK * 2, kStage = kA + kB;
   static constexpr int kStages = BN == 256 ? 5 : 6;
   static constexpr int kBars = 2 * kStages + 4;
-  static constexpr int kShared = 1024 + kStages * kStage + kPairWarps * (kChunkBytes + kSlotBytes) + 8 * kBars + 16;
+  static constexpr int kWarpBytes = kSums ? 32 * kRowBytes : kChunkBytes + kSlotBytes;
+  static constexpr int kShared = 1024 + kStages * kStage + kPairWarps * kWarpBytes + 8 * kBars + 16;
 };
 
 // Tiles of 256 x BN on pairs of SMs (tcgen05 cta_group::2): each block of the
@@ -502,14 +593,14 @@ struct PairShape {
 // Warp 0 loads, warp 1 of the even block issues the products, eight warps of
 // each block add up the partial sums and write the results of one tile while
 // the next one's are formed.
-template <int BN, class E0, class E1>
+template <int BN, class E>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
-k_linear_pair(const __grid_constant__ Work<E0, E1> w, int* err) {
-  using S = PairShape<BN>;
+k_linear_pair(const __grid_constant__ One<E> w, int late, int* err) {
+  using S = PairShape<BN, E>;
   extern __shared__ uint8_t raw_shared[];
   const uint32_t base = (smem_u32(raw_shared) + 1023u) & ~1023u;
   const uint32_t epi = base + S::kStages * S::kStage;
-  const uint32_t bars = epi + kPairWarps * (kChunkBytes + kSlotBytes);
+  const uint32_t bars = epi + kPairWarps * S::kWarpBytes;
   auto full = [&](int s) { return bars + 8u * s; };
   auto empty = [&](int s) { return bars + 8u * (S::kStages + s); };
   auto tfull = [&](int i) { return bars + 8u * (2 * S::kStages + i); };
@@ -520,6 +611,9 @@ k_linear_pair(const __grid_constant__ Work<E0, E1> w, int* err) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const int first = blockIdx.x / 2, step = gridDim.x / 2;
+  const Product& p = w.p;
+  const int nk = p.k;
+  const bool exact = w.e.exact();
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kStages; ++s) {
@@ -545,19 +639,18 @@ k_linear_pair(const __grid_constant__ Work<E0, E1> w, int* err) {
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  begin_kernel(late);
 
   if (warp == 0) {
     if (elect_one()) {
+      const int a_mn = p.a_mn, b_mn = p.b_mn;
+      const CUtensorMap *ma = &p.a, *mb = &p.b;
       int s = 0;
       uint32_t ph = 0;
       for (int tile = first; tile < w.tiles && !*abort_flag; tile += step) {
-        const int which = tile >= w.tiles0;
-        const Product& p = w.p[which];
         int tm, tn;
-        tile_of(p, which ? tile - w.tiles0 : tile, &tm, &tn);
+        tile_of(p, tile, &tm, &tn);
         const int row0 = tm * 256 + int(rank) * 128, col0 = tn * BN + int(rank) * (BN / 2);
-        const int nk = p.k, a_mn = p.a_mn, b_mn = p.b_mn;
-        const CUtensorMap *ma = &p.a, *mb = &p.b;
         for (int kb = 0; kb < nk; ++kb) {
           if (!wait(empty(s), ph ^ 1u, abort_flag, err, ERR_TIMEOUT_PRODUCER)) break;
           const uint32_t sa = base + s * S::kStage, fb = mapa_shared(full(s), 0);
@@ -573,12 +666,11 @@ k_linear_pair(const __grid_constant__ Work<E0, E1> w, int* err) {
       int s = 0, acc = 0;
       uint32_t ph = 0, acc_ph = 0;
       bool ok = true;
+      const uint32_t idesc = idesc_of(p, 256, BN);
+      const uint64_t a0 = operand_desc(base, p.a_mn), b0 = operand_desc(base + S::kA, p.b_mn);
+      const uint32_t a_step = operand_step(p.a_mn), b_step = operand_step(p.b_mn);
+      const int depth = exact ? kDepth : nk;
       for (int tile = first; ok && tile < w.tiles; tile += step) {
-        const Product& p = w.p[tile >= w.tiles0];
-        const uint32_t idesc = idesc_of(p, 256, BN);
-        const uint64_t a0 = operand_desc(base, p.a_mn), b0 = operand_desc(base + S::kA, p.b_mn);
-        const uint32_t a_step = operand_step(p.a_mn), b_step = operand_step(p.b_mn);
-        const int nk = p.k, depth = (tile >= w.tiles0 ? w.e1.exact() : w.e0.exact()) ? kDepth : nk;
         for (int k0 = 0; ok && k0 < nk; k0 += depth) {
           if (!wait(tempty(acc), acc_ph ^ 1u, abort_flag, err, ERR_TIMEOUT_MMA)) { ok = false; break; }
           tc_fence_after();
@@ -603,91 +695,99 @@ k_linear_pair(const __grid_constant__ Work<E0, E1> w, int* err) {
     }
   } else {
     const int ew = warp - 2, q = warp & 3, side = ew >> 2;
-    const uint32_t stage = epi + ew * (kChunkBytes + kSlotBytes), slots = stage + kChunkBytes;
+    const uint32_t stage = epi + ew * S::kWarpBytes, slots = stage + kChunkBytes;
     constexpr int N = BN / 64;   // chunks of a warp
     Draw draw;
-    draw.init(w.e0.drop);
+    draw.init(w.e.drop);
     int acc = 0;
     uint32_t acc_ph = 0;
+    const uint32_t mine = tmem + uint32_t(side * (BN / 2)) + (uint32_t(q * 32) << 16);
     bool ok = true;
+    auto next = [&] {   // hands the accumulator back
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(mapa_shared(tempty(acc), 0));
+      acc ^= 1;
+      if (acc == 0) acc_ph ^= 1u;
+    };
+    auto ready = [&] {
+      const bool r = wait(tfull(acc), acc_ph, abort_flag, err, ERR_TIMEOUT_EPILOGUE);
+      __syncwarp();
+      tc_fence_after();
+      return r;
+    };
     for (int tile = first; ok && tile < w.tiles; tile += step) {
-      const int which = tile >= w.tiles0;
-      const Product& p = w.p[which];
       int tm, tn;
-      tile_of(p, which ? tile - w.tiles0 : tile, &tm, &tn);
+      tile_of(p, tile, &tm, &tn);
       const int64_t m0 = int64_t(tm) * 256 + rank * 128 + q * 32, n0 = int64_t(tn) * BN + side * (BN / 2);
-      const bool here = m0 < p.m;
-      auto fetch = [&](int c) {
-        if (which) w.e1.fetch(slots, c & 1, m0, n0 + 32 * c, lane);
-        else w.e0.fetch(slots, c & 1, m0, n0 + 32 * c, lane);
+      const bool here = m0 < p.m && n0 < p.n;
+      // adds up the partial sums of the tile's K blocks in registers
+      auto add_up = [&](float (&sum)[N][32]) {
+#pragma unroll
+        for (int c = 0; c < N; ++c)
+#pragma unroll
+          for (int j = 0; j < 32; ++j) sum[c][j] = 0.f;
+        for (int k0 = 0; ok && k0 < nk; k0 += kDepth) {
+          if (!ready()) { ok = false; break; }
+          if (here) {
+#pragma unroll
+            for (int c = 0; c < 2 * N; ++c) {   // 16 columns at once: 32 more registers would spill
+              float x[16];
+              tmem_ld16(mine + uint32_t(acc * BN + c * 16), x);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) sum[c / 2][c % 2 * 16 + j] += x[j];
+            }
+          }
+          next();
+        }
       };
-      if (here && n0 < p.n) fetch(0);
-      // the chunk in `stage`; the other half of bf16 slots is refilled before it is
-      // read, FP32 slots behind that
-      auto finish = [&](int c) {
-        copies_done();
-        __syncwarp();
-        const bool ahead = c + 1 < N && n0 + 32 * (c + 1) < p.n, halves = which ? w.e1.halves() : w.e0.halves();
-        if (ahead && halves) fetch(c + 1);
-        if (which) w.e1.chunk(ReadOwn{stage}, slots, c & 1, m0, n0 + 32 * c, lane, draw);
-        else w.e0.chunk(ReadOwn{stage}, slots, c & 1, m0, n0 + 32 * c, lane, draw);
-        if (ahead && !halves) fetch(c + 1);
-        __syncwarp();
-      };
-      auto next = [&] {   // hands the accumulator back
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(mapa_shared(tempty(acc), 0));
-        acc ^= 1;
-        if (acc == 0) acc_ph ^= 1u;
-      };
-      const uint32_t mine = tmem + uint32_t(side * (BN / 2)) + (uint32_t(q * 32) << 16);
-      if (!(which ? w.e1.exact() : w.e0.exact())) {
-        if (p.k == 0) continue;   // no such product: results in bf16 have terms
-        if (!wait(tfull(acc), acc_ph, abort_flag, err, ERR_TIMEOUT_EPILOGUE)) { ok = false; break; }
-        __syncwarp();
-        tc_fence_after();
-        if (here) {
+      if constexpr (S::kSums) {
+        float sum[N][32];
+        add_up(sum);
+        if (!ok || !here) continue;
+#pragma unroll
+        for (int c = 0; c < N; c += kSumColumns / 32)
+          if (n0 + 32 * c < p.n) put_rows(w.e, stage, m0, n0 + 32 * c, lane, &sum[c]);
+      } else {
+        if (here) w.e.fetch(slots, 0, m0, n0, lane);
+        // the chunk in `stage`; the other half of bf16 slots is refilled before it
+        // is read, FP32 slots behind that
+        auto finish = [&](int c) {
+          copies_done();
+          __syncwarp();
+          const bool ahead = c + 1 < N && n0 + 32 * (c + 1) < p.n, halves = w.e.halves();
+          if (ahead && halves) w.e.fetch(slots, (c + 1) & 1, m0, n0 + 32 * (c + 1), lane);
+          w.e.chunk(ReadOwn{stage}, slots, c & 1, m0, n0 + 32 * c, lane, draw);
+          if (ahead && !halves) w.e.fetch(slots, (c + 1) & 1, m0, n0 + 32 * (c + 1), lane);
+          __syncwarp();
+        };
+        if (!exact) {
+          if (!ready()) { ok = false; break; }
+          if (here) {
 #pragma unroll 1
-          for (int c = 0; c < N; ++c) {
-            if (n0 + 32 * c >= p.n) break;
-            float x[32];
-            tmem_ld32(mine + uint32_t(acc * BN + c * 32), x);
-            stage_rows(stage, lane, x);
-            finish(c);
+            for (int c = 0; c < N; ++c) {
+              if (n0 + 32 * c >= p.n) break;
+              float x[32];
+              tmem_ld32(mine + uint32_t(acc * BN + c * 32), x);
+              stage_rows(stage, lane, x);
+              finish(c);
+            }
           }
+          next();
+          continue;
         }
-        next();
-        continue;
-      }
-      float sum[N][32];
+        float sum[N][32];
+        add_up(sum);
+        if (!ok || !here) continue;
 #pragma unroll
-      for (int c = 0; c < N; ++c)
-#pragma unroll
-        for (int j = 0; j < 32; ++j) sum[c][j] = 0.f;
-      for (int k0 = 0; k0 < p.k; k0 += kDepth) {
-        if (!wait(tfull(acc), acc_ph, abort_flag, err, ERR_TIMEOUT_EPILOGUE)) { ok = false; break; }
-        __syncwarp();
-        tc_fence_after();
-        if (here) {
-#pragma unroll
-          for (int c = 0; c < N; ++c) {
-            float x[32];
-            tmem_ld32(mine + uint32_t(acc * BN + c * 32), x);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) sum[c][j] += x[j];
-          }
+        for (int c = 0; c < N; ++c) {
+          if (n0 + 32 * c >= p.n) continue;
+          stage_rows(stage, lane, sum[c]);
+          finish(c);
         }
-        next();
-      }
-      if (!ok || !here) continue;
-#pragma unroll
-      for (int c = 0; c < N; ++c) {
-        if (n0 + 32 * c >= p.n) continue;
-        stage_rows(stage, lane, sum[c]);
-        finish(c);
       }
     }
+    if constexpr (S::kSums) tma_store_wait_all();
   }
   if (*abort_flag) {
     const unsigned long long t0 = globaltimer();
@@ -699,11 +799,12 @@ k_linear_pair(const __grid_constant__ Work<E0, E1> w, int* err) {
   tc_fence_after();
   if (warp == 1)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * BN) : "memory");
+  end_kernel(late);
 }
 
 constexpr int kSplitThreads = 192;
 constexpr int kSplitWarps = 4;   // of the epilogue
-constexpr int kMostSplits = 8;   // blocks of a portable cluster
+constexpr int kMostSplits = 4;   // blocks of a cluster
 
 template <int BN>
 struct SplitShape {
@@ -722,9 +823,9 @@ struct SplitShape {
 // SWAP: the rows of the product are the result's columns (features, of which
 // there are many) and its columns the result's rows (few tokens), so that few
 // tokens leave no part of a tile's 128 rows empty.
-template <int BN, bool SWAP, class E0, class E1>
+template <int BN, bool SWAP, class E>
 __global__ void __launch_bounds__(kSplitThreads, SplitShape<BN>::kBlocks)
-k_linear_split(const __grid_constant__ Work<E0, E1> w, int splits, int* err) {
+k_linear_split(const __grid_constant__ One<E> w, int splits, int late, int* err) {
   using S = SplitShape<BN>;
   extern __shared__ uint8_t raw_shared[];
   const uint32_t base = (smem_u32(raw_shared) + 1023u) & ~1023u;
@@ -738,13 +839,19 @@ k_linear_split(const __grid_constant__ Work<E0, E1> w, int splits, int* err) {
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail) + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tile = blockIdx.x / splits, rank = blockIdx.x % splits;   // clusters are consecutive blocks
-  const int which = tile >= w.tiles0;
-  const Product& p = w.p[which];
+  const Product& p = w.p;
   int tm, tn;
-  tile_of(p, which ? tile - w.tiles0 : tile, &tm, &tn);
+  tile_of(p, tile, &tm, &tn);
   const int kb0 = int(int64_t(p.k) * rank / splits), kb1 = int(int64_t(p.k) * (rank + 1) / splits);
 
-  if (threadIdx.x == 0) {
+  const bool loader = warp == 0 && elect_one();
+  auto load = [&](int kb, int s) {
+    const uint32_t sa = base + s * S::kStage;
+    mbar_expect_tx(full(s), S::kStage);
+    load_operand<128, false>(sa, &p.a, p.a_mn, kb, tm * 128, full(s));
+    load_operand<BN, false>(sa + S::kA, &p.b, p.b_mn, kb, tn * BN, full(s));
+  };
+  if (loader) {
     for (int s = 0; s < S::kStages; ++s) {
       mbar_init(full(s), 1);
       mbar_init(empty(s), 1);
@@ -756,6 +863,9 @@ k_linear_split(const __grid_constant__ Work<E0, E1> w, int splits, int* err) {
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    // the first loads are on their way before tensor memory is there (1 us)
+    begin_kernel(late);
+    for (int s = 0; s < S::kStages && kb0 + s < kb1; ++s) load(kb0 + s, s);
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
@@ -763,10 +873,12 @@ k_linear_split(const __grid_constant__ Work<E0, E1> w, int splits, int* err) {
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  if (!loader) begin_kernel(late);
 
   const int ew = warp - 2, q = warp & 3;
   const uint32_t slots = base + S::kChunks * kChunkBytes + ew * kSlotBytes;   // once the operands are read
@@ -779,17 +891,12 @@ k_linear_split(const __grid_constant__ Work<E0, E1> w, int splits, int* err) {
   };
   bool ok = true;
   if (warp == 0) {
-    if (elect_one()) {
+    if (loader) {
       int s = 0;
       uint32_t ph = 0;
-      const int a_mn = p.a_mn, b_mn = p.b_mn;
-      const CUtensorMap *ma = &p.a, *mb = &p.b;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!wait(empty(s), ph ^ 1u, abort_flag, err, ERR_TIMEOUT_PRODUCER)) break;
-        const uint32_t sa = base + s * S::kStage;
-        mbar_expect_tx(full(s), S::kStage);
-        load_operand<128, false>(sa, ma, a_mn, kb, tm * 128, full(s));
-        load_operand<BN, false>(sa + S::kA, mb, b_mn, kb, tn * BN, full(s));
+      for (int kb = kb0 + S::kStages; kb < kb1; ++kb) {
+        if (!wait(empty(s), ph, abort_flag, err, ERR_TIMEOUT_PRODUCER)) break;
+        load(kb, s);
         if (++s == S::kStages) { s = 0; ph ^= 1u; }
       }
     }
@@ -800,11 +907,11 @@ k_linear_split(const __grid_constant__ Work<E0, E1> w, int splits, int* err) {
       const uint32_t idesc = idesc_of(p, 128, BN);
       const uint64_t a0 = operand_desc(base, p.a_mn), b0 = operand_desc(base + S::kA, p.b_mn);
       const uint32_t a_step = operand_step(p.a_mn), b_step = operand_step(p.b_mn);
-      for (int k0 = kb0; ok && k0 < kb1; k0 += kDepth) {
+      for (int k0 = kb0; ok && k0 < kb1; k0 += kDepthFew) {
         if (!wait(tempty(acc), acc_ph ^ 1u, abort_flag, err, ERR_TIMEOUT_MMA)) break;
         tc_fence_after();
         const uint32_t d = tmem + uint32_t(acc * BN);
-        const int k1 = min(kb1, k0 + kDepth);
+        const int k1 = min(kb1, k0 + kDepthFew);
         for (int kb = k0; kb < k1; ++kb) {
           if (!wait(full(s), ph, abort_flag, err, ERR_TIMEOUT_MMA)) { ok = false; break; }
           tc_fence_after();
@@ -829,7 +936,7 @@ k_linear_split(const __grid_constant__ Work<E0, E1> w, int splits, int* err) {
     for (int c = 0; c < N; ++c)
 #pragma unroll
       for (int j = 0; j < 32; ++j) sum[c][j] = 0.f;
-    for (int k0 = kb0; k0 < kb1; k0 += kDepth) {
+    for (int k0 = kb0; k0 < kb1; k0 += kDepthFew) {
       if (!wait(tfull(acc), acc_ph, abort_flag, err, ERR_TIMEOUT_EPILOGUE)) { ok = false; break; }
       __syncwarp();
       tc_fence_after();
@@ -870,23 +977,17 @@ k_linear_split(const __grid_constant__ Work<E0, E1> w, int splits, int* err) {
     }
   if (warp >= 2 && good) {
     Draw draw;
-    draw.init(w.e0.drop);
+    draw.init(w.e.drop);
     // the cluster's blocks, and their warps, take chunks in turn
     for (int i = rank + splits * ew; i < S::kChunks; i += splits * kSplitWarps) {
       const int quarter = i / N, c = i % N;
       if (!inside(quarter, c)) continue;
       const uint32_t at = base + uint32_t(i * kChunkBytes);
       const int64_t r = row_of(quarter, c), n = col_of(quarter, c);
-      if (which) w.e1.fetch(slots, 0, r, n, lane);
-      else w.e0.fetch(slots, 0, r, n, lane);
+      w.e.fetch(slots, 0, r, n, lane);
       copies_done();
-      if (splits > 1) {
-        if (which) w.e1.chunk(ReadAll{at, splits}, slots, 0, r, n, lane, draw);
-        else w.e0.chunk(ReadAll{at, splits}, slots, 0, r, n, lane, draw);
-      } else {
-        if (which) w.e1.chunk(ReadOwn{at}, slots, 0, r, n, lane, draw);
-        else w.e0.chunk(ReadOwn{at}, slots, 0, r, n, lane, draw);
-      }
+      if (splits > 1) w.e.chunk(ReadAll{at, splits}, slots, 0, r, n, lane, draw);
+      else w.e.chunk(ReadOwn{at}, slots, 0, r, n, lane, draw);
     }
   }
   if (*abort_flag) {
@@ -900,6 +1001,7 @@ k_linear_split(const __grid_constant__ Work<E0, E1> w, int splits, int* err) {
   tc_fence_after();
   if (warp == 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * BN) : "memory");
+  end_kernel(late);
 }
 
 // ------------------------------------------------------------------ operands that are copied first
@@ -909,7 +1011,9 @@ constexpr int kPackThreads = 256;
 // Rows of `cols` elements at any stride to rows that start on 16 bytes; eight
 // elements per thread.  What a row's last piece holds beyond cols is not read.
 __global__ void __launch_bounds__(kPackThreads)
-k_linear_pack(const __nv_bfloat16* in, int64_t stride, __nv_bfloat16* out, int64_t out_stride, int64_t rows, int cols) {
+k_linear_pack(const __nv_bfloat16* in, int64_t stride, __nv_bfloat16* out, int64_t out_stride, int64_t rows, int cols,
+              int late) {
+  begin_kernel(late);
   const int pieces = (cols + 7) / 8;
   const int64_t all = rows * pieces;
   for (int64_t i = int64_t(blockIdx.x) * kPackThreads + threadIdx.x; i < all; i += int64_t(gridDim.x) * kPackThreads) {
@@ -924,6 +1028,7 @@ k_linear_pack(const __nv_bfloat16* in, int64_t stride, __nv_bfloat16* out, int64
     }
     *reinterpret_cast<uint4*>(out + r * out_stride + c) = make_uint4(v[0], v[1], v[2], v[3]);
   }
+  end_kernel(late);
 }
 
 // ------------------------------------------------------------------ bias
@@ -937,20 +1042,87 @@ struct BiasGrad {
   int overwrite;
 };
 
-__global__ void __launch_bounds__(1024) k_bias_grad(const BiasGrad a, const __grid_constant__ Segments sg) {
-  __shared__ float sums[32][33];
-  const int x = threadIdx.x % 32, y = threadIdx.x / 32;
-  const int64_t c = int64_t(blockIdx.x) * 32 + x;
-  float v = 0.f;
-  if (c < a.cols)
-    for (int64_t t = y; t < a.tokens; t += 32) v += tok::to_float(a.dout[t * a.stride + c]);
-  sums[y][x] = v;
+constexpr int kBiasThreads = 256;
+constexpr int kBiasColumns = 64;   // of a block: 128 bytes of a row, eight threads
+constexpr int kBiasRows = kBiasThreads / 8;
+constexpr int kBiasLoads = 8;      // rows a thread has under way
+
+// Sums of dout's columns.  A cluster of blocks shares out the tokens of 64
+// columns; their sums meet in the first block, in the order of the blocks.  VEC:
+// rows start on 16 bytes.  Bound by memory: 16384 x 2304 in 15 us (5 TB/s).
+template <bool VEC>
+__global__ void __launch_bounds__(kBiasThreads)
+k_bias_grad(const BiasGrad a, const __grid_constant__ Segments sg, int blocks, int late) {
+  __shared__ float sums[kBiasRows][kBiasColumns + 4];
+  __shared__ float all[kBiasColumns];
+  begin_kernel(late);
+  const int slab = blockIdx.x / blocks, rank = blockIdx.x % blocks;
+  const int x = threadIdx.x % 8, y = threadIdx.x / 8;
+  const int64_t c = int64_t(slab) * kBiasColumns + x * 8;
+  const int left = int(min(int64_t(8), a.cols - c));
+  const int64_t t0 = a.tokens * rank / blocks, t1 = a.tokens * (rank + 1) / blocks;
+  float v[8] = {};
+  for (int64_t t = t0 + y; t < t1; t += kBiasRows * kBiasLoads) {
+    if constexpr (VEC) {
+      uint4 raw[kBiasLoads];
+#pragma unroll
+      for (int u = 0; u < kBiasLoads; ++u) {
+        raw[u] = make_uint4(0, 0, 0, 0);
+        if (left >= 8 && t + u * kBiasRows < t1)
+          raw[u] = __ldg(reinterpret_cast<const uint4*>(a.dout + (t + u * kBiasRows) * a.stride + c));
+      }
+#pragma unroll
+      for (int u = 0; u < kBiasLoads; ++u) {
+        float f[8];
+        tok::Vec<__nv_bfloat16>::unpack(raw[u], f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] += f[j];
+      }
+    }
+    if (!VEC || left < 8)
+#pragma unroll 1
+      for (int u = 0; u < kBiasLoads; ++u)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (j < left && t + u * kBiasRows < t1) v[j] += tok::to_float(a.dout[(t + u * kBiasRows) * a.stride + c + j]);
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) sums[y][x * 8 + j] = v[j];
   __syncthreads();
-  if (y || c >= a.cols) return;
-  for (int q = 1; q < 32; ++q) v += sums[q][x];
-  int64_t room;
-  float* p = a.accum + sg.place(c, &room);
-  *p = (a.overwrite ? 0.f : *p) + a.scale * v;
+  const int i = threadIdx.x;
+  if (i < kBiasColumns) {
+    float s = 0.f;
+#pragma unroll 8
+    for (int r = 0; r < kBiasRows; ++r) s += sums[r][i];
+    all[i] = s;
+  }
+  __syncwarp();
+  if (blocks > 1) cluster_sync();
+  const int64_t col = int64_t(slab) * kBiasColumns + i;
+  if (rank == 0 && i < kBiasColumns && col < a.cols) {
+    float s = all[i];
+    for (int b = 1; b < blocks; ++b) {
+      float f;
+      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(f) : "r"(mapa_shared(smem_u32(&all[i]), b)));
+      s += f;
+    }
+    int64_t room;
+    float* p = a.accum + sg.place(col, &room);
+    *p = (a.overwrite ? 0.f : *p) + a.scale * s;
+  }
+  __syncwarp();
+  if (blocks > 1) cluster_sync();
+  end_kernel(late);
+}
+
+cudaError_t launch_bias(const BiasGrad& a, const Segments& sg, int late, cudaStream_t s) {
+  const int slabs = (a.cols + kBiasColumns - 1) / kBiasColumns;
+  // up to eight blocks of at least 64 tokens to 64 columns, four per SM
+  int blocks = 1;
+  while (blocks < 8 && int64_t(blocks) * 2 * slabs <= 4 * 152 && a.tokens >= 64 * 2 * blocks) blocks *= 2;
+  const bool vec = !misaligned(a.dout, 16) && (a.tokens <= 1 || a.stride % 8 == 0);
+  return launch(vec ? k_bias_grad<true> : k_bias_grad<false>, unsigned(slabs) * blocks, kBiasThreads, blocks, true, s, 0, a, sg,
+                blocks, late);
 }
 
 // ------------------------------------------------------------------ host
@@ -977,8 +1149,8 @@ struct Operand {
     const int64_t to = (cols + 7) / 8 * 8, pieces = rows * (to / 8);
     __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(*at);
     const unsigned grid = unsigned(std::min<int64_t>((pieces + kPackThreads - 1) / kPackThreads, 16 * kSms));
-    const cudaError_t e = launch(k_linear_pack, grid, kPackThreads, 1, false, s, 0,
-                                 static_cast<const __nv_bfloat16*>(p), stride, out, to, rows, int(cols));
+    const cudaError_t e = launch(k_linear_pack, grid, kPackThreads, 1, true, s, 0,
+                                 static_cast<const __nv_bfloat16*>(p), stride, out, to, rows, int(cols), *launches > 0);
     *at += packed;
     p = out;
     stride = to;
@@ -987,65 +1159,43 @@ struct Operand {
   }
 };
 
-// How a product, or two at once, is run: pairs of SMs and tiles of 256 x bn, or
-// single ones, 128 x bn, with the K blocks shared out to `splits` blocks.
+// How a product is run: pairs of SMs and tiles of 256 x bn, or single ones, 128 x
+// bn, with the K blocks shared out to `splits` blocks.
 struct Plan {
   bool pairs = false, swap = false;
   int bn = 0, splits = 1;
 };
 
-struct Extent {
-  int64_t m, n, k;   // of the product as in D[m][n], k in elements
-};
-
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// The plan of least estimated time.
-// A K block takes a pair 0.30 us at 256 columns and 0.18 at 128, a single SM
-// 0.17 us (bound by the loads of its operands), a tile's results 2 us behind the
-// last one; a cluster's sums 1.5 us.
-Plan plan_of(const Extent* x, int count) {
+// The plan of least estimated time for D[m][n] with k terms.  An SM takes in 64
+// bytes a cycle, which is what a K block of 64 costs: 0.28 us on a pair at 256
+// columns (there the tensor cores take as long), 0.20 at 128, 0.30 on a single SM.
+// Starting, the first operands' latency and the results cost 6, 4.7 and 4.5 us,
+// a cluster's sums 2 more, old FP32 sums on single SMs 3.  Measured (us; chosen
+// first): 1024 x 768 -> 768 6.7 on pairs at 128, 7.8 on single SMs, 9.8 on pairs at
+// 256; its weight's gradient 8.7, 10.0 (four blocks a tile), 12.4; 512 x 4096 ->
+// 1024 11.8 on four blocks a tile, 17.0 on pairs at 128; 2048^3 15.2 on pairs at 256,
+// 18.3 at 128.
+Plan plan_of(int64_t m, int64_t n, int64_t k, bool sums) {
   Plan best;
   double least = 0;
-  auto offer = [&](const Plan& p, double us) {
-    if (!best.bn || us < least) {
-      best = p;
-      least = us;
-    }
+  const double kb = double(ceil_div(k, 64));
+  auto offer = [&](bool pairs, int bn, int splits, double us) {
+    if (best.bn && us >= least) return;
+    best.pairs = pairs;
+    best.bn = bn;
+    best.splits = splits;
+    least = us;
   };
   for (int bn : {256, 128}) {
-    double work = 0, longest = 0;
-    int64_t tiles = 0;
-    for (int i = 0; i < count; ++i) {
-      const int64_t t = ceil_div(x[i].m, 256) * ceil_div(x[i].n, bn);
-      const double one = double(ceil_div(x[i].k, 64)) * (bn == 256 ? 0.30 : 0.18) + 1.0;
-      tiles += t;
-      work += double(t) * one;
-      longest = std::max(longest, one);
-    }
-    const double waves = std::ceil(double(tiles) / kPairs);
-    Plan p;
-    p.pairs = true;
-    p.bn = bn;
-    offer(p, std::max(waves * work / double(tiles), longest) + 3.0);
+    const double waves = std::ceil(double(ceil_div(m, 256) * ceil_div(n, bn)) / kPairs);
+    offer(true, bn, 1, waves * (kb * (bn == 256 ? 0.28 : 0.20) + 0.5) + (bn == 256 ? 5.5 : 4.2));
   }
-  for (int s = 1; s <= kMostSplits; ++s) {
-    double work = 0, longest = 0;
-    int64_t blocks = 0, k = 1 << 30;
-    for (int i = 0; i < count; ++i) {
-      const int64_t t = ceil_div(x[i].m, 128) * ceil_div(x[i].n, 128) * s, kb = ceil_div(x[i].k, 64);
-      const double one = double(ceil_div(kb, s)) * 0.17 + (s > 1 ? 2.5 : 2.0);
-      blocks += t;
-      work += double(t) * one;
-      longest = std::max(longest, one);
-      k = std::min(k, kb);
-    }
-    if (s > 1 && k < 2 * s) break;
-    const double waves = std::ceil(double(blocks) / kSms);
-    Plan p;
-    p.bn = 128;
-    p.splits = s;
-    offer(p, std::max(waves * work / double(blocks), longest) + 1.0);
+  // clusters of 3 and of 8 found no room beside one another: 2 of 152 SMs' worth at most ran at once
+  for (int s = 1; s <= kMostSplits && (s == 1 || kb >= 2 * s); s *= 2) {
+    const double waves = std::ceil(double(ceil_div(m, 128) * ceil_div(n, 128) * s) / (s > 2 ? 144 : kSms));
+    offer(false, 128, s, waves * (std::ceil(kb / s) * 0.30 + 2.0) + 2.5 + (s > 1 ? 2.0 : 0.0) + (sums ? 3.0 : 0.0));
   }
   return best;
 }
@@ -1058,7 +1208,7 @@ Plan plan_few(int64_t tokens, int64_t features, int64_t k) {
   p.swap = true;
   p.bn = tokens <= 32 ? 32 : 64;
   const int64_t tiles = ceil_div(features, 128) * ceil_div(tokens, p.bn), kb = ceil_div(k, 64);
-  while (p.splits < kMostSplits && tiles * (p.splits + 1) <= 2 * kSms && kb >= 2 * (p.splits + 1)) ++p.splits;
+  while (p.splits < kMostSplits && tiles * p.splits * 2 <= 2 * kSms && kb >= 4 * p.splits) p.splits *= 2;
   return p;
 }
 
@@ -1083,9 +1233,8 @@ bool make_product(const Plan& plan, const Operand& a, bool a_mn, const Operand& 
   return map(&p->a, a, a_mn, 128) && map(&p->b, b, b_mn, plan.pairs ? plan.bn / 2 : plan.bn);
 }
 
-template <auto KERNEL, class W>
-cudaError_t launch_shared(unsigned grid, unsigned block, int cluster, int bytes, cudaStream_t s, const W& w,
-                          int splits, int* err) {
+template <auto KERNEL, class... A>
+cudaError_t launch_shared(unsigned grid, unsigned block, int cluster, int bytes, cudaStream_t s, const A&... args) {
   static uint64_t done = 0;   // devices that know how much shared memory this kernel takes
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1095,46 +1244,48 @@ cudaError_t launch_shared(unsigned grid, unsigned block, int cluster, int bytes,
     if (e != cudaSuccess) return e;
     done |= uint64_t(1) << (dev & 63);
   }
-  if constexpr (std::is_invocable_v<decltype(KERNEL), W, int*>)
-    return launch(KERNEL, grid, block, 1, false, s, bytes, w, err);
-  else
-    return launch(KERNEL, grid, block, cluster, false, s, bytes, w, splits, err);
+  return launch(KERNEL, grid, block, cluster, true, s, bytes, args...);
 }
 
-template <class E0, class E1>
-cudaError_t launch_work(const Plan& plan, const Work<E0, E1>& w, cudaStream_t s) {
-  void* err = nullptr;
-  const cudaError_t e = cudaGetSymbolAddress(&err, g_linear_err);
+cudaError_t error_flag(int** out) {
+  void* p = nullptr;
+  const cudaError_t e = cudaGetSymbolAddress(&p, g_linear_err);
+  *out = static_cast<int*>(p);
+  return e;
+}
+
+template <int BN, class E>
+cudaError_t launch_pair(const One<E>& w, int late, cudaStream_t s) {
+  int* err;
+  const cudaError_t e = error_flag(&err);
   if (e != cudaSuccess) return e;
-  int* flag = static_cast<int*>(err);
-  if (plan.pairs) {
-    const unsigned grid = 2 * unsigned(std::min(w.tiles, kPairs));
-    if (plan.bn == 256)
-      return launch_shared<k_linear_pair<256, E0, E1>>(grid, kPairThreads, 2, PairShape<256>::kShared, s, w, 1, flag);
-    return launch_shared<k_linear_pair<128, E0, E1>>(grid, kPairThreads, 2, PairShape<128>::kShared, s, w, 1, flag);
-  }
-  const unsigned grid = unsigned(w.tiles) * plan.splits;
-  if constexpr (std::is_same_v<E1, NoProduct> && !std::is_same_v<E0, WeightGrad>) {
-    if (plan.swap && plan.bn == 32)
-      return launch_shared<k_linear_split<32, true, E0, E1>>(grid, kSplitThreads, plan.splits, SplitShape<32>::kShared, s,
-                                                           w, plan.splits, flag);
-    if (plan.swap)
-      return launch_shared<k_linear_split<64, true, E0, E1>>(grid, kSplitThreads, plan.splits, SplitShape<64>::kShared, s,
-                                                           w, plan.splits, flag);
-  }
-  return launch_shared<k_linear_split<128, false, E0, E1>>(grid, kSplitThreads, plan.splits, SplitShape<128>::kShared, s,
-                                                         w, plan.splits, flag);
+  return launch_shared<k_linear_pair<BN, E>>(2 * unsigned(std::min(w.tiles, kPairs)), kPairThreads, 1,
+                                             PairShape<BN, E>::kShared, s, w, late, err);
+}
+
+template <int BN, bool SWAP, class E>
+cudaError_t launch_split(const One<E>& w, int splits, int late, cudaStream_t s) {
+  int* err;
+  const cudaError_t e = error_flag(&err);
+  if (e != cudaSuccess) return e;
+  return launch_shared<k_linear_split<BN, SWAP, E>>(unsigned(w.tiles) * splits, kSplitThreads, splits,
+                                                    SplitShape<BN>::kShared, s, w, splits, late, err);
 }
 
 // One product.
 template <class E>
-cudaError_t run_one(const Plan& plan, const Operand& a, bool a_mn, const Operand& b, bool b_mn, const E& e,
+cudaError_t run_one(const Plan& plan, const Operand& a, bool a_mn, const Operand& b, bool b_mn, const E& e, int late,
                     cudaStream_t s) {
-  static Work<E, NoProduct> w;   // large; the caller holds the library lock
-  w.e0 = e;
-  if (!make_product(plan, a, a_mn, b, b_mn, &w.p[0])) return cudaErrorInvalidValue;
-  w.tiles0 = w.tiles = w.p[0].tiles_m * w.p[0].tiles_n;
-  return launch_work(plan, w, s);
+  static One<E> w;   // large; the caller holds the library lock
+  w.e = e;
+  if (!make_product(plan, a, a_mn, b, b_mn, &w.p)) return cudaErrorInvalidValue;
+  w.tiles = w.p.tiles_m * w.p.tiles_n;
+  if (plan.pairs) return plan.bn == 256 ? launch_pair<256>(w, late, s) : launch_pair<128>(w, late, s);
+  if constexpr (!std::is_same_v<E, WeightGrad>) {
+    if (plan.swap && plan.bn == 32) return launch_split<32, true>(w, plan.splits, late, s);
+    if (plan.swap) return launch_split<64, true>(w, plan.splits, late, s);
+  }
+  return launch_split<128, false>(w, plan.splits, late, s);
 }
 
 // The sum of launches' tiles stays below 2^31 (each plan has no more than this).
@@ -1324,12 +1475,8 @@ extern "C" int muon_linear(const muon_linear_args_t* args, void* workspace, size
     cudaError_t e = x.pack(&at, s, &launches);
     if (e == cudaSuccess) e = w.pack(&at, s, &launches);
     if (e != cudaSuccess) return lay::end_call(launches, e);
-    if (T <= kFewTokens) {
-      e = run_one(plan_few(T, N, K), w, false, x, false, f, s);
-    } else {
-      const Extent size{T, N, K};
-      e = run_one(plan_of(&size, 1), x, false, w, false, f, s);
-    }
+    e = T <= kFewTokens ? run_one(plan_few(T, N, K), w, false, x, false, f, 0, s)
+                        : run_one(plan_of(T, N, K, false), x, false, w, false, f, 0, s);
     return lay::end_call(launches + 1, e);
   });
 }
@@ -1393,36 +1540,24 @@ extern "C" int muon_linear_grad(const muon_linear_grad_args_t* args, void* works
     g.scale = a.scale;
     if (a.param) g.sg = places.weight;
     const bool dx = a.dx && T, dw = a.param, few = T <= kFewTokens;
-    const Extent size[2] = {{T, K, N}, {N, K, T}};   // of dx and of the weight's gradient
-    if (dx && dw && !few) {
-      // both at once: the tiles of one fill the SMs behind those of the other
-      static Work<InputGrad, WeightGrad> w;   // large; this call holds the library lock
-      const Plan plan = plan_of(size, 2);
-      w.e0 = f;
-      w.e1 = g;
-      e = make_product(plan, o.dout, false, o.weight, true, &w.p[0]) &&
-                  make_product(plan, o.dout, true, o.x, true, &w.p[1])
-              ? cudaSuccess
-              : cudaErrorInvalidValue;
-      w.tiles0 = w.p[0].tiles_m * w.p[0].tiles_n;
-      w.tiles = w.tiles0 + w.p[1].tiles_m * w.p[1].tiles_n;
-      if (e == cudaSuccess) e = launch_work(plan, w, s);
-      ++launches;
-    } else {
-      if (dx) {
-        e = few ? run_one(plan_few(T, K, N), o.weight, true, o.dout, false, f, s)
-                : run_one(plan_of(&size[0], 1), o.dout, false, o.weight, true, f, s);
-        ++launches;
-      }
-      if (dw && e == cudaSuccess) {
-        e = run_one(plan_of(&size[1], 1), o.dout, true, o.x, true, g, s);
-        ++launches;
-      }
-    }
-    if (e != cudaSuccess) return lay::end_call(launches, e);
+    // The call's kernels depend on copies of the operands alone: behind the first
+    // that waits for those, they run beside one another.
+    int late = 0;
     if (a.bias) {
-      const BiasGrad b{static_cast<const __nv_bfloat16*>(a.dout), a.dout_stride, T, N, a.accum, a.scale, a.overwrite};
-      e = launch(k_bias_grad, unsigned((N + 31) / 32), 1024, 1, false, s, 0, b, places.bias);
+      const BiasGrad b{static_cast<const __nv_bfloat16*>(o.dout.p ? o.dout.p : a.dout), o.dout.p ? o.dout.stride : a.dout_stride,
+                       T, N, a.accum, a.scale, a.overwrite};
+      if ((e = launch_bias(b, places.bias, late, s)) != cudaSuccess) return lay::end_call(launches, e);
+      ++launches;
+      late = 1;
+    }
+    if (dx) {
+      e = few ? run_one(plan_few(T, K, N), o.weight, true, o.dout, false, f, late, s)
+              : run_one(plan_of(T, K, N, false), o.dout, false, o.weight, true, f, late, s);
+      ++launches;
+      late = 1;
+    }
+    if (dw && e == cudaSuccess) {
+      e = run_one(plan_of(N, K, T, true), o.dout, true, o.x, true, g, late, s);
       ++launches;
     }
     return lay::end_call(launches, e);

@@ -129,11 +129,11 @@ struct Segments {
 // Launches `kernel` in clusters of `cluster` blocks; early: it may be
 // scheduled while the kernel before it drains (it then calls wait_before).
 template <typename... A, typename... B>
-cudaError_t launch(void (*kernel)(A...), unsigned grid, unsigned block, int cluster, bool early,
+cudaError_t launch(void (*kernel)(A...), unsigned grid, dim3 block, int cluster, bool early,
                    cudaStream_t s, int shared_bytes, B... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(block);
+  cfg.blockDim = block;
   cfg.stream = s;
   cfg.dynamicSmemBytes = shared_bytes;
   cudaLaunchAttribute at[2];
