@@ -580,13 +580,15 @@ def _joined_out(x, keep: int):
 def _activation(name):
     try:
         return ACTIVATIONS[name]
-    except (KeyError, TypeError):
+    except (KeyError, TypeError):   # an unknown name, or nothing that could be one
         raise ValueError(f"unknown activation {name!r}: one of {sorted(k for k in ACTIVATIONS if k)}") from None
 
 
 def _param(p):
     if p is None:
         return None
+    if type(p) is tuple:
+        return p
     if hasattr(p, "dtype"):
         p = (p["offset"], p["rows"], p["cols"])
     return tuple(int(v) for v in p)
@@ -612,6 +614,11 @@ def linear(x, weight, bias=None, activation=None, residual=None, dropout: float 
     residual.  workspace: a contiguous CUDA tensor of at least the bytes
     muon_linear_workspace says (default: a new one, if operands' rows do not
     start on 16 bytes).  Returns out, or (out, pre)."""
+    if stream is None and x.dim() == 2:   # nothing to join: the C half alone
+        r = (_bound or _native()).linear(x, weight, bias, _activation(activation), residual, dropout, rng, site, out,
+                                         out_dtype, pre, workspace)
+        if r is not None:
+            return r
     lead = None if x.dim() == 2 else x.shape[:-1]
     keep = pre is not False and pre is not None
     given = out
@@ -644,6 +651,11 @@ def linear_grad(accum, dout, x, weight, param=None, bias_param=None, parts=None,
     embedding_grad; None: that gradient is not taken (accum and x, which it
     needs, may then be None).  dx: True (a new tensor), False (none; weight may
     then be None) or a tensor to fill."""
+    if stream is None and dout.dim() == 2 and (x is None or x.dim() == 2):
+        r = (_bound or _native()).linear_grad(accum, dout, x, weight, _param(param), _param(bias_param), _parts(parts),
+                                              scale, overwrite, _activation(activation), pre, dx, workspace)
+        if r is not None:
+            return r[0]
     lead = None if dout.dim() == 2 else dout.shape[:-1]
     r = _call("linear_grad", dout, stream, accum, _joined(dout, 1, stream), _joined(x, 1, stream), weight,
               _param(param), _param(bias_param), _parts(parts), scale, overwrite, _activation(activation),
@@ -658,6 +670,10 @@ def dropout(x, rate: float, rng, site: int = 0, residual=None, out=None, stream=
     dropout(dout, rate, rng, site) with the same generator (rng: an int64 CUDA
     tensor (seed, step)).  The draws go by row (leading dimensions joined) and
     column.  out may be x or the residual."""
+    if stream is None and x.dim() == 2:
+        r = (_bound or _native()).dropout(x, rate, rng, site, residual, out)
+        if r is not None:
+            return r
     shape = x.shape
     flat_out = _joined_out(out, 1)
     flat = lambda t: _joined_out(t, 1) if t is out else _joined(t, 1, stream)  # noqa: E731
@@ -698,6 +714,11 @@ def norm_rotary(q, k=None, positions=None, inv_freq=None, axis=None, interleaved
     None: no rotation; norm: divide by the root mean square, times the weight
     if there is one.  q_out, k_out: tensors to fill, q and k themselves too.
     Returns (q, k), k None where none was given."""
+    if stream is None and q.dim() == 3:
+        r = (_bound or _native()).norm_rotary(q, k, positions, inv_freq, axis, interleaved, norm, q_weight, k_weight,
+                                              eps, q_out, k_out)
+        if r is not None:
+            return r
     lead = None if q.dim() == 3 else q.shape[:-2]
     flat = lambda t, o: _joined_out(t, 2) if t is o else _joined(t, 2, stream)  # noqa: E731
     a, b = _call("norm_rotary", q, stream, flat(q, q_out), flat(k, k_out), positions, inv_freq, axis, interleaved, norm,
@@ -723,6 +744,12 @@ def norm_rotary_grad(dq, q, dk=None, k=None, positions=None, inv_freq=None, axis
     dk_out: tensors to fill, dq and dk themselves too.  workspace: a contiguous
     CUDA tensor of at least norm_rotary_grad_workspace(tokens, head_dim) bytes
     (default: a new one)."""
+    if stream is None and dq.dim() == 3:
+        r = (_bound or _native()).norm_rotary_grad(dq, q, dk, k, positions, inv_freq, axis, interleaved, norm, q_weight,
+                                                   k_weight, eps, accum, _param(q_param), _param(k_param),
+                                                   _parts(parts), scale, overwrite, dq_out, dk_out, workspace)
+        if r is not None:
+            return r
     lead = None if dq.dim() == 3 else dq.shape[:-2]
     flat = lambda t, o: _joined_out(t, 2) if t is o else _joined(t, 2, stream)  # noqa: E731
     a, b = _call("norm_rotary_grad", dq, stream, flat(dq, dq_out), flat(q, dq_out), flat(dk, dk_out), flat(k, dk_out),

@@ -10,6 +10,7 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 #include <limits.h>
+#include <stdint.h>
 #include <string.h>
 
 #include "../../include/muon.h"
@@ -622,6 +623,11 @@ static PyObject* make_rows(long long rows, long long cols, PyObject* dtype, PyOb
   return make(Py_BuildValue("(LL)", rows, cols), dtype, like);
 }
 
+/* Whether a matrix's rows start on 16 bytes: the library then reads it where it lies and needs no scratch. */
+static int on16(const void* p, long long rows, long long stride) {
+  return (uintptr_t)p % 16 == 0 && (rows <= 1 || (stride % 8 == 0 && stride < (1ll << 39)));
+}
+
 /* linear(x, weight, bias, activation, residual, rate, rng, site, out, out_dtype, pre, workspace); x, residual, out and
  * pre are matrices.  Returns out, or (out, pre). */
 static PyObject* py_linear(PyObject* self, PyObject* const* a, Py_ssize_t na) {
@@ -698,8 +704,9 @@ static PyObject* py_linear(PyObject* self, PyObject* const* a, Py_ssize_t na) {
   l.x_stride = x.stride;
   l.weight_stride = w.stride;
   l.out_dtype = kind;
-  size_t need, bytes;
-  if (done(g.linear_workspace(&l, &need)) || provide(a[11], need, a[0], &work, &pw, &bytes) ||
+  size_t need = 0, bytes;
+  if ((!(on16(l.x, x.rows, x.stride) && on16(l.weight, w.rows, w.stride)) && done(g.linear_workspace(&l, &need))) ||
+      provide(a[11], need, a[0], &work, &pw, &bytes) ||
       stream_of(device, &stream))
     goto end;
   int rc;
@@ -836,8 +843,11 @@ static PyObject* py_linear_grad(PyObject* self, PyObject* const* a, Py_ssize_t n
   l.nparts = (int32_t)(sums.bytes / (Py_ssize_t)sizeof(muon_partition_t));
   l.scale = sums.scale;
   l.overwrite = sums.overwrite;
-  size_t need, bytes;
-  if (done(g.linear_grad_workspace(&l, &need)) || provide(a[12], need, a[1], &work, &pw, &bytes) ||
+  size_t need = 0, bytes;
+  if ((!(on16(l.dout, d.rows, d.stride) && on16(l.x, d.rows, l.x_stride) &&
+         on16(l.weight, d.cols, l.weight_stride)) &&
+       done(g.linear_grad_workspace(&l, &need))) ||
+      provide(a[12], need, a[1], &work, &pw, &bytes) ||
       stream_of(device, &stream))
     goto end;
   int rc;

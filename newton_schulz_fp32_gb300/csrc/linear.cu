@@ -52,6 +52,22 @@ __device__ __forceinline__ uint4 slot16(uint32_t at) {
   return v;
 }
 
+// A chunk of sums in shared memory: 32 rows of 128 bytes, their 16-byte pieces
+// exchanged by the row's low bits, so that neither a lane's row nor eight lanes'
+// pieces meet in a bank.
+__device__ __forceinline__ uint32_t piece(int row, int granule) {
+  return uint32_t(row) * 128u + (uint32_t(granule ^ (row & 7)) << 4);
+}
+
+__device__ __forceinline__ float at_column(uint32_t stage, int row, int lane) {
+  float x;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(stage + piece(row, lane >> 2) + (lane & 3) * 4) : "memory");
+  return x;
+}
+__device__ __forceinline__ void put_column(uint32_t stage, int row, int lane, float x) {
+  asm volatile("st.shared.f32 [%0], %1;" ::"r"(stage + piece(row, lane >> 2) + (lane & 3) * 4), "f"(x) : "memory");
+}
+
 // A matrix that is read or written beside the sums.
 struct Matrix {
   void* p;
@@ -112,9 +128,63 @@ struct Matrix {
       }
     }
   }
+  // A whole chunk of rows that start anywhere, for a converged warp: a row of 32
+  // elements at once (eight elements of four rows at once, as above, would be 32
+  // pieces of memory to each access: 35 us instead of 9 for 1001 x 1001 -> 763).
+  // raw: column c0 + lane of the rows, all of them on their way at once.
+  __device__ __forceinline__ void load_column(int64_t r0, int64_t c0, int64_t rows, int64_t cols, int lane,
+                                              float (&raw)[32]) const {
+    const int here = c0 + lane < cols ? int(min(int64_t(32), rows - r0)) : 0;
+    const char* q = at(r0, c0 + lane);
+    const int64_t by = stride * (fp32 ? 4 : 2);
+    if (fp32) {
+#pragma unroll
+      for (int r = 0; r < 32; ++r, q += by) raw[r] = r < here ? *reinterpret_cast<const float*>(q) : 0.f;
+    } else {
+#pragma unroll
+      for (int r = 0; r < 32; ++r, q += by)
+        raw[r] = r < here ? tok::to_float(*reinterpret_cast<const __nv_bfloat16*>(q)) : 0.f;
+    }
+  }
+  // The lane's pieces of what its warp has loaded that way.
+  static __device__ __forceinline__ void pieces_of(uint32_t stage, int lane, const float (&raw)[32], float (&f)[4][8]) {
+    __syncwarp();
+#pragma unroll
+    for (int r = 0; r < 32; ++r) put_column(stage, r, lane, raw[r]);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        tok::Vec<float>::unpack(slot16(stage + piece(8 * i + (lane >> 2), 2 * (lane & 3) + h)), f[i] + 4 * h);
+    __syncwarp();
+  }
+  __device__ __forceinline__ void store_rows(uint32_t stage, int64_t r0, int64_t c0, int64_t rows, int64_t cols,
+                                             int lane, const float (&f)[4][8]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(stage + piece(8 * i + (lane >> 2), 2 * (lane & 3) + h)),
+                     "f"(f[i][4 * h]), "f"(f[i][4 * h + 1]), "f"(f[i][4 * h + 2]), "f"(f[i][4 * h + 3])
+                     : "memory");
+    __syncwarp();
+    const int here = int(min(int64_t(32), rows - r0));
+    const bool in = c0 + lane < cols;
+    char* q = at(r0, c0 + lane);
+    const int64_t by = stride * (fp32 ? 4 : 2);
+#pragma unroll 8
+    for (int r = 0; r < 32; ++r, q += by) {
+      const float x = at_column(stage, r, lane);
+      if (!in || r >= here) continue;
+      if (fp32) *reinterpret_cast<float*>(q) = x;
+      else *reinterpret_cast<__nv_bfloat16*>(q) = __float2bfloat16_rn(x);
+    }
+    __syncwarp();
+  }
   __device__ __forceinline__ void fetched(uint32_t slots, int half, int i, const char* q, int left, int lane,
                                           float* f) const {
-    if (!wide || left < 8) return load(q, left, f);
+    if (left < 8) return load(q, left, f);
     if (fp32) {
       tok::Vec<float>::unpack(slot16(slots + (2 * i) * 512 + lane * 16), f);
       tok::Vec<float>::unpack(slot16(slots + (2 * i + 1) * 512 + lane * 16), f + 4);
@@ -159,14 +229,39 @@ struct Forward {
   __device__ __forceinline__ void fetch(uint32_t slots, int half, int64_t t0, int64_t n0, int lane) const {
     if (residual.p) residual.fetch(slots, half, t0, n0, rows, cols, lane);
   }
+  // Eight columns of one token.
+  __device__ __forceinline__ void piece8(float (&v)[8], int64_t t, int64_t n, const Draw& draw) const {
+    const int left = int(min(int64_t(8), cols - n));
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (bias && j < left)
+        v[j] += bias32 ? static_cast<const float*>(bias)[n + j]
+                       : tok::to_float(static_cast<const __nv_bfloat16*>(bias)[n + j]);
+    if (pre.p) pre.store(pre.at(t, n), left, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = lay::activation(v[j], act);
+    if (drop.least) {
+      const uint4 w = draw.at(uint32_t(t), uint32_t(n / 8), drop.site);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = lay::dropped(v[j], lay::draw_of(w, j), drop);
+    }
+    if (residual.p) {
+      float r[8];
+      residual.load(residual.at(t, n), left, r);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] += r[j];
+    }
+    out.store(out.at(t, n), left, v);
+  }
   template <typename Read>
   __device__ __forceinline__ void chunk(const Read& read, uint32_t slots, int half, int64_t t0, int64_t n0, int lane,
                                         const Draw& draw) const {
     const int64_t n = n0 + (lane & 3) * 8, t = t0 + (lane >> 2);
-    const int left = int(min(int64_t(8), cols - n));
-    const int live = int(min(int64_t(4), (rows - t + 7) >> 3));   // of the lane's rows
-    if (left <= 0 || live <= 0) return;
-    float v[4][8];
+    const int left = int(min(int64_t(8), cols - n));                                      // of its columns
+    const int live = left <= 0 ? 0 : int(min(int64_t(4), (rows - t + 7) >> 3));   // of its rows
+    float v[4][8], raw[32];
+    const bool late = residual.p && !residual.wide;   // its rows start anywhere
+    if (late) residual.load_column(t0, n0, rows, cols, lane, raw);
 #pragma unroll
     for (int i = 0; i < 4; ++i) read(8 * i + (lane >> 2), lane & 3, v[i]);
     if (bias) {
@@ -184,12 +279,18 @@ struct Forward {
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[i][j] += b[j];
     }
+    // The conditions on `wide` are the warp's.
     if (pre.p) {
-      char* q = pre.at(t, n);
-      const int64_t by = pre.step();
+      if (pre.wide) {
+        char* q = pre.at(t, n);
+        const int64_t by = pre.step();
 #pragma unroll
-      for (int i = 0; i < 4; ++i, q += by)
-        if (i < live) pre.store(q, left, v[i]);
+        for (int i = 0; i < 4; ++i, q += by)
+          if (i < live) pre.store(q, left, v[i]);
+      } else {
+        __syncwarp();   // the sums have been read
+        pre.store_rows(read.at, t0, n0, rows, cols, lane, v);
+      }
     }
     switch (act) {
       case MUON_ACT_RELU: act32<MUON_ACT_RELU>(v); break;
@@ -207,22 +308,36 @@ struct Forward {
       }
     }
     if (residual.p) {
-      const char* q = residual.at(t, n);
-      const int64_t by = residual.step();
+      if (!late) {
+        const char* q = residual.at(t, n);
+        const int64_t by = residual.step();
 #pragma unroll
-      for (int i = 0; i < 4; ++i, q += by) {
-        if (i >= live) break;
-        float r[8];
-        residual.fetched(slots, half, i, q, left, lane, r);
+        for (int i = 0; i < 4; ++i, q += by) {
+          if (i >= live) break;
+          float r[8];
+          residual.fetched(slots, half, i, q, left, lane, r);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] += r[j];
+          for (int j = 0; j < 8; ++j) v[i][j] += r[j];
+        }
+      } else {
+        float r[4][8];
+        Matrix::pieces_of(read.at, lane, raw, r);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[i][j] += r[i][j];
       }
     }
-    char* q = out.at(t, n);
-    const int64_t by = out.step();
+    if (out.wide) {
+      char* q = out.at(t, n);
+      const int64_t by = out.step();
 #pragma unroll
-    for (int i = 0; i < 4; ++i, q += by)
-      if (i < live) out.store(q, left, v[i]);
+      for (int i = 0; i < 4; ++i, q += by)
+        if (i < live) out.store(q, left, v[i]);
+    } else {
+      __syncwarp();
+      out.store_rows(read.at, t0, n0, rows, cols, lane, v);
+    }
   }
 };
 
@@ -243,18 +358,23 @@ struct InputGrad {
                                         const Draw&) const {
     const int64_t n = n0 + (lane & 3) * 8, t = t0 + (lane >> 2);
     const int left = int(min(int64_t(8), cols - n));
-    const int live = int(min(int64_t(4), (rows - t + 7) >> 3));
-    if (left <= 0 || live <= 0) return;
-    float v[4][8];
+    const int live = left <= 0 ? 0 : int(min(int64_t(4), (rows - t + 7) >> 3));
+    float v[4][8], raw[32];
+    const bool late = act != MUON_ACT_NONE && !pre.wide;
+    if (late) pre.load_column(t0, n0, rows, cols, lane, raw);
 #pragma unroll
     for (int i = 0; i < 4; ++i) read(8 * i + (lane >> 2), lane & 3, v[i]);
     if (act != MUON_ACT_NONE) {
       float u[4][8];
-      const char* q = pre.at(t, n);
-      const int64_t by = pre.step();
+      if (!late) {
+        const char* q = pre.at(t, n);
+        const int64_t by = pre.step();
 #pragma unroll
-      for (int i = 0; i < 4; ++i, q += by)
-        if (i < live) pre.fetched(slots, half, i, q, left, lane, u[i]);
+        for (int i = 0; i < 4; ++i, q += by)
+          if (i < live) pre.fetched(slots, half, i, q, left, lane, u[i]);
+      } else {
+        Matrix::pieces_of(read.at, lane, raw, u);
+      }
       switch (act) {
         case MUON_ACT_RELU: slope32<MUON_ACT_RELU>(v, u); break;
         case MUON_ACT_RELU2: slope32<MUON_ACT_RELU2>(v, u); break;
@@ -262,11 +382,16 @@ struct InputGrad {
         default: slope32<MUON_ACT_SILU>(v, u); break;
       }
     }
-    char* q = dx.at(t, n);
-    const int64_t by = dx.step();
+    if (dx.wide) {
+      char* q = dx.at(t, n);
+      const int64_t by = dx.step();
 #pragma unroll
-    for (int i = 0; i < 4; ++i, q += by)
-      if (i < live) dx.store(q, left, v[i]);
+      for (int i = 0; i < 4; ++i, q += by)
+        if (i < live) dx.store(q, left, v[i]);
+    } else {
+      __syncwarp();
+      dx.store_rows(read.at, t0, n0, rows, cols, lane, v);
+    }
   }
 };
 
@@ -300,24 +425,61 @@ struct WeightGrad {
       copy16(slots + (2 * i + 1) * 512 + lane * 16, p + 4);
     }
   }
+  // Rows of `mask` of a chunk or a part of one, `width` columns from c0, element by
+  // element, 32 columns at once.  at(row, column): its sum.  p and room: where
+  // the lane's own row begins, and how many elements follow in one piece.
+  template <int H, typename At>
+  __device__ __forceinline__ void put_pieces(uint32_t mask, int64_t r0, int64_t c0, int width, int lane, float* p,
+                                             int64_t room, const At& at) const {
+    constexpr int U = 8;   // rows under way
+    while (mask) {
+      float old[U][H];
+      float* q[U][H];
+      int row[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        row[u] = mask ? __ffs(mask) - 1 : -1;
+        mask &= mask - 1;
+        const int from = max(row[u], 0);
+        float* start = reinterpret_cast<float*>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(p), from));
+        const int64_t piece_room = __shfl_sync(0xffffffffu, room, from);
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+          const int c = lane + 32 * h;
+          q[u][h] = nullptr;
+          if (row[u] < 0 || c >= width) continue;
+          int64_t left;
+          q[u][h] = c < piece_room ? start + c : accum + sg.place((r0 + row[u]) * cols + c0 + c, &left);
+          old[u][h] = overwrite ? 0.f : *q[u][h];
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+          if (q[u][h]) *q[u][h] = old[u][h] + at(row[u], lane + 32 * h);
+    }
+  }
   template <typename Read>
   __device__ __forceinline__ void chunk(const Read& read, uint32_t slots, int, int64_t r0, int64_t c0, int lane,
                                         const Draw&) const {
     const int64_t c = c0 + (lane & 3) * 8, r = r0 + (lane >> 2);
     const int left = int(min(int64_t(8), cols - c));
-    const int live = int(min(int64_t(4), (rows - r + 7) >> 3));
-    if (left <= 0 || live <= 0) return;
+    const int live = left <= 0 ? 0 : int(min(int64_t(4), (rows - r + 7) >> 3));
     float v[4][8];
+    bool mine = true;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       read(8 * i + (lane >> 2), lane & 3, v[i]);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[i][j] *= scale;
+      mine = mine && (i >= live || whole(r + 8 * i, c, left));
     }
+    if (__all_sync(0xffffffffu, mine)) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (i >= live) break;
-      if (float* p = whole(r + 8 * i, c, left)) {
+      for (int i = 0; i < 4; ++i) {
+        if (i >= live) break;
+        float* p = whole(r + 8 * i, c, left);
         if (!overwrite) {
           float o[8];
           tok::Vec<float>::unpack(slot16(slots + (2 * i) * 512 + lane * 16), o);
@@ -327,22 +489,31 @@ struct WeightGrad {
         }
         reinterpret_cast<uint4*>(p)[0] = tok::Vec<float>::pack(v[i]);
         reinterpret_cast<uint4*>(p)[1] = tok::Vec<float>::pack(v[i] + 4);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if (j >= left) break;
-          int64_t room;
-          float* q = accum + sg.place((r + 8 * i) * cols + c + j, &room);
-          *q = (overwrite ? 0.f : *q) + v[i][j];
-        }
       }
+      return;
     }
+    const uint32_t stage = read.at;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(stage + piece(8 * i + (lane >> 2), 2 * (lane & 3) + h)),
+                     "f"(v[i][4 * h]), "f"(v[i][4 * h + 1]), "f"(v[i][4 * h + 2]), "f"(v[i][4 * h + 3])
+                     : "memory");
+    __syncwarp();
+    int64_t room = 0;
+    const bool in = r0 + lane < rows;
+    float* p = in ? accum + sg.place((r0 + lane) * cols + c0, &room) : nullptr;
+    put_pieces<1>(__ballot_sync(0xffffffffu, in), r0, c0, int(min(int64_t(32), cols - c0)), lane, p, room,
+                  [&](int row, int) { return at_column(stage, row, lane); });
+    __syncwarp();
   }
 };
 
-// A warp's 32 rows x 64 columns of sums, as the pair kernel hands them to accum:
-// a lane's row lies in shared memory, 272 bytes from the next (so that eight lanes'
-// stores meet in no bank), and goes out as one bulk copy of 256 bytes, added at L2
+// A warp's 32 rows x 32 columns of sums, as the pair kernel hands them to accum:
+// a lane's row lies in shared memory, 144 bytes from the next (so that eight lanes'
+// stores meet in no bank), and goes out as one bulk copy of 128 bytes, added at L2
 // or put in place; a warp so needs no load of the old sums and waits for nothing.
 // Rows that do not start on 16 bytes, and pieces that end inside (columns,
 // partitions), go element by element, 32 columns at once.
@@ -383,42 +554,12 @@ __device__ __forceinline__ void put_rows(const WeightGrad& w, uint32_t stage, in
   uint32_t rest = __ballot_sync(0xffffffffu, p && !whole);
   if (!rest) return;
   __syncwarp();
-  while (rest) {
-    constexpr int U = 4;   // rows under way
-    constexpr int H = kSumColumns / 32;
-    float old[U][H], sum[U][H];
-    float* q[U][H];
-    uint32_t now = rest;
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int row = now ? __ffs(now) - 1 : -1;
-      now &= now - 1;
-#pragma unroll
-      for (int h = 0; h < H; ++h) {
-        q[u][h] = nullptr;
-        const int c = lane + 32 * h;
-        if (row < 0 || c >= width) continue;
-        int64_t left;
-        q[u][h] = w.accum + w.sg.place((r0 + row) * w.cols + c0 + c, &left);
-        old[u][h] = w.overwrite ? 0.f : *q[u][h];
-        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(sum[u][h]) : "r"(stage + uint32_t(row * kRowBytes + c * 4)));
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int h = 0; h < H; ++h)
-        if (q[u][h]) *q[u][h] = old[u][h] + sum[u][h];
-    rest = now;
-  }
+  w.put_pieces<kSumColumns / 32>(rest, r0, c0, width, lane, p, room, [&](int row, int c) {
+    float x;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(stage + uint32_t(row * kRowBytes + c * 4)) : "memory");
+    return x;
+  });
   __syncwarp();   // rows are read before they are written again
-}
-
-// A chunk of sums in shared memory: 32 rows of 128 bytes, their 16-byte pieces
-// exchanged by the row's low bits, so that neither a lane's row nor eight lanes'
-// pieces meet in a bank.
-__device__ __forceinline__ uint32_t piece(int row, int granule) {
-  return uint32_t(row) * 128u + (uint32_t(granule ^ (row & 7)) << 4);
 }
 
 __device__ __forceinline__ void stage_rows(uint32_t at, int lane, const float* x) {   // lane: the row
@@ -521,8 +662,11 @@ constexpr int BK = 64;
 // are summed there and FP32 registers add those (a sum of 32768 terms is then off by
 // 1e-6 of its size, where one pass would leave 6e-5).  What is rounded to bf16 is
 // not: 2^24 terms would have to come together before that showed.
-constexpr int kDepth = 16;      // pairs of SMs
-constexpr int kDepthFew = 4;    // single SMs: sums of few terms, which are nearer to begin with
+// Gradients of up to 2048 tokens are nearer than that to begin with (3e-7 by FP32
+// sums of values whose mean is not 0) and take shorter pieces (1.1e-6 in one pass of
+// 1024 terms, 3e-7 in these); for a layer's results, whose weights have no such
+// mean, one pass of 1024 gives 2.3e-7.
+constexpr int kDepth = 16, kDepthFew = 4, kFewBlocks = 32;
 
 __device__ __forceinline__ uint32_t idesc_of(const Product& p, int m, int n) {
   return make_idesc(p.b_mn != 0, m, n) | (p.a_mn ? 1u << 15 : 0u);
@@ -565,6 +709,16 @@ __device__ __forceinline__ void tmem_ld16(uint32_t at, float* v) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t at, const float* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at),
+      "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])), "r"(__float_as_uint(v[3])),
+      "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])), "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7])),
+      "r"(__float_as_uint(v[8])), "r"(__float_as_uint(v[9])), "r"(__float_as_uint(v[10])), "r"(__float_as_uint(v[11])),
+      "r"(__float_as_uint(v[12])), "r"(__float_as_uint(v[13])), "r"(__float_as_uint(v[14])), "r"(__float_as_uint(v[15]))
+      : "memory");
 }
 
 // Tiles in groups of eight rows of tiles, column by column: what is under way
@@ -614,6 +768,7 @@ k_linear_pair(const __grid_constant__ One<E> w, int late, int* err) {
   const Product& p = w.p;
   const int nk = p.k;
   const bool exact = w.e.exact();
+  const int depth = !exact ? max(nk, 1) : S::kSums && nk <= kFewBlocks ? kDepthFew : kDepth;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kStages; ++s) {
@@ -669,7 +824,6 @@ k_linear_pair(const __grid_constant__ One<E> w, int late, int* err) {
       const uint32_t idesc = idesc_of(p, 256, BN);
       const uint64_t a0 = operand_desc(base, p.a_mn), b0 = operand_desc(base + S::kA, p.b_mn);
       const uint32_t a_step = operand_step(p.a_mn), b_step = operand_step(p.b_mn);
-      const int depth = exact ? kDepth : nk;
       for (int tile = first; ok && tile < w.tiles; tile += step) {
         for (int k0 = 0; ok && k0 < nk; k0 += depth) {
           if (!wait(tempty(acc), acc_ph ^ 1u, abort_flag, err, ERR_TIMEOUT_MMA)) { ok = false; break; }
@@ -721,13 +875,14 @@ k_linear_pair(const __grid_constant__ One<E> w, int late, int* err) {
       tile_of(p, tile, &tm, &tn);
       const int64_t m0 = int64_t(tm) * 256 + rank * 128 + q * 32, n0 = int64_t(tn) * BN + side * (BN / 2);
       const bool here = m0 < p.m && n0 < p.n;
-      // adds up the partial sums of the tile's K blocks in registers
-      auto add_up = [&](float (&sum)[N][32]) {
+      if constexpr (S::kSums) {
+        // adds up the partial sums of the tile's K blocks in registers
+        float sum[N][32];
 #pragma unroll
         for (int c = 0; c < N; ++c)
 #pragma unroll
           for (int j = 0; j < 32; ++j) sum[c][j] = 0.f;
-        for (int k0 = 0; ok && k0 < nk; k0 += kDepth) {
+        for (int k0 = 0; ok && k0 < nk; k0 += depth) {
           if (!ready()) { ok = false; break; }
           if (here) {
 #pragma unroll
@@ -740,51 +895,60 @@ k_linear_pair(const __grid_constant__ One<E> w, int late, int* err) {
           }
           next();
         }
-      };
-      if constexpr (S::kSums) {
-        float sum[N][32];
-        add_up(sum);
         if (!ok || !here) continue;
 #pragma unroll
         for (int c = 0; c < N; c += kSumColumns / 32)
           if (n0 + 32 * c < p.n) put_rows(w.e, stage, m0, n0 + 32 * c, lane, &sum[c]);
       } else {
         if (here) w.e.fetch(slots, 0, m0, n0, lane);
-        // the chunk in `stage`; the other half of bf16 slots is refilled before it
-        // is read, FP32 slots behind that
-        auto finish = [&](int c) {
-          copies_done();
-          __syncwarp();
-          const bool ahead = c + 1 < N && n0 + 32 * (c + 1) < p.n, halves = w.e.halves();
-          if (ahead && halves) w.e.fetch(slots, (c + 1) & 1, m0, n0 + 32 * (c + 1), lane);
-          w.e.chunk(ReadOwn{stage}, slots, c & 1, m0, n0 + 32 * c, lane, draw);
-          if (ahead && !halves) w.e.fetch(slots, (c + 1) & 1, m0, n0 + 32 * (c + 1), lane);
-          __syncwarp();
-        };
-        if (!exact) {
-          if (!ready()) { ok = false; break; }
-          if (here) {
-#pragma unroll 1
-            for (int c = 0; c < N; ++c) {
-              if (n0 + 32 * c >= p.n) break;
-              float x[32];
-              tmem_ld32(mine + uint32_t(acc * BN + c * 32), x);
-              stage_rows(stage, lane, x);
-              finish(c);
-            }
-          }
-          next();
-          continue;
-        }
-        float sum[N][32];
-        add_up(sum);
-        if (!ok || !here) continue;
+        if (nk > depth) {
+          // as above, and the sums back to where the last of them lay
+          float sum[2 * N][16];
 #pragma unroll
-        for (int c = 0; c < N; ++c) {
-          if (n0 + 32 * c >= p.n) continue;
-          stage_rows(stage, lane, sum[c]);
-          finish(c);
+          for (int c = 0; c < 2 * N; ++c)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) sum[c][j] = 0.f;
+          for (int k0 = 0; k0 < nk; k0 += depth) {
+            if (!ready()) { ok = false; break; }
+            if (here) {
+#pragma unroll
+              for (int c = 0; c < 2 * N; ++c) {
+                float x[16];
+                tmem_ld16(mine + uint32_t(acc * BN + c * 16), x);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) sum[c][j] += x[j];
+              }
+            }
+            if (k0 + depth < nk) next();
+          }
+          if (!ok) break;
+          if (here) {
+#pragma unroll
+            for (int c = 0; c < 2 * N; ++c) tmem_st16(mine + uint32_t(acc * BN + c * 16), sum[c]);
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+          }
+        } else if (!ready()) {
+          ok = false;
+          break;
         }
+        if (here) {
+#pragma unroll 1
+          for (int c = 0; c < N && n0 + 32 * c < p.n; ++c) {
+            float x[32];
+            tmem_ld32(mine + uint32_t(acc * BN + c * 32), x);
+            stage_rows(stage, lane, x);
+            copies_done();
+            __syncwarp();
+            // the other half of bf16 slots is refilled before this one is read, FP32
+            // slots behind that
+            const bool ahead = c + 1 < N && n0 + 32 * (c + 1) < p.n, halves = w.e.halves();
+            if (ahead && halves) w.e.fetch(slots, (c + 1) & 1, m0, n0 + 32 * (c + 1), lane);
+            w.e.chunk(ReadOwn{stage}, slots, c & 1, m0, n0 + 32 * c, lane, draw);
+            if (ahead && !halves) w.e.fetch(slots, (c + 1) & 1, m0, n0 + 32 * (c + 1), lane);
+            __syncwarp();
+          }
+        }
+        next();
       }
     }
     if constexpr (S::kSums) tma_store_wait_all();
@@ -809,8 +973,7 @@ constexpr int kMostSplits = 4;   // blocks of a cluster
 template <int BN>
 struct SplitShape {
   static constexpr int kA = 128 * BK * 2, kB = BN * BK * 2, kStage = kA + kB;
-  static constexpr int kBlocks = BN == 128 ? 1 : 2;   // per SM
-  static constexpr int kStages = BN == 128 ? 6 : BN == 64 ? 4 : 5;
+  static constexpr int kStages = BN == 128 ? 6 : BN == 64 ? 9 : 11;
   static constexpr int kBars = 2 * kStages + 4;
   static constexpr int kChunks = kSplitWarps * (BN / 32);
   static constexpr int kShared = 1024 + kStages * kStage + 8 * kBars + 16;
@@ -824,7 +987,7 @@ struct SplitShape {
 // there are many) and its columns the result's rows (few tokens), so that few
 // tokens leave no part of a tile's 128 rows empty.
 template <int BN, bool SWAP, class E>
-__global__ void __launch_bounds__(kSplitThreads, SplitShape<BN>::kBlocks)
+__global__ void __launch_bounds__(kSplitThreads, 1)
 k_linear_split(const __grid_constant__ One<E> w, int splits, int late, int* err) {
   using S = SplitShape<BN>;
   extern __shared__ uint8_t raw_shared[];
@@ -1004,31 +1167,156 @@ k_linear_split(const __grid_constant__ One<E> w, int splits, int late, int* err)
   end_kernel(late);
 }
 
+// ------------------------------------------------------------------ a few tokens
+
+constexpr int kRowWarps = 8;
+
+// Whether k_linear_rows takes the product: one or two tokens, or up to four of a
+// weight of at most 2^22 elements, whose rows start on 16 bytes.  Measured, one
+// after another with other weights each time, against tiles on single SMs: 4096 x
+// 4096, 1 token 7.4 us against 11.2, 2 tokens 11.0 against 11.2, 4 tokens 12.6 against
+// 11.5; 768 x 2304, 4 tokens 3.3 against 5.5; rows at odd places 9.3 against 6.7
+// (copied first).
+constexpr int kRowTokens = 4;
+bool takes_rows(int64_t tokens, int64_t in, int64_t out, bool aligned) {
+  return aligned && (tokens <= 2 || (tokens <= kRowTokens && in * out <= (1 << 22)));
+}
+
+struct RowArgs {
+  const __nv_bfloat16* x;
+  const __nv_bfloat16* w;
+  int64_t x_stride, w_stride;
+  int k;
+  Forward f;
+};
+
+// Eight features for up to T tokens per block, whose warps share out K; sums by
+// FP32 multiply-adds, lanes and warps joined in a fixed order.  Bound by the
+// weight's bytes: every lane has eight loads of 16 bytes on their way, and
+// nothing is set up before them (the tensor cores' way to the same place takes
+// 5 us more: tensor memory, maps, a cluster's sums).  The first pieces of the
+// weight are asked for into L2, where that is always safe, before the kernel
+// waits for the one before it.
+template <int T>
+__global__ void __launch_bounds__(32 * kRowWarps) k_linear_rows(const __grid_constant__ RowArgs a) {
+  __shared__ float sums[kRowWarps][T * 8];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int64_t n0 = int64_t(blockIdx.x) * 8;
+  const int features = int(min(int64_t(8), a.f.cols - n0));
+  const int tokens = int(a.f.rows);
+  const __nv_bfloat16* w = a.w + n0 * a.w_stride;
+  constexpr int kPiece = 256;   // elements of a warp's step
+  const int first = warp * kPiece + lane * 8;
+#pragma unroll
+  for (int r = 0; r < 8; ++r)
+    if (r < features && first < a.k) asm volatile("prefetch.global.L2 [%0];" ::"l"(w + r * a.w_stride + first));
+  begin_kernel(0);
+  float acc[T][8] = {};
+  for (int k = first; k < a.k; k += kRowWarps * kPiece) {
+    float f[8], g[T][8];
+    if (k + 8 <= a.k) {
+      uint4 raw[8], xs[T];
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        raw[r] = make_uint4(0, 0, 0, 0);
+        if (r < features) raw[r] = __ldcs(reinterpret_cast<const uint4*>(w + r * a.w_stride + k));
+      }
+#pragma unroll
+      for (int t = 0; t < T; ++t) {
+        xs[t] = make_uint4(0, 0, 0, 0);
+        if (t < tokens) xs[t] = *reinterpret_cast<const uint4*>(a.x + t * a.x_stride + k);
+      }
+#pragma unroll
+      for (int t = 0; t < T; ++t) tok::Vec<__nv_bfloat16>::unpack(xs[t], g[t]);
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        tok::Vec<__nv_bfloat16>::unpack(raw[r], f);
+#pragma unroll
+        for (int t = 0; t < T; ++t)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) acc[t][r] += f[j] * g[t][j];
+      }
+    } else {
+#pragma unroll
+      for (int t = 0; t < T; ++t)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          g[t][j] = t < tokens && k + j < a.k ? tok::to_float(a.x[t * a.x_stride + k + j]) : 0.f;
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          f[j] = r < features && k + j < a.k ? tok::to_float(w[r * a.w_stride + k + j]) : 0.f;
+#pragma unroll
+        for (int t = 0; t < T; ++t)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) acc[t][r] += f[j] * g[t][j];
+      }
+    }
+  }
+  // 8 T sums over the warp's lanes
+#pragma unroll
+  for (int t = 0; t < T; ++t)
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) acc[t][r] += __shfl_xor_sync(0xffffffffu, acc[t][r], o);
+      if (lane == 0) sums[warp][t * 8 + r] = acc[t][r];
+    }
+  __syncthreads();
+  const int t = threadIdx.x;
+  if (t >= T || t >= tokens) return;
+  float v[8];
+#pragma unroll
+  for (int r = 0; r < 8; ++r) {
+    v[r] = 0.f;
+#pragma unroll
+    for (int q = 0; q < kRowWarps; ++q) v[r] += sums[q][t * 8 + r];
+  }
+  Draw draw;
+  draw.init(a.f.drop);
+  a.f.piece8(v, t, n0, draw);
+}
+
 // ------------------------------------------------------------------ operands that are copied first
 
 constexpr int kPackThreads = 256;
+constexpr int kPackMost = 3;   // operands of a call
+
+struct Pack {
+  const __nv_bfloat16* in;
+  __nv_bfloat16* out;
+  int64_t stride, rows;
+  int cols;
+};
+
+struct Packs {
+  Pack p[kPackMost];
+  int64_t end[kPackMost];   // pieces of the operands up to this one
+  int n;
+};
 
 // Rows of `cols` elements at any stride to rows that start on 16 bytes; eight
-// elements per thread.  What a row's last piece holds beyond cols is not read.
-__global__ void __launch_bounds__(kPackThreads)
-k_linear_pack(const __nv_bfloat16* in, int64_t stride, __nv_bfloat16* out, int64_t out_stride, int64_t rows, int cols,
-              int late) {
-  begin_kernel(late);
-  const int pieces = (cols + 7) / 8;
-  const int64_t all = rows * pieces;
-  for (int64_t i = int64_t(blockIdx.x) * kPackThreads + threadIdx.x; i < all; i += int64_t(gridDim.x) * kPackThreads) {
-    const int64_t r = i / pieces;
-    const int c = int(i - r * pieces) * 8;
-    const unsigned short* q = reinterpret_cast<const unsigned short*>(in) + r * stride + c;
+// elements per thread, all of a call's operands in one launch.  What a row's last
+// piece holds beyond cols is not read.
+__global__ void __launch_bounds__(kPackThreads) k_linear_pack(const __grid_constant__ Packs a) {
+  begin_kernel(0);
+  for (int64_t i = int64_t(blockIdx.x) * kPackThreads + threadIdx.x; i < a.end[kPackMost - 1];
+       i += int64_t(gridDim.x) * kPackThreads) {
+    const int which = i < a.end[0] ? 0 : i < a.end[1] ? 1 : 2;
+    const Pack& p = a.p[which];
+    const int pieces = (p.cols + 7) / 8;
+    const int64_t j = which ? i - a.end[which - 1] : i, r = j / pieces;
+    const int c = int(j - r * pieces) * 8;
+    const unsigned short* q = reinterpret_cast<const unsigned short*>(p.in) + r * p.stride + c;
     uint32_t v[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t lo = c + 2 * j < cols ? q[2 * j] : 0u, hi = c + 2 * j + 1 < cols ? q[2 * j + 1] : 0u;
-      v[j] = lo | hi << 16;
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t lo = c + 2 * k < p.cols ? q[2 * k] : 0u, hi = c + 2 * k + 1 < p.cols ? q[2 * k + 1] : 0u;
+      v[k] = lo | hi << 16;
     }
-    *reinterpret_cast<uint4*>(out + r * out_stride + c) = make_uint4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<uint4*>(p.out + (r * pieces + (c >> 3)) * 8) = make_uint4(v[0], v[1], v[2], v[3]);
   }
-  end_kernel(late);
 }
 
 // ------------------------------------------------------------------ bias
@@ -1129,6 +1417,7 @@ cudaError_t launch_bias(const BiasGrad& a, const Segments& sg, int late, cudaStr
 
 constexpr int kMostFeatures = 1 << 24;
 constexpr int kSms = 152, kPairs = kSms / 2;
+constexpr int kFourfold = 144;   // blocks that run at once as clusters of four (of eight: 120, of three: 138)
 
 // An operand of a product: rows x cols, bf16.
 struct Operand {
@@ -1143,21 +1432,29 @@ struct Operand {
     if (q && (misaligned(q, 16) || stride % 8 || stride >= (int64_t(1) << 39)))
       packed = (size_t(r) * ((c + 7) / 8 * 16) + 255) & ~size_t(255);
   }
-  // Copies it where that is needed; *at moves behind the copy.
-  cudaError_t pack(char** at, cudaStream_t s, int* launches) {
-    if (!packed) return cudaSuccess;
-    const int64_t to = (cols + 7) / 8 * 8, pieces = rows * (to / 8);
-    __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(*at);
-    const unsigned grid = unsigned(std::min<int64_t>((pieces + kPackThreads - 1) / kPackThreads, 16 * kSms));
-    const cudaError_t e = launch(k_linear_pack, grid, kPackThreads, 1, true, s, 0,
-                                 static_cast<const __nv_bfloat16*>(p), stride, out, to, rows, int(cols), *launches > 0);
-    *at += packed;
-    p = out;
-    stride = to;
-    ++*launches;
-    return e;
+  // Adds its copy to a launch's, where it needs one; *at moves behind the copy.
+  void pack(char** at, Packs* all) {
+    if (packed) {
+      const int64_t to = (cols + 7) / 8 * 8;
+      __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(*at);
+      all->p[all->n] = {static_cast<const __nv_bfloat16*>(p), out, stride, rows, int(cols)};
+      const int64_t before = all->n ? all->end[all->n - 1] : 0;
+      for (int i = all->n; i < kPackMost; ++i) all->end[i] = before + rows * (to / 8);
+      ++all->n;
+      *at += packed;
+      p = out;
+      stride = to;
+    }
   }
 };
+
+cudaError_t launch_packs(const Packs& all, cudaStream_t s, int* launches) {
+  if (!all.n) return cudaSuccess;
+  const int64_t blocks = (all.end[kPackMost - 1] + kPackThreads - 1) / kPackThreads;
+  const cudaError_t e = launch(k_linear_pack, unsigned(std::min<int64_t>(blocks, 16 * kSms)), kPackThreads, 1, true, s, 0, all);
+  ++*launches;
+  return e;
+}
 
 // How a product is run: pairs of SMs and tiles of 256 x bn, or single ones, 128 x
 // bn, with the K blocks shared out to `splits` blocks.
@@ -1192,23 +1489,22 @@ Plan plan_of(int64_t m, int64_t n, int64_t k, bool sums) {
     const double waves = std::ceil(double(ceil_div(m, 256) * ceil_div(n, bn)) / kPairs);
     offer(true, bn, 1, waves * (kb * (bn == 256 ? 0.28 : 0.20) + 0.5) + (bn == 256 ? 5.5 : 4.2));
   }
-  // clusters of 3 and of 8 found no room beside one another: 2 of 152 SMs' worth at most ran at once
   for (int s = 1; s <= kMostSplits && (s == 1 || kb >= 2 * s); s *= 2) {
-    const double waves = std::ceil(double(ceil_div(m, 128) * ceil_div(n, 128) * s) / (s > 2 ? 144 : kSms));
+    const double waves = std::ceil(double(ceil_div(m, 128) * ceil_div(n, 128) * s) / (s > 2 ? kFourfold : kSms));
     offer(false, 128, s, waves * (std::ceil(kb / s) * 0.30 + 2.0) + 2.5 + (s > 1 ? 2.0 : 0.0) + (sums ? 3.0 : 0.0));
   }
   return best;
 }
 
 // Few tokens: features are the rows of the tiles, and the K blocks are shared out
-// until there are two blocks per SM: what counts is how many bytes of the weight
-// are on their way (14 MB with 1.5 us of latency under load).
+// while there are SMs for it (a block that holds tensor memory has its SM for
+// itself): what counts is how many bytes of the weight are on their way.
 Plan plan_few(int64_t tokens, int64_t features, int64_t k) {
   Plan p;
   p.swap = true;
   p.bn = tokens <= 32 ? 32 : 64;
   const int64_t tiles = ceil_div(features, 128) * ceil_div(tokens, p.bn), kb = ceil_div(k, 64);
-  while (p.splits < kMostSplits && tiles * p.splits * 2 <= 2 * kSms && kb >= 4 * p.splits) p.splits *= 2;
+  while (p.splits < kMostSplits && tiles * p.splits * 2 <= kFourfold && kb >= 4 * p.splits) p.splits *= 2;
   return p;
 }
 
@@ -1247,10 +1543,18 @@ cudaError_t launch_shared(unsigned grid, unsigned block, int cluster, int bytes,
   return launch(KERNEL, grid, block, cluster, true, s, bytes, args...);
 }
 
+// Where the current device's error flag lies.
 cudaError_t error_flag(int** out) {
-  void* p = nullptr;
-  const cudaError_t e = cudaGetSymbolAddress(&p, g_linear_err);
-  *out = static_cast<int*>(p);
+  static int* at[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (!at[dev & 63]) {
+    void* p = nullptr;
+    e = cudaGetSymbolAddress(&p, g_linear_err);
+    at[dev & 63] = static_cast<int*>(p);
+  }
+  *out = at[dev & 63];
   return e;
 }
 
@@ -1286,6 +1590,14 @@ cudaError_t run_one(const Plan& plan, const Operand& a, bool a_mn, const Operand
     if (plan.swap) return launch_split<64, true>(w, plan.splits, late, s);
   }
   return launch_split<128, false>(w, plan.splits, late, s);
+}
+
+cudaError_t launch_rows(const Operand& x, const Operand& w, const Forward& f, cudaStream_t s) {
+  const RowArgs a{static_cast<const __nv_bfloat16*>(x.p), static_cast<const __nv_bfloat16*>(w.p), x.stride, w.stride,
+                  int(w.cols), f};
+  const int64_t t = f.rows;
+  auto k = t == 1 ? k_linear_rows<1> : t == 2 ? k_linear_rows<2> : k_linear_rows<kRowTokens>;
+  return launch(k, unsigned(ceil_div(w.rows, 8)), 32 * kRowWarps, 1, true, s, 0, a);
 }
 
 // The sum of launches' tiles stays below 2^31 (each plan has no more than this).
@@ -1460,6 +1772,10 @@ extern "C" int muon_linear(const muon_linear_args_t* args, void* workspace, size
     const int K = a.in_features, N = a.out_features;
     if (T == 0) return MUON_OK;
     Operand x(a.x, T, K, a.x_stride), w(a.weight, N, K, a.weight_stride);
+    if (takes_rows(T, K, N, !x.packed && !w.packed)) {
+      if ((rc = lay::begin_call()) != MUON_OK) return rc;
+      return lay::end_call(1, launch_rows(x, w, f, static_cast<cudaStream_t>(stream)));
+    }
     const size_t es = dtype_bytes(a.out_dtype);
     if ((rc = check_workspace(workspace, workspace_bytes, x.packed + w.packed,
                               {Span(a.x, T, a.x_stride, K, 2), Span(a.weight, N, a.weight_stride, K, 2),
@@ -1472,8 +1788,10 @@ extern "C" int muon_linear(const muon_linear_args_t* args, void* workspace, size
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     char* at = static_cast<char*>(workspace);
     int launches = 0;
-    cudaError_t e = x.pack(&at, s, &launches);
-    if (e == cudaSuccess) e = w.pack(&at, s, &launches);
+    Packs packs{};
+    x.pack(&at, &packs);
+    w.pack(&at, &packs);
+    cudaError_t e = launch_packs(packs, s, &launches);
     if (e != cudaSuccess) return lay::end_call(launches, e);
     e = T <= kFewTokens ? run_one(plan_few(T, N, K), w, false, x, false, f, 0, s)
                         : run_one(plan_of(T, N, K, false), x, false, w, false, f, 0, s);
@@ -1519,9 +1837,11 @@ extern "C" int muon_linear_grad(const muon_linear_grad_args_t* args, void* works
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     char* at = static_cast<char*>(workspace);
     int launches = 0;
-    cudaError_t e = o.dout.pack(&at, s, &launches);
-    if (e == cudaSuccess) e = o.weight.pack(&at, s, &launches);
-    if (e == cudaSuccess) e = o.x.pack(&at, s, &launches);
+    Packs packs{};
+    o.dout.pack(&at, &packs);
+    o.weight.pack(&at, &packs);
+    o.x.pack(&at, &packs);
+    cudaError_t e = launch_packs(packs, s, &launches);
     if (e != cudaSuccess) return lay::end_call(launches, e);
     InputGrad f{};
     auto matrix = [&](const void* p, int64_t stride) {

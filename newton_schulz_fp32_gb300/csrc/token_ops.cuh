@@ -189,6 +189,8 @@ inline int segments_of(const muon_param_t& p, const muon_partition_t* parts, int
     return MUON_OK;
   }
   std::vector<std::pair<int64_t, int64_t>> st;
+  bool rising = true;   // in storage too: nothing to sort
+  int64_t end = 0;
   for (int i = 0; i < nparts; ++i) {
     const muon_partition_t& q = parts[i];
     if (q.flat_begin < 0 || q.flat_end < q.flat_begin || q.storage_offset < 0 ||
@@ -197,9 +199,13 @@ inline int segments_of(const muon_param_t& p, const muon_partition_t* parts, int
     if (i > 0 && parts[i - 1].flat_end > q.flat_begin)
       return fail_with(MUON_ERR_INVALID, "partitions must be sorted by flat_begin and must not overlap (at " +
                                          std::to_string(i) + ")");
-    if (q.flat_end > q.flat_begin)
-      st.push_back({q.storage_offset, q.storage_offset + q.flat_end - q.flat_begin});
+    if (q.flat_end == q.flat_begin) continue;
+    rising = rising && q.storage_offset >= end;
+    end = q.storage_offset + (q.flat_end - q.flat_begin);
   }
+  for (int i = 0; i < nparts && !rising; ++i)
+    if (parts[i].flat_end > parts[i].flat_begin)
+      st.push_back({parts[i].storage_offset, parts[i].storage_offset + parts[i].flat_end - parts[i].flat_begin});
   std::sort(st.begin(), st.end());
   for (size_t i = 1; i < st.size(); ++i)
     if (st[i - 1].second > st[i].first) return fail_with(MUON_ERR_INVALID, "partitions overlap in storage");
