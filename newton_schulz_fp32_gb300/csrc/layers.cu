@@ -158,12 +158,9 @@ __device__ __forceinline__ int64_t position(const RotArgs& a, int64_t t, int axi
                  : reinterpret_cast<const int32_t*>(a.positions)[i];
 }
 
-// Whether token t is one: no position is negative.
-__device__ __forceinline__ bool is_token(const RotArgs& a, int64_t t) {
-  bool on = true;
-  if (a.pairs)
-    for (int x = 0; x < a.axes; ++x) on = on && position(a, t, x) >= 0;
-  return on;
+// A token's position on axis `lane`; 0 behind the axes.
+__device__ __forceinline__ int64_t lane_position(const RotArgs& a, int64_t t, int lane) {
+  return a.pairs && lane < a.axes ? position(a, t, lane) : 0;
 }
 
 // cos and sin of a pair's angle: position * turns wraps at whole turns by itself;
@@ -174,15 +171,20 @@ __device__ __forceinline__ void angle(int64_t pos, uint64_t turns, float* c, flo
   sincospif(half_turns, s, c);
 }
 
-// P elements (0 beyond n) as they lie in memory; P > 1: one access, all or nothing.
+// P elements as they lie in memory.  P > 1: one access, always (what a lane has no
+// part in is not added up or stored); P = 1: 0 where n is 0.
 template <typename T, int P>
 struct Part {
   static constexpr int kBytes = P * int(sizeof(T));
   using Raw = std::conditional_t<kBytes == 16, uint4, std::conditional_t<kBytes == 8, uint2, std::conditional_t<kBytes == 4, uint32_t, uint16_t>>>;
   Raw raw;
   __device__ __forceinline__ void load(const T* p, int n) {
-    raw = Raw{};
-    if (n) raw = *reinterpret_cast<const Raw*>(p);
+    if constexpr (P == 1) {
+      raw = Raw{};
+      if (n) raw = *reinterpret_cast<const Raw*>(p);
+    } else {
+      raw = *reinterpret_cast<const Raw*>(p);
+    }
   }
   __device__ __forceinline__ void to(float* f) const {
     if constexpr (sizeof(T) == 4) {
@@ -254,6 +256,7 @@ struct Turns {
       turns[i] = a.turns[i];
       axis[i] = a.axis[i];
     }
+    if (!a.pairs && threadIdx.x == 0) axis[0] = 0;
     __syncthreads();
   }
 };
@@ -283,19 +286,22 @@ struct Units {
         gap[u] = P;
         na[u] = max(0, min(P, a.dim - at[u]));
         nb[u] = max(0, min(P, a.dim - at[u] - P));
+        if (P > 1 && !na[u]) at[u] = 0;   // a lane without a unit reads along with the first
       }
       pair[u] = unit * P;
     }
   }
-  __device__ __forceinline__ void turn_by(const RotArgs& a, const Turns& q, int64_t t, bool on, float (&c)[NU][P],
-                                          float (&s)[NU][P]) const {
+  // position: lane x holds the token's position on axis x.
+  __device__ __forceinline__ void turn_by(const Turns& q, int64_t position, float (&c)[NU][P], float (&s)[NU][P]) const {
 #pragma unroll
     for (int u = 0; u < NU; ++u)
 #pragma unroll
       for (int k = 0; k < P; ++k) {
+        const int i = turned[u] ? pair[u] + k : 0;
+        const int64_t at = __shfl_sync(0xffffffffu, position, q.axis[i]);
         c[u][k] = 1.f;
         s[u][k] = 0.f;
-        if (turned[u] && on) angle(position(a, t, q.axis[pair[u] + k]), q.turns[pair[u] + k], &c[u][k], &s[u][k]);
+        if (turned[u]) angle(at, q.turns[i], &c[u][k], &s[u][k]);
       }
   }
   // The weight's elements, as pairs.
@@ -305,7 +311,7 @@ struct Units {
     for (int u = 0; u < NU; ++u) {
 #pragma unroll
       for (int k = 0; k < 2 * P; ++k) w[u][k] = 1.f;
-      if (!p) continue;
+      if (!p || !na[u]) continue;
       Part<T, P> x, y;
       x.load(static_cast<const T*>(p) + at[u], na[u]);
       y.load(static_cast<const T*>(p) + at[u] + gap[u], nb[u]);
@@ -322,6 +328,49 @@ __device__ __forceinline__ void head_sums(float (&v)[U], int lanes) {
     for (int i = 0; i < U; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
 }
 
+// Where a warp is in its work: tokens (or pieces of their heads), in each the two
+// groups, in each batches of heads.  What comes next is fetched before what is
+// there is worked on, across batches, groups and tokens (16384 tokens of 40
+// heads: 64 us; 70 with a fresh start at each token and group).
+struct Cursor {
+  int64_t task, t;
+  int which, h0, h1;   // group, and its heads in this piece
+  int left;            // heads from this lane's on
+  bool first;          // of its token
+
+  __device__ __forceinline__ bool valid(const RotArgs& a) const { return task < a.n * a.split; }
+  // The group's range of heads in the piece; false if it has none.
+  __device__ __forceinline__ bool range(const RotArgs& a, int in_step) {
+    const int piece = a.split == 1 ? 0 : static_cast<int>(task - t * a.split);
+    const int before = which ? a.group[0].heads : 0;
+    h0 = max(0, piece * a.share - before);
+    h1 = min(a.group[which].heads, (piece + 1) * a.share - before);
+    left = h1 - h0 - in_step;
+    return h0 < h1;
+  }
+  __device__ __forceinline__ void start(const RotArgs& a, int64_t at, int in_step) {
+    task = at;
+    t = a.split == 1 ? task : task / a.split;
+    which = 0;
+    first = true;
+    if (!range(a, in_step)) {   // a piece of the second group alone
+      which = 1;
+      range(a, in_step);
+    }
+  }
+  // The next batch of `heads` heads.
+  __device__ __forceinline__ void next(const RotArgs& a, int heads, int in_step) {
+    first = false;
+    left -= heads;
+    if (left + in_step > 0) return;
+    if (which + 1 < a.groups) {
+      which = 1;
+      if (range(a, in_step)) return;
+    }
+    start(a, task + int64_t(gridDim.x) * kRotWarps, in_step);
+  }
+};
+
 // A warp takes a token's heads, both groups', or a piece of them where tokens are
 // few; `lanes` lanes hold a head, 32 / lanes heads go at once and U of those are
 // under way.  What a token's pairs are multiplied by, cosines and sines with the
@@ -337,120 +386,122 @@ __global__ void __launch_bounds__(32 * kRotWarps, 2) k_norm_rotary(const __grid_
   units.init(a, lane % lanes, lanes);
   tok::wait_before();
   tok::allow_next();
-  const int64_t tasks = a.n * a.split;
-  for (int64_t task = int64_t(blockIdx.x) * kRotWarps + threadIdx.x / 32; task < tasks;
-       task += int64_t(gridDim.x) * kRotWarps) {
-    const int64_t t = a.split == 1 ? task : task / a.split;
-    const int piece = a.split == 1 ? 0 : static_cast<int>(task - t * a.split);
-    const bool on = is_token(a, t);
-    float c[NU][P], s[NU][P];
-    units.turn_by(a, turns, t, on, c, s);
-    int before = 0;   // heads of the groups before this one
-#pragma unroll 1
-    for (int which = 0; which < a.groups; ++which) {
-      const Group& g = a.group[which];
-      const int h0 = max(0, piece * a.share - before), h1 = min(g.heads, (piece + 1) * a.share - before);
-      before += g.heads;
-      if (h0 >= h1) continue;
-      // (a, b) -> r (a ac - b bs, b bc + a as)
-      float ac[NU][P], bs[NU][P], bc[NU][P], as[NU][P];
-      {
-        float w[NU][2 * P];
-        units.template weights<T>(a, g.weight, w);
+  Part<T, P> nx[U][NU], ny[U][NU];   // heads on their way
+  int64_t position = 0;              // of the token on its way
+  auto fetch = [&](const Cursor& c) {
+    const Group& g = a.group[c.which];
+    const T* base = static_cast<const T*>(g.in.p) + c.t * g.in.stride + (c.h1 - first - c.left) * g.in.head;
+    const T* in = base + first * g.in.head;
+    if (c.first) position = lane_position(a, c.t, lane);
 #pragma unroll
-        for (int u = 0; u < NU; ++u)
+    for (int v = 0; v < U; ++v, in += step * g.in.head) {
+      const T* head = v * step < c.left ? in : base;   // behind the last head: one that is there
 #pragma unroll
-          for (int k = 0; k < P; ++k) {
-            ac[u][k] = w[u][2 * k] * c[u][k];
-            as[u][k] = w[u][2 * k] * s[u][k];
-            bc[u][k] = w[u][2 * k + 1] * c[u][k];
-            bs[u][k] = w[u][2 * k + 1] * s[u][k];
-          }
-      }
-      const int64_t iby = g.in.head * step, oby = g.out.head * step;
-      const T* in = static_cast<const T*>(g.in.p) + t * g.in.stride + (h0 + first) * g.in.head;
-      T* out = static_cast<T*>(const_cast<void*>(g.out.p)) + t * g.out.stride + (h0 + first) * g.out.head;
-      Part<T, P> x[U][NU], y[U][NU], nx[U][NU], ny[U][NU];   // these heads, and the next ones on their way
-      auto fetch = [&](int left) {
-#pragma unroll
-        for (int v = 0; v < U; ++v, in += iby) {
-          const bool here = on && v * step < left;
-#pragma unroll
-          for (int u = 0; u < NU; ++u) {
-            const T* q = in + units.at[u];
-            nx[v][u].load(q, here ? units.na[u] : 0);
-            ny[v][u].load(q + units.gap[u], here ? units.nb[u] : 0);
-          }
-        }
-      };
-      fetch(h1 - h0 - first);
-#pragma unroll 1
-      for (int left = h1 - h0 - first; left + first > 0; left -= U * step) {
-#pragma unroll
-        for (int v = 0; v < U; ++v)
-#pragma unroll
-          for (int u = 0; u < NU; ++u) {
-            x[v][u] = nx[v][u];
-            y[v][u] = ny[v][u];
-          }
-        fetch(left - U * step);
-        float r[U];
-        if (S::norm(a.norm)) {
-#pragma unroll
-          for (int v = 0; v < U; ++v) {
-            r[v] = 0.f;
-#pragma unroll
-            for (int u = 0; u < NU; ++u) {
-              float f[2 * P];
-              x[v][u].to(f);
-              y[v][u].to(f + P);
-#pragma unroll
-              for (int k = 0; k < 2 * P; ++k) r[v] += f[k] * f[k];
-            }
-          }
-          head_sums<U>(r, lanes);
-#pragma unroll
-          for (int v = 0; v < U; ++v) r[v] = on ? rsqrtf(r[v] * a.inv_dim + a.eps) : 0.f;
-        } else {
-#pragma unroll
-          for (int v = 0; v < U; ++v) r[v] = 1.f;
-        }
-#pragma unroll
-        for (int v = 0; v < U; ++v, out += oby) {
-          if (v * step >= left) continue;
-#pragma unroll
-          for (int u = 0; u < NU; ++u) {
-            const bool in_pairs = units.turned[u] && inter;
-            float f[2 * P], o[2 * P];
-            to_pairs<T, S>(x[v][u], y[v][u], in_pairs, f);
-#pragma unroll
-            for (int k = 0; k < P; ++k) {
-              o[2 * k] = r[v] * (f[2 * k] * ac[u][k] - f[2 * k + 1] * bs[u][k]);
-              o[2 * k + 1] = r[v] * (f[2 * k + 1] * bc[u][k] + f[2 * k] * as[u][k]);
-            }
-            if (!units.turned[u]) {   // neighbours, not a pair: an infinite one leaves the other alone
-#pragma unroll
-              for (int k = 0; k < P; ++k) {
-                o[2 * k] = r[v] * (f[2 * k] * ac[u][k]);
-                o[2 * k + 1] = r[v] * (f[2 * k + 1] * bc[u][k]);
-              }
-            }
-            Part<T, P> p, q;
-            from_pairs<T, S>(p, q, in_pairs, o);
-            T* to = out + units.at[u];
-            p.store(to, units.na[u]);
-            q.store(to + units.gap[u], units.nb[u]);
-          }
-        }
+      for (int u = 0; u < NU; ++u) {
+        const T* q = head + units.at[u];
+        nx[v][u].load(q, units.na[u]);
+        ny[v][u].load(q + units.gap[u], units.nb[u]);
       }
     }
-  }
+  };
+  Cursor now, then;
+  then.start(a, int64_t(blockIdx.x) * kRotWarps + threadIdx.x / 32, first);
+  if (!then.valid(a)) return;
+  fetch(then);
+  float c[NU][P], s[NU][P];
+  float ac[NU][P], bs[NU][P], bc[NU][P], as[NU][P];   // (a, b) -> r (a ac - b bs, b bc + a as)
+  bool on = true;
+  do {
+    now = then;
+    const int64_t here = position;
+    Part<T, P> x[U][NU], y[U][NU];
+#pragma unroll
+    for (int v = 0; v < U; ++v)
+#pragma unroll
+      for (int u = 0; u < NU; ++u) {
+        x[v][u] = nx[v][u];
+        y[v][u] = ny[v][u];
+      }
+    then.next(a, U * step, first);
+    if (then.valid(a)) fetch(then);
+    const Group& g = a.group[now.which];
+    if (now.first) {
+      on = __all_sync(0xffffffffu, here >= 0);
+      units.turn_by(turns, here, c, s);
+    }
+    if (now.first || now.left + first == now.h1 - now.h0) {
+      float w[NU][2 * P];
+      units.template weights<T>(a, g.weight, w);
+#pragma unroll
+      for (int u = 0; u < NU; ++u)
+#pragma unroll
+        for (int k = 0; k < P; ++k) {
+          ac[u][k] = w[u][2 * k] * c[u][k];
+          as[u][k] = w[u][2 * k] * s[u][k];
+          bc[u][k] = w[u][2 * k + 1] * c[u][k];
+          bs[u][k] = w[u][2 * k + 1] * s[u][k];
+        }
+    }
+    float r[U];
+    if (S::norm(a.norm)) {
+#pragma unroll
+      for (int v = 0; v < U; ++v) {
+        r[v] = 0.f;
+#pragma unroll
+        for (int u = 0; u < NU; ++u) {
+          float f[2 * P];
+          x[v][u].to(f);
+          y[v][u].to(f + P);
+#pragma unroll
+          for (int k = 0; k < 2 * P; ++k) r[v] += f[k] * f[k];
+        }
+        if (P > 1 && !units.na[0]) r[v] = 0.f;   // (NU is 1)
+      }
+      head_sums<U>(r, lanes);
+#pragma unroll
+      for (int v = 0; v < U; ++v) r[v] = rsqrtf(r[v] * a.inv_dim + a.eps);
+    } else {
+#pragma unroll
+      for (int v = 0; v < U; ++v) r[v] = 1.f;
+    }
+    T* out = static_cast<T*>(const_cast<void*>(g.out.p)) + now.t * g.out.stride + (now.h1 - now.left) * g.out.head;
+#pragma unroll
+    for (int v = 0; v < U; ++v, out += step * g.out.head) {
+      if (v * step >= now.left) continue;
+#pragma unroll
+      for (int u = 0; u < NU; ++u) {
+        const bool in_pairs = units.turned[u] && inter;
+        float f[2 * P], o[2 * P];
+        to_pairs<T, S>(x[v][u], y[v][u], in_pairs, f);
+#pragma unroll
+        for (int k = 0; k < P; ++k) {
+          o[2 * k] = r[v] * (f[2 * k] * ac[u][k] - f[2 * k + 1] * bs[u][k]);
+          o[2 * k + 1] = r[v] * (f[2 * k + 1] * bc[u][k] + f[2 * k] * as[u][k]);
+        }
+        if (!units.turned[u]) {   // neighbours, not a pair: an infinite one leaves the other alone
+#pragma unroll
+          for (int k = 0; k < P; ++k) {
+            o[2 * k] = r[v] * (f[2 * k] * ac[u][k]);
+            o[2 * k + 1] = r[v] * (f[2 * k + 1] * bc[u][k]);
+          }
+        }
+        Part<T, P> p, q;
+        from_pairs<T, S>(p, q, in_pairs, o);
+        if (!on) p = q = Part<T, P>{};
+        T* to = out + units.at[u];
+        p.store(to, units.na[u]);
+        q.store(to + units.gap[u], units.nb[u]);
+      }
+    }
+  } while (then.valid(a));
 }
 
 // The gradient: g = dout turned back; with r = 1 / rms and n = x r,
 //     dw += g n,   dx = r (g w - n mean(g w n)).
 // A lane keeps its columns' dw over all tokens of its warp; blocks leave
-// partial sums, which k_norm_join adds in order.
+// partial sums, which k_norm_join adds in order.  (Fetching ahead across tokens, as
+// k_norm_rotary does, took longer here: 124 us with the groups one after the
+// other, 150 with sums of both chosen from, 115 this way.)
 template <typename T, class S>
 __global__ void __launch_bounds__(32 * kRotWarps, 2) k_norm_rotary_grad(const __grid_constant__ RotArgs a, int lanes) {
   constexpr int P = S::P, NU = S::NU, U = NU > 1 ? 1 : 2;
@@ -469,9 +520,10 @@ __global__ void __launch_bounds__(32 * kRotWarps, 2) k_norm_rotary_grad(const __
   for (int64_t task = int64_t(blockIdx.x) * kRotWarps + warp; task < tasks; task += int64_t(gridDim.x) * kRotWarps) {
     const int64_t t = a.split == 1 ? task : task / a.split;
     const int piece = a.split == 1 ? 0 : static_cast<int>(task - t * a.split);
-    const bool on = is_token(a, t);
+    const int64_t position = lane_position(a, t, lane);
+    const bool on = __all_sync(0xffffffffu, position >= 0);
     float c[NU][P], s[NU][P];
-    units.turn_by(a, turns, t, on, c, s);
+    units.turn_by(turns, position, c, s);
 #pragma unroll
     for (int which = 0; which < 2; ++which) {   // unrolled: dw stays in registers
       const Group& g = a.group[which];
@@ -481,23 +533,24 @@ __global__ void __launch_bounds__(32 * kRotWarps, 2) k_norm_rotary_grad(const __
       float w[NU][2 * P];
       units.template weights<T>(a, g.weight, w);
       const int64_t dby = g.in.head * step, xby = g.x.head * step, oby = g.out.head * step;
-      const T* din = static_cast<const T*>(g.in.p) + t * g.in.stride + (h0 + first) * g.in.head;
-      const T* xin = static_cast<const T*>(g.x.p) + t * g.x.stride + (h0 + first) * g.x.head;
+      const T* dbase = static_cast<const T*>(g.in.p) + t * g.in.stride + h0 * g.in.head;   // for what is behind the last head
+      const T* xbase = static_cast<const T*>(g.x.p) + t * g.x.stride + h0 * g.x.head;
+      const T *din = dbase + first * g.in.head, *xin = xbase + first * g.x.head;
       T* out = static_cast<T*>(const_cast<void*>(g.out.p)) + t * g.out.stride + (h0 + first) * g.out.head;
       Part<T, P> p[U][NU], q[U][NU], y[U][NU], z[U][NU];   // heads on their way
       auto fetch = [&](int left) {
 #pragma unroll
         for (int v = 0; v < U; ++v, din += dby, xin += xby) {
-          const bool here = on && v * step < left;
+          const bool here = v * step < left;
 #pragma unroll
           for (int u = 0; u < NU; ++u) {
-            const T* i = din + units.at[u];
-            p[v][u].load(i, here ? units.na[u] : 0);
-            q[v][u].load(i + units.gap[u], here ? units.nb[u] : 0);
+            const T* i = (here ? din : dbase) + units.at[u];
+            p[v][u].load(i, units.na[u]);
+            q[v][u].load(i + units.gap[u], units.nb[u]);
             if (S::norm(a.norm)) {
-              i = xin + units.at[u];
-              y[v][u].load(i, here ? units.na[u] : 0);
-              z[v][u].load(i + units.gap[u], here ? units.nb[u] : 0);
+              i = (here ? xin : xbase) + units.at[u];
+              y[v][u].load(i, units.na[u]);
+              z[v][u].load(i + units.gap[u], units.nb[u]);
             }
           }
         }
@@ -526,7 +579,7 @@ __global__ void __launch_bounds__(32 * kRotWarps, 2) k_norm_rotary_grad(const __
               if (S::norm(a.norm)) to_pairs<T, S>(y[v][u], z[v][u], in_pairs, x[v][u]);
             }
         }
-        fetch(left - U * step);
+        if (left + first > U * step) fetch(left - U * step);
         if (S::norm(a.norm)) {
           float r[U], m[U];
 #pragma unroll
@@ -539,19 +592,21 @@ __global__ void __launch_bounds__(32 * kRotWarps, 2) k_norm_rotary_grad(const __
                 r[v] += x[v][u][k] * x[v][u][k];
                 m[v] += x[v][u][k] * (d[v][u][k] * w[u][k]);
               }
+            if (P > 1 && !units.na[0]) r[v] = m[v] = 0.f;   // (NU is 1)
           }
           head_sums<U>(r, lanes);
           head_sums<U>(m, lanes);
 #pragma unroll
           for (int v = 0; v < U; ++v) {
-            r[v] = on ? rsqrtf(r[v] * a.inv_dim + a.eps) : 0.f;
+            r[v] = rsqrtf(r[v] * a.inv_dim + a.eps);
             m[v] = m[v] * r[v] * a.inv_dim;   // mean of g w n
+            const bool counts = on && v * step < left;
 #pragma unroll
             for (int u = 0; u < NU; ++u)
 #pragma unroll
               for (int k = 0; k < 2 * P; ++k) {
                 const float n = x[v][u][k] * r[v];
-                if (v * step < left) dw[which][u][k] += d[v][u][k] * n;
+                if (counts) dw[which][u][k] += d[v][u][k] * n;
                 d[v][u][k] = r[v] * (d[v][u][k] * w[u][k] - n * m[v]);
               }
           }
@@ -561,11 +616,12 @@ __global__ void __launch_bounds__(32 * kRotWarps, 2) k_norm_rotary_grad(const __
           if (v * step >= left) continue;
 #pragma unroll
           for (int u = 0; u < NU; ++u) {
-            Part<T, P> p, q;
-            from_pairs<T, S>(p, q, units.turned[u] && inter, d[v][u]);
+            Part<T, P> i, j;
+            from_pairs<T, S>(i, j, units.turned[u] && inter, d[v][u]);
+            if (!on) i = j = Part<T, P>{};
             T* to = out + units.at[u];
-            p.store(to, units.na[u]);
-            q.store(to + units.gap[u], units.nb[u]);
+            i.store(to, units.na[u]);
+            j.store(to + units.gap[u], units.nb[u]);
           }
         }
       }
