@@ -18,7 +18,6 @@ constexpr int kSms = 152;
 // ------------------------------------------------------------------ dropout
 
 constexpr int kDropThreads = 128;
-constexpr int kDropRows = 1;   // rows a thread has under way
 
 struct DropArgs {
   const void* x;
@@ -56,38 +55,34 @@ __device__ __forceinline__ void store8(T* p, int left, const float* f) {
   }
 }
 
-// blockDim.x threads along a row, eight columns (one draw of 128 bits) each.
+// blockDim.x threads along a row, eight columns (one draw of 128 bits) each.  Bound
+// by memory: 16384 x 4096 bf16 with a residual in 65 us, 6.2 TB/s of reads and
+// writes; issue slots are 56% busy behind it.  One row per thread and blocks of 128
+// threads were the best of a sweep (two rows 84 us, four 121; 256 threads 72).
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kDropThreads) k_dropout(const DropArgs a) {
   tok::wait_before();
   tok::allow_next();
   Draw draw;
   draw.init(a.d);
-  const int64_t r0 = (int64_t(blockIdx.x) * blockDim.y + threadIdx.y) * kDropRows;
+  const int64_t r = int64_t(blockIdx.x) * blockDim.y + threadIdx.y;
+  if (r >= a.rows) return;
   const int groups = (a.cols + 7) / 8;
   for (int g = threadIdx.x; g < groups; g += blockDim.x) {
     const int c = g * 8, left = a.cols - c;
-    float f[kDropRows][8], add[kDropRows][8];
+    float f[8], add[8];
+    load8<T, VEC>(static_cast<const T*>(a.x) + r * a.xs + c, left, f);
+    if (a.residual) load8<T, VEC>(static_cast<const T*>(a.residual) + r * a.rs + c, left, add);
+    if (a.d.least) {
+      const uint4 w = draw.at(uint32_t(r), g, a.d.site);
 #pragma unroll
-    for (int q = 0; q < kDropRows; ++q) {
-      if (r0 + q >= a.rows) continue;
-      load8<T, VEC>(static_cast<const T*>(a.x) + (r0 + q) * a.xs + c, left, f[q]);
-      if (a.residual) load8<T, VEC>(static_cast<const T*>(a.residual) + (r0 + q) * a.rs + c, left, add[q]);
+      for (int j = 0; j < 8; ++j) f[j] = lay::dropped(f[j], lay::draw_of(w, j), a.d);
     }
+    if (a.residual) {
 #pragma unroll
-    for (int q = 0; q < kDropRows; ++q) {
-      if (r0 + q >= a.rows) continue;
-      if (a.d.least) {
-        const uint4 w = draw.at(uint32_t(r0 + q), g, a.d.site);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[q][j] = lay::dropped(f[q][j], lay::draw_of(w, j), a.d);
-      }
-      if (a.residual) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[q][j] += add[q][j];
-      }
-      store8<T, VEC>(static_cast<T*>(a.out) + (r0 + q) * a.os + c, left, f[q]);
+      for (int j = 0; j < 8; ++j) f[j] += add[j];
     }
+    store8<T, VEC>(static_cast<T*>(a.out) + r * a.os + c, left, f);
   }
 }
 
@@ -102,11 +97,18 @@ cudaError_t launch_dropout(const DropArgs& a, cudaStream_t s) {
   int tx = 1;
   while (tx < groups && tx < kDropThreads) tx *= 2;
   const dim3 block(tx, kDropThreads / tx);
-  const unsigned grid = unsigned((a.rows + int64_t(block.y) * kDropRows - 1) / (int64_t(block.y) * kDropRows));
+  const unsigned grid = unsigned((a.rows + block.y - 1) / block.y);
   return launch(vec ? k_dropout<T, true> : k_dropout<T, false>, grid, block, 1, true, s, 0, a);
 }
 
 // ------------------------------------------------------------------ norm and rotation
+//
+// For a head x with weight w, position p and frequencies f:
+//     n = x / sqrt(mean x^2 + eps) * w,   (a, b) -> (a cos - b sin, b cos + a sin) with the angle p f.
+// Both directions are bound by memory, each element moved once (16384 tokens of 40
+// heads of 128 bf16: 64 us, 5.2 TB/s; the gradients 113 us, 4.4 TB/s, issue slots 66%
+// busy), and short of it by latency: 16 warps per SM hold what is on its way in
+// registers.
 
 constexpr int kMaxPairs = MUON_MAX_HEAD_DIM / 2;
 constexpr int kRotWarps = 8;
@@ -133,7 +135,9 @@ struct Group {
 template <int P_, int NU_, bool FIXED_, bool NORM_, bool INTER_>
 struct Shape {
   static constexpr int P = P_, NU = NU_;
-  static constexpr bool kFixed = FIXED_;   // norm and order of pairs known when compiled
+  // Norm and order of pairs known when compiled, and every lane with a turned unit (all
+  // of a head is turned, and it is a power of two long).
+  static constexpr bool kFixed = FIXED_;
   static __device__ __forceinline__ bool norm(int n) { return kFixed ? NORM_ : n != 0; }
   static __device__ __forceinline__ bool inter(int i) { return kFixed ? INTER_ : i != 0; }
 };
@@ -265,6 +269,9 @@ struct Turns {
 template <class S>
 struct Units {
   static constexpr int P = S::P, NU = S::NU;
+  __device__ __forceinline__ bool turns(int u) const { return S::kFixed || turned[u]; }
+  __device__ __forceinline__ int first_half(int u) const { return S::kFixed ? P : na[u]; }
+  __device__ __forceinline__ int second_half(int u) const { return S::kFixed ? P : nb[u]; }
   int at[NU], gap[NU];     // first element, and how far behind it the other P are
   int na[NU], nb[NU];      // how many there are of either
   bool turned[NU];
@@ -399,8 +406,8 @@ __global__ void __launch_bounds__(32 * kRotWarps, 2) k_norm_rotary(const __grid_
 #pragma unroll
       for (int u = 0; u < NU; ++u) {
         const T* q = head + units.at[u];
-        nx[v][u].load(q, units.na[u]);
-        ny[v][u].load(q + units.gap[u], units.nb[u]);
+        nx[v][u].load(q, units.first_half(u));
+        ny[v][u].load(q + units.gap[u], units.second_half(u));
       }
     }
   };
@@ -425,9 +432,21 @@ __global__ void __launch_bounds__(32 * kRotWarps, 2) k_norm_rotary(const __grid_
     then.next(a, U * step, first);
     if (then.valid(a)) fetch(then);
     const Group& g = a.group[now.which];
+    T* out = static_cast<T*>(const_cast<void*>(g.out.p)) + now.t * g.out.stride + (now.h1 - now.left) * g.out.head;
     if (now.first) {
       on = __all_sync(0xffffffffu, here >= 0);
       units.turn_by(turns, here, c, s);
+    }
+    if (!on) {   // the warp's
+#pragma unroll
+      for (int v = 0; v < U; ++v, out += step * g.out.head)
+#pragma unroll
+        for (int u = 0; u < NU; ++u) {
+          const Part<T, P> zero{};
+          zero.store(out + units.at[u], v * step < now.left ? units.first_half(u) : 0);
+          zero.store(out + units.at[u] + units.gap[u], v * step < now.left ? units.second_half(u) : 0);
+        }
+      continue;
     }
     if (now.first || now.left + first == now.h1 - now.h0) {
       float w[NU][2 * P];
@@ -455,7 +474,7 @@ __global__ void __launch_bounds__(32 * kRotWarps, 2) k_norm_rotary(const __grid_
 #pragma unroll
           for (int k = 0; k < 2 * P; ++k) r[v] += f[k] * f[k];
         }
-        if (P > 1 && !units.na[0]) r[v] = 0.f;   // (NU is 1)
+        if (P > 1 && !units.first_half(0)) r[v] = 0.f;   // (NU is 1)
       }
       head_sums<U>(r, lanes);
 #pragma unroll
@@ -464,13 +483,12 @@ __global__ void __launch_bounds__(32 * kRotWarps, 2) k_norm_rotary(const __grid_
 #pragma unroll
       for (int v = 0; v < U; ++v) r[v] = 1.f;
     }
-    T* out = static_cast<T*>(const_cast<void*>(g.out.p)) + now.t * g.out.stride + (now.h1 - now.left) * g.out.head;
 #pragma unroll
     for (int v = 0; v < U; ++v, out += step * g.out.head) {
       if (v * step >= now.left) continue;
 #pragma unroll
       for (int u = 0; u < NU; ++u) {
-        const bool in_pairs = units.turned[u] && inter;
+        const bool in_pairs = units.turns(u) && inter;
         float f[2 * P], o[2 * P];
         to_pairs<T, S>(x[v][u], y[v][u], in_pairs, f);
 #pragma unroll
@@ -478,7 +496,7 @@ __global__ void __launch_bounds__(32 * kRotWarps, 2) k_norm_rotary(const __grid_
           o[2 * k] = r[v] * (f[2 * k] * ac[u][k] - f[2 * k + 1] * bs[u][k]);
           o[2 * k + 1] = r[v] * (f[2 * k + 1] * bc[u][k] + f[2 * k] * as[u][k]);
         }
-        if (!units.turned[u]) {   // neighbours, not a pair: an infinite one leaves the other alone
+        if (!units.turns(u)) {   // neighbours, not a pair: an infinite one leaves the other alone
 #pragma unroll
           for (int k = 0; k < P; ++k) {
             o[2 * k] = r[v] * (f[2 * k] * ac[u][k]);
@@ -487,10 +505,9 @@ __global__ void __launch_bounds__(32 * kRotWarps, 2) k_norm_rotary(const __grid_
         }
         Part<T, P> p, q;
         from_pairs<T, S>(p, q, in_pairs, o);
-        if (!on) p = q = Part<T, P>{};
         T* to = out + units.at[u];
-        p.store(to, units.na[u]);
-        q.store(to + units.gap[u], units.nb[u]);
+        p.store(to, units.first_half(u));
+        q.store(to + units.gap[u], units.second_half(u));
       }
     }
   } while (then.valid(a));
@@ -545,12 +562,12 @@ __global__ void __launch_bounds__(32 * kRotWarps, 2) k_norm_rotary_grad(const __
 #pragma unroll
           for (int u = 0; u < NU; ++u) {
             const T* i = (here ? din : dbase) + units.at[u];
-            p[v][u].load(i, units.na[u]);
-            q[v][u].load(i + units.gap[u], units.nb[u]);
+            p[v][u].load(i, units.first_half(u));
+            q[v][u].load(i + units.gap[u], units.second_half(u));
             if (S::norm(a.norm)) {
               i = (here ? xin : xbase) + units.at[u];
-              y[v][u].load(i, units.na[u]);
-              z[v][u].load(i + units.gap[u], units.nb[u]);
+              y[v][u].load(i, units.first_half(u));
+              z[v][u].load(i + units.gap[u], units.second_half(u));
             }
           }
         }
@@ -564,7 +581,7 @@ __global__ void __launch_bounds__(32 * kRotWarps, 2) k_norm_rotary_grad(const __
           for (int v = 0; v < U; ++v)
 #pragma unroll
             for (int u = 0; u < NU; ++u) {
-              const bool in_pairs = units.turned[u] && inter;
+              const bool in_pairs = units.turns(u) && inter;
               float f[2 * P];
               to_pairs<T, S>(p[v][u], q[v][u], in_pairs, f);
 #pragma unroll
@@ -572,7 +589,7 @@ __global__ void __launch_bounds__(32 * kRotWarps, 2) k_norm_rotary_grad(const __
                 d[v][u][2 * k] = f[2 * k] * c[u][k] + f[2 * k + 1] * s[u][k];
                 d[v][u][2 * k + 1] = f[2 * k + 1] * c[u][k] - f[2 * k] * s[u][k];
               }
-              if (!units.turned[u]) {
+              if (!units.turns(u)) {
 #pragma unroll
                 for (int k = 0; k < 2 * P; ++k) d[v][u][k] = f[k];
               }
@@ -592,7 +609,7 @@ __global__ void __launch_bounds__(32 * kRotWarps, 2) k_norm_rotary_grad(const __
                 r[v] += x[v][u][k] * x[v][u][k];
                 m[v] += x[v][u][k] * (d[v][u][k] * w[u][k]);
               }
-            if (P > 1 && !units.na[0]) r[v] = m[v] = 0.f;   // (NU is 1)
+            if (P > 1 && !units.first_half(0)) r[v] = m[v] = 0.f;   // (NU is 1)
           }
           head_sums<U>(r, lanes);
           head_sums<U>(m, lanes);
@@ -617,11 +634,11 @@ __global__ void __launch_bounds__(32 * kRotWarps, 2) k_norm_rotary_grad(const __
 #pragma unroll
           for (int u = 0; u < NU; ++u) {
             Part<T, P> i, j;
-            from_pairs<T, S>(i, j, units.turned[u] && inter, d[v][u]);
+            from_pairs<T, S>(i, j, units.turns(u) && inter, d[v][u]);
             if (!on) i = j = Part<T, P>{};
             T* to = out + units.at[u];
-            i.store(to, units.na[u]);
-            j.store(to + units.gap[u], units.nb[u]);
+            i.store(to, units.first_half(u));
+            j.store(to + units.gap[u], units.second_half(u));
           }
         }
       }
@@ -635,14 +652,14 @@ __global__ void __launch_bounds__(32 * kRotWarps, 2) k_norm_rotary_grad(const __
     __syncthreads();
 #pragma unroll
     for (int u = 0; u < NU; ++u) {
-      const bool in_pairs = units.turned[u] && inter;
+      const bool in_pairs = units.turns(u) && inter;
 #pragma unroll
       for (int k = 0; k < 2 * P; ++k) {
         float v = dw[which][u][k];
         for (int o = lanes; o < 32; o *= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
         // the k-th of the lane's values is one of pair k / 2
         const int j = in_pairs ? k : k % 2 * P + k / 2, i = units.at[u] + (j < P ? j : units.gap[u] + (j - P));
-        const bool there = j < P ? j < units.na[u] : j - P < units.nb[u];
+        const bool there = j < P ? j < units.first_half(u) : j - P < units.second_half(u);
         if (first == 0 && there) sums[warp][i] = v;
       }
     }
@@ -815,10 +832,11 @@ cudaError_t launch_heads(RotArgs& a, int blocks, cudaStream_t s) {
   const int per = fits(a, 4, sizeof(T)) ? 4 : fits(a, 2, sizeof(T)) && a.dim <= 128 ? 2 : 1;
   const int lanes = lanes_of(a, per);
   split_heads(&a, 32 / lanes);
+  const bool whole = a.norm && 2 * a.pairs == a.dim && lanes * 8 == a.dim;
   void (*k)(RotArgs, int) = KERNEL<T, Shape<1, 4, false, false, false>>::kernel;
   if (per == 2) k = KERNEL<T, Shape<2, 1, false, false, false>>::kernel;
-  else if (per == 4 && a.norm && a.interleaved) k = KERNEL<T, Shape<4, 1, true, true, true>>::kernel;
-  else if (per == 4 && a.norm) k = KERNEL<T, Shape<4, 1, true, true, false>>::kernel;
+  else if (per == 4 && whole && a.interleaved) k = KERNEL<T, Shape<4, 1, true, true, true>>::kernel;
+  else if (per == 4 && whole) k = KERNEL<T, Shape<4, 1, true, true, false>>::kernel;
   else if (per == 4) k = KERNEL<T, Shape<4, 1, false, false, false>>::kernel;
   if (!blocks) blocks = int(std::min<int64_t>((a.n * a.split + kRotWarps - 1) / kRotWarps, 2 * kSms));
   return launch(k, unsigned(blocks), 32 * kRotWarps, 1, true, s, 0, a, lanes);

@@ -2,6 +2,26 @@
 // dropout and residual, and its gradients: dx through the activation before the
 // layer, and the weight's and bias's summed straight into the flat,
 // partitioned FP32 accumulation buffer.
+//
+//     u = x W^T + b,  out = residual + drop(act(u));
+//     dx = (d W) act'(pre),  accum[W] (+)= s d^T x,  accum[b] (+)= s sum d.
+//
+// All three products are bf16 x bf16 with FP32 sums on the tensor cores; an
+// operand is read as it lies, with its k contiguous or its rows.  Which kernel
+// takes a product is a matter of its sizes (plan_of, plan_few, takes_rows):
+//   k_linear_pair   tiles of 256 x 256 or 256 x 128 on pairs of SMs, persistent.
+//                   Bound by the tensor cores (92% active): 8192 x 4096 -> 14336 in
+//                   495 us, 1945 TFLOP/s, as fast as the library's product alone;
+//                   in long runs by the power limit (604 us with silu and its
+//                   argument kept).
+//   k_linear_split  tiles of 128 x 128 on single SMs, the K blocks shared out in a
+//                   cluster, for products of few tiles; tiles of 128 features x
+//                   32 or 64 tokens for few tokens (4096 -> 14336, 32 tokens 23 us,
+//                   5.1 TB/s of weight).
+//   k_linear_rows   one or two tokens: multiply-adds over the weight's rows (one
+//                   token through 4096 -> 14336 20 us, 5.8 TB/s).
+//   k_linear_pack   operands whose rows do not start on 16 bytes, copied first.
+//   k_bias_grad     sums of dout's columns.
 #include <type_traits>
 
 #include "layers.cuh"
@@ -1576,14 +1596,17 @@ cudaError_t launch_split(const One<E>& w, int splits, int late, cudaStream_t s) 
                                                     SplitShape<BN>::kShared, s, w, splits, late, err);
 }
 
-// One product.
+// A product's kernel arguments; false: the driver refuses a map.
 template <class E>
-cudaError_t run_one(const Plan& plan, const Operand& a, bool a_mn, const Operand& b, bool b_mn, const E& e, int late,
-                    cudaStream_t s) {
-  static One<E> w;   // large; the caller holds the library lock
-  w.e = e;
-  if (!make_product(plan, a, a_mn, b, b_mn, &w.p)) return cudaErrorInvalidValue;
-  w.tiles = w.p.tiles_m * w.p.tiles_n;
+bool prepare(const Plan& plan, const Operand& a, bool a_mn, const Operand& b, bool b_mn, const E& e, One<E>* w) {
+  w->e = e;
+  if (!make_product(plan, a, a_mn, b, b_mn, &w->p)) return false;
+  w->tiles = w->p.tiles_m * w->p.tiles_n;
+  return true;
+}
+
+template <class E>
+cudaError_t launch_one(const Plan& plan, const One<E>& w, int late, cudaStream_t s) {
   if (plan.pairs) return plan.bn == 256 ? launch_pair<256>(w, late, s) : launch_pair<128>(w, late, s);
   if constexpr (!std::is_same_v<E, WeightGrad>) {
     if (plan.swap && plan.bn == 32) return launch_split<32, true>(w, plan.splits, late, s);
@@ -1791,10 +1814,14 @@ extern "C" int muon_linear(const muon_linear_args_t* args, void* workspace, size
     Packs packs{};
     x.pack(&at, &packs);
     w.pack(&at, &packs);
+    static One<Forward> product;   // large; this call holds the library lock
+    const bool few = T <= kFewTokens;
+    const Plan plan = few ? plan_few(T, N, K) : plan_of(T, N, K, false);
+    if (!(few ? prepare(plan, w, false, x, false, f, &product) : prepare(plan, x, false, w, false, f, &product)))
+      return fail_with(MUON_ERR_CUDA, "the driver refuses a map of x or weight");
     cudaError_t e = launch_packs(packs, s, &launches);
     if (e != cudaSuccess) return lay::end_call(launches, e);
-    e = T <= kFewTokens ? run_one(plan_few(T, N, K), w, false, x, false, f, 0, s)
-                        : run_one(plan_of(T, N, K, false), x, false, w, false, f, 0, s);
+    e = launch_one(plan, product, 0, s);
     return lay::end_call(launches + 1, e);
   });
 }
@@ -1841,8 +1868,6 @@ extern "C" int muon_linear_grad(const muon_linear_grad_args_t* args, void* works
     o.dout.pack(&at, &packs);
     o.weight.pack(&at, &packs);
     o.x.pack(&at, &packs);
-    cudaError_t e = launch_packs(packs, s, &launches);
-    if (e != cudaSuccess) return lay::end_call(launches, e);
     InputGrad f{};
     auto matrix = [&](const void* p, int64_t stride) {
       return Matrix{const_cast<void*>(p), stride, 0, !misaligned(p, 16) && (T <= 1 || stride % 8 == 0)};
@@ -1860,6 +1885,22 @@ extern "C" int muon_linear_grad(const muon_linear_grad_args_t* args, void* works
     g.scale = a.scale;
     if (a.param) g.sg = places.weight;
     const bool dx = a.dx && T, dw = a.param, few = T <= kFewTokens;
+    Plan plans[2];
+    static One<InputGrad> first;    // large; this call holds the library lock
+    static One<WeightGrad> second;
+    bool fine = true;
+    if (dx) {
+      plans[0] = few ? plan_few(T, K, N) : plan_of(T, K, N, false);
+      fine = few ? prepare(plans[0], o.weight, true, o.dout, false, f, &first)
+                 : prepare(plans[0], o.dout, false, o.weight, true, f, &first);
+    }
+    if (dw && fine) {
+      plans[1] = plan_of(N, K, T, true);
+      fine = prepare(plans[1], o.dout, true, o.x, true, g, &second);
+    }
+    if (!fine) return fail_with(MUON_ERR_CUDA, "the driver refuses a map of an operand");
+    cudaError_t e = launch_packs(packs, s, &launches);
+    if (e != cudaSuccess) return lay::end_call(launches, e);
     // The call's kernels depend on copies of the operands alone: behind the first
     // that waits for those, they run beside one another.
     int late = 0;
@@ -1871,13 +1912,12 @@ extern "C" int muon_linear_grad(const muon_linear_grad_args_t* args, void* works
       late = 1;
     }
     if (dx) {
-      e = few ? run_one(plan_few(T, K, N), o.weight, true, o.dout, false, f, late, s)
-              : run_one(plan_of(T, K, N, false), o.dout, false, o.weight, true, f, late, s);
+      if ((e = launch_one(plans[0], first, late, s)) != cudaSuccess) return lay::end_call(launches, e);
       ++launches;
       late = 1;
     }
-    if (dw && e == cudaSuccess) {
-      e = run_one(plan_of(N, K, T, true), o.dout, true, o.x, true, g, late, s);
+    if (dw) {
+      e = launch_one(plans[1], second, late, s);
       ++launches;
     }
     return lay::end_call(launches, e);

@@ -111,6 +111,96 @@ def test_forward(T, K, N, way):
         close(u, pre, pre_bound, "pre")
 
 
+LARGE = [(2304, 2112, 2568), (4100, 1096, 4352), (70, 5000, 9000), (1500, 4608, 1160), (12000, 136, 520)]
+
+
+@pytest.mark.parametrize("way", [0, 3, 5])
+@pytest.mark.parametrize("T,K,N", LARGE)
+def test_forward_of_many_tiles(T, K, N, way):
+    """More tiles than pairs of SMs, sums in several pieces, results held while the next tile is formed."""
+    way = WAYS[way]
+    x, w, bias, residual, out = forward_case(T, K, N, way, T + K + N)
+    rng, rate, kind = generator(), way.get("rate", 0.0), way.get("act")
+    r = nsg.linear(x, w, bias, kind, residual, rate, rng, 9, out_dtype=out, pre=way.get("pre", False))
+    y, u = r if way.get("pre") else (r, None)
+    want, bound, pre, pre_bound = forward_form(x, w, bias, kind, residual, rate, rng, 9, out)
+    close(y, want, bound, "out")
+    if u is not None:
+        close(u, pre, pre_bound, "pre")
+
+
+@pytest.mark.parametrize("parts,overwrite", [(0, False), (8, True)])
+@pytest.mark.parametrize("T,K,N", LARGE + [(40, 2568, 4352), (1, 1032, 2056)])
+def test_gradients_of_many_tiles(T, K, N, parts, overwrite):
+    x, dout, w = normal(1, (T, K)), normal(2, (T, N), 0.1), normal(3, (N, K), 1 / math.sqrt(K))
+    pre = normal(4, (T, K))
+    accum, table = buffer(N * K + N, parts) if parts else (normal(9, (N * K + N,), 0.1, FP32), None)
+    flat = (lambda t: t) if table is None else (lambda t: gather(t, table))
+    old = flat(accum).to(D64)
+    dx = nsg.linear_grad(accum, dout, x, w, (0, N, K), (N * K, 1, N), table, 0.5, overwrite, "gelu", pre)
+    want, bound, dw, ew, db, eb = grad_form(dout, x, w, "gelu", pre)
+    close(dx, want, bound, "dx")
+    v = old * (0 if overwrite else 1) + 0.5 * torch.cat([dw.reshape(-1), db])
+    close(flat(accum), v, 0.505 * torch.cat([ew.reshape(-1), eb]) + 2.0 ** -23 * (v.abs() + old.abs()), "accum")
+
+
+@pytest.mark.parametrize("T", [1, 2, 3, 4, 5, 9, 33, 64, 65])
+@pytest.mark.parametrize("K,N", [(256, 8), (2048, 9), (2056, 1031), (4104, 2048)])
+def test_few_tokens(T, K, N):
+    """Every way a few tokens may go, with all that a result may have."""
+    for way in (WAYS[5], dict(bias=FP32, act="silu", residual=True, pre=True, out=FP32)):
+        x, w, bias, residual, out = forward_case(T, K, N, way, T + K + N)
+        args = (bias, way["act"], residual, way.get("rate", 0.0), generator(), 9)
+        y, u = nsg.linear(x, w, *args, out_dtype=out, pre=True)
+        want, bound, pre, pre_bound = forward_form(x, w, *args, out)
+        close(y, want, bound, "out")
+        close(u, pre, pre_bound, "pre")
+        wide = torch.zeros((T, K + 8), dtype=BF16, device="cuda")   # rows with a stride
+        wide[:, :K] = x
+        assert torch.equal(nsg.linear(wide[:, :K], w, *args, out_dtype=out), y)
+
+
+def test_calls_at_the_same_time():
+    """Two streams at once, each with products, gradients and copies of operands of its own."""
+    T, K, N = 700, 1001, 520
+    x, w, dout = normal(1, (T, K)), normal(2, (N, K), 0.03), normal(3, (T, N), 0.1)
+
+    def calls():
+        accum = torch.zeros(N * K + N, device="cuda")
+        y = nsg.linear(x, w, activation="gelu")
+        dx = nsg.linear_grad(accum, dout, x, w, (0, N, K), (N * K, 1, N))
+        return y, dx, accum
+
+    want = calls()
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(3)], []
+    for _ in range(5):
+        for stream in streams:
+            with torch.cuda.stream(stream):
+                got.append(calls())
+    torch.cuda.synchronize()
+    for r in got:
+        assert all(torch.equal(a, b) for a, b in zip(r, want))
+
+
+def test_what_follows_sees_all_of_a_call():
+    """A gradient call's kernels run beside one another; whatever comes next in the stream waits for all of them."""
+    T, K, N = 3000, 1288, 1032
+    x, w, dout = normal(1, (T, K)), normal(2, (N, K), 0.03), normal(3, (T, N), 0.1)
+    accum = torch.zeros(N * K + N, device="cuda")
+    want_dx = nsg.linear_grad(accum, dout, x, w, (0, N, K), (N * K, 1, N), overwrite=True)
+    want = accum.clone()
+    for _ in range(20):
+        dx = torch.full((T, K), 7.0, dtype=BF16, device="cuda")
+        accum.fill_(3.0)
+        nsg.linear_grad(accum, dout, x, w, (0, N, K), (N * K, 1, N), overwrite=True, dx=dx)
+        a, b = dx.clone(), accum.clone()        # torch's kernels
+        y = nsg.linear(dx, w)                   # and the library's, which start early
+        dx.zero_()
+        assert torch.equal(a, want_dx) and torch.equal(b, want)
+        assert torch.equal(y, nsg.linear(want_dx, w))
+
+
 def test_the_same_call_gives_the_same_bits():
     for T, K, N in ((1, 4096, 512), (40, 1000, 768), (700, 4096, 776)):
         x, w, bias, residual, _ = forward_case(T, K, N, WAYS[2], 5)
