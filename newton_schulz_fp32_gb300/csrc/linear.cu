@@ -416,6 +416,32 @@ struct InputGrad {
 };
 
 // accum = (overwrite ? 0 : accum) + scale * acc, at the parameter's place.
+//
+// A warp's 32 rows x 32 columns: a lane's row lies in shared memory, 144 bytes from
+// the next, shifted as its place in accum is against 16 bytes, and goes out as one
+// bulk copy, added at L2 or put in place, so that a warp needs no load of the old
+// sums and waits for nothing.  What lies before the first and behind the last
+// 16-byte piece, up to three elements each, goes by itself: added or stored, once
+// for each element of the gradient, so that the order of the sums is one.  Rows
+// that a partition cuts go element by element.
+constexpr int kRowBytes = 144;
+
+__device__ __forceinline__ void bulk_add(float* dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.reduce.async.bulk.global.shared::cta.bulk_group.add.f32 [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_put(float* dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void add_one(float* dst, float x) {
+  asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(dst), "f"(x) : "memory");
+}
+__device__ __forceinline__ float shared_float(uint32_t at) {
+  float x;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(at) : "memory");
+  return x;
+}
+
 struct WeightGrad {
   float* accum;
   int64_t rows;
@@ -425,162 +451,79 @@ struct WeightGrad {
   Segments sg;
 
   __device__ __forceinline__ bool exact() const { return true; }
-  // The lane's eight elements lie in one piece, on 16 bytes.
-  __device__ __forceinline__ float* whole(int64_t r, int64_t c, int left) const {
-    int64_t room;
-    float* p = accum + sg.place(r * cols + c, &room);
-    return left >= 8 && room >= 8 && (reinterpret_cast<uintptr_t>(p) & 15) == 0 ? p : nullptr;
+  __device__ __forceinline__ void put(float* p, float x) const {
+    if (overwrite) *p = x;
+    else add_one(p, x);
   }
-  __device__ __forceinline__ void fetch(uint32_t slots, int, int64_t r0, int64_t c0, int lane) const {
-    if (overwrite) return;
-    const int64_t c = c0 + (lane & 3) * 8, r = r0 + (lane >> 2);
-    const int left = int(min(int64_t(8), cols - c));
-    if (left < 8) return;
+
+  // x: columns c0 .. c0 + 31 of row r0 + lane.  room: the warp's, 32 * kRowBytes.
+  __device__ __forceinline__ void put_rows(uint32_t room, int64_t r0, int64_t c0, int lane, const float (&x)[32]) const {
+    const int64_t r = r0 + lane;
+    const int width = int(min(int64_t(32), cols - c0));
+    int64_t piece = 0;
+    float* p = r < rows ? accum + sg.place(r * cols + c0, &piece) : nullptr;
+    const bool whole = p && piece >= width;
+    const int shift = whole ? int(reinterpret_cast<uintptr_t>(p) >> 2) & 3 : 0;
+    const uint32_t mine = room + uint32_t(lane * kRowBytes);
+    tma_store_wait_read();   // this lane's row before
+    if (__all_sync(0xffffffffu, shift == 0)) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (r + 8 * i >= rows) break;
-      const float* p = whole(r + 8 * i, c, left);
-      if (!p) continue;
-      copy16(slots + (2 * i) * 512 + lane * 16, p);
-      copy16(slots + (2 * i + 1) * 512 + lane * 16, p + 4);
+      for (int g = 0; g < 8; ++g)
+        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(mine + g * 16), "f"(scale * x[4 * g]),
+                     "f"(scale * x[4 * g + 1]), "f"(scale * x[4 * g + 2]), "f"(scale * x[4 * g + 3])
+                     : "memory");
+    } else {
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(mine + uint32_t(shift + j) * 4), "f"(scale * x[j]) : "memory");
     }
-  }
-  // Rows of `mask` of a chunk or a part of one, `width` columns from c0, element by
-  // element, 32 columns at once.  at(row, column): its sum.  p and room: where
-  // the lane's own row begins, and how many elements follow in one piece.
-  template <int H, typename At>
-  __device__ __forceinline__ void put_pieces(uint32_t mask, int64_t r0, int64_t c0, int width, int lane, float* p,
-                                             int64_t room, const At& at) const {
-    constexpr int U = 8;   // rows under way
-    while (mask) {
-      float old[U][H];
-      float* q[U][H];
-      int row[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        row[u] = mask ? __ffs(mask) - 1 : -1;
-        mask &= mask - 1;
-        const int from = max(row[u], 0);
-        float* start = reinterpret_cast<float*>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(p), from));
-        const int64_t piece_room = __shfl_sync(0xffffffffu, room, from);
-#pragma unroll
-        for (int h = 0; h < H; ++h) {
-          const int c = lane + 32 * h;
-          q[u][h] = nullptr;
-          if (row[u] < 0 || c >= width) continue;
-          int64_t left;
-          q[u][h] = c < piece_room ? start + c : accum + sg.place((r0 + row[u]) * cols + c0 + c, &left);
-          old[u][h] = overwrite ? 0.f : *q[u][h];
-        }
+    if (whole) {
+      const int head = min((4 - shift) & 3, width), mid = (width - head) & ~3;
+      if (mid) {
+        fence_async_smem();
+        const uint32_t from = mine + uint32_t(shift + head) * 4;
+        if (overwrite) bulk_put(p + head, from, mid * 4);
+        else bulk_add(p + head, from, mid * 4);
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
       }
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int h = 0; h < H; ++h)
-          if (q[u][h]) *q[u][h] = old[u][h] + at(row[u], lane + 32 * h);
+      for (int j = 0; j < 3; ++j) {
+        if (j < head) put(p + j, shared_float(mine + uint32_t(shift + j) * 4));
+        const int c = head + mid + j;
+        if (c < width) put(p + c, shared_float(mine + uint32_t(shift + c) * 4));
+      }
     }
+    for (uint32_t cut = __ballot_sync(0xffffffffu, p && !whole); cut; cut &= cut - 1) {
+      const int row = __ffs(cut) - 1;   // its columns to the warp's lanes
+      __syncwarp();
+      int64_t left;
+      if (lane < width)
+        put(accum + sg.place((r0 + row) * cols + c0 + lane, &left), shared_float(room + uint32_t(row * kRowBytes + lane * 4)));
+    }
+    __syncwarp();
   }
+  __device__ __forceinline__ void fetch(uint32_t, int, int64_t, int64_t, int) const {}
+  // A chunk whose sums lie in several blocks, or this one: rows of them, then as above.
   template <typename Read>
-  __device__ __forceinline__ void chunk(const Read& read, uint32_t slots, int, int64_t r0, int64_t c0, int lane,
+  __device__ __forceinline__ void chunk(const Read& read, uint32_t room, int, int64_t r0, int64_t c0, int lane,
                                         const Draw&) const {
-    const int64_t c = c0 + (lane & 3) * 8, r = r0 + (lane >> 2);
-    const int left = int(min(int64_t(8), cols - c));
-    const int live = left <= 0 ? 0 : int(min(int64_t(4), (rows - r + 7) >> 3));
-    float v[4][8];
-    bool mine = true;
+    float v[4][8], x[32];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      read(8 * i + (lane >> 2), lane & 3, v[i]);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] *= scale;
-      mine = mine && (i >= live || whole(r + 8 * i, c, left));
-    }
-    if (__all_sync(0xffffffffu, mine)) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (i >= live) break;
-        float* p = whole(r + 8 * i, c, left);
-        if (!overwrite) {
-          float o[8];
-          tok::Vec<float>::unpack(slot16(slots + (2 * i) * 512 + lane * 16), o);
-          tok::Vec<float>::unpack(slot16(slots + (2 * i + 1) * 512 + lane * 16), o + 4);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) v[i][j] += o[j];
-        }
-        reinterpret_cast<uint4*>(p)[0] = tok::Vec<float>::pack(v[i]);
-        reinterpret_cast<uint4*>(p)[1] = tok::Vec<float>::pack(v[i] + 4);
-      }
-      return;
-    }
-    const uint32_t stage = read.at;
+    for (int i = 0; i < 4; ++i) read(8 * i + (lane >> 2), lane & 3, v[i]);
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(stage + piece(8 * i + (lane >> 2), 2 * (lane & 3) + h)),
+        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(read.at + piece(8 * i + (lane >> 2), 2 * (lane & 3) + h)),
                      "f"(v[i][4 * h]), "f"(v[i][4 * h + 1]), "f"(v[i][4 * h + 2]), "f"(v[i][4 * h + 3])
                      : "memory");
     __syncwarp();
-    int64_t room = 0;
-    const bool in = r0 + lane < rows;
-    float* p = in ? accum + sg.place((r0 + lane) * cols + c0, &room) : nullptr;
-    put_pieces<1>(__ballot_sync(0xffffffffu, in), r0, c0, int(min(int64_t(32), cols - c0)), lane, p, room,
-                  [&](int row, int) { return at_column(stage, row, lane); });
-    __syncwarp();
+#pragma unroll
+    for (int g = 0; g < 8; ++g) tok::Vec<float>::unpack(slot16(read.at + piece(lane, g)), x + 4 * g);
+    put_rows(room, r0, c0, lane, x);
   }
 };
-
-// A warp's 32 rows x 32 columns of sums, as the pair kernel hands them to accum:
-// a lane's row lies in shared memory, 144 bytes from the next (so that eight lanes'
-// stores meet in no bank), and goes out as one bulk copy of 128 bytes, added at L2
-// or put in place; a warp so needs no load of the old sums and waits for nothing.
-// Rows that do not start on 16 bytes, and pieces that end inside (columns,
-// partitions), go element by element, 32 columns at once.
-constexpr int kSumColumns = 32;
-constexpr int kRowBytes = kSumColumns * 4 + 16;
-
-__device__ __forceinline__ void bulk_add(float* dst, uint32_t src, uint32_t bytes) {
-  asm volatile("cp.reduce.async.bulk.global.shared::cta.bulk_group.add.f32 [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes)
-               : "memory");
-}
-__device__ __forceinline__ void bulk_put(float* dst, uint32_t src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
-}
-
-// x: the lane's row, kSumColumns columns from c0.
-__device__ __forceinline__ void put_rows(const WeightGrad& w, uint32_t stage, int64_t r0, int64_t c0, int lane,
-                                         const float (*x)[32]) {
-  const uint32_t mine = stage + uint32_t(lane * kRowBytes);
-  tma_store_wait_read();   // this lane's row before
-  const float scale = w.scale;
-#pragma unroll
-  for (int g = 0; g < kSumColumns / 4; ++g)
-    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(mine + g * 16), "f"(scale * x[g / 8][g % 8 * 4]),
-                 "f"(scale * x[g / 8][g % 8 * 4 + 1]), "f"(scale * x[g / 8][g % 8 * 4 + 2]),
-                 "f"(scale * x[g / 8][g % 8 * 4 + 3])
-                 : "memory");
-  const int64_t r = r0 + lane;
-  const int width = int(min(int64_t(kSumColumns), w.cols - c0));
-  int64_t room = 0;
-  float* p = r < w.rows ? w.accum + w.sg.place(r * w.cols + c0, &room) : nullptr;
-  const bool whole = p && room >= width && (reinterpret_cast<uintptr_t>(p) & 15) == 0 && width % 4 == 0;
-  if (whole) {
-    fence_async_smem();
-    if (w.overwrite) bulk_put(p, mine, width * 4);
-    else bulk_add(p, mine, width * 4);
-    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-  }
-  uint32_t rest = __ballot_sync(0xffffffffu, p && !whole);
-  if (!rest) return;
-  __syncwarp();
-  w.put_pieces<kSumColumns / 32>(rest, r0, c0, width, lane, p, room, [&](int row, int c) {
-    float x;
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(stage + uint32_t(row * kRowBytes + c * 4)) : "memory");
-    return x;
-  });
-  __syncwarp();   // rows are read before they are written again
-}
 
 __device__ __forceinline__ void stage_rows(uint32_t at, int lane, const float* x) {   // lane: the row
 #pragma unroll
@@ -917,8 +860,8 @@ k_linear_pair(const __grid_constant__ One<E> w, int late, int* err) {
         }
         if (!ok || !here) continue;
 #pragma unroll
-        for (int c = 0; c < N; c += kSumColumns / 32)
-          if (n0 + 32 * c < p.n) put_rows(w.e, stage, m0, n0 + 32 * c, lane, &sum[c]);
+        for (int c = 0; c < N; ++c)
+          if (n0 + 32 * c < p.n) w.e.put_rows(stage, m0, n0 + 32 * c, lane, sum[c]);
       } else {
         if (here) w.e.fetch(slots, 0, m0, n0, lane);
         if (nk > depth) {
@@ -997,7 +940,8 @@ struct SplitShape {
   static constexpr int kBars = 2 * kStages + 4;
   static constexpr int kChunks = kSplitWarps * (BN / 32);
   static constexpr int kShared = 1024 + kStages * kStage + 8 * kBars + 16;
-  static_assert(kChunks * kChunkBytes + kSplitWarps * kSlotBytes <= kStages * kStage,
+  static constexpr int kRoom = 32 * kRowBytes;   // a warp's slots, or its rows on their way to accum
+  static_assert(kRoom >= kSlotBytes && kChunks * kChunkBytes + kSplitWarps * kRoom <= kStages * kStage,
                 "sums and slots take the operands' place");
 };
 
@@ -1064,7 +1008,7 @@ k_linear_split(const __grid_constant__ One<E> w, int splits, int late, int* err)
   if (!loader) begin_kernel(late);
 
   const int ew = warp - 2, q = warp & 3;
-  const uint32_t slots = base + S::kChunks * kChunkBytes + ew * kSlotBytes;   // once the operands are read
+  const uint32_t slots = base + S::kChunks * kChunkBytes + ew * S::kRoom;   // once the operands are read
   constexpr int N = BN / 32;
   // where chunk (quarter of the rows, 32 columns) lies in the result
   auto row_of = [&](int quarter, int c) { return SWAP ? int64_t(tn) * BN + 32 * c : int64_t(tm) * 128 + 32 * quarter; };
@@ -1172,6 +1116,7 @@ k_linear_split(const __grid_constant__ One<E> w, int splits, int late, int* err)
       if (splits > 1) w.e.chunk(ReadAll{at, splits}, slots, 0, r, n, lane, draw);
       else w.e.chunk(ReadOwn{at}, slots, 0, r, n, lane, draw);
     }
+    if constexpr (std::is_same_v<E, WeightGrad>) tma_store_wait_all();
   }
   if (*abort_flag) {
     const unsigned long long t0 = globaltimer();
