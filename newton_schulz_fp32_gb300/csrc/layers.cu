@@ -106,7 +106,7 @@ cudaError_t launch_dropout(const DropArgs& a, cudaStream_t s) {
 // For a head x with weight w, position p and frequencies f:
 //     n = x / sqrt(mean x^2 + eps) * w,   (a, b) -> (a cos - b sin, b cos + a sin) with the angle p f.
 // Both directions are bound by memory, each element moved once (16384 tokens of 40
-// heads of 128 bf16: 64 us, 5.2 TB/s; the gradients 113 us, 4.4 TB/s, issue slots 66%
+// heads of 128 bf16: 64 us, 5.2 TB/s; the gradients 111 us, 4.5 TB/s, issue slots 60%
 // busy), and short of it by latency: 16 warps per SM hold what is on its way in
 // registers.
 

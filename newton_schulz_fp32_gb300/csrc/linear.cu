@@ -55,8 +55,8 @@ __device__ __forceinline__ void end_kernel(int late) {
 // A warp takes a chunk of 32 rows x 32 columns of the result.  Its lane has, in
 // turn, eight consecutive columns of row 8 i + lane / 4, i = 0 .. 3: 16 bytes of
 // bf16 and the eight elements that one draw of dropout serves.  What is added to
-// the chunk or multiplies it (residual, argument of the activation, old sums)
-// is fetched ahead by asynchronous copies into slots of the lane's own.
+// the chunk or multiplies it (residual, argument of the activation) is fetched
+// ahead by asynchronous copies into slots of the lane's own.
 
 constexpr int kSlotBytes = 4096;    // a warp's slots: a chunk of FP32, or two of bf16
 constexpr int kChunkBytes = 4096;   // a chunk of FP32 sums
@@ -243,7 +243,7 @@ struct Forward {
   int cols, bias32, act;
   Dropout drop;
 
-  // Sums of a result in FP32 are added up in registers, see kDepth.
+  // A result in FP32 is summed in pieces of kDepth K blocks.
   __device__ __forceinline__ bool exact() const { return out.fp32; }
   __device__ __forceinline__ bool halves() const { return !residual.fp32; }
   __device__ __forceinline__ void fetch(uint32_t slots, int half, int64_t t0, int64_t n0, int lane) const {
@@ -623,13 +623,13 @@ constexpr int BK = 64;
 // Tensor memory's additions cut off instead of rounding, all in one direction: half
 // a unit of 2^-23 every 16 terms.  For a result in FP32 so many K blocks of 64 terms
 // are summed there and FP32 registers add those (a sum of 32768 terms is then off by
-// 1e-6 of its size, where one pass would leave 6e-5).  What is rounded to bf16 is
-// not: 2^24 terms would have to come together before that showed.
+// 1e-6 of its size, where one pass would leave 6e-5).  What is rounded to bf16, by
+// 2e-3, is summed in one pass up to 65536 terms (2e-4 at worst).
 // Gradients of up to 2048 tokens are nearer than that to begin with (3e-7 by FP32
 // sums of values whose mean is not 0) and take shorter pieces (1.1e-6 in one pass of
 // 1024 terms, 3e-7 in these); for a layer's results, whose weights have no such
 // mean, one pass of 1024 gives 2.3e-7.
-constexpr int kDepth = 16, kDepthFew = 4, kFewBlocks = 32;
+constexpr int kDepth = 16, kDepthFew = 4, kFewBlocks = 32, kMostBlocks = 1024;
 
 __device__ __forceinline__ uint32_t idesc_of(const Product& p, int m, int n) {
   return make_idesc(p.b_mn != 0, m, n) | (p.a_mn ? 1u << 15 : 0u);
@@ -731,7 +731,7 @@ k_linear_pair(const __grid_constant__ One<E> w, int late, int* err) {
   const Product& p = w.p;
   const int nk = p.k;
   const bool exact = w.e.exact();
-  const int depth = !exact ? max(nk, 1) : S::kSums && nk <= kFewBlocks ? kDepthFew : kDepth;
+  const int depth = !exact && nk <= kMostBlocks ? max(nk, 1) : S::kSums && nk <= kFewBlocks ? kDepthFew : kDepth;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kStages; ++s) {
@@ -1433,12 +1433,16 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // The plan of least estimated time for D[m][n] with k terms.  An SM takes in 64
 // bytes a cycle, which is what a K block of 64 costs: 0.28 us on a pair at 256
 // columns (there the tensor cores take as long), 0.20 at 128, 0.30 on a single SM.
-// Starting, the first operands' latency and the results cost 6, 4.7 and 4.5 us,
-// a cluster's sums 2 more, old FP32 sums on single SMs 3.  Measured (us; chosen
-// first): 1024 x 768 -> 768 6.7 on pairs at 128, 7.8 on single SMs, 9.8 on pairs at
-// 256; its weight's gradient 8.7, 10.0 (four blocks a tile), 12.4; 512 x 4096 ->
-// 1024 11.8 on four blocks a tile, 17.0 on pairs at 128; 2048^3 15.2 on pairs at 256,
-// 18.3 at 128.
+// Starting, the first operands' latency and the results cost 7.2, 4.7 and 4.5 us, a
+// cluster's sums 2 more.  Sums into accum (a weight's gradient, both operands along
+// their rows, each row a piece of bulk copies) cost 8.8, 5.7 and 8.5, however many
+// blocks share them out, and pieces of kDepthFew K blocks more for each.  Measured
+// on pairs at 128 / pairs at 256 / single SMs without a split / by 2 / by 4 (us,
+// chosen: *): 1024 x 768 -> 768 7.8* / 12.0 / 8.9 / 9.4 / 16.5; 512 x 4096 -> 1024
+// 18.0 / 25.5 / 20.8 / 15.1 / 12.0*; 1024 x 1024 -> 4096 13.0* / 13.9 / 19.5 / 38 / 66;
+// 2048^3 19.4 / 18.2* / 27 / 45 / 74; their weights' gradients of 512 x 768 -> 768
+// 7.6* / 11.1 / 10.7 / 9.3 / 9.0; 2048 x 768 -> 768 13.9 / 19.7 / 16.9 / 12.4 / 10.7*;
+// 2048 x 1024 -> 1024 14.3 / 19.9 / 17.1 / 12.9* / 20.3; 2048^3 26.0 / 21.2* / 35 / 50 / 77.
 Plan plan_of(int64_t m, int64_t n, int64_t k, bool sums) {
   Plan best;
   double least = 0;
@@ -1452,11 +1456,18 @@ Plan plan_of(int64_t m, int64_t n, int64_t k, bool sums) {
   };
   for (int bn : {256, 128}) {
     const double waves = std::ceil(double(ceil_div(m, 256) * ceil_div(n, bn)) / kPairs);
-    offer(true, bn, 1, waves * (kb * (bn == 256 ? 0.28 : 0.20) + 0.5) + (bn == 256 ? 5.5 : 4.2));
+    double block = bn == 256 ? 0.28 : 0.20, more = 0.5, start = bn == 256 ? 7.2 : 4.7;
+    if (sums) {
+      block = kb > kFewBlocks ? (bn == 256 ? 0.26 : 0.20) : bn == 256 ? 0.345 : 0.27;
+      more = bn == 256 ? 4.0 : 3.1;
+      start = bn == 256 ? 8.8 : 5.7;
+    }
+    offer(true, bn, 1, waves * kb * block + (waves - 1) * more + start);
   }
   for (int s = 1; s <= kMostSplits && (s == 1 || kb >= 2 * s); s *= 2) {
     const double waves = std::ceil(double(ceil_div(m, 128) * ceil_div(n, 128) * s) / (s > 2 ? kFourfold : kSms));
-    offer(false, 128, s, waves * (std::ceil(kb / s) * 0.30 + 2.0) + 2.5 + (s > 1 ? 2.0 : 0.0) + (sums ? 3.0 : 0.0));
+    offer(false, 128, s, sums ? waves * (std::ceil(kb / s) * 0.27 + 8.2) + 0.3
+                              : waves * (std::ceil(kb / s) * 0.30 + 2.0) + 2.5 + (s > 1 ? 2.0 : 0.0));
   }
   return best;
 }

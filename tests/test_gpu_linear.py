@@ -129,6 +129,14 @@ def test_forward_of_many_tiles(T, K, N, way):
         close(u, pre, pre_bound, "pre")
 
 
+def test_very_many_terms():
+    """More terms of a bf16 result than are summed in one pass."""
+    T, K, N = 300, 66000, 9000
+    x, w, bias, _, _ = forward_case(T, K, N, WAYS[1], 1)
+    want, bound, *_ = forward_form(x, w, bias, "gelu", None, 0.0, None, 0, BF16)
+    close(nsg.linear(x, w, bias, "gelu"), want, bound, "out")
+
+
 @pytest.mark.parametrize("parts,overwrite", [(0, False), (8, True)])
 @pytest.mark.parametrize("T,K,N", LARGE + [(40, 2568, 4352), (1, 1032, 2056)])
 def test_gradients_of_many_tiles(T, K, N, parts, overwrite):
