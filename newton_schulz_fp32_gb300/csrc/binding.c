@@ -1004,6 +1004,11 @@ static int turns_of(PyObject* positions, PyObject* freq, PyObject* axis, PyObjec
     axes = dims ? PyLong_AsLongLong(PyTuple_GET_ITEM(shape, dims - 1)) : -1;
   }
   Py_DECREF(shape);
+  if (n == 0 && t->axis.buf) {   /* an empty batch's positions do not tell: as many as the pairs name */
+    axes = 1;
+    for (int i = 0; i < t->pairs; ++i)
+      if (((const int32_t*)t->axis.buf)[i] >= axes) axes = ((const int32_t*)t->axis.buf)[i] + 1ll;
+  }
   if (axes < 1 || axes > INT_MAX || count != n * axes)
     return refuse("%s must be one per token, or tokens x axes", "positions");
   t->axes = (int)axes;

@@ -296,6 +296,16 @@ def test_layouts_of_heads():
     assert not bool(accum.any())
 
 
+def test_no_tokens_on_several_axes():
+    freq, axis = nsg.rotary_frequencies(64, sections=[8, 12, 12])
+    nothing, pos = (torch.empty((0, *n), dtype=t, device="cuda") for n, t in (((3, 64), BF16), ((3,), torch.int64)))
+    accum = torch.ones(64, device="cuda")
+    assert nsg.norm_rotary(nothing, None, pos, freq, axis)[0].shape == (0, 3, 64)
+    assert nsg.norm_rotary_grad(nothing, nothing, None, None, pos, freq, axis, accum=accum,
+                                q_param=(0, 1, 64))[0].shape == (0, 3, 64)
+    assert bool((accum == 1).all())
+
+
 def test_tokens_that_are_none_may_hold_anything():
     freq, axis = nsg.rotary_frequencies(128)
     T = 40

@@ -321,6 +321,16 @@ def test_tensors_on_another_device_make_it_current(machine):
         nsg.linear(x, m.tensor(torch.zeros(4, 8, dtype=torch.bfloat16), 0))
 
 
+@pytest.mark.parametrize("shape", [(0, 3), (2, 0, 3), (0,)])
+def test_no_tokens_on_several_axes(machine, shape):
+    """Positions of an empty batch say nothing about their axes: the pairs' do."""
+    freq, axis = nsg.rotary_frequencies(8, sections=[1, 1, 2])
+    x = machine.tensor(torch.zeros(*shape[:-1], 2, 8) if len(shape) > 1 else torch.zeros(0, 2, 8))
+    nsg.norm_rotary(x, None, machine.tensor(torch.zeros(shape, dtype=torch.int64)), freq, axis)
+    args = machine.layer_calls[-1][1]
+    assert args[3] == 0 and args[9] == 3
+
+
 # ------------------------------------------------------------------ the forms
 
 @pytest.mark.parametrize("kind", ["relu", "relu2", "gelu", "silu"])
