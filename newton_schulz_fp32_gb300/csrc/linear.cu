@@ -1430,7 +1430,7 @@ struct Plan {
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// The plan of least estimated time for D[m][n] with k terms.  An SM takes in 64
+// The plan of least estimated time for D[m][n] with k terms on `sms` SMs.  An SM takes in 64
 // bytes a cycle, which is what a K block of 64 costs: 0.28 us on a pair at 256
 // columns (there the tensor cores take as long), 0.20 at 128, 0.30 on a single SM.
 // Starting, the first operands' latency and the results cost 7.2, 4.7 and 4.5 us, a
@@ -1443,7 +1443,7 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // 2048^3 19.4 / 18.2* / 27 / 45 / 74; their weights' gradients of 512 x 768 -> 768
 // 7.6* / 11.1 / 10.7 / 9.3 / 9.0; 2048 x 768 -> 768 13.9 / 19.7 / 16.9 / 12.4 / 10.7*;
 // 2048 x 1024 -> 1024 14.3 / 19.9 / 17.1 / 12.9* / 20.3; 2048^3 26.0 / 21.2* / 35 / 50 / 77.
-Plan plan_of(int64_t m, int64_t n, int64_t k, bool sums) {
+Plan plan_of(int64_t m, int64_t n, int64_t k, bool sums, int sms = kSms) {
   Plan best;
   double least = 0;
   const double kb = double(ceil_div(k, 64));
@@ -1455,7 +1455,7 @@ Plan plan_of(int64_t m, int64_t n, int64_t k, bool sums) {
     least = us;
   };
   for (int bn : {256, 128}) {
-    const double waves = std::ceil(double(ceil_div(m, 256) * ceil_div(n, bn)) / kPairs);
+    const double waves = std::ceil(double(ceil_div(m, 256) * ceil_div(n, bn)) / (sms / 2));
     double block = bn == 256 ? 0.28 : 0.20, more = 0.5, start = bn == 256 ? 7.2 : 4.7;
     if (sums) {
       block = kb > kFewBlocks ? (bn == 256 ? 0.26 : 0.20) : bn == 256 ? 0.345 : 0.27;
@@ -1465,11 +1465,20 @@ Plan plan_of(int64_t m, int64_t n, int64_t k, bool sums) {
     offer(true, bn, 1, waves * kb * block + (waves - 1) * more + start);
   }
   for (int s = 1; s <= kMostSplits && (s == 1 || kb >= 2 * s); s *= 2) {
-    const double waves = std::ceil(double(ceil_div(m, 128) * ceil_div(n, 128) * s) / (s > 2 ? kFourfold : kSms));
+    const double waves = std::ceil(double(ceil_div(m, 128) * ceil_div(n, 128) * s) / (s > 2 ? sms - (kSms - kFourfold) : sms));
     offer(false, 128, s, sums ? waves * (std::ceil(kb / s) * 0.27 + 8.2) + 0.3
                               : waves * (std::ceil(kb / s) * 0.30 + 2.0) + 2.5 + (s > 1 ? 2.0 : 0.0));
   }
   return best;
+}
+
+// SMs for a kernel that is launched beside one of so many tiles: what that leaves, if
+// it is a third of them at least, else all (it then comes after the other).  Both
+// gradients and the bias of 1024 x 768 -> 768 take 12.6 us so, 17.4 with the weight's
+// planned for all SMs; of 1024 x 768 -> 2304 20.5 and 23.0.
+int beside(const Plan& plan, int tiles) {
+  const int64_t left = kSms - int64_t(tiles) * (plan.pairs ? 2 : plan.splits);
+  return int(left >= kSms / 3 ? left / 2 * 2 : kSms);
 }
 
 // Few tokens: features are the rows of the tiles, and the K blocks are shared out
@@ -1851,7 +1860,8 @@ extern "C" int muon_linear_grad(const muon_linear_grad_args_t* args, void* works
                  : prepare(plans[0], o.dout, false, o.weight, true, f, &first);
     }
     if (dw && fine) {
-      plans[1] = plan_of(N, K, T, true);
+      const int left = dx ? beside(plans[0], first.tiles) : kSms;
+      plans[1] = plan_of(N, K, T, true, left);
       fine = prepare(plans[1], o.dout, true, o.x, true, g, &second);
     }
     if (!fine) return fail_with(MUON_ERR_CUDA, "the driver refuses a map of an operand");
