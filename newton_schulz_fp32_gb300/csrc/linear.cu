@@ -8,7 +8,7 @@
 //
 // All three products are bf16 x bf16 with FP32 sums on the tensor cores; an
 // operand is read as it lies, with its k contiguous or its rows.  Which kernel
-// takes a product is a matter of its sizes (plan_of, plan_few, takes_rows):
+// takes a product is a matter of its sizes (offers_of, plan_few, takes_rows):
 //   k_linear_pair   tiles of 256 x 256 or 256 x 128 on pairs of SMs, persistent.
 //                   Bound by the tensor cores (92% active): 8192 x 4096 -> 14336 in
 //                   495 us, 1945 TFLOP/s, as fast as the library's product alone;
@@ -18,8 +18,9 @@
 //                   cluster, for products of few tiles; tiles of 128 features x
 //                   32 or 64 tokens for few tokens (4096 -> 14336, 32 tokens 23 us,
 //                   5.1 TB/s of weight).
-//   k_linear_rows   one or two tokens: multiply-adds over the weight's rows (one
-//                   token through 4096 -> 14336 20 us, 5.8 TB/s).
+//   k_linear_rows   one or two tokens (up to four of a small weight): multiply-adds
+//                   over the weight's rows (one token through 4096 -> 14336 20 us,
+//                   5.8 TB/s).
 //   k_linear_pack   operands whose rows do not start on 16 bytes, copied first.
 //   k_bias_grad     sums of dout's columns.
 #include <type_traits>
@@ -1262,8 +1263,9 @@ struct Packs {
 };
 
 // Rows of `cols` elements at any stride to rows that start on 16 bytes; eight
-// elements per thread, all of a call's operands in one launch.  What a row's last
-// piece holds beyond cols is not read.
+// elements per thread, all of a call's operands in one launch (words instead of
+// elements, or two pieces per thread, gained 0.2 of 20 us).  What a row's last piece
+// holds beyond cols is not read.
 __global__ void __launch_bounds__(kPackThreads) k_linear_pack(const __grid_constant__ Packs a) {
   begin_kernel(0);
   for (int64_t i = int64_t(blockIdx.x) * kPackThreads + threadIdx.x; i < a.end[kPackMost - 1];
@@ -1382,6 +1384,7 @@ cudaError_t launch_bias(const BiasGrad& a, const Segments& sg, int late, cudaStr
 
 constexpr int kMostFeatures = 1 << 24;
 constexpr int kSms = 152, kPairs = kSms / 2;
+constexpr int kLeast = 16;        // SMs that a kernel beside another is given at least
 constexpr int kFourfold = 144;   // blocks that run at once as clusters of four (of eight: 120, of three: 138)
 
 // An operand of a product: rows x cols, bf16.
@@ -1443,42 +1446,51 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // 2048^3 19.4 / 18.2* / 27 / 45 / 74; their weights' gradients of 512 x 768 -> 768
 // 7.6* / 11.1 / 10.7 / 9.3 / 9.0; 2048 x 768 -> 768 13.9 / 19.7 / 16.9 / 12.4 / 10.7*;
 // 2048 x 1024 -> 1024 14.3 / 19.9 / 17.1 / 12.9* / 20.3; 2048^3 26.0 / 21.2* / 35 / 50 / 77.
-Plan plan_of(int64_t m, int64_t n, int64_t k, bool sums, int sms = kSms) {
-  Plan best;
-  double least = 0;
+struct Offer {
+  Plan plan;
+  double us;
+  int64_t sms;   // that it holds
+};
+
+constexpr int kOffers = 5;
+
+// more: results have something done to them (us for each tile that an SM or a pair forms).
+int offers_of(int64_t m, int64_t n, int64_t k, bool sums, bool more, int sms, Offer* out) {
   const double kb = double(ceil_div(k, 64));
-  auto offer = [&](bool pairs, int bn, int splits, double us) {
-    if (best.bn && us >= least) return;
-    best.pairs = pairs;
-    best.bn = bn;
-    best.splits = splits;
-    least = us;
+  int count = 0;
+  auto offer = [&](bool pairs, int bn, int splits, int64_t tiles, double us) {
+    Offer& o = out[count++];
+    o.plan.pairs = pairs;
+    o.plan.bn = bn;
+    o.plan.splits = splits;
+    o.us = us;
+    o.sms = std::min<int64_t>(sms, tiles * (pairs ? 2 : splits));
   };
   for (int bn : {256, 128}) {
-    const double waves = std::ceil(double(ceil_div(m, 256) * ceil_div(n, bn)) / (sms / 2));
-    double block = bn == 256 ? 0.28 : 0.20, more = 0.5, start = bn == 256 ? 7.2 : 4.7;
+    const int64_t tiles = ceil_div(m, 256) * ceil_div(n, bn);
+    const double waves = double(ceil_div(tiles, sms / 2)), worked = more ? waves * (bn == 256 ? 3.7 : 1.8) : 0.0;
+    double block = bn == 256 ? 0.28 : 0.20, again = 0.5, start = bn == 256 ? 7.2 : 4.7;
     if (sums) {
       block = kb > kFewBlocks ? (bn == 256 ? 0.26 : 0.20) : bn == 256 ? 0.345 : 0.27;
-      more = bn == 256 ? 4.0 : 3.1;
+      again = bn == 256 ? 4.0 : 3.1;
       start = bn == 256 ? 8.8 : 5.7;
     }
-    offer(true, bn, 1, waves * kb * block + (waves - 1) * more + start);
+    offer(true, bn, 1, tiles, waves * kb * block + (waves - 1) * again + start + worked);
   }
+  const int64_t tiles = ceil_div(m, 128) * ceil_div(n, 128);
   for (int s = 1; s <= kMostSplits && (s == 1 || kb >= 2 * s); s *= 2) {
-    const double waves = std::ceil(double(ceil_div(m, 128) * ceil_div(n, 128) * s) / (s > 2 ? sms - (kSms - kFourfold) : sms));
-    offer(false, 128, s, sums ? waves * (std::ceil(kb / s) * 0.27 + 8.2) + 0.3
-                              : waves * (std::ceil(kb / s) * 0.30 + 2.0) + 2.5 + (s > 1 ? 2.0 : 0.0));
+    const double waves = double(ceil_div(tiles * s, s > 2 ? std::max(4, sms - (kSms - kFourfold)) : sms));
+    offer(false, 128, s, tiles, sums ? waves * (double(ceil_div(int64_t(kb), s)) * 0.27 + 8.2) + 0.3
+                                     : waves * (double(ceil_div(int64_t(kb), s)) * 0.30 + 2.0 + (more ? 3.2 / s : 0.0)) +
+                                           2.5 + (s > 1 ? 2.0 : 0.0));
   }
-  return best;
+  return count;
 }
 
-// SMs for a kernel that is launched beside one of so many tiles: what that leaves, if
-// it is a third of them at least, else all (it then comes after the other).  Both
-// gradients and the bias of 1024 x 768 -> 768 take 12.6 us so, 17.4 with the weight's
-// planned for all SMs; of 1024 x 768 -> 2304 20.5 and 23.0.
-int beside(const Plan& plan, int tiles) {
-  const int64_t left = kSms - int64_t(tiles) * (plan.pairs ? 2 : plan.splits);
-  return int(left >= kSms / 3 ? left / 2 * 2 : kSms);
+Offer offer_of(int64_t m, int64_t n, int64_t k, bool sums, bool more, int sms) {
+  Offer all[kOffers];
+  const int count = offers_of(m, n, k, sums, more, sms, all);
+  return *std::min_element(all, all + count, [](const Offer& a, const Offer& b) { return a.us < b.us; });
 }
 
 // Few tokens: features are the rows of the tiles, and the K blocks are shared out
@@ -1494,6 +1506,42 @@ Plan plan_few(int64_t tokens, int64_t features, int64_t k) {
 }
 
 constexpr int kFewTokens = 64;
+
+// The plans of both gradients: the weight's beside the inputs', on the SMs that one
+// leaves, where that is quicker than one after the other, which saves 2 us of starting
+// (us, with the bias's; one after the other: 2048 x 768 -> 768 15.5 and 18.7; 4096 x 512
+// -> 512 14.9 and 19.5; 1024 x 768 -> 768 12.7 and 17.4; 16384 x 256 -> 256 with a slope
+// 28.8 and 38.2).
+void plan_both(int64_t tokens, int64_t in, int64_t out, bool slope, Plan* dx, Plan* dw) {
+  Offer first[kOffers];
+  int count = 1;
+  if (tokens <= kFewTokens) {
+    first[0].plan = plan_few(tokens, in, out);
+    first[0].sms = ceil_div(in, 128) * ceil_div(tokens, first[0].plan.bn) * first[0].plan.splits;
+    first[0].us = 7.0;
+  } else {
+    count = offers_of(tokens, in, out, false, slope, kSms, first);
+  }
+  const Offer after = offer_of(out, in, tokens, true, false, kSms);
+  double least = 0;
+  for (int i = 0; i < count; ++i) {
+    const int left = int(std::max<int64_t>(0, kSms - first[i].sms)) / 2 * 2;
+    double us = first[i].us + after.us - 2.0;
+    Plan second = after.plan;
+    if (left >= kLeast) {
+      const Offer beside = offer_of(out, in, tokens, true, false, left);
+      if (std::max(first[i].us, beside.us) < us) {
+        us = std::max(first[i].us, beside.us);
+        second = beside.plan;
+      }
+    }
+    if (i == 0 || us < least) {
+      least = us;
+      *dx = first[i].plan;
+      *dw = second;
+    }
+  }
+}
 
 // The product of a and b, whose k lies along their columns (or, mn, along their
 // rows), as the plan's tiles.  False: the driver refuses a map.
@@ -1781,7 +1829,8 @@ extern "C" int muon_linear(const muon_linear_args_t* args, void* workspace, size
     w.pack(&at, &packs);
     static One<Forward> product;   // large; this call holds the library lock
     const bool few = T <= kFewTokens;
-    const Plan plan = few ? plan_few(T, N, K) : plan_of(T, N, K, false);
+    const bool more = a.activation != MUON_ACT_NONE || f.drop.least || a.pre || a.residual;
+    const Plan plan = few ? plan_few(T, N, K) : offer_of(T, N, K, false, more, kSms).plan;
     if (!(few ? prepare(plan, w, false, x, false, f, &product) : prepare(plan, x, false, w, false, f, &product)))
       return fail_with(MUON_ERR_CUDA, "the driver refuses a map of x or weight");
     cudaError_t e = launch_packs(packs, s, &launches);
@@ -1854,16 +1903,13 @@ extern "C" int muon_linear_grad(const muon_linear_grad_args_t* args, void* works
     static One<InputGrad> first;    // large; this call holds the library lock
     static One<WeightGrad> second;
     bool fine = true;
-    if (dx) {
-      plans[0] = few ? plan_few(T, K, N) : plan_of(T, K, N, false);
+    if (dx && dw) plan_both(T, K, N, slope, &plans[0], &plans[1]);
+    else if (dx) plans[0] = few ? plan_few(T, K, N) : offer_of(T, K, N, false, slope, kSms).plan;
+    else if (dw) plans[1] = offer_of(N, K, T, true, false, kSms).plan;
+    if (dx)
       fine = few ? prepare(plans[0], o.weight, true, o.dout, false, f, &first)
                  : prepare(plans[0], o.dout, false, o.weight, true, f, &first);
-    }
-    if (dw && fine) {
-      const int left = dx ? beside(plans[0], first.tiles) : kSms;
-      plans[1] = plan_of(N, K, T, true, left);
-      fine = prepare(plans[1], o.dout, true, o.x, true, g, &second);
-    }
+    if (dw && fine) fine = prepare(plans[1], o.dout, true, o.x, true, g, &second);
     if (!fine) return fail_with(MUON_ERR_CUDA, "the driver refuses a map of an operand");
     cudaError_t e = launch_packs(packs, s, &launches);
     if (e != cudaSuccess) return lay::end_call(launches, e);
