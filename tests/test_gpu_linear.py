@@ -138,7 +138,8 @@ def test_very_many_terms():
 
 
 @pytest.mark.parametrize("parts,overwrite", [(0, False), (8, True)])
-@pytest.mark.parametrize("T,K,N", LARGE + [(40, 2568, 4352), (1, 1032, 2056)])
+@pytest.mark.parametrize("T,K,N", LARGE + [(40, 2568, 4352), (1, 1032, 2056), (2048, 768, 768), (4096, 512, 512),
+                                            (16384, 256, 256), (2047, 1001, 763)])
 def test_gradients_of_many_tiles(T, K, N, parts, overwrite):
     x, dout, w = normal(1, (T, K)), normal(2, (T, N), 0.1), normal(3, (N, K), 1 / math.sqrt(K))
     pre = normal(4, (T, K))
