@@ -755,8 +755,8 @@ MUON_API int muon_dropout(const void* x, int64_t x_stride, const void* residual,
  *           (a, b) -> (a cos - b sin, b cos + a sin)
  * Pair i is elements (i, pairs + i), or (2 i, 2 i + 1) if interleaved; the
  * elements behind the pairs are not turned.  Angles are formed as whole turns
- * in 64-bit fixed point, so far positions lose nothing but the 2^-53 of
- * inv_freq itself.  A token with a NEGATIVE position on any axis is no token:
+ * in 64-bit fixed point, so far positions lose nothing but 2^-52 of inv_freq
+ * and a step of 2^-64 turns a position.  A token with a NEGATIVE position on any axis is no token:
  * its heads are not read and its rows of out are zeros.
  *   groups    : host, n_groups = 1 or 2 (queries, keys): x and out device, of
  *               dtype, element d of head h of token t at t * stride +

@@ -782,10 +782,11 @@ int make_rotation(RotArgs* a, int n_groups, int dtype, int64_t n_tokens, int hea
   for (int i = 0; i < pairs; ++i) {
     if (!std::isfinite(inv_freq[i])) return fail_with(MUON_ERR_INVALID, "inv_freq must be finite");
     if (axis && (axis[i] < 0 || axis[i] >= axes)) return fail_with(MUON_ERR_INVALID, "axis must be in [0, axes)");
-    // turns per position, of which the whole ones do not matter
-    const double turns = inv_freq[i] / 6.283185307179586476925;
-    const double part = std::ldexp(turns - std::floor(turns), 64);
-    a->turns[i] = part >= 18446744073709551615.0 ? 0 : static_cast<uint64_t>(part);
+    // turns per position, of which the whole ones do not matter; those of a pair that turns backwards are taken from a
+    // whole turn in fixed point, where a small one's last bits stay
+    const double turns = std::fabs(inv_freq[i]) / 6.283185307179586476925;
+    const uint64_t part = static_cast<uint64_t>(std::ldexp(turns - std::floor(turns), 64));   // below 2^64: turns is not
+    a->turns[i] = inv_freq[i] < 0 ? ~part + 1 : part;                                         // below 0
     a->axis[i] = static_cast<uint8_t>(axis ? axis[i] : 0);
   }
   return MUON_OK;
