@@ -765,8 +765,9 @@ MUON_API int muon_dropout(const void* x, int64_t x_stride, const void* residual,
  *               nothing else.  Rows of different tokens or heads of an out may
  *               not overlap: head_stride >= head_dim and either stride >=
  *               heads' span or head_stride >= tokens' span
- *   positions : device, n_tokens x axes of positions_type, contiguous; NULL if
- *               pairs = 0
+ *   positions : device, n_tokens x axes of positions_type, contiguous; may be
+ *               NULL if pairs = 0: then every token is one (and axes and
+ *               positions_type are not looked at)
  *   inv_freq  : host, pairs finite doubles (radians per position)
  *   axis      : host, pairs of [0, axes), or NULL: 0
  * Errors: MUON_ERR_INVALID; head_dim is in [1, 256], axes in [1, 8]. */

@@ -709,7 +709,8 @@ def norm_rotary(q, k=None, positions=None, inv_freq=None, axis=None, interleaved
     and keys in one pass: q and k tokens x heads x head_dim (leading dimensions
     are joined), bf16 or fp32, of any strides whose heads are contiguous, such
     as parts of one packed projection.  positions: int32 or int64, one per
-    token or tokens x axes, a negative one meaning "no token" (zeros);
+    token or tokens x axes, a negative one meaning "no token" (zeros), also
+    where nothing is turned (None then: every token is one);
     inv_freq, axis: numpy float64 and int32, as rotary_frequencies gives them,
     None: no rotation; norm: divide by the root mean square, times the weight
     if there is one.  q_out, k_out: tensors to fill, q and k themselves too.

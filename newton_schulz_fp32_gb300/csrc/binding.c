@@ -979,17 +979,18 @@ static int turns_of(PyObject* positions, PyObject* freq, PyObject* axis, PyObjec
   t->interleaved = PyObject_IsTrue(interleaved);
   t->norm = PyObject_IsTrue(norm);
   if (t->interleaved < 0 || t->norm < 0 || real(eps, &t->eps)) return -1;
-  if (freq == Py_None) return 0;
-  if (PyObject_GetBuffer(freq, &t->freq, PyBUF_ND | PyBUF_FORMAT)) return -1;
-  if (t->freq.ndim != 1 || t->freq.itemsize != 8 || !t->freq.format || t->freq.format[strlen(t->freq.format) - 1] != 'd')
-    return refuse("%s must be a 1-D float64 array", "inv_freq");
-  if (t->freq.len / 8 > INT_MAX) return refuse("%s is too long", "inv_freq");
-  t->pairs = (int)(t->freq.len / 8);
-  if (axis != Py_None) {
-    if (PyObject_GetBuffer(axis, &t->axis, PyBUF_ND | PyBUF_FORMAT)) return -1;
-    if (t->axis.ndim != 1 || t->axis.itemsize != 4 || !t->axis.format ||
-        t->axis.format[strlen(t->axis.format) - 1] != 'i' || t->axis.len / 4 != t->pairs)
-      return refuse("%s must be a 1-D int32 array of inv_freq's length", "axis");
+  if (freq != Py_None) {
+    if (PyObject_GetBuffer(freq, &t->freq, PyBUF_ND | PyBUF_FORMAT)) return -1;
+    if (t->freq.ndim != 1 || t->freq.itemsize != 8 || !t->freq.format || t->freq.format[strlen(t->freq.format) - 1] != 'd')
+      return refuse("%s must be a 1-D float64 array", "inv_freq");
+    if (t->freq.len / 8 > INT_MAX) return refuse("%s is too long", "inv_freq");
+    t->pairs = (int)(t->freq.len / 8);
+    if (axis != Py_None) {
+      if (PyObject_GetBuffer(axis, &t->axis, PyBUF_ND | PyBUF_FORMAT)) return -1;
+      if (t->axis.ndim != 1 || t->axis.itemsize != 4 || !t->axis.format ||
+          t->axis.format[strlen(t->axis.format) - 1] != 'i' || t->axis.len / 4 != t->pairs)
+        return refuse("%s must be a 1-D int32 array of inv_freq's length", "axis");
+    }
   }
   if (positions == Py_None) return t->pairs ? refuse("%s are needed for a rotation", "positions") : 0;
   long long count;

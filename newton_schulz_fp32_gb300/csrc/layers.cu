@@ -162,9 +162,9 @@ __device__ __forceinline__ int64_t position(const RotArgs& a, int64_t t, int axi
                  : reinterpret_cast<const int32_t*>(a.positions)[i];
 }
 
-// A token's position on axis `lane`; 0 behind the axes.
+// A token's position on axis `lane`; 0 behind the axes (of which there are none without positions).
 __device__ __forceinline__ int64_t lane_position(const RotArgs& a, int64_t t, int lane) {
-  return a.pairs && lane < a.axes ? position(a, t, lane) : 0;
+  return lane < a.axes ? position(a, t, lane) : 0;
 }
 
 // cos and sin of a pair's angle: position * turns wraps at whole turns by itself;
@@ -769,13 +769,13 @@ int make_rotation(RotArgs* a, int n_groups, int dtype, int64_t n_tokens, int hea
   a->eps = eps;
   a->inv_dim = 1.f / float(head_dim);
   a->interleaved = interleaved;
-  if (!pairs) return MUON_OK;
+  if (!pairs && !positions) return MUON_OK;
   if (positions_type != MUON_INDEX_INT32 && positions_type != MUON_INDEX_INT64)
     return fail_with(MUON_ERR_INVALID, "unknown positions_type");
   if (axes < 1 || axes > MUON_MAX_AXES) return fail_with(MUON_ERR_INVALID, "axes must be in [1, MUON_MAX_AXES]");
   if (n_tokens > 0 && (!positions || misaligned(positions, positions_type == MUON_INDEX_INT64 ? 8 : 4)))
     return fail_with(MUON_ERR_INVALID, "positions is NULL or misaligned");
-  if (!inv_freq) return fail_with(MUON_ERR_INVALID, "inv_freq is NULL");
+  if (pairs && !inv_freq) return fail_with(MUON_ERR_INVALID, "inv_freq is NULL");
   a->positions = positions;
   a->pos64 = positions_type == MUON_INDEX_INT64;
   a->axes = axes;
@@ -933,7 +933,7 @@ extern "C" int muon_norm_rotary(const muon_heads_t* groups, int n_groups, int dt
     if (n_tokens == 0) return MUON_OK;
     if (n_tokens * total > (int64_t(1) << 33))
       return fail_with(MUON_ERR_UNSUPPORTED, "too many heads for one launch");
-    const Span pos(positions, pairs ? n_tokens : 0, axes, axes, a.pos64 ? 8 : 4);
+    const Span pos(a.positions, n_tokens, a.axes, a.axes, a.pos64 ? 8 : 4);
     for (int i = 0; i < n_groups; ++i) {
       for (int j = 0; j < n_groups; ++j) {
         const bool in_place = i == j && in[j].p == out[i].p && in[j].stride == out[i].stride &&
@@ -1023,7 +1023,7 @@ extern "C" int muon_norm_rotary_grad(const muon_heads_grad_t* groups, int n_grou
       return fail_with(MUON_ERR_INVALID, "workspace is NULL, misaligned or too small");
     if (n_tokens * total > (int64_t(1) << 33))
       return fail_with(MUON_ERR_UNSUPPORTED, "too many heads for one launch");
-    const Span pos(positions, pairs ? n_tokens : 0, axes, axes, a.pos64 ? 8 : 4);
+    const Span pos(a.positions, n_tokens, a.axes, a.axes, a.pos64 ? 8 : 4);
     const Span work(workspace, need ? 1 : 0, int64_t(need), int64_t(need), 1);
     const Span sums(accum, any ? 1 : 0, accum_elems, accum_elems, 4);
     if (work.meets(sums) || work.meets(pos) || sums.meets(pos))
