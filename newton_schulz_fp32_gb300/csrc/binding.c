@@ -959,6 +959,12 @@ static int head_weight(PyObject* t, const char* name, long long dim, int kind, c
   return 0;
 }
 
+/* Whether a buffer is one row of elements of this machine's own type `code`, `size` bytes each. */
+static int row_of(const Py_buffer* b, char code, Py_ssize_t size) {
+  const char* f = b->format;
+  return b->ndim == 1 && b->itemsize == size && f && *f != '>' && *f != '!' && f[strlen(f) - 1] == code;
+}
+
 /* positions (tensor or None), inv_freq and axis (buffers of float64 and int32, or None). */
 typedef struct {
   void* positions;
@@ -981,14 +987,12 @@ static int turns_of(PyObject* positions, PyObject* freq, PyObject* axis, PyObjec
   if (t->interleaved < 0 || t->norm < 0 || real(eps, &t->eps)) return -1;
   if (freq != Py_None) {
     if (PyObject_GetBuffer(freq, &t->freq, PyBUF_ND | PyBUF_FORMAT)) return -1;
-    if (t->freq.ndim != 1 || t->freq.itemsize != 8 || !t->freq.format || t->freq.format[strlen(t->freq.format) - 1] != 'd')
-      return refuse("%s must be a 1-D float64 array", "inv_freq");
+    if (!row_of(&t->freq, 'd', 8)) return refuse("%s must be a 1-D float64 array", "inv_freq");
     if (t->freq.len / 8 > INT_MAX) return refuse("%s is too long", "inv_freq");
     t->pairs = (int)(t->freq.len / 8);
     if (axis != Py_None) {
       if (PyObject_GetBuffer(axis, &t->axis, PyBUF_ND | PyBUF_FORMAT)) return -1;
-      if (t->axis.ndim != 1 || t->axis.itemsize != 4 || !t->axis.format ||
-          t->axis.format[strlen(t->axis.format) - 1] != 'i' || t->axis.len / 4 != t->pairs)
+      if (!row_of(&t->axis, 'i', 4) || t->axis.len / 4 != t->pairs)
         return refuse("%s must be a 1-D int32 array of inv_freq's length", "axis");
     }
   }

@@ -1,4 +1,5 @@
-"""Positions without a rotation, on the host: they are looked at, checked and passed on."""
+"""Arguments of heads that are seldom seen, on the host: positions without a rotation are looked at, checked and
+passed on; arrays of another byte order are refused."""
 
 import numpy as np
 import pytest
@@ -32,3 +33,15 @@ def test_positions_reach_the_library(machine, shape, type_, axes, freq):  # noqa
     for bad in (torch.zeros(4, dtype=type_), torch.zeros(5), torch.zeros((5, 2), dtype=type_)[:, 0]):
         with pytest.raises(ValueError, match="positions"):
             nsg.norm_rotary(machine.tensor(torch.zeros(5, 2, 8)), None, machine.tensor(bad), freq)
+
+
+def test_arrays_of_another_byte_order_are_refused(machine):  # noqa: F811
+    """Their bytes would be read the wrong way round."""
+    q, pos = machine.tensor(torch.zeros(5, 2, 8)), machine.tensor(torch.zeros(5, dtype=torch.int64))
+    freq, axis = np.ones(4), np.zeros(4, dtype=np.int32)
+    for f, a, word in ((freq.astype(">f8"), axis, "inv_freq must be"), (freq, axis.astype(">i4"), "axis must be")):
+        with pytest.raises(ValueError, match=word):
+            nsg.norm_rotary(q, None, pos, f, a)
+    for f, a in ((freq, axis), (freq.astype("<f8"), axis.astype("<i4"))):
+        nsg.norm_rotary(q, None, pos, f, a)
+    assert len(machine.layer_calls) == 2
