@@ -244,7 +244,7 @@ struct Forward {
   int cols, bias32, act;
   Dropout drop;
 
-  // A result in FP32 is summed in pieces of kDepth K blocks.
+  // A result in FP32 is summed in passes of kDepth K blocks, not kDepthRounded.
   __device__ __forceinline__ bool exact() const { return out.fp32; }
   __device__ __forceinline__ bool halves() const { return !residual.fp32; }
   __device__ __forceinline__ void fetch(uint32_t slots, int half, int64_t t0, int64_t n0, int lane) const {
@@ -621,16 +621,17 @@ struct One {
 
 constexpr int BK = 64;
 
-// Tensor memory's additions cut off instead of rounding, all in one direction: half
-// a unit of 2^-23 every 16 terms.  For a result in FP32 so many K blocks of 64 terms
-// are summed there and FP32 registers add those (a sum of 32768 terms is then off by
-// 1e-6 of its size, where one pass would leave 6e-5).  What is rounded to bf16, by
-// 2e-3, is summed in one pass up to 65536 terms (2e-4 at worst).
-// Gradients of up to 2048 tokens are nearer than that to begin with (3e-7 by FP32
-// sums of values whose mean is not 0) and take shorter pieces (1.1e-6 in one pass of
-// 1024 terms, 3e-7 in these); for a layer's results, whose weights have no such
-// mean, one pass of 1024 gives 2.3e-7.
-constexpr int kDepth = 16, kDepthFew = 4, kFewBlocks = 32, kMostBlocks = 1024;
+// Tensor memory adds 16 terms at a time and cuts off instead of rounding, all in one
+// direction: about half a unit of 2^-23 of the sum a step at first, and more once the
+// sum is 2^8 times a term and the last of a product's 16 bits lie below its unit.  Of
+// terms of one sign one pass loses 3.8e-7 of its sum (256 terms), 2.2e-6 (1024), 1.4e-5
+// (4096), 8.3e-5 (16384), 3.9e-4 (65536).  So a sum is formed in passes of so many K
+// blocks of 64 terms, which FP32 registers add up: 16 for a result in FP32 and for
+// accum; 64 for what is rounded to bf16, by up to 3.9e-3 (8192 x 14336 -> 4096 takes 2%
+// longer than in one pass; in passes of 16 8192 x 4096 -> 14336 would take 5% longer, with
+// a residual 15%); 4 for gradients of up to 2048 tokens, the more exact ones, where a K
+// block of 256 x 256 takes 0.345 us instead of 0.26.
+constexpr int kDepth = 16, kDepthRounded = 64, kDepthFew = 4, kFewBlocks = 32;
 
 __device__ __forceinline__ uint32_t idesc_of(const Product& p, int m, int n) {
   return make_idesc(p.b_mn != 0, m, n) | (p.a_mn ? 1u << 15 : 0u);
@@ -732,7 +733,7 @@ k_linear_pair(const __grid_constant__ One<E> w, int late, int* err) {
   const Product& p = w.p;
   const int nk = p.k;
   const bool exact = w.e.exact();
-  const int depth = !exact && nk <= kMostBlocks ? max(nk, 1) : S::kSums && nk <= kFewBlocks ? kDepthFew : kDepth;
+  const int depth = !exact ? kDepthRounded : S::kSums && nk <= kFewBlocks ? kDepthFew : kDepth;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kStages; ++s) {
