@@ -785,7 +785,6 @@ static PyObject* py_linear_grad(PyObject* self, PyObject* const* a, Py_ssize_t n
   if (bf16_rows(a[1], "dout", &d, &p)) return NULL;
   l.dout = p;
   if (param_of(a[4], "param", &param, &l.param) || param_of(a[5], "bias_param", &bias, &l.bias)) return NULL;
-  if (d.cols > INT_MAX) return refuse("%s has too many columns", "dout"), NULL;
   long long in = -1;
   if (a[2] != Py_None) {
     if (bf16_rows(a[2], "x", &x, &p)) return NULL;

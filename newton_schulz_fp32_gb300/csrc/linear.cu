@@ -1308,10 +1308,10 @@ constexpr int kBiasLoads = 8;      // rows a thread has under way
 // rows start on 16 bytes.  Bound by memory: 16384 x 2304 in 15 us (5 TB/s).
 template <bool VEC>
 __global__ void __launch_bounds__(kBiasThreads)
-k_bias_grad(const BiasGrad a, const __grid_constant__ Segments sg, int blocks, int late) {
+k_bias_grad(const BiasGrad a, const __grid_constant__ Segments sg, int blocks) {
   __shared__ float sums[kBiasRows][kBiasColumns + 4];
   __shared__ float all[kBiasColumns];
-  begin_kernel(late);
+  begin_kernel(0);   // the call's first, but for copies of operands
   const int slab = blockIdx.x / blocks, rank = blockIdx.x % blocks;
   const int x = threadIdx.x % 8, y = threadIdx.x / 8;
   const int64_t c = int64_t(slab) * kBiasColumns + x * 8;
@@ -1368,17 +1368,16 @@ k_bias_grad(const BiasGrad a, const __grid_constant__ Segments sg, int blocks, i
   }
   __syncwarp();
   if (blocks > 1) cluster_sync();
-  end_kernel(late);
 }
 
-cudaError_t launch_bias(const BiasGrad& a, const Segments& sg, int late, cudaStream_t s) {
+cudaError_t launch_bias(const BiasGrad& a, const Segments& sg, cudaStream_t s) {
   const int slabs = (a.cols + kBiasColumns - 1) / kBiasColumns;
   // up to eight blocks of at least 64 tokens to 64 columns, four per SM
   int blocks = 1;
   while (blocks < 8 && int64_t(blocks) * 2 * slabs <= 4 * 152 && a.tokens >= 64 * 2 * blocks) blocks *= 2;
   const bool vec = !misaligned(a.dout, 16) && (a.tokens <= 1 || a.stride % 8 == 0);
   return launch(vec ? k_bias_grad<true> : k_bias_grad<false>, unsigned(slabs) * blocks, kBiasThreads, blocks, true, s, 0, a, sg,
-                blocks, late);
+                blocks);
 }
 
 // ------------------------------------------------------------------ host
@@ -1920,7 +1919,7 @@ extern "C" int muon_linear_grad(const muon_linear_grad_args_t* args, void* works
     if (a.bias) {
       const BiasGrad b{static_cast<const __nv_bfloat16*>(o.dout.p ? o.dout.p : a.dout), o.dout.p ? o.dout.stride : a.dout_stride,
                        T, N, a.accum, a.scale, a.overwrite};
-      if ((e = launch_bias(b, places.bias, late, s)) != cudaSuccess) return lay::end_call(launches, e);
+      if ((e = launch_bias(b, places.bias, s)) != cudaSuccess) return lay::end_call(launches, e);
       ++launches;
       late = 1;
     }
