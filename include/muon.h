@@ -759,8 +759,10 @@ MUON_API int muon_dropout(const void* x, int64_t x_stride, const void* residual,
  * Pair i is elements (i, pairs + i), or (2 i, 2 i + 1) if interleaved; the
  * elements behind the pairs are not turned.  Angles are formed as whole turns
  * in 64-bit fixed point, so far positions lose nothing but 2^-52 of inv_freq
- * and a step of 2^-64 turns a position.  A token with a NEGATIVE position on any axis is no token:
- * its heads are not read and its rows of out are zeros.
+ * and a step of 2^-64 turns a position.  The mean of squares is FP32: a head
+ * whose squares pass its range comes out as zeros (NaN where it is infinite).
+ * A token with a NEGATIVE position on any axis is no token: its rows of out are
+ * zeros, whatever its heads hold; their memory is read all the same.
  *   groups    : host, n_groups = 1 or 2 (queries, keys): x and out device, of
  *               dtype, element d of head h of token t at t * stride +
  *               h * head_stride + d; weight device, head_dim of dtype, or NULL.
@@ -795,7 +797,7 @@ MUON_API int muon_norm_rotary(const muon_heads_t* groups, int n_groups, int dtyp
  *     accum[param] = (overwrite ? 0 : accum[param]) + scale * d loss / d weight
  * (param: rows * cols = head_dim).  x is the heads before the norm; it is not
  * looked at if norm = 0.  Tokens with a negative position take no part: their
- * rows of dx are zeros.  dx may be dout itself, or x itself (same address and
+ * rows of dx are zeros, whatever dout and x hold there (both are read).  dx may be dout itself, or x itself (same address and
  * strides).
  *   workspace : muon_norm_rotary_grad_workspace bytes, needed for a param
  * Errors: as muon_norm_rotary and muon_embedding_grad. */

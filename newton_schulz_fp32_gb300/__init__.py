@@ -46,6 +46,7 @@ EXPORTED = ["muon_accumulate", "muon_accumulate_n", "muon_step", "muon_newton_sc
             "muon_preference_loss", "muon_preference_loss_workspace", "muon_linear",
             "muon_linear_workspace", "muon_linear_grad", "muon_linear_grad_workspace", "muon_dropout",
             "muon_norm_rotary", "muon_norm_rotary_grad", "muon_norm_rotary_grad_workspace"]
+# gelu is the tanh form, u (1 + tanh(sqrt(2 / pi) (u + 0.044715 u^3))) / 2
 ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "relu2": 2, "gelu": 3, "silu": 4}
 CLIP_MODES = {"update": 0, "grad": 1}
 
@@ -607,7 +608,7 @@ def linear(x, weight, bias=None, activation=None, residual=None, dropout: float 
     """residual + dropout(activation(x weight^T + bias)) (muon_linear): x
     tokens x in_features (leading dimensions are joined, by a copy where their
     layout needs one), weight out_features x in_features, both bf16; bias bf16
-    or fp32; activation one of ACTIVATIONS.  out_dtype: bf16 or fp32 (default:
+    or fp32; activation one of ACTIVATIONS ("gelu": its tanh form).  out_dtype: bf16 or fp32 (default:
     out's, the residual's or bf16).  rng: an int64 CUDA tensor (seed, step),
     site: which of the model's dropouts this is.  pre: True or a bf16 tensor to
     fill: x weight^T + bias is kept too, for the gradient.  out may be the
@@ -709,8 +710,9 @@ def norm_rotary(q, k=None, positions=None, inv_freq=None, axis=None, interleaved
     and keys in one pass: q and k tokens x heads x head_dim (leading dimensions
     are joined), bf16 or fp32, of any strides whose heads are contiguous, such
     as parts of one packed projection.  positions: int32 or int64, one per
-    token or tokens x axes, a negative one meaning "no token" (zeros), also
-    where nothing is turned (None then: every token is one);
+    token (as many as there are tokens, whatever their shape) or tokens x axes, a
+    negative one meaning "no token" (zeros), also where nothing is turned (None
+    then: every token is one);
     inv_freq, axis: numpy float64 and int32, as rotary_frequencies gives them,
     None: no rotation; norm: divide by the root mean square, times the weight
     if there is one.  q_out, k_out: tensors to fill, q and k themselves too.

@@ -56,9 +56,9 @@ __device__ __forceinline__ void store8(T* p, int left, const float* f) {
 }
 
 // blockDim.x threads along a row, eight columns (one draw of 128 bits) each.  Bound
-// by memory: 16384 x 4096 bf16 with a residual in 65 us, 6.2 TB/s of reads and
+// by memory: 16384 x 4096 bf16 with a residual in 61 us, 6.6 TB/s of reads and
 // writes; issue slots are 56% busy behind it.  One row per thread and blocks of 128
-// threads were the best of a sweep (two rows 84 us, four 121; 256 threads 72).
+// threads were the best of a sweep (65 us then; two rows 84, four 121; 256 threads 72).
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kDropThreads) k_dropout(const DropArgs a) {
   tok::wait_before();
@@ -106,7 +106,7 @@ cudaError_t launch_dropout(const DropArgs& a, cudaStream_t s) {
 // For a head x with weight w, position p and frequencies f:
 //     n = x / sqrt(mean x^2 + eps) * w,   (a, b) -> (a cos - b sin, b cos + a sin) with the angle p f.
 // Both directions are bound by memory, each element moved once (16384 tokens of 40
-// heads of 128 bf16: 64 us, 5.2 TB/s; the gradients 111 us, 4.5 TB/s, issue slots 60%
+// heads of 128 bf16: 57 us, 5.9 TB/s; the gradients 103 us, 4.9 TB/s, issue slots 60%
 // busy), and short of it by latency: 16 warps per SM hold what is on its way in
 // registers.
 
@@ -338,7 +338,8 @@ __device__ __forceinline__ void head_sums(float (&v)[U], int lanes) {
 // Where a warp is in its work: tokens (or pieces of their heads), in each the two
 // groups, in each batches of heads.  What comes next is fetched before what is
 // there is worked on, across batches, groups and tokens (16384 tokens of 40
-// heads: 64 us; 70 with a fresh start at each token and group).
+// heads, when that was the last step: 64 us against 70 with a fresh start at each
+// token and group).
 struct Cursor {
   int64_t task, t;
   int which, h0, h1;   // group, and its heads in this piece
@@ -517,8 +518,8 @@ __global__ void __launch_bounds__(32 * kRotWarps, 2) k_norm_rotary(const __grid_
 //     dw += g n,   dx = r (g w - n mean(g w n)).
 // A lane keeps its columns' dw over all tokens of its warp; blocks leave
 // partial sums, which k_norm_join adds in order.  (Fetching ahead across tokens, as
-// k_norm_rotary does, took longer here: 124 us with the groups one after the
-// other, 150 with sums of both chosen from, 115 this way.)
+// k_norm_rotary does, took longer here: 8% with the groups one after the other, 30%
+// with sums of both chosen from.)
 template <typename T, class S>
 __global__ void __launch_bounds__(32 * kRotWarps, 2) k_norm_rotary_grad(const __grid_constant__ RotArgs a, int lanes) {
   constexpr int P = S::P, NU = S::NU, U = NU > 1 ? 1 : 2;

@@ -68,9 +68,10 @@ constexpr float kGelu3 = 0.07135481627260025f;   // 0.044715 of it
 
 __device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
 
-// __expf's error grows with its argument (2 + |x| / 2 units or so); the sigmoid
-// of an argument where that shows is within 2^-24 of 0 or 1, or is what a value
-// that small is rounded to anyway.
+// CUDA bounds __expf's error by 2 + floor(|1.173 x|) units and __fdividef's by 2, so
+// that the sigmoid is off by (4 + 1.2 |x|) 2^-23 of itself at most where it is small,
+// by less than that next to 1.  Where 1 + exp(-x) passes 2^126 (x < -87.3), __fdividef
+// gives 0 for what is below 2^-126.
 __device__ __forceinline__ float activation(float u, int kind) {
   switch (kind) {
     case MUON_ACT_RELU: return u > 0.f ? u : u == u ? 0.f : u;

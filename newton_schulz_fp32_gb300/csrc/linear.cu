@@ -1305,7 +1305,8 @@ constexpr int kBiasLoads = 8;      // rows a thread has under way
 
 // Sums of dout's columns.  A cluster of blocks shares out the tokens of 64
 // columns; their sums meet in the first block, in the order of the blocks.  VEC:
-// rows start on 16 bytes.  Bound by memory: 16384 x 2304 in 15 us (5 TB/s).
+// rows start on 16 bytes.  Bound by memory: 8192 x 8192 in 26 us (5.2 TB/s), 16384 x
+// 2304 in 20 (13 where dout lies in L2).
 template <bool VEC>
 __global__ void __launch_bounds__(kBiasThreads)
 k_bias_grad(const BiasGrad a, const __grid_constant__ Segments sg, int blocks) {
@@ -1439,7 +1440,7 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // Starting, the first operands' latency and the results cost 7.2, 4.7 and 4.5 us, a
 // cluster's sums 2 more.  Sums into accum (a weight's gradient, both operands along
 // their rows, each row a piece of bulk copies) cost 8.8, 5.7 and 8.5, however many
-// blocks share them out, and pieces of kDepthFew K blocks more for each.  Measured
+// blocks share them out, and passes of kDepthFew K blocks more for each.  Measured
 // on pairs at 128 / pairs at 256 / single SMs without a split / by 2 / by 4 (us,
 // chosen: *): 1024 x 768 -> 768 7.8* / 12.0 / 8.9 / 9.4 / 16.5; 512 x 4096 -> 1024
 // 18.0 / 25.5 / 20.8 / 15.1 / 12.0*; 1024 x 1024 -> 4096 13.0* / 13.9 / 19.5 / 38 / 66;
