@@ -807,12 +807,14 @@ static PyObject* py_linear_grad(PyObject* self, PyObject* const* a, Py_ssize_t n
   }
   if (in < 0) in = l.param ? l.param->cols : 1;
   if (sums_of(a[0], a[6], a[7], a[8], l.param || l.bias, &sums)) return NULL;
-  if (a[10] != Py_None) {
-    if (matrix(a[10], "pre", d.rows, in, 0, &s, &p)) return NULL;
-    l.pre = p;
-    l.pre_stride = s.stride;
-  } else if (want_dx && act != MUON_ACT_NONE && d.rows) {
-    return refuse("%s is needed for the activation's slope", "pre"), NULL;
+  if (want_dx && act != MUON_ACT_NONE) {   /* looked at for the slope alone */
+    if (a[10] == Py_None) {
+      if (d.rows) return refuse("%s is needed for the activation's slope", "pre"), NULL;
+    } else {
+      if (matrix(a[10], "pre", d.rows, in, 0, &s, &p)) return NULL;
+      l.pre = p;
+      l.pre_stride = s.stride;
+    }
   }
   PyObject* tensors[7] = {a[1], a[0], a[2], a[3], a[10], PyBool_Check(a[11]) ? NULL : a[11], a[12]};
   const int here = placed(tensors, 7, &device);
